@@ -82,7 +82,9 @@ typedef enum {
   SSD_ERR_UNSUPPORTED = 8, /* no launch configuration fits this device / shape   */
   SSD_ERR_WORKSPACE = 9,   /* workspace missing or smaller than required         */
   SSD_ERR_GAMMA = 10,      /* (device) a per-request gamma above gamma_max       */
-  SSD_ERR_DRAW = 11        /* (device) a draw found no token of positive weight  */
+  SSD_ERR_DRAW = 11,       /* (device) a draw found no token of positive weight  */
+  SSD_ERR_PAGE = 12,       /* (device) a page number outside [0, n_pages)        */
+  SSD_ERR_LENGTH = 13      /* (device) a length or count out of range            */
 } ssd_status;
 
 typedef enum { SSD_BF16 = 0, SSD_F32 = 1 } ssd_dtype;
@@ -358,6 +360,90 @@ ssd_status ssd_debug_saguaro_stats(const void* target_logits, const void* draft_
  * for request b < B and position i < W, the accept, resample / bonus and
  * Saguaro uniforms (Philox4x32-10 words 0, 1, 2 of counter (b, i, 0, 0)). */
 ssd_status ssd_debug_uniforms(uint64_t seed, int B, int W, float* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The target's key/value cache, held in 4 bits: written as tokens arrive, read
+ * back, and attended to by the gamma + 1 query tokens of a verification round.
+ * A rejected draft token is undone by not advancing the request's length; its
+ * place is written again by a later call.
+ *
+ * Numbers: 16 consecutive elements of a head's row share a scale
+ *   s = max|x| / 7 rounded to 4 bits of significand (multiples of 2^-17 below
+ *   2^-14, at most 240), one byte; each element is the integer x / s rounded to
+ * the nearest, ties to even, and held to -7..7.  4.5 bits per element; the
+ * values n s are exact in bf16.  Rounding is decided exactly: the same inputs
+ * give the same cache on every path.  A NaN makes its whole group read back as
+ * NaN; infinities and magnitudes above 1680 saturate at 7 * 240.
+ *
+ * Pages: a pool of n_pages pages of page_size tokens (a multiple of 16) holds
+ * for each kv head blocks of 16 tokens of 18 * head_dim bytes.  Request b's
+ * token at position t lives in page page_table[b, t / page_size].  Requests may
+ * share pages that no call writes.  The order of bytes inside a block is the
+ * library's own: only ssd_kv_append writes it.
+ * --------------------------------------------------------------------------- */
+typedef struct {
+  void* pages;               /* n_pages * ssd_kv_page_bytes(...) bytes, 16-byte aligned */
+  int64_t n_pages;
+  int n_kv_heads;            /* >= 1                                               */
+  int head_dim;              /* 64, 128 or 256                                     */
+  int page_size;             /* tokens per page, a multiple of 16                  */
+  int max_pages;             /* width of the page table                            */
+  const int32_t* page_table; /* device [B, max_pages]                              */
+} ssd_kv_cache;
+
+/* Bytes of one page (0 for a bad shape). */
+size_t ssd_kv_page_bytes(int n_kv_heads, int head_dim, int page_size);
+
+/* Workspace of the calls below (0 for a bad shape): a status word, read by
+ * ssd_read_status, and the attention's partial results.  n_q = 0 gives what
+ * ssd_kv_append and ssd_kv_read need.  Zero it once (ssd_workspace_init). */
+size_t ssd_kv_workspace_bytes(int n_q, int n_heads, int n_kv_heads, int head_dim);
+
+/* Write n_new[b] new tokens of each request at positions kv_len[b] ..
+ * kv_len[b] + n_new[b] - 1.
+ *
+ *   kv_len    device [B]: tokens the request's cache holds before the call (not
+ *             changed); n_new device [B], or NULL: n tokens of every request
+ *   k, v      [B, n, n_kv_heads, head_dim] bf16 or fp32, any element strides of
+ *             request, token and head, elements of a head contiguous; rows past
+ *             n_new[b] are not read
+ *
+ * Blocks that the call writes to belong to one request of the call. */
+ssd_status ssd_kv_append(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_new, const void* k,
+                         const int64_t k_strides[3], const void* v, const int64_t v_strides[3], ssd_dtype dtype, int B,
+                         int n, void* workspace, size_t ws_bytes, void* stream);
+
+/* The values held for positions start[b] .. start[b] + count[b] - 1 (count NULL:
+ * n of every request), as out_k, out_v [B, n, n_kv_heads, head_dim], contiguous
+ * and 16-byte aligned.  Rows past count[b] are zero.  bf16 and fp32 hold them
+ * exactly. */
+ssd_status ssd_kv_read(const ssd_kv_cache* cache, const int32_t* start, const int32_t* count, ssd_dtype dtype, int B,
+                       int n, void* out_k, void* out_v, void* workspace, size_t ws_bytes, void* stream);
+
+/* Attention of n_q[b] query tokens of each request (gamma + 1 of a
+ * verification round, or 1) over its cache.
+ *
+ *   q         [B, n, n_heads, head_dim] bf16 or fp32, strides as for k; query
+ *             head j reads kv head j / (n_heads / n_kv_heads)
+ *   kv_len    device [B], as for ssd_kv_append: query i sits at position
+ *             kv_len[b] + i and sees the positions up to its own.  past_only
+ *             != 0: only those below kv_len[b] (the new tokens' own keys are
+ *             attended to elsewhere and joined by out_lse)
+ *   n_q       device [B], or NULL: n of every request
+ *   scale     factor of q.k (finite)
+ *   window    > 0: only the last `window` positions up to the query's own
+ *   out       [B, n, n_heads, head_dim], q's type, contiguous, 16-byte aligned
+ *   out_lse   [B, n, n_heads] fp32 or NULL: log sum exp(scale q.k)
+ *
+ * Rows that see nothing, and rows past n_q[b], have out = 0 and lse = -inf.
+ * What lies in masked places, NaN included, changes nothing.  1 <= n <=
+ * SSD_MAX_GAMMA + 1, n_heads / n_kv_heads at most 128.  A request with a bad
+ * length, or one that visits a bad page, has NaN outputs (ssd_kv_read: the rows
+ * on that page; ssd_kv_append writes nothing for them) and sets a status bit. */
+ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_q, const void* q,
+                            const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
+                            int window, int past_only, void* out, float* out_lse, void* workspace, size_t ws_bytes,
+                            void* stream);
 
 /* Read and clear the device status word of a workspace.  Synchronises
  * `stream`.  *status gets SSD_OK or the lowest-numbered device error seen

@@ -16,6 +16,7 @@
 
 #include "ssdv_device.cuh"
 #include "ssdv_internal.h"
+#include "ssdv_kv.cuh"
 
 namespace ssdv {
 
@@ -844,11 +845,163 @@ const char* ssd_status_str(ssd_status status) {
     case SSD_ERR_UNSUPPORTED: return "SSD_ERR_UNSUPPORTED: no launch configuration fits";
     case SSD_ERR_WORKSPACE: return "SSD_ERR_WORKSPACE: workspace missing or too small";
     case SSD_ERR_GAMMA: return "SSD_ERR_GAMMA: a per-request gamma above gamma_max";
+    case SSD_ERR_PAGE: return "SSD_ERR_PAGE: a page number outside the pool";
+    case SSD_ERR_LENGTH: return "SSD_ERR_LENGTH: a length or count out of range";
     case SSD_ERR_DRAW: return "SSD_ERR_DRAW: a draw found no token of positive weight";
   }
   return "unknown ssd_status";
 }
 
 const char* ssd_last_error(void) { return g_last_error.c_str(); }
+
+}  // extern "C"
+
+namespace ssdv {
+namespace {
+
+constexpr int kMaxHeadsPerKv = 128;
+constexpr size_t kKvWorkOffset = 256;  // partial results, after the status word
+
+bool kv_dim_valid(int D) { return D == 64 || D == 128 || D == 256; }
+
+// What the three cache calls share: the cache, the batch and the workspace.
+ssd_status kv_check(const ssd_kv_cache* c, const int32_t* len, const int32_t* count, ssd_dtype dtype, int B, int n,
+                    void* workspace, size_t ws_bytes, size_t need) {
+  if (esize_of(dtype) == 0) return fail(SSD_ERR_DTYPE, "unknown dtype %d", static_cast<int>(dtype));
+  if (!c || !c->pages || !c->page_table || !len || !workspace) return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 65535 || !kv_dim_valid(c->head_dim) || c->page_size < kKvBlock ||
+      c->page_size % kKvBlock || c->max_pages < 1 || c->n_pages < 1 || c->n_pages > INT32_MAX)
+    return fail(SSD_ERR_SHAPE, "bad cache: n_pages=%lld n_kv_heads=%d head_dim=%d page_size=%d max_pages=%d",
+                static_cast<long long>(c->n_pages), c->n_kv_heads, c->head_dim, c->page_size, c->max_pages);
+  if (static_cast<long long>(c->max_pages) * c->page_size > (1 << 30))
+    return fail(SSD_ERR_SHAPE, "max_pages * page_size above 2^30 tokens");
+  if (B < 1 || n < 1) return fail(SSD_ERR_SHAPE, "bad shape B=%d n=%d", B, n);
+  if (!aligned_to(c->pages, 16) || !aligned_to(c->page_table, 4) || !aligned_to(len, 4) ||
+      (count && !aligned_to(count, 4)) || !aligned_to(workspace, 16))
+    return fail(SSD_ERR_ALIGN, "pages and workspace need 16-byte alignment, int32 arrays 4-byte");
+  if (ws_bytes < need) return fail(SSD_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", ws_bytes, need);
+  return SSD_OK;
+}
+
+KvCacheArgs kv_cache_args(const ssd_kv_cache* c) {
+  return {static_cast<uint8_t*>(c->pages), static_cast<long long>(c->n_pages), c->n_kv_heads, c->page_size,
+          c->max_pages, c->page_table};
+}
+
+// Strides in elements; vec: every head's row starts on a 16-byte boundary.
+ssd_status kv_strides(const void* p, const int64_t* st, int es, long long* out, bool* vec) {
+  if (!aligned_to(p, es)) return fail(SSD_ERR_ALIGN, "a pointer is not aligned to its element size");
+  *vec = *vec && aligned_to(p, 16);
+  for (int i = 0; i < 3; ++i) {
+    if (st[i] < 0) return fail(SSD_ERR_SHAPE, "a negative stride");
+    out[i] = st[i];
+    *vec = *vec && st[i] * es % 16 == 0;
+  }
+  return SSD_OK;
+}
+
+}  // namespace
+}  // namespace ssdv
+
+extern "C" {
+
+size_t ssd_kv_page_bytes(int n_kv_heads, int head_dim, int page_size) {
+  if (n_kv_heads < 1 || !kv_dim_valid(head_dim) || page_size < kKvBlock || page_size % kKvBlock) return 0;
+  return static_cast<size_t>(page_size / kKvBlock) * n_kv_heads * kv_block_bytes(head_dim);
+}
+
+size_t ssd_kv_workspace_bytes(int n_q, int n_heads, int n_kv_heads, int head_dim) {
+  if (n_q == 0) return kKvWorkOffset;
+  if (n_q < 0 || n_q > SSD_MAX_GAMMA + 1 || n_kv_heads < 1 || n_heads < n_kv_heads || n_heads % n_kv_heads ||
+      n_heads / n_kv_heads > kMaxHeadsPerKv || !kv_dim_valid(head_dim))
+    return 0;
+  return kKvWorkOffset + kv_attention_work_bytes(n_q * (n_heads / n_kv_heads), head_dim);
+}
+
+ssd_status ssd_kv_append(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_new, const void* k,
+                         const int64_t k_strides[3], const void* v, const int64_t v_strides[3], ssd_dtype dtype, int B,
+                         int n, void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  ssd_status st = kv_check(cache, kv_len, n_new, dtype, B, n, workspace, ws_bytes, kKvWorkOffset);
+  if (st != SSD_OK) return st;
+  if (!k || !v || !k_strides || !v_strides) return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  KvStoreArgs a = {};
+  bool vec = true;
+  st = kv_strides(k, k_strides, esize_of(dtype), a.ks, &vec);
+  if (st == SSD_OK) st = kv_strides(v, v_strides, esize_of(dtype), a.vs, &vec);
+  if (st != SSD_OK) return st;
+  if (static_cast<double>(B) * (n / kKvBlock + 2) * cache->n_kv_heads * cache->head_dim >= 68719476736.0)
+    return fail(SSD_ERR_SHAPE, "grid too large");
+  a.c = kv_cache_args(cache);
+  a.start = kv_len;
+  a.count = n_new;
+  a.B = B;
+  a.n = n;
+  a.k = k;
+  a.v = v;
+  a.status = static_cast<int32_t*>(workspace);
+  const cudaError_t e = launch_kv_append(a, cache->head_dim, esize_of(dtype), vec, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SSD_OK : cuda_fail(e, "cache append launch");
+}
+
+ssd_status ssd_kv_read(const ssd_kv_cache* cache, const int32_t* start, const int32_t* count, ssd_dtype dtype, int B,
+                       int n, void* out_k, void* out_v, void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  const ssd_status st = kv_check(cache, start, count, dtype, B, n, workspace, ws_bytes, kKvWorkOffset);
+  if (st != SSD_OK) return st;
+  if (!out_k || !out_v) return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  if (!aligned_to(out_k, 16) || !aligned_to(out_v, 16)) return fail(SSD_ERR_ALIGN, "outputs need 16-byte alignment");
+  if (static_cast<double>(B) * (n / kKvBlock + 2) * cache->n_kv_heads * cache->head_dim >= 68719476736.0)
+    return fail(SSD_ERR_SHAPE, "grid too large");
+  KvStoreArgs a = {};
+  a.c = kv_cache_args(cache);
+  a.start = start;
+  a.count = count;
+  a.B = B;
+  a.n = n;
+  a.out_k = out_k;
+  a.out_v = out_v;
+  a.status = static_cast<int32_t*>(workspace);
+  const cudaError_t e = launch_kv_read(a, cache->head_dim, esize_of(dtype), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SSD_OK : cuda_fail(e, "cache read launch");
+}
+
+ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_q, const void* q,
+                            const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
+                            int window, int past_only, void* out, float* out_lse, void* workspace, size_t ws_bytes,
+                            void* stream) {
+  g_last_error.clear();
+  if (!(fabsf(scale) <= 3.0e38f)) return fail(SSD_ERR_SHAPE, "scale is not finite");
+  if (window < 0) return fail(SSD_ERR_SHAPE, "window=%d is negative", window);
+  ssd_status st = kv_check(cache, kv_len, n_q, dtype, B, n, workspace, ws_bytes, 0);
+  if (st != SSD_OK) return st;
+  if (!q || !q_strides || !out) return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  const size_t need = ssd_kv_workspace_bytes(n, n_heads, cache->n_kv_heads, cache->head_dim);
+  if (need == 0 || B > 65535)
+    return fail(SSD_ERR_SHAPE, "bad shape B=%d n=%d n_heads=%d n_kv_heads=%d", B, n, n_heads, cache->n_kv_heads);
+  if (ws_bytes < need) return fail(SSD_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", ws_bytes, need);
+  if (!aligned_to(out, 16) || (out_lse && !aligned_to(out_lse, 4)))
+    return fail(SSD_ERR_ALIGN, "out needs 16-byte alignment, out_lse 4-byte");
+  KvAttnArgs a = {};
+  bool vec = true;
+  st = kv_strides(q, q_strides, esize_of(dtype), a.qs, &vec);
+  if (st != SSD_OK) return st;
+  a.c = kv_cache_args(cache);
+  a.kv_len = kv_len;
+  a.n_q = n_q;
+  a.B = B;
+  a.nq = n;
+  a.heads = n_heads;
+  a.q = q;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.window = window;
+  a.past_only = past_only != 0;
+  a.out = out;
+  a.lse = out_lse;
+  a.status = static_cast<int32_t*>(workspace);
+  a.work = static_cast<uint8_t*>(workspace) + kKvWorkOffset;
+  const cudaError_t e = launch_kv_attention(a, cache->head_dim, esize_of(dtype), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SSD_OK : cuda_fail(e, "cache attention launch");
+}
 
 }  // extern "C"

@@ -9,6 +9,7 @@ missing the first call raises -- build it with ``build.build()`` (or
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -27,7 +28,7 @@ MAX_TOPK = 8
 STATUS_NAMES = {
     0: "SSD_OK", 1: "SSD_ERR_NULL", 2: "SSD_ERR_SHAPE", 3: "SSD_ERR_DTYPE", 4: "SSD_ERR_ALIGN",
     5: "SSD_ERR_TOKEN_RANGE", 6: "SSD_ERR_TEMPERATURE", 7: "SSD_ERR_CUDA", 8: "SSD_ERR_UNSUPPORTED",
-    9: "SSD_ERR_WORKSPACE", 10: "SSD_ERR_GAMMA", 11: "SSD_ERR_DRAW",
+    9: "SSD_ERR_WORKSPACE", 10: "SSD_ERR_GAMMA", 11: "SSD_ERR_DRAW", 12: "SSD_ERR_PAGE", 13: "SSD_ERR_LENGTH",
 }
 
 
@@ -39,6 +40,13 @@ class SsdError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+
+
+class KvCacheStruct(ctypes.Structure):
+    """ssd_kv_cache of include/ssdv.h."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_table", ctypes.c_void_p)]
 
 
 def _declare(lib):
@@ -62,6 +70,13 @@ def _declare(lib):
     lib.ssd_verify_top_p.argtypes = [P, P, I, P, I, I, I, F, F, U64, P, P, P, SZ, P]
     lib.ssd_verify_top_p_workspace_bytes.argtypes = [I, I]
     lib.ssd_verify_top_p_workspace_bytes.restype = SZ
+    lib.ssd_kv_page_bytes.argtypes = [I, I, I]
+    lib.ssd_kv_page_bytes.restype = SZ
+    lib.ssd_kv_workspace_bytes.argtypes = [I, I, I, I]
+    lib.ssd_kv_workspace_bytes.restype = SZ
+    lib.ssd_kv_append.argtypes = [P, P, P, P, P, P, P, I, I, I, P, SZ, P]
+    lib.ssd_kv_read.argtypes = [P, P, P, I, I, I, P, P, P, SZ, P]
+    lib.ssd_kv_attention.argtypes = [P, P, P, P, P, I, I, I, I, F, I, I, P, P, P, SZ, P]
     lib.ssd_read_status.argtypes = [P, SZ, P, P]
     lib.ssd_debug_uniforms.argtypes = [U64, I, I, P, P]
     lib.ssd_status_str.argtypes = [I]
@@ -72,7 +87,7 @@ def _declare(lib):
                  "ssd_verify_ragged", "ssd_verify_ragged_pipelined", "ssd_saguaro_prespec", "ssd_debug_rowstats",
                  "ssd_debug_saguaro_stats", "ssd_read_status",
                  "ssd_verify_saguaro", "ssd_cache_check", "ssd_verify_saguaro_draft", "ssd_verify_top_p",
-                 "ssd_debug_uniforms"):
+                 "ssd_kv_append", "ssd_kv_read", "ssd_kv_attention", "ssd_debug_uniforms"):
         getattr(lib, name).restype = I
     return lib
 
@@ -407,6 +422,171 @@ def cache_check(bonus_topk: torch.Tensor, out_tokens: torch.Tensor, n_accepted: 
                                  _dev(n_accepted, "n_accepted", torch.int32), B, W - 1, k, _dev(hit, "hit"),
                                  _dev(n_hits, "n_hits"), _stream(stream)))
     return hit, n_hits
+
+
+KV_BLOCK = 16  # tokens per block of a cache page, elements per scale
+_kv_ws_cache = {}
+
+
+def kv_workspace_bytes(n_q: int = 0, n_heads: int = 0, n_kv_heads: int = 0, head_dim: int = 0) -> int:
+    return int(lib().ssd_kv_workspace_bytes(n_q, n_heads, n_kv_heads, head_dim))
+
+
+def make_kv_workspace(n_q: int = 0, n_heads: int = 0, n_kv_heads: int = 0, head_dim: int = 0, device=None) -> torch.Tensor:
+    """A zeroed device workspace for kv_append and kv_read (no arguments) or for
+    kv_attention of up to n_q query tokens."""
+    n = kv_workspace_bytes(n_q, n_heads, n_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError(f"no workspace for n_q={n_q} n_heads={n_heads} n_kv_heads={n_kv_heads} head_dim={head_dim}")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def make_kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 64, device=None) -> torch.Tensor:
+    """A pool of cache pages: uint8 [n_pages, n_kv_heads, page_size / 16, 18 * head_dim], all values zero."""
+    if n_pages < 1 or lib().ssd_kv_page_bytes(n_kv_heads, head_dim, page_size) == 0:
+        raise ValueError(f"no cache of n_pages={n_pages} n_kv_heads={n_kv_heads} head_dim={head_dim} "
+                         f"page_size={page_size}: head_dim is 64, 128 or 256, page_size a multiple of {KV_BLOCK}")
+    return torch.zeros(n_pages, n_kv_heads, page_size // KV_BLOCK, 18 * head_dim, dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def _kv_cache(cache: torch.Tensor, page_table: torch.Tensor, B: int):
+    ptr = _dev(cache, "cache", torch.uint8)
+    table = _dev(page_table, "page_table", torch.int32)
+    if cache.dim() != 4 or cache.shape[3] % 18:
+        raise ValueError("cache must be [n_pages, n_kv_heads, page_size / 16, 18 * head_dim] (make_kv_cache)")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}, max_pages], got {list(page_table.shape)}")
+    n_pages, heads, blocks, block = cache.shape
+    return KvCacheStruct(ptr, n_pages, heads, block // 18, blocks * KV_BLOCK, page_table.shape[1], table)
+
+
+def _kv_counts(t: Optional[torch.Tensor], name: str, B: int):
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != B:
+        raise ValueError(f"{name} must be [{B}], got {list(t.shape)}")
+    return _dev(t, name, torch.int32)
+
+
+def _kv_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int):
+    """Pointer and strides of [B, n, heads, head_dim] rows: any strides but the last."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dim() != 4 or t.shape[3] != dim or (heads is not None and t.shape[2] != heads):
+        raise ValueError(f"{name} must be [B, n, {heads or 'n_heads'}, {dim}], got {list(t.shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return t.data_ptr(), (ctypes.c_int64 * 3)(st[0], st[1], st[2])
+
+
+def _kv_stream(stream, device):
+    """(raw stream, context that makes it current): outputs and workspaces are
+    allocated on the stream that uses them."""
+    raw = _stream(stream)
+    if stream is None or raw == torch.cuda.current_stream(device).cuda_stream:
+        return raw, contextlib.nullcontext()
+    return raw, torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                  else torch.cuda.ExternalStream(raw, device=device))
+
+
+def _kv_workspace(need: int, device, raw: int, given: Optional[torch.Tensor]):
+    if given is not None:
+        return given
+    if need == 0:
+        return torch.empty(16, dtype=torch.uint8, device=device)  # the call names the bad argument
+    if torch.cuda.is_current_stream_capturing():
+        # a graph keeps its own workspace: the cached one may be replaced by a larger
+        return torch.zeros(need, dtype=torch.uint8, device=device)
+    key = (device.index, raw)
+    ws = _kv_ws_cache.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        _kv_ws_cache[key] = ws
+    return ws
+
+
+def kv_workspace(device=None, stream=None) -> Optional[torch.Tensor]:
+    """The workspace that the kv_ calls without one use on this stream (None before
+    the first), for read_status."""
+    device = torch.device(device if device is not None else "cuda")
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    return _kv_ws_cache.get((index, _stream(stream)))
+
+
+def kv_append(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+              n_new: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ssd_kv_append: write k, v [B, n, n_kv_heads, head_dim] (bf16 or fp32, any strides but the last) at positions
+    kv_len[b] .. kv_len[b] + n_new[b] - 1.  kv_len is not changed."""
+    B, n = k.shape[:2]
+    c = _kv_cache(cache, page_table, B)
+    kp, ks = _kv_rows(k, "k", c.n_kv_heads, c.head_dim)
+    vp, vs = _kv_rows(v, "v", c.n_kv_heads, c.head_dim)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must have one shape and dtype")
+    lens, news = _kv_counts(kv_len, "kv_len", B), _kv_counts(n_new, "n_new", B)
+    if B == 0 or n == 0:
+        return
+    raw, ctx = _kv_stream(stream, cache.device)
+    with ctx:
+        ws = _kv_workspace(256, cache.device, raw, workspace)
+    _check(lib().ssd_kv_append(ctypes.byref(c), lens, news, kp, ks, vp, vs, _dtype_code(k), B, n,
+                               _dev(ws, "workspace"), ws.numel(), raw))
+
+
+def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, n: int, dtype=torch.bfloat16,
+            count: Optional[torch.Tensor] = None, out=None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """ssd_kv_read: (k, v) [B, n, n_kv_heads, head_dim], the values held for positions start[b] .. start[b] +
+    count[b] - 1 (rows past count[b] are zero); out: a pair of tensors to write them to."""
+    B = page_table.shape[0]
+    c = _kv_cache(cache, page_table, B)
+    starts, counts = _kv_counts(start, "start", B), _kv_counts(count, "count", B)
+    shape = (B, int(n), c.n_kv_heads, c.head_dim)
+    raw, ctx = _kv_stream(stream, cache.device)
+    with ctx:
+        k, v = out if out is not None else (torch.empty(shape, dtype=dtype, device=cache.device),
+                                            torch.empty(shape, dtype=dtype, device=cache.device))
+        ws = _kv_workspace(256, cache.device, raw, workspace)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != v.dtype:
+        raise ValueError(f"out must be two tensors {list(shape)} of one dtype")
+    if B == 0 or n == 0:
+        return k, v
+    _check(lib().ssd_kv_read(ctypes.byref(c), starts, counts, _dtype_code(k), B, int(n), _dev(k, "out k"),
+                             _dev(v, "out v"), _dev(ws, "workspace"), ws.numel(), raw))
+    return k, v
+
+
+def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q: torch.Tensor,
+                 n_q: Optional[torch.Tensor] = None, scale: Optional[float] = None, window: int = 0,
+                 past_only: bool = False, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 return_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """ssd_kv_attention: q [B, n, n_heads, head_dim] (bf16 or fp32, any strides but the last), query i of request b at
+    position kv_len[b] + i.  scale defaults to head_dim ** -0.5.  Returns out like q, contiguous, or (out, lse
+    [B, n, n_heads] float32) with return_lse (or a given lse)."""
+    B, n, heads = q.shape[:3]
+    c = _kv_cache(cache, page_table, B)
+    qp, qs = _kv_rows(q, "q", None, c.head_dim)
+    lens, counts = _kv_counts(kv_len, "kv_len", B), _kv_counts(n_q, "n_q", B)
+    raw, ctx = _kv_stream(stream, cache.device)
+    with ctx:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty(B, n, heads, dtype=torch.float32, device=q.device)
+        if workspace is None and B and n:
+            workspace = _kv_workspace(kv_workspace_bytes(n, heads, c.n_kv_heads, c.head_dim), cache.device, raw, None)
+    if out.shape != q.shape or (lse is not None and tuple(lse.shape) != (B, n, heads)):
+        raise ValueError("out must be shaped like q and lse [B, n, n_heads]")
+    if B and n:
+        _check(lib().ssd_kv_attention(ctypes.byref(c), lens, counts, qp, qs, _dtype_code(q), B, n, heads,
+                                      float(scale) if scale is not None else c.head_dim ** -0.5, int(window),
+                                      int(past_only), _dev(out, "out", q.dtype),
+                                      _dev(lse, "lse", torch.float32) if lse is not None else None,
+                                      _dev(workspace, "workspace"), workspace.numel(), raw))
+    return (out, lse) if lse is not None else out
 
 
 def debug_rowstats(target, draft, draft_tokens, temperature, seed, workspace=None, stream=None):
