@@ -979,6 +979,8 @@ ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, co
   const size_t need = ssd_kv_workspace_bytes(n, n_heads, cache->n_kv_heads, cache->head_dim);
   if (need == 0 || B > 65535)
     return fail(SSD_ERR_SHAPE, "bad shape B=%d n=%d n_heads=%d n_kv_heads=%d", B, n, n_heads, cache->n_kv_heads);
+  if (static_cast<double>(B) * n_heads * n * (cache->max_pages * (cache->page_size / kKvBlock) / 4 + 1) >= 274877906944.0)
+    return fail(SSD_ERR_SHAPE, "B * n * n_heads * max_pages too large");  // a team's tiles are counted in 32 bits
   if (ws_bytes < need) return fail(SSD_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", ws_bytes, need);
   if (!aligned_to(out, 16) || (out_lse && !aligned_to(out_lse, 4)))
     return fail(SSD_ERR_ALIGN, "out needs 16-byte alignment, out_lse 4-byte");
