@@ -40,7 +40,8 @@ namespace {
 constexpr int kTile = 64;        // tokens per tile: four blocks
 constexpr int kBias = 15;        // weights are at most 2^kBias
 constexpr int kBand = 29;        // octaves below that in which fp16 keeps 11 bits
-constexpr int kBands = 5;        // passes a tile may take; weights below 2^-145 of its largest are dropped
+constexpr int kBands = 5;        // passes a tile may take; weights below 2^-141 of its largest are dropped
+constexpr float kSmallest = 6.103515625e-05f;  // 2^(kBias - kBand)
 constexpr float kLowUp = 2048.f; // the second fp16 part of a weight is held this much up
 constexpr int kMaxSms = 160;     // the workspace is sized for this many CTAs
 constexpr int kSmem = 229000;    // dynamic shared memory, at most
@@ -131,6 +132,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -153,9 +160,26 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// 16 + u of the pairs at bits 9:6, 256 + u of those at bits 5:2.
-__device__ __forceinline__ uint32_t pair_hi(uint32_t w) { return (w & 0x03C003C0u) | 0x4C004C00u; }
-__device__ __forceinline__ uint32_t pair_lo(uint32_t w) { return (w & 0x003C003Cu) | 0x5C005C00u; }
+// 16 + u of the pairs at bits 9:6, 256 + u of those at bits 5:2: one three-input
+// operation each, for which the or-ed constants are kept in registers.
+struct Bases {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Bases make_bases() {
+  Bases b;
+  asm volatile("mov.b32 %0, 0x4C004C00;\n\tmov.b32 %1, 0x5C005C00;" : "=r"(b.hi), "=r"(b.lo));
+  return b;
+}
+__device__ __forceinline__ uint32_t pair_hi(uint32_t w, const Bases& b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, 0x03C003C0, %2, 0xEA;" : "=r"(d) : "r"(w), "r"(b.hi));
+  return d;
+}
+__device__ __forceinline__ uint32_t pair_lo(uint32_t w, const Bases& b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, 0x003C003C, %2, 0xEA;" : "=r"(d) : "r"(w), "r"(b.lo));
+  return d;
+}
 constexpr uint32_t kMinus24 = 0xCE00CE00u, kMinus264 = 0xDC20DC20u;  // fp16 pairs
 
 __device__ __forceinline__ uint4 lds128(uint32_t p) {
@@ -168,17 +192,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t p) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
   return v;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t p) {
-  unsigned short v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t p) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(p));
-  return v;
-}
-
 // ---- the list of work ----
 
 // What a request's rows see together, and its tiles.
@@ -242,6 +255,19 @@ struct Rows {
   float o[kSteps][NT][4];
   float f[NT][2];  // factor of a row's scores (log2 units)
   float m[NT][2], l[NT][2];
+  // the lane's offsets in a tile: its first key row, that row's scales, its
+  // values' block, its first value chunk there
+  uint32_t key_at, scale_at, value_at, row_at;
+  Bases bases;
+  __device__ __forceinline__ void place(int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    const uint32_t blk = (r >> 1) * block_stride(D);
+    key_at = blk + (r & 1) * (D / 2) + (D == 64 ? c * 8 : c * 16) + (D == 256 ? (r & 1) * 64 : 0);
+    scale_at = blk + kv_k_scales(D) + (D == 64 ? c * 16 + (r & 1) * 8 : c * 32 + (r & 1) * 16);
+    value_at = c * block_stride(D);
+    row_at = r * 16;
+    bases = make_bases();
+  }
 };
 
 // The element of a head that lane quarter c holds first in step s.
@@ -276,8 +302,10 @@ __device__ __forceinline__ void load_queries(const AttnLaunch& L, Rows<E, D, NT>
     // the row's largest element to [2^12, 2^13)
     int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     ex = max(-100, min(ex, 127));
-    const float up = __uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23);
-    const float f = L.a.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23);
+    // the scale's sign goes to the query, so that the largest product is the
+    // largest score
+    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), L.a.scale_log2);
+    const float f = fabsf(L.a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23);
     w.f[nt][0] = __shfl_sync(~0u, f, (2 * c) * 4);
     w.f[nt][1] = __shfl_sync(~0u, f, (2 * c + 1) * 4);
 #pragma unroll
@@ -315,46 +343,46 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
   float s[4][NA][4];
   // scores
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int hh = 0; hh < (D == 256 ? 2 : 1); ++hh) {
+    constexpr int kWords = D == 64 ? 2 : 4;
+    const uint32_t blk = base + w.key_at;
+    uint32_t sv[4];  // D = 64: bytes 2 j + y of 8; else bytes 2 y + g of word j (token y of two, group g of two)
+    if constexpr (D == 64) {
+      const uint2 x = lds64(base + w.scale_at);
+      sv[0] = x.x, sv[1] = x.x >> 16, sv[2] = x.y, sv[3] = x.y >> 16;
+    } else {
+      const uint4 x = lds128(base + w.scale_at + hh * 128);
+      sv[0] = x.x, sv[1] = x.y, sv[2] = x.z, sv[3] = x.w;
+    }
 #pragma unroll
-    for (int nt = 0; nt < NA; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][nt][e] = 0.f;
-    const int ta = 4 * j + (r & 1);
-    const uint32_t blk = base + (r >> 1) * kStride;
-#pragma unroll
-    for (int hh = 0; hh < (D == 256 ? 2 : 1); ++hh) {
-      constexpr int kWords = D == 64 ? 2 : 4;
-      uint32_t wa[kWords], wb[kWords], sa[kWords / 2], sb[kWords / 2];
+    for (int j = 0; j < 4; ++j) {
+      uint32_t wa[kWords], wb[kWords];
       if constexpr (D == 64) {
-        const uint2 xa = lds64(blk + ta * 32 + c * 8), xb = lds64(blk + (ta + 2) * 32 + c * 8);
+        const uint2 xa = lds64(blk + 4 * j * 32), xb = lds64(blk + (4 * j + 2) * 32);
         wa[0] = xa.x, wa[1] = xa.y, wb[0] = xb.x, wb[1] = xb.y;
-        sa[0] = lds8(blk + kv_k_scales(D) + ta * 4 + c) * 0x00800080u;
-        sb[0] = lds8(blk + kv_k_scales(D) + (ta + 2) * 4 + c) * 0x00800080u;
       } else {
-        const int half = D == 256 ? (hh ^ (ta & 1)) * 64 : 0;
-        const uint4 xa = lds128(blk + ta * (D / 2) + half + c * 16), xb = lds128(blk + (ta + 2) * (D / 2) + half + c * 16);
+        const uint32_t at = hh ? blk + 64 - (r & 1) * 128 : blk;  // odd tokens' halves are exchanged
+        const uint4 xa = lds128(at + 4 * j * (D / 2)), xb = lds128(at + (4 * j + 2) * (D / 2));
         wa[0] = xa.x, wa[1] = xa.y, wa[2] = xa.z, wa[3] = xa.w;
         wb[0] = xb.x, wb[1] = xb.y, wb[2] = xb.z, wb[3] = xb.w;
-        const uint32_t ba = lds16(blk + kv_k_scales(D) + ta * (D / 16) + hh * 8 + c * 2);
-        const uint32_t bb = lds16(blk + kv_k_scales(D) + (ta + 2) * (D / 16) + hh * 8 + c * 2);
-        sa[0] = (ba & 0xFFu) * 0x00800080u, sa[1] = (ba >> 8) * 0x00800080u;
-        sb[0] = (bb & 0xFFu) * 0x00800080u, sb[1] = (bb >> 8) * 0x00800080u;
       }
 #pragma unroll
       for (int g = 0; g < kWords / 2; ++g) {
-        const uint32_t a24 = mul2(sa[g], kMinus24), a264 = mul2(sa[g], kMinus264);
-        const uint32_t b24 = mul2(sb[g], kMinus24), b264 = mul2(sb[g], kMinus264);
+        const uint32_t sa = __byte_perm(sv[j], 0, D == 64 ? 0x4040 : 0x4040 + 0x0101 * g) << 7;
+        const uint32_t sb = __byte_perm(sv[j], 0, D == 64 ? 0x4141 : 0x4040 + 0x0101 * (2 + g)) << 7;
+        const uint32_t a24 = mul2(sa, kMinus24), a264 = mul2(sa, kMinus264);
+        const uint32_t b24 = mul2(sb, kMinus24), b264 = mul2(sb, kMinus264);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {  // two words, two steps each
           const int word = 2 * g + (x >> 1), step = hh * 8 + 2 * word + (x & 1);
           const uint32_t ua = x & 1 ? __funnelshift_r(wa[word], wa[word], 8) : wa[word];
           const uint32_t ub = x & 1 ? __funnelshift_r(wb[word], wb[word], 8) : wb[word];
-          const uint32_t a[4] = {fma2(pair_hi(ua), sa[g], a24), fma2(pair_hi(ub), sb[g], b24),
-                                 fma2(pair_lo(ua), sa[g], a264), fma2(pair_lo(ub), sb[g], b264)};
+          const uint32_t a[4] = {fma2(pair_hi(ua, w.bases), sa, a24), fma2(pair_hi(ub, w.bases), sb, b24),
+                                 fma2(pair_lo(ua, w.bases), sa, a264), fma2(pair_lo(ub, w.bases), sb, b264)};
 #pragma unroll
           for (int nt = 0; nt < NA; ++nt) {
-            mma(s[j][nt], a, w.q[nt][step][0], w.q[nt][step][1]);
+            if (step == 0) mma_first(s[j][nt], a, w.q[nt][step][0], w.q[nt][step][1]);
+            else mma(s[j][nt], a, w.q[nt][step][0], w.q[nt][step][1]);
             if constexpr (W::kF32) mma(s[j][nt], a, w.q[nt][step][2], w.q[nt][step][3]);
           }
         }
@@ -367,19 +395,11 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
   uint32_t more = 0;
 #pragma unroll
   for (int nt = 0; nt < NA; ++nt) {
-    float top[2] = {-INFINITY, -INFINITY}, low[2] = {INFINITY, INFINITY};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[j][nt][e] *= w.f[nt][e & 1];
-        low[e & 1] = fminf(low[e & 1], s[j][nt][e]);
-      }
     if (edge) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int i = (row0 + nt * 8 + 2 * c + x) / L.per;
-        const int lo = row_lo(L.a, sp.len, i), hi = i < sp.nq ? row_hi(L.a, sp.len, i) : 0;
+        const int lo = row_lo(L.a, sp.len, i), hi = min(row_hi(L.a, sp.len, i), sp.hi);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -389,47 +409,70 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
           }
       }
     }
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[j][nt][e]);
     float fall[2], ref[2], sum[2] = {0.f, 0.f};
-    bool wide = band != 0, grown = false;
+    bool grown = false;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 4));
       top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 8));
       top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 16));
-      wide |= low[x] < top[x] - kBand;
+      if (top[x] != -INFINITY) top[x] *= w.f[nt][x];  // f >= 0
       const float m = fmaxf(w.m[nt][x], top[x]), zero = m == -INFINITY ? 0.f : m;
       grown |= m != w.m[nt][x];
       fall[x] = ex2(w.m[nt][x] - zero);  // the sums so far
       w.m[nt][x] = m;
       top[x] = top[x] == -INFINITY ? zero : top[x];
       grow[nt][x] = ex2(top[x] - zero - kBand * band);
-      ref[x] = top[x] - kBias;
+      ref[x] = kBias - top[x];
     }
-    if (__any_sync(~0u, wide)) {
-      // some weight leaves fp16's normal range: this pass takes the scores from
-      // kBand band to kBand (band + 1) below the top, up by kBand band
+    float e[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e[j][k] = ex2(fmaf(s[j][nt][k], w.f[nt][k & 1], ref[k & 1]));
+    bool small = false;  // a weight below fp16's normal range
+    if (edge) {
+      // (a factor of zero makes no number of a masked score)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = s[j][nt][e], under = top[e & 1] - x;
-          const int at = under >= kBand * kBands ? kBands : under >= kBand ? static_cast<int>(under * (1.f / kBand)) : 0;
+        for (int k = 0; k < 4; ++k) {
+          const bool seen = s[j][nt][k] != -INFINITY;
+          e[j][k] = seen ? e[j][k] : 0.f;
+          small |= seen && e[j][k] < kSmallest;
+        }
+    }
+    __half2 least = __float2half2_rn(1.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 ha = __floats2half2_rn(e[j][0], e[j][1]), hb = __floats2half2_rn(e[j][2], e[j][3]);
+      sum[0] += e[j][0] + e[j][2];
+      sum[1] += e[j][1] + e[j][3];
+      least = __hmin2(least, __hmin2(ha, hb));
+      p[j][nt][0] = half2_bits(ha);
+      p[j][nt][1] = half2_bits(hb);
+    }
+    // below 2^-14 fp16 keeps fewer bits: those weights go to a later band
+    if (!edge) small = __low2float(least) < kSmallest || __high2float(least) < kSmallest;
+    if (__any_sync(~0u, small) || band) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float u = fmaf(s[j][nt][k], w.f[nt][k & 1], ref[k & 1]);
+          int at = u >= kBias - kBand ? 0 : min(kBands, static_cast<int>((kBias - u) * (1.f / kBand)));
+          if (edge && s[j][nt][k] == -INFINITY) at = kBands;
           if (band == 0 && at > 0 && at < kBands) more |= 1u << at;
-          sum[e & 1] += ex2(x - ref[e & 1]);
-          s[j][nt][e] = at == band ? ex2(x - ref[e & 1] + kBand * band) : 0.f;
+          e[j][k] = at == band ? ex2(u + kBand * band) : 0.f;
         }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[j][nt][e] = ex2(s[j][nt][e] - ref[e & 1]);
-          sum[e & 1] += s[j][nt][e];
-        }
+        p[j][nt][0] = half2_bits(__floats2half2_rn(e[j][0], e[j][1]));
+        p[j][nt][1] = half2_bits(__floats2half2_rn(e[j][2], e[j][3]));
+      }
     }
     if (band == 0) {
       w.l[nt][0] = w.l[nt][0] * fall[0] + sum[0] * grow[nt][0];
@@ -444,25 +487,24 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float p0 = s[j][nt][0], p1 = s[j][nt][1], p2 = s[j][nt][2], p3 = s[j][nt][3];
-      const __half2 ha = __floats2half2_rn(p0, p1), hb = __floats2half2_rn(p2, p3);
-      p[j][nt][0] = transpose8(half2_bits(ha));
-      p[j][nt][1] = transpose8(half2_bits(hb));
       if constexpr (W::kF32) {
-        const float2 fa = __half22float2(ha), fb = __half22float2(hb);
-        p[j][nt][2] = transpose8(half2_bits(__floats2half2_rn((p0 - fa.x) * kLowUp, (p1 - fa.y) * kLowUp)));
-        p[j][nt][3] = transpose8(half2_bits(__floats2half2_rn((p2 - fb.x) * kLowUp, (p3 - fb.y) * kLowUp)));
+        const float2 fa = __half22float2(*reinterpret_cast<__half2*>(&p[j][nt][0]));
+        const float2 fb = __half22float2(*reinterpret_cast<__half2*>(&p[j][nt][1]));
+        p[j][nt][2] = transpose8(half2_bits(__floats2half2_rn((e[j][0] - fa.x) * kLowUp, (e[j][1] - fa.y) * kLowUp)));
+        p[j][nt][3] = transpose8(half2_bits(__floats2half2_rn((e[j][2] - fb.x) * kLowUp, (e[j][3] - fb.y) * kLowUp)));
       }
+      p[j][nt][0] = transpose8(p[j][nt][0]);
+      p[j][nt][1] = transpose8(p[j][nt][1]);
     }
   }
   // values: lane quarter c takes block c, lane row r the elements r D/8 ..
-  const uint32_t blk = base + c * kStride;
+  const uint32_t blk = base + w.value_at;
   constexpr int kGroups = D == 256 ? 2 : 1;
 #pragma unroll
   for (int gg = 0; gg < kGroups; ++gg) {
     const int group = D == 64 ? r >> 1 : D == 128 ? r : 2 * r + gg;
-    const uint4 sv = lds128(blk + kv_v_scales(D) + group * kKvBlock);
-    uint32_t sc[4] = {sv.x, sv.y, sv.z, sv.w};
+    const uint4 vs = lds128(blk + kv_v_scales(D) + group * kKvBlock);
+    uint32_t sc[4] = {vs.x, vs.y, vs.z, vs.w};
     uint32_t nans = 0;  // tokens of block c whose values of this group are NaN
     if (edge) {
       // what no row sees counts nothing whatever its bytes are; a NaN that some
@@ -487,21 +529,26 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
 #pragma unroll
     for (int ii = 0; ii < W::kSteps / kGroups; ++ii) {
       const int i = gg * (W::kSteps / kGroups) + ii;
-      const uint4 v = lds128(blk + kv_v_codes(D) + (i * 8 + r) * 16);
+      const uint4 v = lds128(blk + kv_v_codes(D) + i * 128 + w.row_at);
       const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-      float t[NA][4] = {};
-      [[maybe_unused]] float t2[NA][4] = {};
+      float t[NA][4];
+      [[maybe_unused]] float t2[NA][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t w0 = word[j >> 1], w1 = word[2 + (j >> 1)];
         const uint32_t u0 = j & 1 ? __funnelshift_r(w0, w0, 8) : w0;
         const uint32_t u1 = j & 1 ? __funnelshift_r(w1, w1, 8) : w1;
-        const uint32_t a[4] = {fma2(pair_hi(u0), ss[j][0], ss[j][1]), fma2(pair_hi(u1), ss[j][0], ss[j][1]),
-                               fma2(pair_lo(u0), ss[j][2], ss[j][3]), fma2(pair_lo(u1), ss[j][2], ss[j][3])};
+        const uint32_t a[4] = {fma2(pair_hi(u0, w.bases), ss[j][0], ss[j][1]), fma2(pair_hi(u1, w.bases), ss[j][0], ss[j][1]),
+                               fma2(pair_lo(u0, w.bases), ss[j][2], ss[j][3]), fma2(pair_lo(u1, w.bases), ss[j][2], ss[j][3])};
 #pragma unroll
         for (int nt = 0; nt < NA; ++nt) {
-          mma(t[nt], a, p[j][nt][0], p[j][nt][1]);
-          if constexpr (W::kF32) mma(t2[nt], a, p[j][nt][2], p[j][nt][3]);
+          if (j == 0) {
+            mma_first(t[nt], a, p[j][nt][0], p[j][nt][1]);
+            if constexpr (W::kF32) mma_first(t2[nt], a, p[j][nt][2], p[j][nt][3]);
+          } else {
+            mma(t[nt], a, p[j][nt][0], p[j][nt][1]);
+            if constexpr (W::kF32) mma(t2[nt], a, p[j][nt][2], p[j][nt][3]);
+          }
         }
       }
 #pragma unroll
@@ -521,7 +568,7 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int i = (row0 + nt * 8 + 2 * c + x) / L.per;
-            const int lo = row_lo(L.a, sp.len, i), hi = i < sp.nq ? row_hi(L.a, sp.len, i) : 0;
+            const int lo = row_lo(L.a, sp.len, i), hi = min(row_hi(L.a, sp.len, i), sp.hi);
             const int from = max(0, min(lo - first, 16)), to = max(0, min(hi - first, 16));
             if (there & ((1u << to) - 1u) & ~((1u << from) - 1u))
 #pragma unroll
@@ -662,6 +709,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attention_kernel(const Attn
   }
 
   W w;
+  w.place(lane);
   int done = 0;
   while (done < n_tiles && alive) {
     const int b = at.b, h = at.hr / RT, pass0 = (at.hr % RT) * L.rows_pass;
@@ -684,7 +732,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attention_kernel(const Attn
       }
       bad |= flags[team * S + st] != 0;
       const int pos0 = (sp.tile0 + first + k) * kTile;
-      const bool edge = pos0 < lo_last || pos0 + kTile > hi_first || row0 + active * 8 > nrows;
+      const bool edge = pos0 < lo_last || pos0 + kTile > hi_first;
       for (uint32_t todo = active ? 1 : 0; todo;) {
         const int band = __ffs(todo) - 1;
         todo &= todo - 1;
@@ -717,18 +765,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attention_kernel(const Attn
         l += __shfl_xor_sync(~0u, l, 4);
         l += __shfl_xor_sync(~0u, l, 8);
         l += __shfl_xor_sync(~0u, l, 16);
-        if (bad) l = __int_as_float(0x7FC00000);
         const int row = row0 + nt * 8 + 2 * c + xx;
+        if (row >= nrows) l = 0.f;  // a padded query's row went along with its tile
+        if (bad) l = __int_as_float(0x7FC00000);
         if (nt >= own || row >= L.rows) continue;
         if (whole) {
           const int i = row / L.per;
           const long long orow = (static_cast<long long>(b) * a.nq + i) * a.heads + h * L.per + row % L.per;
-          const float inv = bad ? l : l > 0.f || l != l ? 1.f / l : 0.f;
+          const float inv = 1.f / l;
           float y[D / 8];
 #pragma unroll
           for (int i2 = 0; i2 < W::kSteps; ++i2) {
-            y[2 * i2] = w.o[i2][nt][xx] * inv;
-            y[2 * i2 + 1] = w.o[i2][nt][2 + xx] * inv;
+            y[2 * i2] = l == 0.f ? 0.f : w.o[i2][nt][xx] * inv;
+            y[2 * i2 + 1] = l == 0.f ? 0.f : w.o[i2][nt][2 + xx] * inv;
           }
           E* out = static_cast<E*>(a.out) + orow * D + r * (D / 8);
           if constexpr (W::kF32) {
@@ -822,10 +871,10 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnLaunch L) {
   }
   const int i = row / L.per, h = d.y / RT;
   const long long orow = (static_cast<long long>(d.x) * L.a.nq + i) * L.a.heads + h * L.per + row % L.per;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = 1.f / l;
   E* out = static_cast<E*>(L.a.out) + orow * D + lane * kPer;
 #pragma unroll
-  for (int v = 0; v < kPer; ++v) out[v] = static_cast<E>(y[v] * inv);
+  for (int v = 0; v < kPer; ++v) out[v] = static_cast<E>(l == 0.f ? 0.f : y[v] * inv);
   if (L.a.lse && lane == 0)
     L.a.lse[orow] = l == 0.f ? -INFINITY : (ref + (log2f(l) - kBias)) * 0.69314718055994531f;
 }

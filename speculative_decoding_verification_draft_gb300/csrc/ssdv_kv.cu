@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(KvStoreArgs a, int 
         for (int e = 0; e < 8; ++e) word |= kv_place(u[8 * w + e], e);
         *reinterpret_cast<uint32_t*>(k.block + k_word_offset<D>(t, 2 * k.g + w)) = word;
       }
-      k.block[kv_k_scales(D) + t * G + k.g] = static_cast<uint8_t>(byte);
+      k.block[k_scale_offset<D>(t, k.g)] = static_cast<uint8_t>(byte);
     }
   } else {
     uint32_t word[16] = {}, keep = 0xFFFFFFFFu;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(KvStoreArgs a) {
     for (int d = 0; d < 16; ++d) x[d] = k.bad && live ? __int_as_float(0x7FC00000) : 0.f;
     if (live && k.block) {
       if (!values) {
-        const float s = kv_scale(k.block[kv_k_scales(D) + t * G + k.g]);
+        const float s = kv_scale(k.block[k_scale_offset<D>(t, k.g)]);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const uint32_t word = *reinterpret_cast<const uint32_t*>(k.block + k_word_offset<D>(t, 2 * k.g + w));

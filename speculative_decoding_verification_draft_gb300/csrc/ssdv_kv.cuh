@@ -20,7 +20,10 @@
 //            (shared-memory banks)
 //   V codes  [D / 16][8][2][16 tokens x 4 bits]: entry (i, r, e) is element
 //            r D/8 + 2 i + e; word 0 tokens 0..7, word 1 tokens 8..15
-//   K scales [16 tokens][D / 16],  V scales [D / 16][16 tokens]
+//   K scales, D bytes: for each 8 groups 4 pairs of groups, for each pair the
+//            even tokens' two scales, then the odd tokens' (D = 64: 4 groups, for
+//            each the even tokens' scale, then the odd tokens')
+//   V scales [D / 16][16 tokens]
 // A word holds 8 codes n + 8 as four pairs, pair p = entries 2p (low half-word)
 // and 2p + 1 (high): pair 0 at bits 9:6 of each half-word and pair 1 at bits
 // 5:2; pairs 2 and 3 the same after a rotation right by 8.  Or-ing 0x4C00 to
@@ -102,6 +105,13 @@ __device__ __forceinline__ int v_word_offset(int d, int half) {
   constexpr int per = D / 8;
   const int r = d / per, i = (d % per) >> 1, e = d & 1;
   return kv_v_codes(D) + (((i * 8 + r) * 2 + e) << 3) + (half << 2);
+}
+
+// Byte offset of the K scale of token t, group g.
+template <int D>
+__device__ __forceinline__ int k_scale_offset(int t, int g) {
+  const int at = D == 64 ? g * 16 + (t & 1) * 8 + (t >> 1) : (g >> 1) * 32 + (t & 1) * 16 + (t >> 1) * 2 + (g & 1);
+  return kv_k_scales(D) + at;
 }
 
 // Code u (0..15) of entry e in its word, and back.
