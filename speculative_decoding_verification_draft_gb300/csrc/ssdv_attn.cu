@@ -44,38 +44,57 @@ constexpr int kBands = 5;        // passes a tile may take; weights below 2^-141
 constexpr float kSmallest = 6.103515625e-05f;  // 2^(kBias - kBand)
 constexpr float kLowUp = 2048.f; // the second fp16 part of a weight is held this much up
 constexpr int kMaxSms = 160;     // the workspace is sized for this many CTAs
-constexpr int kSmem = 229000;    // dynamic shared memory, at most
+constexpr int kSmem = 226000;    // dynamic shared memory, at most
+constexpr int kWarps = 8;        // computing warps per CTA, one CTA per SM
+constexpr int kThreads = 384;    // and four more, of which one keeps the copies going
 constexpr int kMaxStages = 48;   // per CTA
 constexpr int kHead = 1024;      // before the stages: 16 bytes of barriers and a flag per stage
-constexpr int kWarps = 8;        // per CTA, one CTA per SM: up to 255 registers a thread
 
 // Blocks lie 18 D + 32 bytes apart in shared memory: four consecutive blocks
 // then start 32 bytes apart in the banks, which the value loads need.
 __host__ __device__ constexpr int block_stride(int D) { return kv_block_bytes(D) + 32; }
 __host__ __device__ constexpr int stage_bytes(int D) { return 4 * block_stride(D); }
 
-// How the rows of a kv head are spread: up to nt n-tiles of 8 rows per warp, r
-// warps (1, 2, 4 or 8) per team, all reading the same tile, rt passes over the
-// cache; t teams per CTA with s stages each.
-struct AttnShape {
-  int nt, r, t, s, rt;
-};
-
-// Most n-tiles per warp that keep a warp's fragments in registers.
-__host__ __device__ constexpr int max_nt(int D, bool f32) {
-  return D == 64 ? (f32 ? 2 : 4) : D == 128 ? (f32 ? 2 : 3) : 1;
+// Most n-tiles of 8 rows whose fragments stay in the registers of one warp, or
+// of a pair of warps that halve the tile (p = 2: each takes half the tokens of
+// the scores and half the elements of the values).
+__host__ __device__ constexpr int max_nt(int D, bool f32, int p) {
+  if (p == 1) return f32 ? (D == 256 ? 0 : 1) : D == 256 ? 1 : 2;
+  return f32 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : D == 256 ? 2 : 6;
+}
+// A pair keeps its queries in shared memory; a single warp has registers for them.
+__host__ __device__ constexpr int query_bytes(int D, int nt, bool f32) { return nt * 8 * D * (f32 ? 4 : 2); }
+// Two buffers of weights, then the maxima of both halves, the factors, the sums
+// and the bands to come.
+__host__ __device__ constexpr int exchange_bytes(int nt, bool f32) {
+  return 2 * nt * 1024 * (f32 ? 2 : 1) + (2 * 2 + 1 + 2) * nt * 32 + 128;
+}
+__host__ __device__ constexpr int pair_bytes(int D, int nt, bool f32) {
+  return query_bytes(D, nt, f32) + exchange_bytes(nt, f32);
 }
 
+// How the rows of a kv head are spread: nt n-tiles per warp or pair, g groups of
+// rows per team (all reading the same tile), rt passes over the cache; t teams
+// per CTA with s stages each.
+struct AttnShape {
+  int nt, p, g, t, s, rt;
+};
+
 AttnShape attn_shape(int rows, int D, bool f32) {
-  AttnShape p;
-  const int n8 = (rows + 7) / 8, most = max_nt(D, f32);
-  p.r = n8 <= most ? 1 : n8 <= 2 * most ? 2 : n8 <= 4 * most ? 4 : 8;
-  p.nt = std::min((n8 + p.r - 1) / p.r, most);
-  p.rt = (n8 + p.r * p.nt - 1) / (p.r * p.nt);
-  p.t = kWarps / p.r;
-  if (D == 256 && p.t == kWarps) p.t = 6;  // two stages each need it
-  p.s = std::min({8, kMaxStages / p.t, (kSmem - kHead) / (p.t * stage_bytes(D))});
-  return p;
+  AttnShape a;
+  const int n8 = (rows + 7) / 8;
+  a.p = n8 <= max_nt(D, f32, 1) ? 1 : 2;
+  const int most = max_nt(D, f32, a.p);
+  a.g = n8 <= most ? 1 : n8 <= 2 * most ? 2 : 4;
+  a.nt = std::min((n8 + a.g - 1) / a.g, most);
+  if (a.p == 2 && !f32 && D != 256) a.nt = std::max(a.nt, 3);
+  a.rt = (n8 + a.g * a.nt - 1) / (a.g * a.nt);
+  a.t = kWarps / (a.p * a.g);
+  const int pairs = a.p == 2 ? a.g * pair_bytes(D, a.nt, f32) : 0;  // per team
+  const auto stages = [&] { return ((kSmem - kHead) / a.t - pairs) / stage_bytes(D); };
+  while (stages() < 2) --a.t;
+  a.s = std::min({8, kMaxStages / a.t, stages()});
+  return a;
 }
 
 struct AttnLaunch {
@@ -83,7 +102,7 @@ struct AttnLaunch {
   AttnShape p;
   int per;          // query heads per kv head
   int rows;         // nq * per
-  int rows_pass;    // r * nt * 8
+  int rows_pass;    // g * nt * 8
   int4* desc;       // [teams]: request, head * rt + pass, parts, first slot
   float2* ml;       // [2 teams, rows_pass]: maximum and sum of a part
   float* o;         // [2 teams, rows_pass, D]
@@ -103,20 +122,30 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, int bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// False if the phase did not complete within the limit (some seconds).
+__device__ __forceinline__ bool bar_test(uint32_t bar, int parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// True two seconds after the first call with since = 0: every wait ends.
+__device__ __forceinline__ bool late(unsigned long long& since) {
+  unsigned long long now;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+  if (since == 0) since = now;
+  return now - since > 2000000000ull;
+}
+// False if the phase did not complete in that time.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, int parity) {
-  for (int i = 0; i < (1 << 22); ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
-  return false;
+  unsigned long long since = 0;
+  while (!bar_test(bar, parity))
+    if (late(since)) return false;
+  return true;
 }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -127,20 +156,20 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int byt
 // ---- fragments ----
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -192,6 +221,21 @@ __device__ __forceinline__ uint2 lds64(uint32_t p) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
   return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t p, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t p, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(p), "r"(v.x), "r"(v.y) : "memory");
+}
+
 // ---- the list of work ----
 
 // What a request's rows see together, and its tiles.
@@ -239,36 +283,82 @@ struct Place {
   }
 };
 
-template <typename E>
-__device__ __forceinline__ float query_at(const E* p, int d) {
-  return static_cast<float>(p[d]);
-}
-
 // ---- the kernel ----
 
-template <typename E, int D, int NT>
+// What a warp keeps of its rows: fragments of the queries (one warp alone),
+// sums, maxima, and where its lanes read in a tile.
+template <typename E, int D, int NT, int P>
 struct Rows {
   static constexpr bool kF32 = sizeof(E) == 4;
   static constexpr int kSteps = D / 16;  // k16 steps of a key row, and m16 tiles of a value row
   static constexpr int kParts = kF32 ? 2 : 1;
-  uint32_t q[NT][kSteps][2 * kParts];
-  float o[kSteps][NT][4];
-  float f[NT][2];  // factor of a row's scores (log2 units)
+  static constexpr int kJ = 4 / P;       // sets of 16 tokens that the warp scores
+  static constexpr int kI = kSteps / P;  // value tiles that it sums
+  uint32_t q[P == 1 ? NT : 1][P == 1 ? kSteps : 1][2 * kParts];
+  float f[P == 1 ? NT : 1][2];  // factor of a row's scores (log2 units)
+  float o[kI][NT][4];
   float m[NT][2], l[NT][2];
-  // the lane's offsets in a tile: its first key row, that row's scales, its
-  // values' block, its first value chunk there
-  uint32_t key_at, scale_at, value_at, row_at;
+  // offsets in a tile: the lane's first key row, that row's scales, its values
+  uint32_t key_at, scale_at, value_at;
+  int pw;           // which of a pair
+  uint32_t shared;  // a pair's queries and exchange
+  const int2* span; // positions that each row sees
   Bases bases;
-  __device__ __forceinline__ void place(int lane) {
+
+  static constexpr int kWeights = NT * 1024 * kParts;  // bytes of a tile's weights
+  __device__ __forceinline__ uint32_t weights_at(int buf, int j, int nt, int lane) const {
+    return shared + query_bytes(D, NT, kF32) + buf * kWeights + (j * NT + nt) * 256 * kParts + lane * 8 * kParts;
+  }
+  __device__ __forceinline__ uint32_t tops_at(int buf, int half) const {
+    return shared + query_bytes(D, NT, kF32) + 2 * kWeights + (buf * 2 + half) * NT * 32;
+  }
+  __device__ __forceinline__ uint32_t factors_at() const { return tops_at(2, 0); }
+  __device__ __forceinline__ uint32_t sums_at(int half) const { return tops_at(2, 1) + half * NT * 32; }
+  __device__ __forceinline__ uint32_t more_at(int buf, int half) const { return sums_at(2) + (buf * 2 + half) * 4; }
+
+  __device__ __forceinline__ void place(int lane, int pw_, uint32_t shared_, const int2* span_) {
     const int r = lane >> 2, c = lane & 3;
     const uint32_t blk = (r >> 1) * block_stride(D);
-    key_at = blk + (r & 1) * (D / 2) + (D == 64 ? c * 8 : c * 16) + (D == 256 ? (r & 1) * 64 : 0);
-    scale_at = blk + kv_k_scales(D) + (D == 64 ? c * 16 + (r & 1) * 8 : c * 32 + (r & 1) * 16);
-    value_at = c * block_stride(D);
-    row_at = r * 16;
+    pw = pw_;
+    shared = shared_;
+    span = span_;
+    key_at = blk + (r & 1) * (D / 2) + (D == 64 ? c * 8 : c * 16) + pw * kJ * 4 * (D / 2);
+    scale_at = blk + kv_k_scales(D) + (D == 64 ? c * 16 + (r & 1) * 8 + pw * 4 : c * 32 + (r & 1) * 16 + pw * 8);
+    value_at = c * block_stride(D) + kv_v_codes(D) + pw * kI * 128 + r * 16;
     bases = make_bases();
   }
+  __device__ __forceinline__ void query(int nt, int step, int lane, uint32_t (&b)[2 * kParts]) const {
+    if constexpr (P == 1) {
+#pragma unroll
+      for (int x = 0; x < 2 * kParts; ++x) b[x] = q[nt][step][x];
+    } else if constexpr (kF32) {
+      const uint4 v = lds128(shared + (nt * kSteps + step) * 512 + lane * 16);
+      b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+    } else {
+      const uint2 v = lds64(shared + (nt * kSteps + step) * 256 + lane * 8);
+      b[0] = v.x, b[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void set_query(int nt, int step, int lane, const uint32_t (&b)[2 * kParts]) {
+    if constexpr (P == 1) {
+#pragma unroll
+      for (int x = 0; x < 2 * kParts; ++x) q[nt][step][x] = b[x];
+    } else if constexpr (kF32) {
+      sts128(shared + (nt * kSteps + step) * 512 + lane * 16, make_uint4(b[0], b[1], b[2], b[3]));
+    } else {
+      sts64(shared + (nt * kSteps + step) * 256 + lane * 8, make_uint2(b[0], b[1]));
+    }
+  }
 };
+
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ float2 lds_f2(uint32_t p) {
+  const uint2 v = lds64(p);
+  return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+}
+__device__ __forceinline__ void sts_f2(uint32_t p, float x, float y) {
+  sts64(p, make_uint2(__float_as_uint(x), __float_as_uint(y)));
+}
 
 // The element of a head that lane quarter c holds first in step s.
 template <int D>
@@ -277,169 +367,209 @@ __device__ __forceinline__ int key_element(int c, int s) {
   return c * (D / 4) + s * 4;
 }
 
-template <typename E, int D, int NT>
-__device__ __forceinline__ void load_queries(const AttnLaunch& L, Rows<E, D, NT>& w, int b, int h, int row0, int nrows,
-                                             int lane) {
-  using W = Rows<E, D, NT>;
+template <typename E, int D, int NT, int P>
+__device__ __forceinline__ void load_queries(const AttnLaunch& L, Rows<E, D, NT, P>& w, int b, int h, int row0, int nrows,
+                                             const Span& sp, int2* span, int lane, int sync) {
+  using W = Rows<E, D, NT, P>;
   const int r = lane >> 2, c = lane & 3;
+  __syncwarp();  // the rows before are done with shared memory
+  for (int k = lane; k < NT * 8; k += 32) {
+    const int i = (row0 + k) / L.per;
+    span[k] = make_int2(row_lo(L.a, sp.len, i), min(row_hi(L.a, sp.len, i), sp.hi));
+  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int row = row0 + nt * 8 + r;
-    float x[W::kSteps][4];
-    float top = 0.f;
-    const bool real = row < nrows;
-    const int i = real ? row / L.per : 0, g = real ? row % L.per : 0;
-    const E* p = static_cast<const E*>(L.a.q) + b * L.a.qs[0] + i * L.a.qs[1] + (h * L.per + g) * L.a.qs[2];
+    if (P == 1 || nt % 2 == w.pw) {
+      const int row = row0 + nt * 8 + r;
+      float x[W::kSteps][4];
+      float top = 0.f;
+      const bool real = row < nrows;
+      const int i = real ? row / L.per : 0, g = real ? row % L.per : 0;
+      const E* p = static_cast<const E*>(L.a.q) + b * L.a.qs[0] + i * L.a.qs[1] + (h * L.per + g) * L.a.qs[2];
 #pragma unroll
-    for (int s = 0; s < W::kSteps; ++s)
+      for (int s = 0; s < W::kSteps; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[s][e] = real ? query_at(p, key_element<D>(c, s) + e) : 0.f;
-        top = fmaxf(top, fabsf(x[s][e]));
-      }
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-    // the row's largest element to [2^12, 2^13)
-    int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-    ex = max(-100, min(ex, 127));
-    // the scale's sign goes to the query, so that the largest product is the
-    // largest score
-    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), L.a.scale_log2);
-    const float f = fabsf(L.a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23);
-    w.f[nt][0] = __shfl_sync(~0u, f, (2 * c) * 4);
-    w.f[nt][1] = __shfl_sync(~0u, f, (2 * c + 1) * 4);
-#pragma unroll
-    for (int s = 0; s < W::kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float y0 = x[s][2 * e] * up, y1 = x[s][2 * e + 1] * up;
-        const __half2 hi = __floats2half2_rn(y0, y1);
-        w.q[nt][s][e] = half2_bits(hi);
-        if constexpr (W::kF32) {
-          const float2 back = __half22float2(hi);
-          w.q[nt][s][2 + e] = half2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
+        for (int e = 0; e < 4; ++e) {
+          x[s][e] = real ? static_cast<float>(p[key_element<D>(c, s) + e]) : 0.f;
+          top = fmaxf(top, fabsf(x[s][e]));
         }
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      // the row's largest element to [2^12, 2^13)
+      int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      ex = max(-100, min(ex, 127));
+      // the scale's sign goes to the query, so that the largest product is the
+      // largest score
+      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), L.a.scale_log2);
+      const float f = fabsf(L.a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23);
+      const float f0 = __shfl_sync(~0u, f, (2 * c) * 4), f1 = __shfl_sync(~0u, f, (2 * c + 1) * 4);
+      if constexpr (P == 1) {
+        w.f[nt][0] = f0, w.f[nt][1] = f1;
+      } else if (r == 0) {
+        sts_f2(w.factors_at() + nt * 32 + c * 8, f0, f1);
       }
+#pragma unroll
+      for (int s = 0; s < W::kSteps; ++s) {
+        uint32_t part[2 * W::kParts];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float y0 = x[s][2 * e] * up, y1 = x[s][2 * e + 1] * up;
+          const __half2 hi = __floats2half2_rn(y0, y1);
+          part[e] = half2_bits(hi);
+          if constexpr (W::kF32) {
+            const float2 back = __half22float2(hi);
+            part[2 + e] = half2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y));
+          }
+        }
+        w.set_query(nt, s, lane, part);
+      }
+    }
     w.m[nt][0] = w.m[nt][1] = -INFINITY;
     w.l[nt][0] = w.l[nt][1] = 0.f;
 #pragma unroll
-    for (int i2 = 0; i2 < W::kSteps; ++i2)
+    for (int i2 = 0; i2 < W::kI; ++i2)
 #pragma unroll
       for (int e = 0; e < 4; ++e) w.o[i2][nt][e] = 0.f;
   }
+  __syncwarp();
+  if constexpr (P == 2) pair_sync(sync);
 }
 
 // One tile at `base` (shared memory) for the first NA n-tiles.  Token t of
 // block k is row (k, t) of the fragments: S tile j holds tokens 4 j .. 4 j + 3
 // of every block, fragment row r of it token 4 j + r % 2 of block r / 2 and row
-// r + 8 the token two later.  `edge`: some row does not see some token.  Returns
-// the further bands (bits) that a first pass, band 0, leaves to be done.
-template <typename E, int D, int NT, int NA>
-__device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT>& w, uint32_t base, int pos0, bool edge,
-                                          const Span& sp, int row0, int lane, int band) {
-  using W = Rows<E, D, NT>;
-  constexpr int kStride = block_stride(D);
+// r + 8 the token two later.  Of a pair, a warp scores two of the four j and
+// hands the weights to the other, then sums half of the elements over all
+// tokens; the one barrier per tile suffices because buffers alternate.
+// `edge`: some row does not see some token.  Returns the further bands (bits)
+// that a first pass, band 0, leaves to be done.
+template <typename E, int D, int NT, int P, int NA>
+__device__ __forceinline__ uint32_t tile_step(Rows<E, D, NT, P>& w, uint32_t base, int pos0, bool edge, int lo_seen,
+                                              int hi_seen, int lane, int sync, int buf, int band) {
+  using W = Rows<E, D, NT, P>;
   const int r = lane >> 2, c = lane & 3;
-  float s[4][NA][4];
-  // scores
+  float s[W::kJ][NA][4];
+  // scores: kSets sets of 16 tokens go side by side, so that consecutive matrix
+  // instructions do not wait on one another's sums
+  constexpr int kSets = NA == 1 ? W::kJ : 2;
 #pragma unroll
   for (int hh = 0; hh < (D == 256 ? 2 : 1); ++hh) {
     constexpr int kWords = D == 64 ? 2 : 4;
-    const uint32_t blk = base + w.key_at;
-    uint32_t sv[4];  // D = 64: bytes 2 j + y of 8; else bytes 2 y + g of word j (token y of two, group g of two)
-    if constexpr (D == 64) {
+    // D = 256: odd tokens' halves are exchanged
+    const uint32_t blk = base + w.key_at + (D == 256 ? (hh ^ (r & 1)) * 64 : 0);
+    uint32_t sv[4];  // D = 64: bytes y of word j; else bytes 2 y + g (token y of two, group g of two)
+    if constexpr (D == 64 && P == 1) {
       const uint2 x = lds64(base + w.scale_at);
       sv[0] = x.x, sv[1] = x.x >> 16, sv[2] = x.y, sv[3] = x.y >> 16;
-    } else {
+    } else if constexpr (D == 64) {
+      sv[0] = lds32(base + w.scale_at), sv[1] = sv[0] >> 16;
+    } else if constexpr (P == 1) {
       const uint4 x = lds128(base + w.scale_at + hh * 128);
       sv[0] = x.x, sv[1] = x.y, sv[2] = x.z, sv[3] = x.w;
+    } else {
+      const uint2 x = lds64(base + w.scale_at + hh * 128);
+      sv[0] = x.x, sv[1] = x.y;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t wa[kWords], wb[kWords];
-      if constexpr (D == 64) {
-        const uint2 xa = lds64(blk + 4 * j * 32), xb = lds64(blk + (4 * j + 2) * 32);
-        wa[0] = xa.x, wa[1] = xa.y, wb[0] = xb.x, wb[1] = xb.y;
-      } else {
-        const uint32_t at = hh ? blk + 64 - (r & 1) * 128 : blk;  // odd tokens' halves are exchanged
-        const uint4 xa = lds128(at + 4 * j * (D / 2)), xb = lds128(at + (4 * j + 2) * (D / 2));
-        wa[0] = xa.x, wa[1] = xa.y, wa[2] = xa.z, wa[3] = xa.w;
-        wb[0] = xb.x, wb[1] = xb.y, wb[2] = xb.z, wb[3] = xb.w;
+    for (int j0 = 0; j0 < W::kJ; j0 += kSets) {
+      uint32_t wa[kSets][kWords], wb[kSets][kWords];
+#pragma unroll
+      for (int j = 0; j < kSets; ++j) {
+        const uint32_t at = blk + 4 * (j0 + j) * (D / 2);
+        if constexpr (D == 64) {
+          const uint2 xa = lds64(at), xb = lds64(at + 2 * (D / 2));
+          wa[j][0] = xa.x, wa[j][1] = xa.y, wb[j][0] = xb.x, wb[j][1] = xb.y;
+        } else {
+          const uint4 xa = lds128(at), xb = lds128(at + 2 * (D / 2));
+          wa[j][0] = xa.x, wa[j][1] = xa.y, wa[j][2] = xa.z, wa[j][3] = xa.w;
+          wb[j][0] = xb.x, wb[j][1] = xb.y, wb[j][2] = xb.z, wb[j][3] = xb.w;
+        }
       }
 #pragma unroll
       for (int g = 0; g < kWords / 2; ++g) {
-        const uint32_t sa = __byte_perm(sv[j], 0, D == 64 ? 0x4040 : 0x4040 + 0x0101 * g) << 7;
-        const uint32_t sb = __byte_perm(sv[j], 0, D == 64 ? 0x4141 : 0x4040 + 0x0101 * (2 + g)) << 7;
-        const uint32_t a24 = mul2(sa, kMinus24), a264 = mul2(sa, kMinus264);
-        const uint32_t b24 = mul2(sb, kMinus24), b264 = mul2(sb, kMinus264);
+        uint32_t sc[kSets][6];
+#pragma unroll
+        for (int j = 0; j < kSets; ++j) {
+          sc[j][0] = __byte_perm(sv[j0 + j], 0, D == 64 ? 0x4040 : 0x4040 + 0x0101 * g) << 7;
+          sc[j][1] = __byte_perm(sv[j0 + j], 0, D == 64 ? 0x4141 : 0x4040 + 0x0101 * (2 + g)) << 7;
+          sc[j][2] = mul2(sc[j][0], kMinus24), sc[j][3] = mul2(sc[j][0], kMinus264);
+          sc[j][4] = mul2(sc[j][1], kMinus24), sc[j][5] = mul2(sc[j][1], kMinus264);
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {  // two words, two steps each
           const int word = 2 * g + (x >> 1), step = hh * 8 + 2 * word + (x & 1);
-          const uint32_t ua = x & 1 ? __funnelshift_r(wa[word], wa[word], 8) : wa[word];
-          const uint32_t ub = x & 1 ? __funnelshift_r(wb[word], wb[word], 8) : wb[word];
-          const uint32_t a[4] = {fma2(pair_hi(ua, w.bases), sa, a24), fma2(pair_hi(ub, w.bases), sb, b24),
-                                 fma2(pair_lo(ua, w.bases), sa, a264), fma2(pair_lo(ub, w.bases), sb, b264)};
+          uint32_t q[NA][2 * W::kParts];
 #pragma unroll
-          for (int nt = 0; nt < NA; ++nt) {
-            if (step == 0) mma_first(s[j][nt], a, w.q[nt][step][0], w.q[nt][step][1]);
-            else mma(s[j][nt], a, w.q[nt][step][0], w.q[nt][step][1]);
-            if constexpr (W::kF32) mma(s[j][nt], a, w.q[nt][step][2], w.q[nt][step][3]);
+          for (int nt = 0; nt < NA; ++nt) w.query(nt, step, lane, q[nt]);
+#pragma unroll
+          for (int j = 0; j < kSets; ++j) {
+            const uint32_t ua = x & 1 ? __funnelshift_r(wa[j][word], wa[j][word], 8) : wa[j][word];
+            const uint32_t ub = x & 1 ? __funnelshift_r(wb[j][word], wb[j][word], 8) : wb[j][word];
+            const uint32_t a[4] = {
+                fma2(pair_hi(ua, w.bases), sc[j][0], sc[j][2]), fma2(pair_hi(ub, w.bases), sc[j][1], sc[j][4]),
+                fma2(pair_lo(ua, w.bases), sc[j][0], sc[j][3]), fma2(pair_lo(ub, w.bases), sc[j][1], sc[j][5])};
+#pragma unroll
+            for (int nt = 0; nt < NA; ++nt) {
+              if (step == 0) mma_first(s[j0 + j][nt], a, q[nt][0], q[nt][1]);
+              else mma(s[j0 + j][nt], a, q[nt][0], q[nt][1]);
+              if constexpr (W::kF32) mma(s[j0 + j][nt], a, q[nt][2], q[nt][3]);
+            }
           }
         }
       }
     }
   }
-  // weights: 2^kBias at the tile's own maximum of the row
+  // weights: 2^kBias at the maximum of the row in the warp's tokens
   uint32_t p[4][NA][2 * W::kParts];
-  float grow[NA][2];  // factor of this pass's products
+  float grow[NA][P][2];  // factors of this pass's products
+  float sum[NA][2];
   uint32_t more = 0;
 #pragma unroll
   for (int nt = 0; nt < NA; ++nt) {
+    float f[2];
+    if constexpr (P == 1) {
+      f[0] = w.f[nt][0], f[1] = w.f[nt][1];
+    } else {
+      const float2 x = lds_f2(w.factors_at() + nt * 32 + c * 8);
+      f[0] = x.x, f[1] = x.y;
+    }
     if (edge) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int i = (row0 + nt * 8 + 2 * c + x) / L.per;
-        const int lo = row_lo(L.a, sp.len, i), hi = min(row_hi(L.a, sp.len, i), sp.hi);
+        const int2 seen = w.span[nt * 8 + 2 * c + x];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < W::kJ; ++j)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const int pos = pos0 + (r >> 1) * kKvBlock + 4 * j + (r & 1) + 2 * y;
-            if (pos < lo || pos >= hi) s[j][nt][2 * y + x] = -INFINITY;
+            const int pos = pos0 + (r >> 1) * kKvBlock + 4 * (w.pw * W::kJ + j) + (r & 1) + 2 * y;
+            if (pos < seen.x || pos >= seen.y) s[j][nt][2 * y + x] = -INFINITY;
           }
       }
     }
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < W::kJ; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[j][nt][e]);
-    float fall[2], ref[2], sum[2] = {0.f, 0.f};
-    bool grown = false;
+      for (int k = 0; k < 4; ++k) top[k & 1] = fmaxf(top[k & 1], s[j][nt][k]);
+    float ref[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 4));
       top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 8));
       top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 16));
-      if (top[x] != -INFINITY) top[x] *= w.f[nt][x];  // f >= 0
-      const float m = fmaxf(w.m[nt][x], top[x]), zero = m == -INFINITY ? 0.f : m;
-      grown |= m != w.m[nt][x];
-      fall[x] = ex2(w.m[nt][x] - zero);  // the sums so far
-      w.m[nt][x] = m;
-      top[x] = top[x] == -INFINITY ? zero : top[x];
-      grow[nt][x] = ex2(top[x] - zero - kBand * band);
-      ref[x] = kBias - top[x];
+      if (top[x] != -INFINITY) top[x] *= f[x];  // f >= 0
+      ref[x] = kBias - (top[x] == -INFINITY ? 0.f : top[x]);
     }
-    float e[4][4];
+    float e[W::kJ][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < W::kJ; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) e[j][k] = ex2(fmaf(s[j][nt][k], w.f[nt][k & 1], ref[k & 1]));
+      for (int k = 0; k < 4; ++k) e[j][k] = ex2(fmaf(s[j][nt][k], f[k & 1], ref[k & 1]));
     bool small = false;  // a weight below fp16's normal range
     if (edge) {
       // (a factor of zero makes no number of a masked score)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < W::kJ; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const bool seen = s[j][nt][k] != -INFINITY;
@@ -447,63 +577,124 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
           small |= seen && e[j][k] < kSmallest;
         }
     }
+    sum[nt][0] = sum[nt][1] = 0.f;
     __half2 least = __float2half2_rn(1.f);
+    uint32_t ph[W::kJ][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < W::kJ; ++j) {
       const __half2 ha = __floats2half2_rn(e[j][0], e[j][1]), hb = __floats2half2_rn(e[j][2], e[j][3]);
-      sum[0] += e[j][0] + e[j][2];
-      sum[1] += e[j][1] + e[j][3];
+      sum[nt][0] += e[j][0] + e[j][2];
+      sum[nt][1] += e[j][1] + e[j][3];
       least = __hmin2(least, __hmin2(ha, hb));
-      p[j][nt][0] = half2_bits(ha);
-      p[j][nt][1] = half2_bits(hb);
+      ph[j][0] = half2_bits(ha);
+      ph[j][1] = half2_bits(hb);
     }
     // below 2^-14 fp16 keeps fewer bits: those weights go to a later band
     if (!edge) small = __low2float(least) < kSmallest || __high2float(least) < kSmallest;
     if (__any_sync(~0u, small) || band) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < W::kJ; ++j) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float u = fmaf(s[j][nt][k], w.f[nt][k & 1], ref[k & 1]);
+          const float u = fmaf(s[j][nt][k], f[k & 1], ref[k & 1]);
           int at = u >= kBias - kBand ? 0 : min(kBands, static_cast<int>((kBias - u) * (1.f / kBand)));
           if (edge && s[j][nt][k] == -INFINITY) at = kBands;
           if (band == 0 && at > 0 && at < kBands) more |= 1u << at;
           e[j][k] = at == band ? ex2(u + kBand * band) : 0.f;
         }
-        p[j][nt][0] = half2_bits(__floats2half2_rn(e[j][0], e[j][1]));
-        p[j][nt][1] = half2_bits(__floats2half2_rn(e[j][2], e[j][3]));
+        ph[j][0] = half2_bits(__floats2half2_rn(e[j][0], e[j][1]));
+        ph[j][1] = half2_bits(__floats2half2_rn(e[j][2], e[j][3]));
       }
     }
+#pragma unroll
+    for (int j = 0; j < W::kJ; ++j) {
+      uint32_t y[2 * W::kParts];
+      y[0] = transpose8(ph[j][0]);
+      y[1] = transpose8(ph[j][1]);
+      if constexpr (W::kF32) {
+        const float2 fa = __half22float2(*reinterpret_cast<__half2*>(&ph[j][0]));
+        const float2 fb = __half22float2(*reinterpret_cast<__half2*>(&ph[j][1]));
+        y[2] = transpose8(half2_bits(__floats2half2_rn((e[j][0] - fa.x) * kLowUp, (e[j][1] - fa.y) * kLowUp)));
+        y[3] = transpose8(half2_bits(__floats2half2_rn((e[j][2] - fb.x) * kLowUp, (e[j][3] - fb.y) * kLowUp)));
+      }
+      if constexpr (P == 1) {
+#pragma unroll
+        for (int x = 0; x < 2 * W::kParts; ++x) p[j][nt][x] = y[x];
+      } else {
+        const uint32_t at = w.weights_at(buf, w.pw * W::kJ + j, nt, lane);
+        if constexpr (W::kF32) sts128(at, make_uint4(y[0], y[1], y[2], y[3]));
+        else sts64(at, make_uint2(y[0], y[1]));
+      }
+    }
+    if constexpr (P == 1) {
+      grow[nt][0][0] = top[0], grow[nt][0][1] = top[1];
+    } else if (r == 0) {
+      sts_f2(w.tops_at(buf, w.pw) + nt * 32 + c * 8, top[0], top[1]);
+    }
+  }
+  more = __any_sync(~0u, more) ? __reduce_or_sync(~0u, more) : 0u;
+  if constexpr (P == 2) {
+    if (lane == 0) sts32(w.more_at(buf, w.pw), more);
+    pair_sync(sync);
+    more = lds32(w.more_at(buf, 0)) | lds32(w.more_at(buf, 1));
+#pragma unroll
+    for (int nt = 0; nt < NA; ++nt) {
+#pragma unroll
+      for (int h = 0; h < P; ++h) {
+        const float2 x = lds_f2(w.tops_at(buf, h) + nt * 32 + c * 8);
+        grow[nt][h][0] = x.x, grow[nt][h][1] = x.y;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t at = w.weights_at(buf, j, nt, lane);
+        if constexpr (W::kF32) {
+          const uint4 x = lds128(at);
+          p[j][nt][0] = x.x, p[j][nt][1] = x.y, p[j][nt][2] = x.z, p[j][nt][3] = x.w;
+        } else {
+          const uint2 x = lds64(at);
+          p[j][nt][0] = x.x, p[j][nt][1] = x.y;
+        }
+      }
+    }
+  }
+  // the row's maximum so far, and what that makes of the sums so far and of
+  // this tile's
+#pragma unroll
+  for (int nt = 0; nt < NA; ++nt) {
+    float fall[2];
+    bool grown = false;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float m = w.m[nt][x];
+#pragma unroll
+      for (int h = 0; h < P; ++h) m = fmaxf(m, grow[nt][h][x]);
+      const float zero = m == -INFINITY ? 0.f : m;
+      grown |= m != w.m[nt][x];
+      fall[x] = ex2(w.m[nt][x] - zero);
+      w.m[nt][x] = m;
+#pragma unroll
+      for (int h = 0; h < P; ++h) grow[nt][h][x] = ex2(grow[nt][h][x] - zero - kBand * band);
+    }
     if (band == 0) {
-      w.l[nt][0] = w.l[nt][0] * fall[0] + sum[0] * grow[nt][0];
-      w.l[nt][1] = w.l[nt][1] * fall[1] + sum[1] * grow[nt][1];
+      const float g0 = P == 2 && w.pw ? grow[nt][P - 1][0] : grow[nt][0][0];
+      const float g1 = P == 2 && w.pw ? grow[nt][P - 1][1] : grow[nt][0][1];
+      w.l[nt][0] = w.l[nt][0] * fall[0] + sum[nt][0] * g0;
+      w.l[nt][1] = w.l[nt][1] * fall[1] + sum[nt][1] * g1;
       if (__any_sync(~0u, grown)) {
 #pragma unroll
-        for (int i = 0; i < W::kSteps; ++i) {
+        for (int i = 0; i < W::kI; ++i) {
           w.o[i][nt][0] *= fall[0], w.o[i][nt][2] *= fall[0];
           w.o[i][nt][1] *= fall[1], w.o[i][nt][3] *= fall[1];
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (W::kF32) {
-        const float2 fa = __half22float2(*reinterpret_cast<__half2*>(&p[j][nt][0]));
-        const float2 fb = __half22float2(*reinterpret_cast<__half2*>(&p[j][nt][1]));
-        p[j][nt][2] = transpose8(half2_bits(__floats2half2_rn((e[j][0] - fa.x) * kLowUp, (e[j][1] - fa.y) * kLowUp)));
-        p[j][nt][3] = transpose8(half2_bits(__floats2half2_rn((e[j][2] - fb.x) * kLowUp, (e[j][3] - fb.y) * kLowUp)));
-      }
-      p[j][nt][0] = transpose8(p[j][nt][0]);
-      p[j][nt][1] = transpose8(p[j][nt][1]);
-    }
   }
   // values: lane quarter c takes block c, lane row r the elements r D/8 ..
-  const uint32_t blk = base + w.value_at;
-  constexpr int kGroups = D == 256 ? 2 : 1;
+  constexpr int kGroups = D == 256 && P == 1 ? 2 : 1;
 #pragma unroll
   for (int gg = 0; gg < kGroups; ++gg) {
-    const int group = D == 64 ? r >> 1 : D == 128 ? r : 2 * r + gg;
-    const uint4 vs = lds128(blk + kv_v_scales(D) + group * kKvBlock);
+    const int group = D == 64 ? r >> 1 : D == 128 ? r : 2 * r + (P == 1 ? gg : w.pw);
+    const uint4 vs = lds128(base + c * block_stride(D) + kv_v_scales(D) + group * kKvBlock);
     uint32_t sc[4] = {vs.x, vs.y, vs.z, vs.w};
     uint32_t nans = 0;  // tokens of block c whose values of this group are NaN
     if (edge) {
@@ -513,7 +704,7 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const uint32_t byte = (sc[k >> 2] >> ((k & 3) * 8)) & 0xFFu;
-        const bool seen = first + k >= sp.lo && first + k < sp.hi;
+        const bool seen = first + k >= lo_seen && first + k < hi_seen;
         if (seen && byte == kKvNanByte) nans |= 1u << k;
         if (!seen || byte == kKvNanByte) sc[k >> 2] &= ~(0xFFu << ((k & 3) * 8));
       }
@@ -521,43 +712,57 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
     uint32_t ss[4][4];  // per j: scales of its two token pairs and their offsets
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      ss[j][0] = __byte_perm(sc[j], 0, 0x1404) >> 1;
+      ss[j][0] = __byte_perm(sc[j], 0, 0x4140) << 7;
       ss[j][1] = mul2(ss[j][0], kMinus24);
-      ss[j][2] = __byte_perm(sc[j], 0, 0x3424) >> 1;
+      ss[j][2] = __byte_perm(sc[j], 0, 0x4342) << 7;
       ss[j][3] = mul2(ss[j][2], kMinus264);
     }
+    constexpr int kMost = W::kI / kGroups, kSide = NA == 1 ? (kMost < 4 ? kMost : 4) : NA == 2 ? 2 : 1;
 #pragma unroll
-    for (int ii = 0; ii < W::kSteps / kGroups; ++ii) {
-      const int i = gg * (W::kSteps / kGroups) + ii;
-      const uint4 v = lds128(blk + kv_v_codes(D) + i * 128 + w.row_at);
-      const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-      float t[NA][4];
-      [[maybe_unused]] float t2[NA][4];
+    for (int ii = 0; ii < kMost; ii += kSide) {
+      const int i0 = gg * kMost + ii;
+      uint32_t word[kSide][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w0 = word[j >> 1], w1 = word[2 + (j >> 1)];
-        const uint32_t u0 = j & 1 ? __funnelshift_r(w0, w0, 8) : w0;
-        const uint32_t u1 = j & 1 ? __funnelshift_r(w1, w1, 8) : w1;
-        const uint32_t a[4] = {fma2(pair_hi(u0, w.bases), ss[j][0], ss[j][1]), fma2(pair_hi(u1, w.bases), ss[j][0], ss[j][1]),
-                               fma2(pair_lo(u0, w.bases), ss[j][2], ss[j][3]), fma2(pair_lo(u1, w.bases), ss[j][2], ss[j][3])};
-#pragma unroll
-        for (int nt = 0; nt < NA; ++nt) {
-          if (j == 0) {
-            mma_first(t[nt], a, p[j][nt][0], p[j][nt][1]);
-            if constexpr (W::kF32) mma_first(t2[nt], a, p[j][nt][2], p[j][nt][3]);
-          } else {
-            mma(t[nt], a, p[j][nt][0], p[j][nt][1]);
-            if constexpr (W::kF32) mma(t2[nt], a, p[j][nt][2], p[j][nt][3]);
-          }
-        }
+      for (int i = 0; i < kSide; ++i) {
+        const uint4 v = lds128(base + w.value_at + (i0 + i) * 128);
+        word[i][0] = v.x, word[i][1] = v.y, word[i][2] = v.z, word[i][3] = v.w;
       }
 #pragma unroll
-      for (int nt = 0; nt < NA; ++nt)
+      for (int h = 0; h < P; ++h) {
+        float t[kSide][NA][4];
+        [[maybe_unused]] float t2[kSide][NA][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (W::kF32) t[nt][e] = fmaf(t2[nt][e], 1.f / kLowUp, t[nt][e]);
-          w.o[i][nt][e] = fmaf(t[nt][e], grow[nt][e & 1], w.o[i][nt][e]);
-        }
+        for (int jj = 0; jj < W::kJ; ++jj)
+#pragma unroll
+          for (int i = 0; i < kSide; ++i) {
+            const int j = h * W::kJ + jj;
+            const uint32_t w0 = word[i][j >> 1], w1 = word[i][2 + (j >> 1)];
+            const uint32_t u0 = j & 1 ? __funnelshift_r(w0, w0, 8) : w0;
+            const uint32_t u1 = j & 1 ? __funnelshift_r(w1, w1, 8) : w1;
+            const uint32_t a[4] = {
+                fma2(pair_hi(u0, w.bases), ss[j][0], ss[j][1]), fma2(pair_hi(u1, w.bases), ss[j][0], ss[j][1]),
+                fma2(pair_lo(u0, w.bases), ss[j][2], ss[j][3]), fma2(pair_lo(u1, w.bases), ss[j][2], ss[j][3])};
+#pragma unroll
+            for (int nt = 0; nt < NA; ++nt) {
+              if (jj == 0) {
+                mma_first(t[i][nt], a, p[j][nt][0], p[j][nt][1]);
+                if constexpr (W::kF32) mma_first(t2[i][nt], a, p[j][nt][2], p[j][nt][3]);
+              } else {
+                mma(t[i][nt], a, p[j][nt][0], p[j][nt][1]);
+                if constexpr (W::kF32) mma(t2[i][nt], a, p[j][nt][2], p[j][nt][3]);
+              }
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < kSide; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NA; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (W::kF32) t[i][nt][k] = fmaf(t2[i][nt][k], 1.f / kLowUp, t[i][nt][k]);
+              w.o[i0 + i][nt][k] = fmaf(t[i][nt][k], grow[nt][h][k & 1], w.o[i0 + i][nt][k]);
+            }
+      }
     }
     if (edge && __any_sync(~0u, nans)) {
       for (int k = 0; k < 4; ++k) {
@@ -567,192 +772,189 @@ __device__ __forceinline__ uint32_t tile_step(const AttnLaunch& L, Rows<E, D, NT
         for (int nt = 0; nt < NA; ++nt)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int i = (row0 + nt * 8 + 2 * c + x) / L.per;
-            const int lo = row_lo(L.a, sp.len, i), hi = min(row_hi(L.a, sp.len, i), sp.hi);
-            const int from = max(0, min(lo - first, 16)), to = max(0, min(hi - first, 16));
+            const int2 seen = w.span[nt * 8 + 2 * c + x];
+            const int from = max(0, min(seen.x - first, 16)), to = max(0, min(seen.y - first, 16));
             if (there & ((1u << to) - 1u) & ~((1u << from) - 1u))
 #pragma unroll
-              for (int ii = 0; ii < W::kSteps / kGroups; ++ii) {
-                w.o[gg * (W::kSteps / kGroups) + ii][nt][x] = __int_as_float(0x7FC00000);
-                w.o[gg * (W::kSteps / kGroups) + ii][nt][2 + x] = __int_as_float(0x7FC00000);
+              for (int ii = 0; ii < kMost; ++ii) {
+                w.o[gg * kMost + ii][nt][x] = __int_as_float(0x7FC00000);
+                w.o[gg * kMost + ii][nt][2 + x] = __int_as_float(0x7FC00000);
               }
           }
       }
     }
   }
-  return __any_sync(~0u, more) ? __reduce_or_sync(~0u, more) : 0u;
+  return more;
 }
 
-template <typename E, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1) kv_attention_kernel(const AttnLaunch L) {
-  using W = Rows<E, D, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long scan[kWarps * 32 + kWarps];
-  const KvAttnArgs& a = L.a;
-  const int R = L.p.r, T = L.p.t, S = L.p.s, RT = L.p.rt;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
-  const int team = warp / R;
-  // the warp's place among the team's rows; rotated so that a short last group
-  // does not always meet the same quarter of the SM
-  const int part = (warp % R + team * R / 4) % R;
-  const bool producer = warp % R == 0;
-  const uint32_t base = smem_u32(smem);
-  const uint32_t bars = base, data = base + kHead;
-  volatile int* flags = reinterpret_cast<int*>(smem + 16 * kMaxStages);  // [T * S]: the stage lacks a bad page's block
-  const auto full = [&](int st) { return bars + (team * S + st) * 16; };
-  const auto empty = [&](int st) { return bars + (team * S + st) * 16 + 8; };
-  const auto stage = [&](int st) { return data + (team * S + st) * stage_bytes(D); };
-  if (tid < T * S) {
-    bar_init(bars + tid * 16, 1);
-    bar_init(bars + tid * 16 + 8, R);
-    flags[tid] = 0;
-  }
-  // how many tiles there are, and where the teams begin
-  const int chunk = (a.B + nthr - 1) / nthr;
-  long long mine = 0;
-  for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) mine += find_span(a, b).tiles;
-  long long x = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(~0u, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) scan[kWarps * 32 + warp] = x;
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int v = 0; v < nthr / 32; ++v) {
-    if (v < warp) before += scan[kWarps * 32 + v];
-    total += scan[kWarps * 32 + v];
-  }
-  __syncthreads();
-  scan[tid] = before + x - mine;
-  __syncthreads();
-  const int per_request = a.c.kv_heads * RT;
-  const long long units = total * per_request;
-  const long long teams = static_cast<long long>(gridDim.x) * T;
-  const long long quota = (units + teams - 1) / teams;
-  const long long me = static_cast<long long>(blockIdx.x) * T + team;
-  const long long u_begin = me * quota, u_end = min(units, u_begin + quota);
-  if (u_begin >= u_end) {
-    if (producer && lane == 0) L.desc[me] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  Place at;
-  long long u0;  // first unit of the request
-  {
-    int lo = 0, hi = nthr - 1;  // last thread whose requests begin at or before u_begin
+// The CTA's view of the list: prefix sums of the requests' tiles.
+struct List {
+  const long long* scan;
+  int chunk, threads, per_request;
+  long long units, quota;
+  // The place of unit u, and the first unit of its request's tiles.
+  __device__ __forceinline__ Place find(const KvAttnArgs& a, long long u) const {
+    int lo = 0, hi = threads - 1;  // last thread whose requests begin at or before u
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (scan[mid] * per_request <= u_begin && mid * chunk < a.B) lo = mid;
+      if (scan[mid] * per_request <= u && mid * chunk < a.B) lo = mid;
       else hi = mid - 1;
     }
+    Place at;
     at.b = lo * chunk;
-    u0 = scan[lo] * per_request;
+    long long u0 = scan[lo] * per_request;
     at.s = find_span(a, at.b);
-    while (u0 + static_cast<long long>(at.s.tiles) * per_request <= u_begin) {
+    while (u0 + static_cast<long long>(at.s.tiles) * per_request <= u) {
       u0 += static_cast<long long>(at.s.tiles) * per_request;
       at.s = find_span(a, ++at.b);
     }
-    const long long k = u_begin - u0;
+    const long long k = u - u0;
     at.hr = static_cast<int>(k / at.s.tiles);
     at.tile = static_cast<int>(k % at.s.tiles);
+    return at;
   }
-  if (producer && lane == 0) {
+};
+
+// Keeps the copies of all teams going: four lanes per team, a block each.
+template <int D>
+__device__ __forceinline__ void produce(const AttnLaunch& L, const List& list, uint32_t bars, uint32_t data,
+                                        volatile int* flags, int lane) {
+  const KvAttnArgs& a = L.a;
+  const int S = L.p.s, RT = L.p.rt, team = lane >> 2;
+  const int bpp = a.c.page_size / kKvBlock;
+  const long long head_bytes = static_cast<long long>(bpp) * kv_block_bytes(D), page_bytes = head_bytes * a.c.kv_heads;
+  const long long u = (static_cast<long long>(blockIdx.x) * L.p.t + team) * list.quota;
+  int left = team < L.p.t && u < list.units ? static_cast<int>(min(list.units - u, list.quota)) : 0;
+  Place pr = {};
+  int put = 0, phase = 1;     // empty stages at first
+  int sub = 0, column = 0;    // this lane's block: of which page column, and where in the page
+  int page = 0;
+  bool want = false;          // the next tile has this lane's block
+  const auto locate = [&]() {
+    const int pb = (pr.s.tile0 + pr.tile) * (kTile / kKvBlock) + (lane & 3);
+    column = pb / bpp;
+    sub = pb % bpp;
+  };
+  const auto fetch_page = [&]() {
+    const int pos = (pr.s.tile0 + pr.tile) * kTile + (lane & 3) * kKvBlock;
+    want = pos < pr.s.hi && pos + kKvBlock > pr.s.lo;
+    if (want) page = a.c.page_table[static_cast<long long>(pr.b) * a.c.max_pages + column];
+  };
+  if (left) {
+    pr = list.find(a, u);
+    locate();
+    fetch_page();
+  }
+  __syncwarp();
+  unsigned long long idle = 0;
+  while (__any_sync(~0u, left > 0)) {
+    const uint32_t bar = bars + (team * S + put) * 16;
+    bool ready = left > 0 && (lane & 3) == 0 && bar_test(bar + 8, phase);
+    ready = __shfl_sync(~0u, ready, lane & 28);
+    if (!__any_sync(~0u, ready)) {
+      if (late(idle)) break;
+      continue;
+    }
+    idle = 0;
+    const bool ok = ready && want && page >= 0 && page < a.c.n_pages;
+    const uint32_t okm = __ballot_sync(~0u, ok) >> (lane & 28) & 15u;
+    const uint32_t bad = __ballot_sync(~0u, ready && want && !ok) >> (lane & 28) & 15u;
+    if (ready && (lane & 3) == 0) {
+      flags[team * S + put] = bad != 0;
+      if (bad) atomicOr(a.status, 1 << SSD_ERR_PAGE);
+      bar_expect(bar, __popc(okm) * kv_block_bytes(D));
+    }
+    __syncwarp();
+    if (ok)
+      bulk_copy(data + (team * S + put) * stage_bytes(D) + (lane & 3) * block_stride(D),
+                a.c.pages + page * page_bytes + pr.hr / RT * head_bytes + static_cast<long long>(sub) * kv_block_bytes(D),
+                kv_block_bytes(D), bar);
+    if (ready) {
+      if (++put == S) put = 0, phase ^= 1;
+      if (--left) {
+        pr.next(a, list.per_request);
+        if (pr.tile == 0 || bpp < 4) {
+          locate();
+        } else if ((sub += 4) >= bpp) {
+          sub -= bpp;
+          ++column;
+        }
+        fetch_page();
+      }
+    }
+    __syncwarp();
+  }
+  if (left > 0 && (lane & 3) == 0) atomicOr(a.status, 1 << SSD_ERR_CUDA);
+}
+
+template <typename E, int D, int NT, int P>
+__device__ __forceinline__ void consume(const AttnLaunch& L, const List& list, uint32_t bars, uint32_t data,
+                                        volatile int* flags, int2* spans, int warp, int lane) {
+  using W = Rows<E, D, NT, P>;
+  const KvAttnArgs& a = L.a;
+  const int S = L.p.s, RT = L.p.rt, G = L.p.g, T = L.p.t;
+  const int team = warp / (P * G), group = warp / P % G, pw = warp % P;
+  const int sync = 1 + warp / P;  // the pair's barrier
+  const long long me = static_cast<long long>(blockIdx.x) * T + team;
+  const long long u_begin = me * list.quota, u_end = min(list.units, u_begin + list.quota);
+  const bool first_warp = group == 0 && pw == 0;
+  if (u_begin >= u_end) {
+    if (first_warp && lane == 0) L.desc[me] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  Place at = list.find(a, u_begin);
+  if (first_warp && lane == 0) {
     // the first team to begin inside a row's tiles has its parts joined
-    const long long seg = u_begin - at.tile, prev = seg / quota;
+    const long long seg = u_begin - at.tile, prev = seg / list.quota;
     int4 d = make_int4(at.b, at.hr, 0, 0);
     if (at.tile > 0 && prev == me - 1) {
-      d.z = static_cast<int>((seg + at.s.tiles - 1) / quota - prev + 1);
-      d.w = static_cast<int>(2 * prev + (seg > prev * quota ? 1 : 0));
+      d.z = static_cast<int>((seg + at.s.tiles - 1) / list.quota - prev + 1);
+      d.w = static_cast<int>(2 * prev + (seg > prev * list.quota ? 1 : 0));
     }
     L.desc[me] = d;
   }
-
-  // producing: lanes 0..3 of the team's first warp copy a block each
-  const int n_tiles = static_cast<int>(u_end - u_begin);
-  const int bpp = a.c.page_size / kKvBlock;
-  Place pr = at;
-  int issued = 0, page = -2;  // page of this lane's block of the next tile; -2: no block
-  const auto fetch_page = [&]() {
-    const int pos = (pr.s.tile0 + pr.tile) * kTile + (lane & 3) * kKvBlock;
-    page = -2;
-    if (pos < pr.s.hi && pos + kKvBlock > pr.s.lo)
-      page = a.c.page_table[static_cast<long long>(pr.b) * a.c.max_pages + pos / kKvBlock / bpp];
-  };
-  const auto issue = [&]() -> bool {
-    const int st = issued % S;
-    if (R > 1 && issued >= S && !bar_wait(empty(st), (issued / S - 1) & 1)) return false;
-    const int pb = (pr.s.tile0 + pr.tile) * (kTile / kKvBlock) + (lane & 3);
-    const bool want = page != -2, ok = page >= 0 && page < a.c.n_pages;
-    const uint32_t okm = __ballot_sync(~0u, ok) & 15u, badm = __ballot_sync(~0u, want && !ok) & 15u;
-    if (lane == 0) {
-      flags[team * S + st] = badm != 0;
-      if (badm) atomicOr(a.status, 1 << SSD_ERR_PAGE);
-      bar_expect(full(st), __popc(okm) * kv_block_bytes(D));
-    }
-    __syncwarp();
-    if (lane < 4 && ok) {
-      const long long k = (static_cast<long long>(page) * a.c.kv_heads + pr.hr / RT) * bpp + pb % bpp;
-      bulk_copy(stage(st) + lane * block_stride(D), a.c.pages + k * kv_block_bytes(D), kv_block_bytes(D), full(st));
-    }
-    ++issued;
-    if (issued < n_tiles) {
-      pr.next(a, per_request);
-      fetch_page();
-    }
-    return true;
-  };
-  bool alive = true;
-  if (producer) {
-    fetch_page();
-    while (issued < n_tiles && issued < S) issue();
-  }
-
   W w;
-  w.place(lane);
+  w.place(lane, pw,
+          P == 2 ? data + T * S * stage_bytes(D) + (warp / P) * pair_bytes(D, NT, W::kF32) : 0u, spans);
+  const int n_tiles = static_cast<int>(u_end - u_begin);
+  int take = 0, phase = 0, buf = 0;
   int done = 0;
-  while (done < n_tiles && alive) {
+  bool dead = false;  // a copy did not arrive in time: go through the motions, without waiting
+  while (done < n_tiles) {
     const int b = at.b, h = at.hr / RT, pass0 = (at.hr % RT) * L.rows_pass;
     const int first = at.tile, count = min(n_tiles - done, at.s.tiles - at.tile);
     const Span sp = at.s;
     const int nrows = sp.bad ? 0 : sp.nq * L.per;  // real rows of the request
-    // the request's n-tiles, spread evenly over the team
+    // the request's n-tiles, spread evenly over the team's groups
     const int n8 = max(0, (min(nrows - pass0, L.rows_pass) + 7) / 8);
-    const int row0 = pass0 + part * n8 / R * 8;
-    const int own = (part + 1) * n8 / R - part * n8 / R;
+    const int row0 = pass0 + group * n8 / G * 8;
+    const int own = (group + 1) * n8 / G - group * n8 / G;
     const int active = sp.hi > sp.lo ? own : 0;
     const int lo_last = row_lo(a, sp.len, sp.nq - 1), hi_first = row_hi(a, sp.len, 0);
     bool bad = sp.bad;
-    load_queries<E, D, NT>(L, w, b, h, row0, nrows, lane);
+    load_queries<E, D, NT, P>(L, w, b, h, row0, nrows, sp, spans, lane, sync);
     for (int k = 0; k < count; ++k, ++done) {
-      const int st = done % S;
-      if (!bar_wait(full(st), (done / S) & 1)) {
-        alive = false;
-        break;
-      }
-      bad |= flags[team * S + st] != 0;
+      const uint32_t bar = bars + (team * S + take) * 16;
+      if (!dead && !bar_wait(bar, phase)) dead = true;
+      bad |= flags[team * S + take] != 0;
+      const uint32_t tile = data + (team * S + take) * stage_bytes(D);
       const int pos0 = (sp.tile0 + first + k) * kTile;
       const bool edge = pos0 < lo_last || pos0 + kTile > hi_first;
       for (uint32_t todo = active ? 1 : 0; todo;) {
         const int band = __ffs(todo) - 1;
         todo &= todo - 1;
-        if (active == 1) todo |= tile_step<E, D, NT, 1>(L, w, stage(st), pos0, edge, sp, row0, lane, band);
-        if constexpr (NT >= 2)
-          if (active == 2) todo |= tile_step<E, D, NT, 2>(L, w, stage(st), pos0, edge, sp, row0, lane, band);
-        if constexpr (NT >= 3)
-          if (active == 3) todo |= tile_step<E, D, NT, 3>(L, w, stage(st), pos0, edge, sp, row0, lane, band);
-        if constexpr (NT >= 4)
-          if (active == 4) todo |= tile_step<E, D, NT, 4>(L, w, stage(st), pos0, edge, sp, row0, lane, band);
+        constexpr int kHalf = (NT + 1) / 2;
+        if (kHalf < NT && active <= kHalf)
+          todo |= tile_step<E, D, NT, P, kHalf>(w, tile, pos0, edge, sp.lo, sp.hi, lane, sync, buf, band);
+        else
+          todo |= tile_step<E, D, NT, P, NT>(w, tile, pos0, edge, sp.lo, sp.hi, lane, sync, buf, band);
+        buf ^= 1;
       }
       __syncwarp();
-      if (R > 1 && lane == 0) bar_arrive(empty(st));
-      // a team of several warps refills a tile late, when the others are done
-      if (producer && issued < n_tiles && issued < done + 1 + S - (R > 1 ? 1 : 0) && !issue()) {
-        alive = false;
-        break;
-      }
+      if (lane == 0) bar_arrive(bar + 8);
+      if (++take == S) take = 0, phase ^= 1;
     }
-    if (!alive) break;
+    bad |= dead;
     // this part's sums
     const int r = lane >> 2, c = lane & 3;
     const bool whole = first == 0 && count == sp.tiles;
@@ -760,60 +962,69 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attention_kernel(const Attn
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int xx = 0; xx < 2; ++xx) {
-        float l = w.l[nt][xx];
-        l += __shfl_xor_sync(~0u, l, 4);
-        l += __shfl_xor_sync(~0u, l, 8);
-        l += __shfl_xor_sync(~0u, l, 16);
-        const int row = row0 + nt * 8 + 2 * c + xx;
-        if (row >= nrows) l = 0.f;  // a padded query's row went along with its tile
-        if (bad) l = __int_as_float(0x7FC00000);
+      for (int x = 0; x < 2; ++x) {
+        w.l[nt][x] += __shfl_xor_sync(~0u, w.l[nt][x], 4);
+        w.l[nt][x] += __shfl_xor_sync(~0u, w.l[nt][x], 8);
+        w.l[nt][x] += __shfl_xor_sync(~0u, w.l[nt][x], 16);
+      }
+    if constexpr (P == 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (r == 0) sts_f2(w.sums_at(pw) + nt * 32 + c * 8, w.l[nt][0], w.l[nt][1]);
+      pair_sync(sync);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 l0 = lds_f2(w.sums_at(0) + nt * 32 + c * 8), l1 = lds_f2(w.sums_at(1) + nt * 32 + c * 8);
+        w.l[nt][0] = l0.x + l1.x;
+        w.l[nt][1] = l0.y + l1.y;
+      }
+      pair_sync(sync);
+    }
+    constexpr int kOwn = 2 * W::kI;  // elements of a row that a lane holds
+    const int d0 = r * (D / 8) + pw * kOwn;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int row = row0 + nt * 8 + 2 * c + x;
         if (nt >= own || row >= L.rows) continue;
+        float l = row < nrows ? w.l[nt][x] : 0.f;  // a padded query's row went along with its tile
+        if (bad) l = __int_as_float(0x7FC00000);
         if (whole) {
           const int i = row / L.per;
           const long long orow = (static_cast<long long>(b) * a.nq + i) * a.heads + h * L.per + row % L.per;
           const float inv = 1.f / l;
-          float y[D / 8];
+          E* out = static_cast<E*>(a.out) + orow * D + d0;
 #pragma unroll
-          for (int i2 = 0; i2 < W::kSteps; ++i2) {
-            y[2 * i2] = l == 0.f ? 0.f : w.o[i2][nt][xx] * inv;
-            y[2 * i2 + 1] = l == 0.f ? 0.f : w.o[i2][nt][2 + xx] * inv;
-          }
-          E* out = static_cast<E*>(a.out) + orow * D + r * (D / 8);
-          if constexpr (W::kF32) {
+          for (int v = 0; v < kOwn / 4; ++v) {
+            float y[4];
 #pragma unroll
-            for (int v = 0; v < D / 32; ++v)
-              reinterpret_cast<float4*>(out)[v] = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
-          } else {
-#pragma unroll
-            for (int v = 0; v < D / 64; ++v) {
-              uint32_t z[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 hh = __floats2bfloat162_rn(y[8 * v + 2 * e], y[8 * v + 2 * e + 1]);
-                z[e] = *reinterpret_cast<const uint32_t*>(&hh);
-              }
-              reinterpret_cast<uint4*>(out)[v] = make_uint4(z[0], z[1], z[2], z[3]);
+            for (int k = 0; k < 4; ++k) y[k] = l == 0.f ? 0.f : w.o[2 * v + (k >> 1)][nt][x + 2 * (k & 1)] * inv;
+            if constexpr (W::kF32) {
+              reinterpret_cast<float4*>(out)[v] = make_float4(y[0], y[1], y[2], y[3]);
+            } else {
+              const __nv_bfloat162 ya = __floats2bfloat162_rn(y[0], y[1]), yb = __floats2bfloat162_rn(y[2], y[3]);
+              reinterpret_cast<uint2*>(out)[v] =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&ya), *reinterpret_cast<const uint32_t*>(&yb));
             }
           }
-          if (a.lse && r == 0)
-            a.lse[orow] = l == 0.f ? -INFINITY : (w.m[nt][xx] + (log2f(l) - kBias)) * 0.69314718055994531f;
+          if (a.lse && r == 0 && pw == 0)
+            a.lse[orow] = l == 0.f ? -INFINITY : (w.m[nt][x] + (log2f(l) - kBias)) * 0.69314718055994531f;
         } else {
           const long long at_row = slot * L.rows_pass + (row - pass0);
-          float* o = L.o + at_row * D + r * (D / 8);
+          float4* o = reinterpret_cast<float4*>(L.o + at_row * D + d0);
 #pragma unroll
-          for (int v = 0; v < D / 32; ++v)
-            reinterpret_cast<float4*>(o)[v] = make_float4(w.o[2 * v][nt][xx], w.o[2 * v][nt][2 + xx],
-                                                          w.o[2 * v + 1][nt][xx], w.o[2 * v + 1][nt][2 + xx]);
-          if (r == 0) L.ml[at_row] = make_float2(w.m[nt][xx], l);
+          for (int v = 0; v < kOwn / 4; ++v)
+            o[v] = make_float4(w.o[2 * v][nt][x], w.o[2 * v][nt][2 + x], w.o[2 * v + 1][nt][x], w.o[2 * v + 1][nt][2 + x]);
+          if (r == 0 && pw == 0) L.ml[at_row] = make_float2(w.m[nt][x], l);
         }
       }
     if (first == 0) {
       // rows past the request's own (all of them if its lengths are bad)
-      if (sp.bad && at.hr == 0 && part == 0 && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
+      if (sp.bad && at.hr == 0 && first_warp && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
       const float none = sp.bad ? __int_as_float(0x7FC00000) : 0.f;
       const int end = min(pass0 + L.rows_pass, L.rows);
-      for (int row = pass0 + 8 * n8 + part; row < end; row += R) {
+      for (int row = pass0 + 8 * n8 + group * P + pw; row < end; row += G * P) {
         const long long orow = (static_cast<long long>(b) * a.nq + row / L.per) * a.heads + h * L.per + row % L.per;
         for (int d = lane; d < D; d += 32) static_cast<E*>(a.out)[orow * D + d] = static_cast<E>(none);
         if (a.lse && lane == 0) a.lse[orow] = sp.bad ? none : -INFINITY;
@@ -822,16 +1033,64 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv_attention_kernel(const Attn
     at.tile += count;
     if (at.tile == at.s.tiles) {
       at.tile = at.s.tiles - 1;
-      at.next(a, per_request);
+      at.next(a, list.per_request);
     }
   }
-  if (!alive) {
-    // a copy did not arrive in time: say so, and wait (with the same limit) for
-    // the copies still in flight before the shared memory goes
+  if (dead) {
+    // say so, and give the copies still in flight the same time again before
+    // the shared memory goes
     if (lane == 0) atomicOr(a.status, 1 << SSD_ERR_CUDA);
-    if (producer)
-      for (int k = done; k < issued; ++k)
-        if (!bar_wait(full(k % S), (k / S) & 1)) break;
+    bar_wait(bars + (team * S + (take + S - 1) % S) * 16, take ? phase : phase ^ 1);
+  }
+}
+
+template <typename E, int D, int NT, int P>
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const __grid_constant__ AttnLaunch L) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long scan[kThreads], sums[kThreads / 32];
+  __shared__ int2 spans[kWarps][NT * 8];
+  const KvAttnArgs& a = L.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t bars = smem_u32(smem), data = bars + kHead;
+  volatile int* flags = reinterpret_cast<int*>(smem + 16 * kMaxStages);  // the stage lacks a bad page's block
+  if (tid < L.p.t * L.p.s) {
+    bar_init(bars + tid * 16, 1);
+    bar_init(bars + tid * 16 + 8, P * L.p.g);
+    flags[tid] = 0;
+  }
+  // how many tiles there are, and where the requests' begin
+  List list;
+  list.scan = scan;
+  list.threads = kThreads;
+  list.chunk = (a.B + kThreads - 1) / kThreads;
+  list.per_request = a.c.kv_heads * L.p.rt;
+  long long mine = 0;
+  for (int b = tid * list.chunk; b < min(a.B, (tid + 1) * list.chunk); ++b) mine += find_span(a, b).tiles;
+  long long x = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int v = 0; v < kThreads / 32; ++v) {
+    if (v < warp) before += sums[v];
+    total += sums[v];
+  }
+  scan[tid] = before + x - mine;
+  __syncthreads();
+  const long long teams = static_cast<long long>(gridDim.x) * L.p.t;
+  list.units = total * list.per_request;
+  list.quota = (list.units + teams - 1) / teams;
+  // 128 x (224 + 224 + 56) registers: the 384 x 168 of the launch
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kWarps) produce<D>(L, list, bars, data, flags, lane);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (warp < L.p.t * L.p.g * P) consume<E, D, NT, P>(L, list, bars, data, flags, spans[warp], warp, lane);
   }
 }
 
@@ -879,12 +1138,12 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnLaunch L) {
     L.a.lse[orow] = l == 0.f ? -INFINITY : (ref + (log2f(l) - kBias)) * 0.69314718055994531f;
 }
 
-template <typename E, int D, int NT>
-cudaError_t launch_nt(const AttnLaunch& L, int sms, cudaStream_t s) {
-  const int smem = kHead + L.p.t * L.p.s * stage_bytes(D);
-  cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<E, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename E, int D, int NT, int P>
+cudaError_t launch_shape(const AttnLaunch& L, int sms, cudaStream_t s) {
+  const int smem = kHead + L.p.t * (L.p.s * stage_bytes(D) + (P == 2 ? L.p.g * pair_bytes(D, NT, sizeof(E) == 4) : 0));
+  cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<E, D, NT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kv_attention_kernel<E, D, NT><<<sms, L.p.t * L.p.r * 32, smem, s>>>(L);
+  kv_attention_kernel<E, D, NT, P><<<sms, kThreads, smem, s>>>(L);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
@@ -899,16 +1158,19 @@ cudaError_t launch_nt(const AttnLaunch& L, int sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<E, D>, L);
 }
 
+template <typename E, int D, int P, int NT>
+cudaError_t launch_rows(const AttnLaunch& L, int sms, cudaStream_t s) {
+  constexpr bool kF32 = sizeof(E) == 4;
+  if constexpr (NT <= max_nt(D, kF32, P) && (P == 1 || NT >= (kF32 || D == 256 ? 1 : 3))) {
+    if (L.p.nt == NT) return launch_shape<E, D, NT, P>(L, sms, s);
+  }
+  if constexpr (NT > 1) return launch_rows<E, D, P, NT - 1>(L, sms, s);
+  return cudaErrorInvalidValue;
+}
+
 template <typename E, int D>
 cudaError_t launch_dim(const AttnLaunch& L, int sms, cudaStream_t s) {
-  constexpr int kMost = max_nt(D, sizeof(E) == 4);
-  if constexpr (kMost >= 4)
-    if (L.p.nt == 4) return launch_nt<E, D, 4>(L, sms, s);
-  if constexpr (kMost >= 3)
-    if (L.p.nt == 3) return launch_nt<E, D, 3>(L, sms, s);
-  if constexpr (kMost >= 2)
-    if (L.p.nt == 2) return launch_nt<E, D, 2>(L, sms, s);
-  return launch_nt<E, D, 1>(L, sms, s);
+  return L.p.p == 1 ? launch_rows<E, D, 1, 2>(L, sms, s) : launch_rows<E, D, 2, 6>(L, sms, s);
 }
 
 struct WorkLayout {
@@ -916,7 +1178,7 @@ struct WorkLayout {
 };
 WorkLayout work_layout(const AttnShape& p, int D) {
   WorkLayout w;
-  const size_t teams = static_cast<size_t>(kMaxSms) * p.t, rows = 2 * teams * p.r * p.nt * 8;
+  const size_t teams = static_cast<size_t>(kMaxSms) * p.t, rows = 2 * teams * p.g * p.nt * 8;
   w.desc = 0;
   w.ml = w.desc + teams * sizeof(int4);
   w.o = (w.ml + rows * sizeof(float2) + 255) / 256 * 256;
@@ -941,7 +1203,7 @@ cudaError_t launch_kv_attention(const KvAttnArgs& a, int D, int esize, cudaStrea
   L.per = a.heads / a.c.kv_heads;
   L.rows = a.nq * L.per;
   L.p = attn_shape(L.rows, D, esize == 4);
-  L.rows_pass = L.p.r * L.p.nt * 8;
+  L.rows_pass = L.p.g * L.p.nt * 8;
   const WorkLayout w = work_layout(L.p, D);
   L.desc = reinterpret_cast<int4*>(a.work + w.desc);
   L.ml = reinterpret_cast<float2*>(a.work + w.ml);
