@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libssdv.so")
 SOURCES = ["ssdv_api.cu", "ssdv_verify.cu", "ssdv_saguaro.cu", "ssdv_topp.cu",
-           "ssdv_kv.cu", "ssdv_attn.cu"]
+           "ssdv_kv.cu", "ssdv_attn.cu", "ssdv_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -24,12 +24,7 @@
 // with a smaller one, which real scores hardly hold, is passed over again for
 // the octaves below.  Each tile's product is added to the row's fp32 sums with
 // its own power of two, and maxima and sums of weights are in fp32.
-//
-// Work is split evenly whatever the lengths: every team of warps takes the same
-// number of tiles of the list (request, kv head, tile).  Rows whose tiles are
-// split between teams leave partial sums in the workspace, which a second
-// kernel joins in the teams' order, so results do not depend on timing.
-#include "ssdv_kv.cuh"
+#include "ssdv_attn.cuh"
 
 #include <algorithm>
 
@@ -39,11 +34,8 @@ namespace {
 
 constexpr int kTile = 64;        // tokens per tile: four blocks
 constexpr int kBias = 15;        // weights are at most 2^kBias
-constexpr int kBand = 29;        // octaves below that in which fp16 keeps 11 bits
-constexpr int kBands = 5;        // passes a tile may take; weights below 2^-141 of its largest are dropped
-constexpr float kSmallest = 6.103515625e-05f;  // 2^(kBias - kBand)
 constexpr float kLowUp = 2048.f; // the second fp16 part of a weight is held this much up
-constexpr int kMaxSms = 160;     // the workspace is sized for this many CTAs
+constexpr int kTcRows = 0;       // more rows than this take ssdv_attn_tc.cu (bf16, 128 elements)
 constexpr int kSmem = 226000;    // dynamic shared memory, at most
 constexpr int kWarps = 8;        // computing warps per CTA, one CTA per SM
 constexpr int kThreads = 384;    // and four more, of which one keeps the copies going
@@ -73,16 +65,17 @@ __host__ __device__ constexpr int pair_bytes(int D, int nt, bool f32) {
   return query_bytes(D, nt, f32) + exchange_bytes(nt, f32);
 }
 
-// How the rows of a kv head are spread: nt n-tiles per warp or pair, g groups of
-// rows per team (all reading the same tile), rt passes over the cache; t teams
-// per CTA with s stages each.
-struct AttnShape {
-  int nt, p, g, t, s, rt;
-};
-
 AttnShape attn_shape(int rows, int D, bool f32) {
   AttnShape a;
   const int n8 = (rows + 7) / 8;
+  a.tc = D == 128 && !f32 && rows > kTcRows;
+  if (a.tc) {
+    // passes of 16 to 80 rows, as even as they come
+    a.rt = (rows + 79) / 80;
+    a.nt = ((rows + a.rt - 1) / a.rt + 15) / 16 * 2;
+    a.p = a.g = a.t = a.s = 1;
+    return a;
+  }
   a.p = n8 <= max_nt(D, f32, 1) ? 1 : 2;
   const int most = max_nt(D, f32, a.p);
   a.g = n8 <= most ? 1 : n8 <= 2 * most ? 2 : 4;
@@ -95,62 +88,6 @@ AttnShape attn_shape(int rows, int D, bool f32) {
   while (stages() < 2) --a.t;
   a.s = std::min({8, kMaxStages / a.t, stages()});
   return a;
-}
-
-struct AttnLaunch {
-  KvAttnArgs a;
-  AttnShape p;
-  int per;          // query heads per kv head
-  int rows;         // nq * per
-  int rows_pass;    // g * nt * 8
-  int4* desc;       // [teams]: request, head * rt + pass, parts, first slot
-  float2* ml;       // [2 teams, rows_pass]: maximum and sum of a part
-  float* o;         // [2 teams, rows_pass, D]
-};
-
-// ---- mbarriers and bulk copies ----
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void bar_init(uint32_t bar, int count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, int bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool bar_test(uint32_t bar, int parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-// True two seconds after the first call with since = 0: every wait ends.
-__device__ __forceinline__ bool late(unsigned long long& since) {
-  unsigned long long now;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
-  if (since == 0) since = now;
-  return now - since > 2000000000ull;
-}
-// False if the phase did not complete in that time.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, int parity) {
-  unsigned long long since = 0;
-  while (!bar_test(bar, parity))
-    if (late(since)) return false;
-  return true;
-}
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
 }
 
 // ---- fragments ----
@@ -172,117 +109,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-
-// 16 + u of the pairs at bits 9:6, 256 + u of those at bits 5:2: one three-input
-// operation each, for which the or-ed constants are kept in registers.
-struct Bases {
-  uint32_t hi, lo;
-};
-__device__ __forceinline__ Bases make_bases() {
-  Bases b;
-  asm volatile("mov.b32 %0, 0x4C004C00;\n\tmov.b32 %1, 0x5C005C00;" : "=r"(b.hi), "=r"(b.lo));
-  return b;
-}
-__device__ __forceinline__ uint32_t pair_hi(uint32_t w, const Bases& b) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, 0x03C003C0, %2, 0xEA;" : "=r"(d) : "r"(w), "r"(b.hi));
-  return d;
-}
-__device__ __forceinline__ uint32_t pair_lo(uint32_t w, const Bases& b) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, 0x003C003C, %2, 0xEA;" : "=r"(d) : "r"(w), "r"(b.lo));
-  return d;
-}
-constexpr uint32_t kMinus24 = 0xCE00CE00u, kMinus264 = 0xDC20DC20u;  // fp16 pairs
-
-__device__ __forceinline__ uint4 lds128(uint32_t p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t p) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t p) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p));
-  return v;
-}
-__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t p, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ void sts64(uint32_t p, uint2 v) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(p), "r"(v.x), "r"(v.y) : "memory");
-}
-
-// ---- the list of work ----
-
-// What a request's rows see together, and its tiles.
-struct Span {
-  int len, nq;     // query rows i < nq are real
-  int lo, hi;      // positions some row sees
-  int tile0, tiles;  // at least one tile, so that some team writes the outputs
-  bool bad;
-};
-__device__ __forceinline__ Span find_span(const KvAttnArgs& a, int b) {
-  Span s;
-  s.len = a.kv_len[b];
-  s.nq = a.n_q ? a.n_q[b] : a.nq;
-  s.bad = s.len < 0 || s.nq < 0 || s.nq > a.nq ||
-          static_cast<long long>(s.len) + (a.past_only ? 0 : s.nq) >
-              static_cast<long long>(a.c.max_pages) * a.c.page_size;
-  s.lo = s.hi = s.tile0 = 0;
-  s.tiles = 1;
-  if (s.bad || s.nq == 0) return s;
-  s.hi = a.past_only ? s.len : s.len + s.nq;
-  s.lo = a.window ? max(0, s.len + 1 - a.window) : 0;
-  if (s.lo >= s.hi) {
-    s.lo = s.hi = 0;
-    return s;
-  }
-  s.tile0 = s.lo / kTile;
-  s.tiles = (s.hi + kTile - 1) / kTile - s.tile0;
-  return s;
-}
-__device__ __forceinline__ int row_lo(const KvAttnArgs& a, int len, int i) {
-  return a.window ? max(0, len + i + 1 - a.window) : 0;
-}
-__device__ __forceinline__ int row_hi(const KvAttnArgs& a, int len, int i) { return a.past_only ? len : len + i + 1; }
-
-// A place in the list.
-struct Place {
-  int b, hr, tile;  // request, head * rt + pass, tile of the request's span
-  Span s;
-  __device__ __forceinline__ void next(const KvAttnArgs& a, int per_request) {
-    if (++tile < s.tiles) return;
-    tile = 0;
-    if (++hr < per_request) return;
-    hr = 0;
-    if (++b < a.B) s = find_span(a, b);
-  }
-};
-
 // ---- the kernel ----
 
 // What a warp keeps of its rows: fragments of the queries (one warp alone),
@@ -787,37 +613,9 @@ __device__ __forceinline__ uint32_t tile_step(Rows<E, D, NT, P>& w, uint32_t bas
   return more;
 }
 
-// The CTA's view of the list: prefix sums of the requests' tiles.
-struct List {
-  const long long* scan;
-  int chunk, threads, per_request;
-  long long units, quota;
-  // The place of unit u, and the first unit of its request's tiles.
-  __device__ __forceinline__ Place find(const KvAttnArgs& a, long long u) const {
-    int lo = 0, hi = threads - 1;  // last thread whose requests begin at or before u
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (scan[mid] * per_request <= u && mid * chunk < a.B) lo = mid;
-      else hi = mid - 1;
-    }
-    Place at;
-    at.b = lo * chunk;
-    long long u0 = scan[lo] * per_request;
-    at.s = find_span(a, at.b);
-    while (u0 + static_cast<long long>(at.s.tiles) * per_request <= u) {
-      u0 += static_cast<long long>(at.s.tiles) * per_request;
-      at.s = find_span(a, ++at.b);
-    }
-    const long long k = u - u0;
-    at.hr = static_cast<int>(k / at.s.tiles);
-    at.tile = static_cast<int>(k % at.s.tiles);
-    return at;
-  }
-};
-
 // Keeps the copies of all teams going: four lanes per team, a block each.
 template <int D>
-__device__ __forceinline__ void produce(const AttnLaunch& L, const List& list, uint32_t bars, uint32_t data,
+__device__ __forceinline__ void produce(const AttnLaunch& L, const List<kTile>& list, uint32_t bars, uint32_t data,
                                         volatile int* flags, int lane) {
   const KvAttnArgs& a = L.a;
   const int S = L.p.s, RT = L.p.rt, team = lane >> 2;
@@ -825,7 +623,7 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List& list, u
   const long long head_bytes = static_cast<long long>(bpp) * kv_block_bytes(D), page_bytes = head_bytes * a.c.kv_heads;
   const long long u = (static_cast<long long>(blockIdx.x) * L.p.t + team) * list.quota;
   int left = team < L.p.t && u < list.units ? static_cast<int>(min(list.units - u, list.quota)) : 0;
-  Place pr = {};
+  Place<kTile> pr = {};
   int put = 0, phase = 1;     // empty stages at first
   int sub = 0, column = 0;    // this lane's block: of which page column, and where in the page
   int page = 0;
@@ -888,7 +686,7 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List& list, u
 }
 
 template <typename E, int D, int NT, int P>
-__device__ __forceinline__ void consume(const AttnLaunch& L, const List& list, uint32_t bars, uint32_t data,
+__device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& list, uint32_t bars, uint32_t data,
                                         volatile int* flags, int2* spans, int warp, int lane) {
   using W = Rows<E, D, NT, P>;
   const KvAttnArgs& a = L.a;
@@ -902,17 +700,8 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List& list, u
     if (first_warp && lane == 0) L.desc[me] = make_int4(0, 0, 0, 0);
     return;
   }
-  Place at = list.find(a, u_begin);
-  if (first_warp && lane == 0) {
-    // the first team to begin inside a row's tiles has its parts joined
-    const long long seg = u_begin - at.tile, prev = seg / list.quota;
-    int4 d = make_int4(at.b, at.hr, 0, 0);
-    if (at.tile > 0 && prev == me - 1) {
-      d.z = static_cast<int>((seg + at.s.tiles - 1) / list.quota - prev + 1);
-      d.w = static_cast<int>(2 * prev + (seg > prev * list.quota ? 1 : 0));
-    }
-    L.desc[me] = d;
-  }
+  Place<kTile> at = list.find(a, u_begin);
+  if (first_warp && lane == 0) L.desc[me] = list.parts(at, me);
   W w;
   w.place(lane, pw,
           P == 2 ? data + T * S * stage_bytes(D) + (warp / P) * pair_bytes(D, NT, W::kF32) : 0u, spans);
@@ -987,8 +776,8 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List& list, u
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int row = row0 + nt * 8 + 2 * c + x;
-        if (nt >= own || row >= L.rows) continue;
-        float l = row < nrows ? w.l[nt][x] : 0.f;  // a padded query's row went along with its tile
+        if (nt >= own || row >= nrows) continue;  // (a padded query's row went along with its tile)
+        float l = w.l[nt][x];
         if (bad) l = __int_as_float(0x7FC00000);
         if (whole) {
           const int i = row / L.per;
@@ -1024,7 +813,7 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List& list, u
       if (sp.bad && at.hr == 0 && first_warp && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
       const float none = sp.bad ? __int_as_float(0x7FC00000) : 0.f;
       const int end = min(pass0 + L.rows_pass, L.rows);
-      for (int row = pass0 + 8 * n8 + group * P + pw; row < end; row += G * P) {
+      for (int row = max(pass0, nrows) + group * P + pw; row < end; row += G * P) {
         const long long orow = (static_cast<long long>(b) * a.nq + row / L.per) * a.heads + h * L.per + row % L.per;
         for (int d = lane; d < D; d += 32) static_cast<E*>(a.out)[orow * D + d] = static_cast<E>(none);
         if (a.lse && lane == 0) a.lse[orow] = sp.bad ? none : -INFINITY;
@@ -1058,32 +847,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const __grid_
     bar_init(bars + tid * 16 + 8, P * L.p.g);
     flags[tid] = 0;
   }
-  // how many tiles there are, and where the requests' begin
-  List list;
-  list.scan = scan;
-  list.threads = kThreads;
-  list.chunk = (a.B + kThreads - 1) / kThreads;
-  list.per_request = a.c.kv_heads * L.p.rt;
-  long long mine = 0;
-  for (int b = tid * list.chunk; b < min(a.B, (tid + 1) * list.chunk); ++b) mine += find_span(a, b).tiles;
-  long long x = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(~0u, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sums[warp] = x;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int v = 0; v < kThreads / 32; ++v) {
-    if (v < warp) before += sums[v];
-    total += sums[v];
-  }
-  scan[tid] = before + x - mine;
-  __syncthreads();
-  const long long teams = static_cast<long long>(gridDim.x) * L.p.t;
-  list.units = total * list.per_request;
-  list.quota = (list.units + teams - 1) / teams;
+  List<kTile> list;
+  list.build(a, a.c.kv_heads * L.p.rt, gridDim.x * L.p.t, scan, sums);
   // 128 x (224 + 224 + 56) registers: the 384 x 168 of the launch
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -1105,7 +871,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnLaunch L) {
   const int RT = L.p.rt, local = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int row = (d.y % RT) * L.rows_pass + local;
   const int nrows = (L.a.n_q ? L.a.n_q[d.x] : L.a.nq) * L.per;
-  if (local >= L.rows_pass || row >= min(L.rows, (nrows + 7) / 8 * 8)) return;
+  if (local >= L.rows_pass || row >= nrows) return;
   // the first part's slot is d.w, the k-th after it is slot 0 of team d.w / 2 + k
   const auto slot = [&](int k) -> long long { return k == 0 ? d.w : 2LL * (d.w / 2 + k); };
   float m = -INFINITY;
@@ -1138,14 +904,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnLaunch L) {
     L.a.lse[orow] = l == 0.f ? -INFINITY : (ref + (log2f(l) - kBias)) * 0.69314718055994531f;
 }
 
-template <typename E, int D, int NT, int P>
-cudaError_t launch_shape(const AttnLaunch& L, int sms, cudaStream_t s) {
-  const int smem = kHead + L.p.t * (L.p.s * stage_bytes(D) + (P == 2 ? L.p.g * pair_bytes(D, NT, sizeof(E) == 4) : 0));
-  cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<E, D, NT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kv_attention_kernel<E, D, NT, P><<<sms, kThreads, smem, s>>>(L);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+template <typename E, int D>
+cudaError_t launch_join(const AttnLaunch& L, int sms, cudaStream_t s) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -1156,6 +916,17 @@ cudaError_t launch_shape(const AttnLaunch& L, int sms, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<E, D>, L);
+}
+
+template <typename E, int D, int NT, int P>
+cudaError_t launch_shape(const AttnLaunch& L, int sms, cudaStream_t s) {
+  const int smem = kHead + L.p.t * (L.p.s * stage_bytes(D) + (P == 2 ? L.p.g * pair_bytes(D, NT, sizeof(E) == 4) : 0));
+  cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<E, D, NT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kv_attention_kernel<E, D, NT, P><<<sms, kThreads, smem, s>>>(L);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_join<E, D>(L, sms, s);
 }
 
 template <typename E, int D, int P, int NT>
@@ -1208,6 +979,10 @@ cudaError_t launch_kv_attention(const KvAttnArgs& a, int D, int esize, cudaStrea
   L.desc = reinterpret_cast<int4*>(a.work + w.desc);
   L.ml = reinterpret_cast<float2*>(a.work + w.ml);
   L.o = reinterpret_cast<float*>(a.work + w.o);
+  if (L.p.tc) {
+    e = launch_attention_tc(L, sms, stream);
+    return e == cudaSuccess ? launch_join<__nv_bfloat16, 128>(L, sms, stream) : e;
+  }
   if (esize == 2) {
     if (D == 64) return launch_dim<__nv_bfloat16, 64>(L, sms, stream);
     if (D == 128) return launch_dim<__nv_bfloat16, 128>(L, sms, stream);
