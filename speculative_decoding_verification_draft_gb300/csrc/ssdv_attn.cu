@@ -70,8 +70,8 @@ AttnShape attn_shape(int rows, int D, bool f32) {
   const int n8 = (rows + 7) / 8;
   a.tc = D == 128 && !f32 && rows > kTcRows;
   if (a.tc) {
-    // passes of 16 to 80 rows, as even as they come
-    a.rt = (rows + 79) / 80;
+    // passes of 16 to 64 rows, as even as they come
+    a.rt = (rows + 63) / 64;
     a.nt = ((rows + a.rt - 1) / a.rt + 15) / 16 * 2;
     a.p = a.g = a.t = a.s = 1;
     return a;
@@ -644,7 +644,7 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List<kTile>& 
     fetch_page();
   }
   __syncwarp();
-  unsigned long long idle = 0;
+  long long idle = 0;
   while (__any_sync(~0u, left > 0)) {
     const uint32_t bar = bars + (team * S + put) * 16;
     bool ready = left > 0 && (lane & 3) == 0 && bar_test(bar + 8, phase);

@@ -68,19 +68,21 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, int parity) {
       : "memory");
   return done != 0;
 }
-// True two seconds after the first call with since = 0: every wait ends.
-__device__ __forceinline__ bool late(unsigned long long& since) {
-  unsigned long long now;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+// True some 2^32 cycles (two seconds) after the first call with since = 0: every
+// wait ends.
+__device__ __forceinline__ bool late(long long& since) {
+  const long long now = clock64();
   if (since == 0) since = now;
-  return now - since > 2000000000ull;
+  return now - since > (1ll << 32);
 }
-// False if the phase did not complete in that time.
+// False if the phase did not complete within 2^24 tries of about a hundred cycles.
+// The loop is as short as it gets: warps that wait take instruction fetches from
+// those that work.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, int parity) {
-  unsigned long long since = 0;
-  while (!bar_test(bar, parity))
-    if (late(since)) return false;
-  return true;
+#pragma unroll 1
+  for (int i = 1 << 24; i; --i)
+    if (bar_test(bar, parity)) return true;
+  return false;
 }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -239,6 +241,7 @@ struct List {
     chunk = (a.B + threads - 1) / threads;
     per_request = heads_passes;
     long long mine = 0;
+#pragma unroll 1
     for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) mine += find_span<kTile>(a, b).tiles;
     long long x = mine;
     for (int o = 1; o < 32; o <<= 1) {
@@ -248,6 +251,7 @@ struct List {
     if (lane == 31) sums[warp] = x;
     __syncthreads();
     long long before = 0, total = 0;
+#pragma unroll 1
     for (int v = 0; v < threads / 32; ++v) {
       if (v < warp) before += sums[v];
       total += sums[v];

@@ -17,18 +17,18 @@
 // Sixteen warps with one job each, joined by mbarriers:
 //   0-3   weights: scores from tensor memory, softmax, weights to shared memory
 //   4-7   keys: codes to tensor memory
-//   8-11  values: codes to tensor memory; then each tile's product is added to
-//         the fp32 sums in registers with its rows' factors
+//   8-11  values: codes to tensor memory; corrections of the sums; results
 //   12    bulk copies of the tiles' blocks   13  issues the matrix instructions
-//   14-15 queries
+//   14    queries   15  finds the CTA's parts of the list
 // Every buffer is double, so that a tile's scores, the tile before's weights and
 // the values of both overlap.
 //
-// Weights are fp16, 2^(x - m + kFast) with m the row's maximum so far, while all
-// of a tile's lie in [2^-14, 2^15], where fp16 keeps 11 bits; then the tile's
-// product is simply added.  Otherwise the tile takes its own maximum (at 2^15)
-// and a factor, and the weights below 2^-14 are passed over again, kBand octaves
-// a pass, as in ssdv_attn.cu.
+// Weights are fp16, 2^(x - m + kFast), with m a maximum of the row so far; while
+// all of a tile's lie in [2^-14, 2^15], where fp16 keeps 11 bits, its products are
+// added up in tensor memory and m stays.  Otherwise m follows the row's maximum,
+// the values' warps rescale the sums, and weights below 2^-14 are passed over
+// again, kBand octaves a pass, into a sum of their own that is added with its
+// power of two.  Sums of weights and maxima are fp32.
 #include "ssdv_attn.cuh"
 
 #include <algorithm>
@@ -43,6 +43,8 @@ constexpr int kD = 128;
 constexpr int kThreads = 512;
 constexpr int kFast = 9, kTop = 15;
 constexpr int kMaxStages = 8;
+constexpr float kBandUp = 536870912.f;  // 2^kBand
+constexpr int kRing = 8;  // parts described ahead
 // Blocks lie 16 bytes past a multiple of 128 apart: the eight lanes of a phase,
 // four blocks' two tokens, then read different banks.
 constexpr int kBlockStride = kv_block_bytes(kD) + 16;
@@ -62,15 +64,19 @@ enum : int {
   kWeightsEmpty = 26,   // [2] product computed         -> weights
   kValuesFull = 28,     // [2] values unpacked          -> matrix
   kValuesEmpty = 30,    // [2] tile's products computed -> values
-  kSumFull = 32,        // [2] product computed         -> values
-  kSumEmpty = 34,       // [2] product read             -> matrix
-  kInfoEmpty = 36,      // [2] factors read             -> weights
+  kOutFull = 32,        // [2] a part's products are all added -> values
+  kOutEmpty = 34,       // [2] its sums read            -> matrix
+  kInfoEmpty = 36,      // [2] a tile's word read       -> weights
   kQueryFull = 38,      // [2] queries written          -> matrix, weights
   kQueryEmpty = 40,     // [2] queries done with        -> queries
-  kEndFull = 42,        // a part's sums of weights     -> values
+  kEndFull = 42,        // a part's sums and maxima     -> values
   kEndEmpty = 43,       // read                         -> weights
-  kDone = 44,           // all matrix instructions are done
-  kBars = 45
+  kFixFull = 44,        // products so far added, or a band's computed -> values
+  kFixDone = 45,        // sums corrected               -> matrix
+  kDone = 46,           // all matrix instructions are done
+  kPartFull = 48,       // [kRing] a part is described      -> all
+  kPartEmpty = 56,      // [kRing] all have done with it    -> plan
+  kBars = 64
 };
 
 // Shared memory after the head, for N rows.
@@ -84,27 +90,25 @@ struct Smem {
   static constexpr int fr = nans + 2 * 128;             // [N] factor and reference of the fast weights
   static constexpr int maxima = fr + 8 * N;             // [N]
   static constexpr int tops = maxima + 4 * N;           // [4][N]
-  static constexpr int refs = tops + 16 * N;            // [N] references of a tile's own weights
-  static constexpr int gaps = refs + 4 * N;             // [N] tile's maximum below the row's
-  static constexpr int grow = gaps + 4 * N;             // [2][N]
-  static constexpr int fall = grow + 8 * N;             // [2][N]
+  static constexpr int fall = tops + 16 * N;            // [2][N]
   static constexpr int factors = fall + 8 * N;          // [2][N]
-  static constexpr int spans = factors + 8 * N;         // [2][N] int2
-  static constexpr int ends = spans + 16 * N;           // [4][N] sums, [N] maxima
-  static constexpr int words = ends + 20 * N;           // info [2], bands, tensor memory address, flags [8]
+  static constexpr int ends = factors + 8 * N;          // [4][N] sums, [N] maxima
+  static constexpr int rows = ends + 20 * N;            // [N] a finished row's place (8 bytes) and factor
+  static constexpr int parts = rows + 16 * N;           // [kRing] 64 bytes
+  static constexpr int words = parts + 64 * kRing;           // info [2], bands, tensor memory address, flags [8]
   static constexpr int stages = (words + 64 + 127) / 128 * 128;
   static constexpr int kStages = (kSmem - stages) / kStage < kMaxStages ? (kSmem - stages) / kStage : kMaxStages;
   static constexpr int total = stages + kStages * kStage + 1024;  // the operands begin at a multiple of 1024
 };
-constexpr int kInfoSlow = 1, kInfoLast = 2;
+constexpr int kInfoRescale = 1, kInfoLast = 2;  // and the band from bit 8
 
 // Tensor memory columns: keys and values twice 64 (128 fp16 a lane), scores twice
-// N, products once or twice N.
+// N, sums of a part once or twice N, a band's products N.
 template <int N>
 struct Tmem {
-  static constexpr int keys = 0, values = 128, scores = 256, sums = 256 + 2 * N;
-  static constexpr int kSums = N <= 64 ? 2 : 1;
-  static_assert(sums + kSums * N <= 512, "tensor memory");
+  static constexpr int kOuts = N <= 48 ? 2 : 1;
+  static constexpr int keys = 0, values = 128, scores = 256, outs = 256 + 2 * N, band = outs + kOuts * N;
+  static_assert(band + N <= 512, "tensor memory");
 };
 
 // ---- tcgen05 ----
@@ -112,8 +116,13 @@ struct Tmem {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// (one lane's)
+__device__ __forceinline__ void tc_commit(uint32_t bar, bool leader) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(static_cast<uint32_t>(leader))
+      : "memory");
 }
 // 16 columns of the warp's 32 lanes; not to be used before tc_wait_ld.
 __device__ __forceinline__ void tc_ld16(uint32_t at, float* x) {
@@ -122,6 +131,20 @@ __device__ __forceinline__ void tc_ld16(uint32_t at, float* x) {
       : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]),
         "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
       : "r"(at));
+}
+__device__ __forceinline__ void tc_ld4(uint32_t at, float* x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+               : "r"(at));
+}
+__device__ __forceinline__ void tc_wait_ld4(float* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]));
+}
+__device__ __forceinline__ void tc_st4(uint32_t at, const float (&x)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3])
+               : "memory");
 }
 // Waits for the loads; the registers pass through, so that no use moves ahead.
 template <int N>
@@ -134,22 +157,25 @@ __device__ __forceinline__ void tc_wait_ld(float* x) {
                    "+f"(x[i + 6]), "+f"(x[i + 7]), "+f"(x[i + 8]), "+f"(x[i + 9]), "+f"(x[i + 10]), "+f"(x[i + 11]),
                    "+f"(x[i + 12]), "+f"(x[i + 13]), "+f"(x[i + 14]), "+f"(x[i + 15]));
 }
-__device__ __forceinline__ void tc_st32(uint32_t at, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+__device__ __forceinline__ void tc_st16(uint32_t at, const float (&x)[16]) {
+  uint32_t v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(x[i]);
+  tc_st16(at, v);
+}
 // D [128 x N] in tensor memory (+)= A [128 x 16] in tensor memory, B [N x 16] in shared memory.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, bool leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
 // fp16 x fp16 -> fp32, both operands contraction-major, M = 128.
@@ -178,6 +204,10 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
       : "r"(id), "r"(static_cast<uint32_t>(x))
       : "memory");
   return r != 0;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t p) {
+  const uint2 v = lds64(p);
+  return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
 }
 __device__ __forceinline__ float lds_f(uint32_t p) { return __uint_as_float(lds32(p)); }
 __device__ __forceinline__ void sts_f(uint32_t p, float x) { sts32(p, __float_as_uint(x)); }
@@ -208,68 +238,120 @@ struct Waiter {
 };
 
 // A CTA's share of the list, part by part: tiles of one (request, head, pass).
+// One warp finds them (64-bit divisions, searches: much code, kept in one place)
+// and describes them in a ring in shared memory.
 struct Part {
-  int b, hr, first, count;
-  bool later;  // not the first of the CTA's
-  Span s;
-  __device__ __forceinline__ bool active() const { return s.hi > s.lo; }
+  int b, head, pass0, first, count;  // first: among the row's tiles
+  int len, nq, lo, hi, tile0;        // as in Span
+  int flags;
+  static constexpr int kLater = 1, kWhole = 2, kBad = 4, kEnd = 8;
+  __device__ __forceinline__ bool active() const { return hi > lo; }
 };
-struct Parts {
-  const KvAttnArgs& a;
-  const List<kTile>& list;
-  Place<kTile> at;
-  int left;
-  bool begun = false;
-  __device__ __forceinline__ Parts(const KvAttnArgs& a_, const List<kTile>& l) : a(a_), list(l) {
-    const long long u = blockIdx.x * l.quota;
-    left = u < l.units ? static_cast<int>(min(l.units - u, l.quota)) : 0;
-    if (left) at = l.find(a, u);
-  }
-  __device__ __forceinline__ bool next(Part& p) {
-    if (!left) return false;
-    p.b = at.b, p.hr = at.hr, p.first = at.tile, p.s = at.s;
-    p.count = min(left, at.s.tiles - at.tile);
-    p.later = begun;
-    begun = true;
-    left -= p.count;
-    at.tile += p.count - 1;
-    if (left) at.next(a, list.per_request);
-    return true;
+template <int N>
+struct Ring {
+  const uint32_t base;
+  Waiter& w;
+  int n = 0;
+  __device__ __forceinline__ Ring(uint32_t base_, Waiter& w_) : base(base_), w(w_) {}
+  // The next part; false when there is none.
+  __device__ __forceinline__ bool next(Part& p, int lane) {
+    const int at = n % kRing;
+    w.wait(kPartFull + at, n / kRing);
+    const uint32_t from = base + Smem<N>::parts + at * 64;
+    const uint4 x = lds128(from), y = lds128(from + 16), z = lds128(from + 32);
+    p.b = x.x, p.head = x.y, p.pass0 = x.z, p.first = x.w;
+    p.count = y.x, p.len = y.y, p.nq = y.z, p.lo = y.w;
+    p.hi = z.x, p.tile0 = z.y, p.flags = z.z;
+    __syncwarp();
+    if (lane == 0) w.arrive(kPartEmpty + at);
+    ++n;
+    return !w.dead && !(p.flags & Part::kEnd);
   }
 };
+
+template <int N>
+__device__ __forceinline__ void plan_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, Waiter w, int lane) {
+  const long long u = blockIdx.x * list.quota;
+  int left = u < list.units ? static_cast<int>(min(list.units - u, list.quota)) : 0;
+  Place<kTile> at = {};
+  if (left) at = list.find(L.a, u);
+  if (lane == 0) L.desc[blockIdx.x] = left ? list.parts(at, blockIdx.x) : make_int4(0, 0, 0, 0);
+  bool later = false;
+#pragma unroll 1
+  for (int n = 0;; ++n) {
+    const int slot = n % kRing, count = left ? min(left, at.s.tiles - at.tile) : 0;
+    const bool end = left == 0;
+    w.wait(kPartEmpty + slot, (n / kRing) ^ 1);
+    if (lane == 0) {
+      const uint32_t to = base + Smem<N>::parts + slot * 64;
+      const int flags = (later ? Part::kLater : 0) | (at.tile == 0 && count == at.s.tiles ? Part::kWhole : 0) |
+                        (at.s.bad ? Part::kBad : 0) | (end ? Part::kEnd : 0);
+      sts128(to, make_uint4(at.b, at.hr / L.p.rt, at.hr % L.p.rt * N, at.tile));
+      sts128(to + 16, make_uint4(count, at.s.len, at.s.nq, at.s.lo));
+      sts128(to + 32, make_uint4(at.s.hi, at.s.tile0, flags, 0));
+      w.arrive(kPartFull + slot);
+    }
+    if (end || w.dead) break;
+    later = true;
+    left -= count;
+    at.tile += count - 1;
+    if (left) at.next(L.a, list.per_request);
+  }
+  if (w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+}
+
+// Which rows of a pass see the token at `pos`: [x, y).
+template <int N>
+__device__ __forceinline__ int2 rows_seeing(const AttnLaunch& L, const Part& p, int pos) {
+  const KvAttnArgs& a = L.a;
+  if (pos < p.lo || pos >= p.hi) return make_int2(0, 0);
+  // query i sees it if i >= pos - len (its own key included) and i < pos - len + window
+  const int i = pos - p.len;
+  const int lo = a.past_only || i <= 0 ? 0 : i * L.per - p.pass0;
+  const long long hi = a.window ? static_cast<long long>(i + a.window) * L.per - p.pass0 : N;
+  return make_int2(max(lo, 0), static_cast<int>(max(0ll, min(hi, static_cast<long long>(N)))));
+}
 
 // ---- bulk copies (warp 12): eight lanes, a block each ----
 
 template <int N>
-__device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, Waiter w, int lane) {
+__device__ __forceinline__ void copy_role(const AttnLaunch& L, uint32_t base, Waiter w, int lane) {
   constexpr int S = Smem<N>::kStages;
   const KvAttnArgs& a = L.a;
   const int bpp = a.c.page_size / kKvBlock;
   const long long head_bytes = static_cast<long long>(bpp) * kv_block_bytes(kD), page_bytes = head_bytes * a.c.kv_heads;
-  Parts parts(a, list);
+  Ring<N> parts(base, w);
   Part p;
   int st = 0;
   uint32_t phase = 1;
-  while (parts.next(p)) {
+  while (parts.next(p, lane)) {
     if (!p.active()) continue;
     const int32_t* table = a.c.page_table + static_cast<long long>(p.b) * a.c.max_pages;
-    const long long head = p.hr / L.p.rt * head_bytes;
-    const auto column = [&](int k) { return ((p.s.tile0 + p.first + k) * kBlocks + (lane & 7)) / bpp; };
+    const long long head = p.head * head_bytes;
     const auto seen = [&](int k) {
-      const int pos = (p.s.tile0 + p.first + k) * kTile + (lane & 7) * kKvBlock;
-      return k < p.count && pos < p.s.hi && pos + kKvBlock > p.s.lo;
+      const int pos = (p.tile0 + p.first + k) * kTile + (lane & 7) * kKvBlock;
+      return k < p.count && pos < p.hi && pos + kKvBlock > p.lo;
     };
+    // the lane's block: its page's column of the table, and its place in the page;
     // page numbers are read a tile ahead
+    int col = ((p.tile0 + p.first) * kBlocks + (lane & 7)) / bpp;
+    int sub = ((p.tile0 + p.first) * kBlocks + (lane & 7)) - col * bpp;
     bool want = seen(0);
-    int col = column(0), page = want ? table[col] : 0;
+    int page = want ? table[col] : 0;
+#pragma unroll 1
     for (int k = 0; k < p.count; ++k) {
-      const int sub = (p.s.tile0 + p.first + k) * kBlocks + (lane & 7) - col * bpp;
       const bool ok = want && page >= 0 && page < a.c.n_pages;
       const int got = __popc(__ballot_sync(~0u, ok) & 0xFFu);
       const bool lacks = (__ballot_sync(~0u, want && !ok) & 0xFFu) != 0;
       const long long at = page * page_bytes + head + static_cast<long long>(sub) * kv_block_bytes(kD);
+      sub += kBlocks;
+      if (sub >= bpp) {
+        const int q = bpp >= kBlocks ? 1 : sub / bpp;
+        col += q;
+        sub -= q * bpp;
+      }
       const bool want_next = seen(k + 1);
-      const int col_next = column(k + 1), page_next = want_next ? table[col_next] : 0;
+      const int page_next = want_next ? table[col] : 0;
       w.wait(kEmpty + st, phase);
       const uint32_t bar = w.bars + (kFull + st) * 8;
       if (lane == 0) {
@@ -281,139 +363,159 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
       if (lane < 8 && ok && !w.dead)
         bulk_copy(base + Smem<N>::stages + st * kStage + lane * kBlockStride, a.c.pages + at, kv_block_bytes(kD), bar);
       if (++st == S) st = 0, phase ^= 1;
-      want = want_next, col = col_next, page = page_next;
+      want = want_next, page = page_next;
     }
   }
   if (w.dead) {
     // copies still in flight get the same time again before the shared memory goes
     if (lane == 0) atomicOr(a.status, 1 << SSD_ERR_CUDA);
-    unsigned long long since = 0;
+    long long since = 0;
     while (!late(since)) {
     }
   }
 }
 
-// ---- queries (warps 14, 15): every other row each ----
+// ---- queries (warp 14) ----
 
 template <int N>
-__device__ __forceinline__ void query_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, Waiter w, int warp,
-                                           int lane) {
+__device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, Waiter w, int lane) {
   const KvAttnArgs& a = L.a;
-  Parts parts(a, list);
+  Ring<N> parts(base, w);
   Part p;
-  int n = 0;
-  while (parts.next(p)) {
+  int n_parts = 0;
+  while (parts.next(p, lane)) {
     if (!p.active()) continue;
-    const int qb = n & 1;
-    w.wait(kQueryEmpty + qb, (n >> 1) ^ 1);
-    const int h = p.hr / L.p.rt, pass0 = p.hr % L.p.rt * N, nrows = p.s.nq * L.per;
-#pragma unroll 4
-    for (int k = warp; k < N; k += 2) {
-      const int row = pass0 + k;
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (row < nrows) {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + p.b * a.qs[0] + row / L.per * a.qs[1] +
-                                 (h * L.per + row % L.per) * a.qs[2] + lane * 4;
-        if ((reinterpret_cast<uintptr_t>(q) & 7) == 0) {
-          const uint2 v = *reinterpret_cast<const uint2*>(q);
-          x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-          x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-        } else {
+    const int qb = n_parts & 1, nrows = p.nq * L.per;
+    w.wait(kQueryEmpty + qb, (n_parts >> 1) ^ 1);
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + p.b * a.qs[0] + p.head * L.per * a.qs[2] + lane * 4;
+    int i = p.pass0 / L.per, g = p.pass0 % L.per;  // the row's query token and head
+#pragma unroll 1
+    for (int k0 = 0; k0 < N; k0 += 8) {
+      float x[8][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = static_cast<float>(q[e]);
+      for (int k = 0; k < 8; ++k) {
+        uint2 v = make_uint2(0, 0);
+        if (p.pass0 + k0 + k < nrows) {
+          const __nv_bfloat16* q = from + i * a.qs[1] + g * a.qs[2];
+          if ((reinterpret_cast<uintptr_t>(q) & 7) == 0) {
+            v = *reinterpret_cast<const uint2*>(q);
+          } else {
+            const unsigned short* h = reinterpret_cast<const unsigned short*>(q);
+            v = make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+          }
         }
+        if (++g == L.per) g = 0, ++i;
+        x[k][0] = __uint_as_float(v.x << 16), x[k][1] = __uint_as_float(v.x & 0xFFFF0000u);
+        x[k][2] = __uint_as_float(v.y << 16), x[k][3] = __uint_as_float(v.y & 0xFFFF0000u);
       }
-      float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-      top = warp_max(top);
-      // as in ssdv_attn.cu: the row's largest element to [2^12, 2^13), the
-      // scale's sign to the query
-      int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-      ex = max(-100, min(ex, 127));
-      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), a.scale_log2);
-      const uint32_t at = base + Smem<N>::query + qb * Smem<N>::kOperand + operand_byte<N>(k, lane * 4);
-      sts64(at, make_uint2(half2_bits(__floats2half2_rn(x[0] * up, x[1] * up)),
-                           half2_bits(__floats2half2_rn(x[2] * up, x[3] * up))));
-      if (lane == 0) {
-        sts_f(base + Smem<N>::factors + (qb * N + k) * 4,
-              fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23));
-        const int i = row / L.per;
-        sts64(base + Smem<N>::spans + (qb * N + k) * 8,
-              make_uint2(row_lo(a, p.s.len, i), min(row_hi(a, p.s.len, i), p.s.hi)));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float top =
+            warp_max(fmaxf(fmaxf(fabsf(x[k][0]), fabsf(x[k][1])), fmaxf(fabsf(x[k][2]), fabsf(x[k][3]))));
+        // as in ssdv_attn.cu: the row's largest element to [2^12, 2^13), the
+        // scale's sign to the query
+        int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        ex = max(-100, min(ex, 127));
+        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), a.scale_log2);
+        sts64(base + Smem<N>::query + qb * Smem<N>::kOperand + operand_byte<N>(k0 + k, lane * 4),
+              make_uint2(half2_bits(__floats2half2_rn(x[k][0] * up, x[k][1] * up)),
+                         half2_bits(__floats2half2_rn(x[k][2] * up, x[k][3] * up))));
+        if (lane == 0)
+          sts_f(base + Smem<N>::factors + (qb * N + k0 + k) * 4,
+                fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23));
       }
     }
     async_fence();
     __syncwarp();
     if (lane == 0) w.arrive(kQueryFull + qb);
-    ++n;
+    ++n_parts;
   }
   if (w.dead && lane == 0) atomicOr(a.status, 1 << SSD_ERR_CUDA);
 }
 
-// ---- matrix instructions (one thread) ----
+// ---- matrix instructions (warp 13; one lane issues them, the warp stays together) ----
 
 template <int N>
-__device__ __forceinline__ void matrix_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, uint32_t tmem,
-                                            Waiter w) {
-  constexpr uint32_t idesc = tc_idesc(N);
-  Parts parts(L.a, list);
+__device__ __forceinline__ void matrix_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int lane) {
+  const bool leader = lane == 0;
+  // D (+)= A B over 128 of the contraction: A 8 columns, B 32 bytes a step
+  const auto product = [&](uint32_t d, uint32_t a, uint32_t b, bool add) {
+    // (a broadcast is what tells the compiler that the warp agrees on a number)
+    d = __shfl_sync(~0u, d, 0), a = __shfl_sync(~0u, a, 0), b = __shfl_sync(~0u, b, 0);
+    const uint64_t operand = tc_operand(b);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      tc_mma(d, a + s * 8, operand + (s >> 2) * (N * 8) + (s & 3) * 2, tc_idesc(N), s > 0 || add, leader);
+  };
+  Ring<N> parts(base, w);
   Part p;
   p.count = 0;
-  int in_part = 0, n_parts = 0, scored = 0;
-  // scores of the next tile, if there is one
-  const auto scores = [&]() -> bool {
-    while (in_part == p.count) {
-      if (!parts.next(p)) return false;
-      in_part = p.active() ? 0 : p.count;
+  int k = 0, n_parts = 0, n_outs = 0, scored = 0, tile = 0, it = 0, fixes = 0;
+  // the scores go one tile ahead: whether there is a tile to add up, and whether
+  // it is its part's first and last
+  bool more = true, have = false, is_first = false, is_last = false;
+#pragma unroll 1
+  while (more || have) {
+    while (more && k == p.count) {
+      more = parts.next(p, lane);
+      k = more && p.active() ? 0 : p.count;
     }
-    const int sb = scored & 1, qb = n_parts & 1;
-    if (in_part == 0) w.wait(kQueryFull + qb, n_parts >> 1);
-    w.wait(kKeysFull + sb, scored >> 1);
-    w.wait(kScoresEmpty + sb, (scored >> 1) ^ 1);
-    tc_fence_after();
-    if (!w.dead) {
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        tc_mma(tmem + Tmem<N>::scores + sb * N, tmem + Tmem<N>::keys + sb * 64 + s * 8,
-               tc_operand(base + Smem<N>::query + qb * Smem<N>::kOperand + (s >> 2) * (N * 128) + (s & 3) * 32), idesc,
-               s > 0);
-      tc_commit(w.bars + (kScoresFull + sb) * 8);
-      tc_commit(w.bars + (kKeysEmpty + sb) * 8);
-    }
-    ++scored;
-    if (++in_part == p.count) {
-      if (!w.dead) tc_commit(w.bars + (kQueryEmpty + qb) * 8);
-      ++n_parts;
-    }
-    return true;
-  };
-  int tile = 0, it = 0;
-  bool more = scores();
-  while (more) {
-    more = scores();
-    const int vb = tile & 1;
-    for (bool first = true, last = false; !last; first = false) {
-      const int pb = it & 1, tb = it % Tmem<N>::kSums;
-      if (first) w.wait(kValuesFull + vb, tile >> 1);
-      w.wait(kWeightsFull + pb, it >> 1);
-      w.wait(kSumEmpty + tb, it / Tmem<N>::kSums + 1);
-      last = w.dead || (lds32(base + Smem<N>::words + pb * 4) & kInfoLast);
+    const bool first = k == 0, last_tile = k == p.count - 1;
+    if (more) {
+      const int sb = scored & 1, qb = n_parts & 1;
+      if (first) w.wait(kQueryFull + qb, n_parts >> 1);
+      w.wait(kKeysFull + sb, scored >> 1);
+      w.wait(kScoresEmpty + sb, (scored >> 1) ^ 1);
       tc_fence_after();
       if (!w.dead) {
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-          tc_mma(tmem + Tmem<N>::sums + tb * N, tmem + Tmem<N>::values + vb * 64 + s * 8,
-                 tc_operand(base + Smem<N>::weight + pb * Smem<N>::kOperand + (s >> 2) * (N * 128) + (s & 3) * 32), idesc,
-                 s > 0);
-        tc_commit(w.bars + (kSumFull + tb) * 8);
-        tc_commit(w.bars + (kWeightsEmpty + pb) * 8);
-        if (last) tc_commit(w.bars + (kValuesEmpty + vb) * 8);
+        product(tmem + Tmem<N>::scores + sb * N, tmem + Tmem<N>::keys + sb * 64,
+                base + Smem<N>::query + qb * Smem<N>::kOperand, false);
+        tc_commit(w.bars + (kScoresFull + sb) * 8, leader);
+        tc_commit(w.bars + (kKeysEmpty + sb) * 8, leader);
+        if (last_tile) tc_commit(w.bars + (kQueryEmpty + qb) * 8, leader);
       }
-      ++it;
+      ++scored;
+      ++k;
+      n_parts += last_tile;
     }
-    ++tile;
+    if (have) {
+      const int vb = tile & 1, ob = n_outs % Tmem<N>::kOuts;
+      const uint32_t out = tmem + Tmem<N>::outs + ob * N;
+      w.wait(kValuesFull + vb, tile >> 1);
+      if (is_first) w.wait(kOutEmpty + ob, n_outs / Tmem<N>::kOuts + 1);
+#pragma unroll 1
+      for (bool last = false; !last; ++it) {
+        const int pb = it & 1;
+        w.wait(kWeightsFull + pb, it >> 1);
+        const uint32_t info = __shfl_sync(~0u, lds32(base + Smem<N>::words + pb * 4), 0), band = info >> 8;
+        last = w.dead || (info & kInfoLast);
+        if (!w.dead && (info & kInfoRescale)) {
+          // the sums so far are rescaled first
+          tc_commit(w.bars + kFixFull * 8, leader);
+          w.wait(kFixDone, fixes++);
+        }
+        tc_fence_after();
+        if (!w.dead) {
+          product(band ? tmem + Tmem<N>::band : out, tmem + Tmem<N>::values + vb * 64,
+                  base + Smem<N>::weight + pb * Smem<N>::kOperand, band == 0 && !is_first);
+          tc_commit(w.bars + (kWeightsEmpty + pb) * 8, leader);
+          if (band) {
+            tc_commit(w.bars + kFixFull * 8, leader);
+            w.wait(kFixDone, fixes++);
+            tc_fence_after();
+          }
+          if (last) tc_commit(w.bars + (kValuesEmpty + vb) * 8, leader);
+          if (last && is_last) tc_commit(w.bars + (kOutFull + ob) * 8, leader);
+        }
+      }
+      ++tile;
+      n_outs += is_last;
+    }
+    have = more;
+    is_first = first, is_last = last_tile;
   }
-  if (w.dead) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
-  tc_commit(w.bars + kDone * 8);
+  if (w.dead && leader) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+  tc_commit(w.bars + kDone * 8, leader);
   bar_wait(w.bars + kDone * 8, 0);
 }
 
@@ -421,51 +523,46 @@ __device__ __forceinline__ void matrix_role(const AttnLaunch& L, const List<kTil
 // of block l % 4 + 4 (u / 2) ----
 
 template <int N>
-__device__ __forceinline__ void key_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, uint32_t tmem, Waiter w,
-                                         int warp, int lane) {
+__device__ __forceinline__ void key_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int warp, int lane) {
   constexpr int S = Smem<N>::kStages;
   const Bases bases = make_bases();
   const int blk = (lane & 3) + 4 * (warp >> 1), t = ((lane >> 2) & 1) | ((lane >> 3) << 1) | ((warp & 1) << 3);
   const uint32_t codes = base + Smem<N>::stages + blk * kBlockStride + t * (kD / 2);
   const uint32_t scales = base + Smem<N>::stages + blk * kBlockStride + kv_k_scales(kD) + (t & 1) * 16 + (t >> 1) * 2;
-  Parts parts(L.a, list);
+  Ring<N> parts(base, w);
   Part p;
   int st = 0, tile = 0;
   uint32_t phase = 0;
-  while (parts.next(p)) {
+  while (parts.next(p, lane)) {
     if (!p.active()) continue;
+#pragma unroll 1
     for (int k = 0; k < p.count; ++k, ++tile) {
       const int kb = tile & 1;
       w.wait(kFull + st, phase);
       const uint32_t from = codes + st * kStage, sfrom = scales + st * kStage;
+      w.wait(kKeysEmpty + kb, (tile >> 1) ^ 1);
+      tc_fence_after();
+      const uint32_t into = tmem + (static_cast<uint32_t>(warp * 32) << 16) + Tmem<N>::keys + kb * 64;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {  // 32 elements, two groups, at a time
+        const uint4 c = lds128(from + q * 16);
+        const uint32_t word[4] = {c.x, c.y, c.z, c.w}, b = lds16(sfrom + q * 32);
+        uint32_t v[16];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint4 c0 = lds128(from + half * 32), c1 = lds128(from + half * 32 + 16);
-        const uint32_t word[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        uint32_t v[32];
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t s = __byte_perm(b, 0, 0x4040 + 0x0101 * g) << 7;
+          const uint32_t s24 = mul2(s, kMinus24), s264 = mul2(s, kMinus264);
 #pragma unroll
-        for (int g2 = 0; g2 < 2; ++g2) {
-          const uint32_t b = lds16(sfrom + (half * 2 + g2) * 32);
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const uint32_t s = __byte_perm(b, 0, 0x4040 + 0x0101 * g) << 7;
-            const uint32_t s24 = mul2(s, kMinus24), s264 = mul2(s, kMinus264);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int i = g2 * 4 + g * 2 + x;
-              const uint32_t u = __funnelshift_r(word[i], word[i], 8);
-              v[4 * i] = fma2(pair_hi(word[i], bases), s, s24);
-              v[4 * i + 1] = fma2(pair_lo(word[i], bases), s, s264);
-              v[4 * i + 2] = fma2(pair_hi(u, bases), s, s24);
-              v[4 * i + 3] = fma2(pair_lo(u, bases), s, s264);
-            }
+          for (int x = 0; x < 2; ++x) {
+            const int i = g * 2 + x;
+            const uint32_t u = __funnelshift_r(word[i], word[i], 8);
+            v[4 * i] = fma2(pair_hi(word[i], bases), s, s24);
+            v[4 * i + 1] = fma2(pair_lo(word[i], bases), s, s264);
+            v[4 * i + 2] = fma2(pair_hi(u, bases), s, s24);
+            v[4 * i + 3] = fma2(pair_lo(u, bases), s, s264);
           }
         }
-        if (half == 0) {
-          w.wait(kKeysEmpty + kb, (tile >> 1) ^ 1);
-          tc_fence_after();
-        }
-        tc_st32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + Tmem<N>::keys + kb * 64 + half * 32, v);
+        tc_st16(into + q * 16, v);
       }
       tc_wait_st();
       tc_fence_before();
@@ -480,182 +577,170 @@ __device__ __forceinline__ void key_role(const AttnLaunch& L, const List<kTile>&
   if (w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
 
-// ---- weights (warps 0-3): a thread has one token of the tile, the keys' order ----
+// ---- weights (warps 0-3): a thread has one token of the tile, in the keys' order ----
 
 template <int N>
-__device__ __forceinline__ void weight_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, uint32_t tmem,
-                                            Waiter w, int warp, int lane) {
+__device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int warp, int lane) {
   using M = Smem<N>;
   constexpr int kSync = 1;
   const int tid = warp * 32 + lane;
   const int token = ((lane & 3) + 4 * (warp >> 1)) * kKvBlock + (((lane >> 2) & 1) | ((lane >> 3) << 1) | ((warp & 1) << 3));
-  const uint32_t scores = tmem + (static_cast<uint32_t>(warp * 32) << 16) + Tmem<N>::scores;
   uint32_t to[8];  // where the thread's column of the weights lies in rows 0..7
 #pragma unroll
   for (int r = 0; r < 8; ++r) to[r] = base + M::weight + operand_byte<N>(r, token);
-  Parts parts(L.a, list);
+  Ring<N> parts(base, w);
   Part p;
   int n_parts = 0, tile = 0, it = 0;
-  while (parts.next(p)) {
+  while (parts.next(p, lane)) {
     if (!p.active()) continue;
     const int qb = n_parts & 1;
     w.wait(kQueryFull + qb, n_parts >> 1);
     if (tid < N) {
-      // an infinite reference makes the first tile take its own
+      // an infinite reference makes the first tile set it
       sts64(base + M::fr + tid * 8, make_uint2(lds32(base + M::factors + (qb * N + tid) * 4), 0x7F800000u));
       sts_f(base + M::maxima + tid * 4, -INFINITY);
     }
     group_sync(kSync);
-    const int lo_last = row_lo(L.a, p.s.len, p.s.nq - 1), hi_first = row_hi(L.a, p.s.len, 0);
+    const int lo_last = row_lo(L.a, p.len, p.nq - 1), hi_first = row_hi(L.a, p.len, 0);
     float l[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) l[n] = 0.f;
+#pragma unroll 1
     for (int k = 0; k < p.count; ++k, ++tile) {
       const int sb = tile & 1;
-      const int pos0 = (p.s.tile0 + p.first + k) * kTile, pos = pos0 + token;
+      const int pos0 = (p.tile0 + p.first + k) * kTile;
       const bool edge = pos0 < lo_last || pos0 + kTile > hi_first;
-      float s[N];
-      const auto load = [&]() {
-#pragma unroll
-        for (int n = 0; n < N; n += 16) tc_ld16(scores + sb * N + n, s + n);
-        tc_wait_ld<N>(s);
-        if (edge) {
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const uint2 seen = lds64(base + M::spans + (qb * N + n) * 8);
-            if (pos < static_cast<int>(seen.x) || pos >= static_cast<int>(seen.y)) s[n] = -INFINITY;
-          }
-        }
-      };
-      const auto put = [&](int n, uint32_t pair) {
-        sts16(to[n & 7] + (it & 1) * M::kOperand + (n >> 3) * 1024, pair);
-        sts16(to[(n + 1) & 7] + (it & 1) * M::kOperand + (n >> 3) * 1024, pair >> 16);
+      int2 seen = make_int2(0, N);  // rows that see the token
+      if (edge) seen = rows_seeing<N>(L, p, pos0 + token);
+      const uint32_t scores = tmem + (static_cast<uint32_t>(warp * 32) << 16) + Tmem<N>::scores + sb * N;
+      const auto put = [&](int n0, int n, uint32_t pair) {
+        const uint32_t at = (it & 1) * M::kOperand + n0 * 128 + (n >> 3) * 1024;
+        sts16(to[n & 7] + at, pair);
+        sts16(to[(n + 1) & 7] + at, pair >> 16);
       };
       w.wait(kScoresFull + sb, tile >> 1);
       tc_fence_after();
-      load();
       w.wait(kWeightsEmpty + (it & 1), (it >> 1) ^ 1);
-      bool out = false;
-      __half2 least = __float2half2_rn(1.f), most = least;
+      w.wait(kInfoEmpty + (it & 1), (it >> 1) ^ 1);
+      bool rescaled = false;
+      int bands = 0;  // passes to come
+      float u[N];
+#pragma unroll 1
+      for (;;) {
+        float least = 0.f, most = 0.f;
+#pragma unroll
+        for (int n = 0; n < N; n += 16) tc_ld16(scores + n, u + n);
+        tc_wait_ld<N>(u);
+#pragma unroll
+        for (int n = 0; n < N; n += 2) {
+          const uint4 fr = lds128(base + M::fr + n * 8);
+          u[n] = fmaf(u[n], __uint_as_float(fr.x), __uint_as_float(fr.y));
+          u[n + 1] = fmaf(u[n + 1], __uint_as_float(fr.z), __uint_as_float(fr.w));
+        }
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const bool in = n >= seen.x && n < seen.y;
+            least = fminf(least, in ? u[n] : 0.f);
+            u[n] = in ? u[n] : -INFINITY;
+            most = fmaxf(most, u[n]);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < N; n += 2) {
+            least = fminf(least, fminf(u[n], u[n + 1]));
+            most = fmaxf(most, fmaxf(u[n], u[n + 1]));
+          }
+        }
+        const bool high = most > kTop, low = least < kTop - kBand;
+        if (!group_any(kSync, high || low)) break;
+        if (rescaled || !group_any(kSync, high)) {
+          // below 2^-14 fp16 keeps fewer bits: what it loses goes to later passes
+          const int need = low ? static_cast<int>(fminf((kTop - least) * (1.f / kBand), kBands - 1.f)) : 0;
+          const int most_needed = __reduce_max_sync(~0u, need);
+          if (lane == 0 && most_needed)
+            atomicMax(reinterpret_cast<int*>(__cvta_shared_to_generic(base + M::words + 8)), most_needed);
+          group_sync(kSync);
+          bands = lds32(base + M::words + 8);
+          group_sync(kSync);
+          if (tid == 0) sts32(base + M::words + 8, 0);
+          break;
+        }
+        // the rows' maxima follow the tile's
+#pragma unroll 1
+        for (int n0 = 0; n0 < N; n0 += 16) {
+          float s[16], keep = -INFINITY;
+          tc_ld16(scores + n0, s);
+          tc_wait_ld<16>(s);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const float top = warp_max(!edge || (n0 + n >= seen.x && n0 + n < seen.y) ? s[n] : -INFINITY);
+            if (lane == n) keep = top;
+          }
+          if (lane < 16) sts_f(base + M::tops + (warp * N + n0 + lane) * 4, keep);
+        }
+        group_sync(kSync);
+        if (tid < N) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) top = fmaxf(top, lds_f(base + M::tops + (x * N + tid) * 4));
+          const float f = lds_f(base + M::fr + tid * 8), old = lds_f(base + M::maxima + tid * 4);
+          if (top != -INFINITY) top *= f;
+          const float m = fmaxf(old, top);
+          sts_f(base + M::maxima + tid * 4, m);
+          sts_f(base + M::fr + tid * 8 + 4, m == -INFINITY ? INFINITY : kFast - m);
+          sts_f(base + M::fall + ((it & 1) * N + tid) * 4, old == -INFINITY ? 0.f : ex2(old - m));
+        }
+        group_sync(kSync);
+#pragma unroll
+        for (int n = 0; n < N; ++n) l[n] *= lds_f(base + M::fall + ((it & 1) * N + n) * 4);
+        rescaled = true;
+      }
 #pragma unroll
       for (int n = 0; n < N; n += 2) {
-        const uint4 fr = lds128(base + M::fr + n * 8);
-        const float e0 = ex2(fmaf(s[n], __uint_as_float(fr.x), __uint_as_float(fr.y)));
-        const float e1 = ex2(fmaf(s[n + 1], __uint_as_float(fr.z), __uint_as_float(fr.w)));
-        if (edge) {
-          const bool seen0 = s[n] != -INFINITY, seen1 = s[n + 1] != -INFINITY;
-          s[n] = seen0 ? e0 : 0.f, s[n + 1] = seen1 ? e1 : 0.f;
-          out |= (seen0 && (e0 < kSmallest || e0 > 32768.f)) || (seen1 && (e1 < kSmallest || e1 > 32768.f));
-          put(n, half2_bits(__floats2half2_rn(s[n], s[n + 1])));
-        } else {
-          s[n] = e0, s[n + 1] = e1;
-          const __half2 h = __floats2half2_rn(e0, e1);
-          least = __hmin2(least, h);
-          most = __hmax2(most, h);
-          put(n, half2_bits(h));
-        }
+        u[n] = ex2(u[n]), u[n + 1] = ex2(u[n + 1]);
+        l[n] += u[n], l[n + 1] += u[n + 1];
+        put(0, n, half2_bits(__floats2half2_rn(u[n], u[n + 1])));
       }
-      if (!edge)
-        out = __low2float(least) < kSmallest || __high2float(least) < kSmallest || __low2float(most) > 32768.f ||
-              __high2float(most) > 32768.f;
-      if (!group_any(kSync, out)) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) l[n] += s[n];
-        w.wait(kInfoEmpty + (it & 1), (it >> 1) ^ 1);
-        if (tid == 0) sts32(base + M::words + (it & 1) * 4, kInfoLast);
+#pragma unroll 1
+      for (int band = 0;; ++band) {
+        if (tid == 0)
+          sts32(base + M::words + (it & 1) * 4,
+                (rescaled && band == 0 ? kInfoRescale : 0) | (band == bands ? kInfoLast : 0) | (band << 8));
         async_fence();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          w.arrive(kScoresEmpty + sb);
+          if (band == bands) w.arrive(kScoresEmpty + sb);
           w.arrive(kWeightsFull + (it & 1));
         }
         ++it;
-        continue;
-      }
-      // the tile's own maxima
-      load();
-      float keep[(N + 31) / 32];
+        if (band == bands) break;
+        w.wait(kWeightsEmpty + (it & 1), (it >> 1) ^ 1);
+        w.wait(kInfoEmpty + (it & 1), (it >> 1) ^ 1);
+        // what the passes before lost of weights below 2^-14, kBand octaves up each time
+#pragma unroll 1
+        for (int n0 = 0; n0 < N; n0 += 16) {
+          float s[16];
+          tc_ld16(scores + n0, s);
+          tc_wait_ld<16>(s);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float top = warp_max(s[n]);
-        if (lane == (n & 31)) keep[n >> 5] = top;
-      }
-#pragma unroll
-      for (int j = 0; j < (N + 31) / 32; ++j)
-        if (j * 32 + lane < N) sts_f(base + M::tops + (warp * N + j * 32 + lane) * 4, keep[j]);
-      w.wait(kInfoEmpty + (it & 1), (it >> 1) ^ 1);
-      group_sync(kSync);
-      if (tid < N) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) top = fmaxf(top, lds_f(base + M::tops + (u * N + tid) * 4));
-        const float f = lds_f(base + M::fr + tid * 8), old = lds_f(base + M::maxima + tid * 4);
-        if (top != -INFINITY) top *= f;
-        const float m = fmaxf(old, top), zero = m == -INFINITY ? 0.f : m;
-        if (top == -INFINITY) top = zero;
-        sts_f(base + M::maxima + tid * 4, m);
-        sts_f(base + M::fr + tid * 8 + 4, m == -INFINITY ? INFINITY : kFast - m);
-        sts_f(base + M::refs + tid * 4, kTop - top);
-        sts_f(base + M::gaps + tid * 4, top - zero);
-        sts_f(base + M::grow + ((it & 1) * N + tid) * 4, ex2(top - zero + (kFast - kTop)));
-        sts_f(base + M::fall + ((it & 1) * N + tid) * 4, ex2(old - zero));
-      }
-      if (tid == 0) sts32(base + M::words + 8, 0);
-      group_sync(kSync);
-      uint32_t bands = 0;
-      for (uint32_t todo = 1; todo;) {
-        const int band = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int ib = it & 1;
-        if (band) {
-          w.wait(kWeightsEmpty + ib, (it >> 1) ^ 1);
-          w.wait(kInfoEmpty + ib, (it >> 1) ^ 1);
-          if (tid < N) {
-            sts_f(base + M::grow + (ib * N + tid) * 4,
-                  ex2(lds_f(base + M::gaps + tid * 4) + (kFast - kTop - kBand * band)));
-            sts_f(base + M::fall + (ib * N + tid) * 4, 1.f);
+          for (int n = 0; n < 16; ++n) {
+            const float2 fr = lds_f2(base + M::fr + (n0 + n) * 8);
+            s[n] = !edge || (n0 + n >= seen.x && n0 + n < seen.y) ? ex2(fmaf(s[n], fr.x, fr.y)) : 0.f;
           }
-        }
+#pragma unroll 1
+          for (int x = 0; x <= band; ++x)
 #pragma unroll
-        for (int n = 0; n < N; n += 2) {
-          uint32_t pair = 0;
+            for (int n = 0; n < 16; ++n)
+              s[n] = fabsf(s[n]) < kSmallest ? (s[n] - __half2float(__float2half_rn(s[n]))) * kBandUp : 0.f;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float u = fmaf(s[n + x], lds_f(base + M::fr + (n + x) * 8), lds_f(base + M::refs + (n + x) * 4));
-            int at = u >= kTop - kBand ? 0 : min(kBands, static_cast<int>((kTop - u) * (1.f / kBand)));
-            const bool seen = !edge || s[n + x] != -INFINITY;
-            if (!seen) at = kBands;
-            if (band == 0) {
-              const float e = seen ? ex2(u) : 0.f;
-              l[n + x] = l[n + x] * lds_f(base + M::fall + (ib * N + n + x) * 4) +
-                         e * lds_f(base + M::grow + (ib * N + n + x) * 4);
-              if (at > 0 && at < kBands) bands |= 1u << at;
-            }
-            const float e = at == band ? ex2(u + kBand * band) : 0.f;
-            pair |= static_cast<uint32_t>(__half_as_ushort(__float2half_rn(e))) << (16 * x);
-          }
-          put(n, pair);
+          for (int n = 0; n < 16; n += 2) put(n0, n, half2_bits(__floats2half2_rn(s[n], s[n + 1])));
         }
-        if (band == 0) {
-          bands = __reduce_or_sync(~0u, bands);
-          if (lane == 0 && bands) atomicOr(reinterpret_cast<uint32_t*>(__cvta_shared_to_generic(base + M::words + 8)), bands);
-          group_sync(kSync);
-          todo = lds32(base + M::words + 8);
-        }
-        if (tid == 0) sts32(base + M::words + ib * 4, kInfoSlow | (todo ? 0 : kInfoLast));
-        async_fence();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (!todo) w.arrive(kScoresEmpty + sb);
-          w.arrive(kWeightsFull + ib);
-        }
-        ++it;
       }
     }
-    // the part's sums over the warp's tokens: pairs of rows are exchanged, so
-    // that each step halves what a lane holds
+    // the part's sums over the warp's tokens: rows are exchanged, so that each
+    // step halves what a lane holds
     int width = N, row = 0;
 #pragma unroll
     for (int bit = 16; bit; bit >>= 1) {
@@ -704,36 +789,31 @@ struct Values {
   Waiter w;
   const int tid, lane, group, element;
   const Bases bases;
-  float o[N];
-  int it = 0, n_parts = 0;
-  uint32_t nans[4] = {};  // tokens of the pending tile whose values of this group are NaN
+  int it = 0, n_parts = 0, fixes = 0;
 
   __device__ __forceinline__ Values(const AttnLaunch& L_, uint32_t base_, uint32_t tmem_, Waiter w_, int warp, int lane_)
       : L(L_), a(L_.a), base(base_), tmem(tmem_ + (static_cast<uint32_t>(warp * 32) << 16)), w(w_), tid(warp * 32 + lane_),
-        lane(lane_), group((tid >> 1) & 7), element(((tid >> 1) & 7) * 16 + (tid >> 4) * 2 + (tid & 1)), bases(make_bases()) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) o[n] = 0.f;
-  }
+        lane(lane_), group((tid >> 1) & 7), element(((tid >> 1) & 7) * 16 + (tid >> 4) * 2 + (tid & 1)), bases(make_bases()) {}
 
-  // A tile's codes to tensor memory; `found`: its NaN (edge tiles, whose other
-  // rows must not see them; elsewhere a NaN is every row's).
-  __device__ __forceinline__ void unpack(int stage, int vb, int tile, int pos0, bool edge, const Span& sp,
-                                         uint32_t (&found)[4]) {
+  // A tile's codes to tensor memory.  Returns the rows (bits) that see a NaN among
+  // the values of this group in an edge tile, whose other rows must not see it;
+  // elsewhere a NaN is every row's.
+  __device__ __forceinline__ unsigned long long unpack(int stage, int vb, int tile, int pos0, bool edge, const Part& q) {
     const uint32_t data = base + M::stages + stage * kStage, table = base + M::table + vb * 4096;
     const int blk = tid >> 4, half = tid & 1;  // whose scales this thread expands, for its own group
     uint2 sv = lds64(data + blk * kBlockStride + kv_v_scales(kD) + group * 16 + half * 8);
     if (edge) {
       uint32_t mask = 0;
-      uint32_t sc[2] = {sv.x, sv.y};
       const int first = pos0 + blk * kKvBlock + half * 8;
-#pragma unroll
+      unsigned long long bytes = sv.x | static_cast<unsigned long long>(sv.y) << 32;
+#pragma unroll 1
       for (int k = 0; k < 8; ++k) {
-        const uint32_t byte = (sc[k >> 2] >> ((k & 3) * 8)) & 0xFFu;
-        const bool seen = first + k >= sp.lo && first + k < sp.hi;
+        const uint32_t byte = static_cast<uint32_t>(bytes >> (k * 8)) & 0xFFu;
+        const bool seen = first + k >= q.lo && first + k < q.hi;
         if (seen && byte == kKvNanByte) mask |= 1u << k;
-        if (!seen || byte == kKvNanByte) sc[k >> 2] &= ~(0xFFu << ((k & 3) * 8));
+        if (!seen || byte == kKvNanByte) bytes &= ~(0xFFull << (k * 8));
       }
-      sv = make_uint2(sc[0], sc[1]);
+      sv = make_uint2(static_cast<uint32_t>(bytes), static_cast<uint32_t>(bytes >> 32));
       asm volatile("st.shared.u8 [%0], %1;" ::"r"(base + M::nans + vb * 128 + blk * 16 + group * 2 + half), "r"(mask) : "memory");
     }
 #pragma unroll
@@ -746,30 +826,37 @@ struct Values {
     group_sync(kSync);
     w.wait(kValuesEmpty + vb, (tile >> 1) ^ 1);
     tc_fence_after();
+#pragma unroll 1
+    for (int two = 0; two < 4; ++two) {  // two blocks at a time
+      uint32_t v[16];
 #pragma unroll
-    for (int quad = 0; quad < 2; ++quad) {
-      uint32_t v[32];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint2 c = lds64(data + (quad * 4 + b) * kBlockStride + kv_v_codes(kD) + tid * 8);
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t from = table + (two * 2 + b) * 512 + group * 16;
+        const uint2 c = lds64(data + (two * 2 + b) * kBlockStride + kv_v_codes(kD) + tid * 8);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t word = k ? c.y : c.x, turned = __funnelshift_r(word, word, 8);
-          const uint4 e0 = lds128(table + (quad * 4 + b) * 512 + (2 * k) * 128 + group * 16);
-          const uint4 e1 = lds128(table + (quad * 4 + b) * 512 + (2 * k + 1) * 128 + group * 16);
+          const uint4 e0 = lds128(from + (2 * k) * 128), e1 = lds128(from + (2 * k + 1) * 128);
           v[b * 8 + k * 4] = fma2(pair_hi(word, bases), e0.x, e0.y);
           v[b * 8 + k * 4 + 1] = fma2(pair_lo(word, bases), e0.z, e0.w);
           v[b * 8 + k * 4 + 2] = fma2(pair_hi(turned, bases), e1.x, e1.y);
           v[b * 8 + k * 4 + 3] = fma2(pair_lo(turned, bases), e1.z, e1.w);
         }
       }
-      tc_st32(tmem + Tmem<N>::values + vb * 64 + quad * 32, v);
+      tc_st16(tmem + Tmem<N>::values + vb * 64 + two * 16, v);
     }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) found[x] = 0;
-    if (edge)
-#pragma unroll
-      for (int b = 0; b < 8; ++b) found[b >> 1] |= lds16(base + M::nans + vb * 128 + b * 16 + group * 2) << (16 * (b & 1));
+    unsigned long long rows = 0;
+    if (edge) {
+#pragma unroll 1
+      for (int b = 0; b < kBlocks; ++b) {
+        uint32_t nans = lds16(base + M::nans + vb * 128 + b * 16 + group * 2);
+#pragma unroll 1
+        for (; nans; nans &= nans - 1) {
+          const int2 seen = rows_seeing<N>(L, q, pos0 + b * kKvBlock + __ffs(nans) - 1);
+          for (int n = seen.x; n < seen.y; ++n) rows |= 1ull << n;
+        }
+      }
+    }
     tc_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -777,146 +864,161 @@ struct Values {
       w.arrive(kEmpty + stage);
       w.arrive(kValuesFull + vb);
     }
+    return rows;
   }
 
-  // Adds the products of a tile that began at pos0.
-  __device__ __forceinline__ void gather(const Part& q, int pos0) {
-    if (nans[0] | nans[1] | nans[2] | nans[3]) {
-      const int pass0 = q.hr % L.p.rt * N;
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int i = (pass0 + n) / L.per;
-        const int lo = max(0, min(row_lo(a, q.s.len, i) - pos0, kTile));
-        const int hi = max(0, min(min(row_hi(a, q.s.len, i), q.s.hi) - pos0, kTile));
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int from = max(0, min(lo - 32 * x, 32)), to = max(0, min(hi - 32 * x, 32));
-          const uint32_t below = to == 32 ? ~0u : (1u << to) - 1u, skip = from == 32 ? ~0u : (1u << from) - 1u;
-          if (nans[x] & below & ~skip) o[n] = __int_as_float(0x7FC00000);
-        }
-      }
-    }
-    __syncwarp();
-    for (bool last = false; !last;) {
-      const int tb = it % Tmem<N>::kSums, ib = it & 1;
-      w.wait(kSumFull + tb, it / Tmem<N>::kSums);
-      tc_fence_after();
+  // Follows a tile's weights: corrects the sums where the tile asks for it.
+  __device__ __forceinline__ void follow(bool first) {
+#pragma unroll 1
+    for (bool last = false; !last; ++it) {
+      const int ib = it & 1;
+      w.wait(kWeightsFull + ib, it >> 1);
       const uint32_t info = lds32(base + M::words + ib * 4);
       last = w.dead || (info & kInfoLast);
+      const int band = info >> 8;
+      if (band || (info & kInfoRescale)) {
+        w.wait(kFixFull, fixes++);
+        tc_fence_after();
+        const uint32_t out = tmem + Tmem<N>::outs + n_parts % Tmem<N>::kOuts * N;
+        const float up = band ? ex2(static_cast<float>(-kBand * band)) : 0.f;
+        if (band || !first) {
+#pragma unroll 1
+          for (int n = 0; n < N; n += 4) {
+            float x[4], t[4];
+            tc_ld4(out + n, x);
+            tc_ld4(tmem + (band ? Tmem<N>::band + n : Tmem<N>::outs), t);
+            tc_wait_ld4(x);
+            tc_wait_ld4(t);
 #pragma unroll
-      for (int n = 0; n < N; n += 16) {
-        float t[16];
-        tc_ld16(tmem + Tmem<N>::sums + tb * N + n, t);
-        tc_wait_ld<16>(t);
-        if (info & kInfoSlow) {
-#pragma unroll
-          for (int y = 0; y < 16; ++y)
-            o[n + y] = o[n + y] * lds_f(base + M::fall + (ib * N + n + y) * 4) +
-                       t[y] * lds_f(base + M::grow + (ib * N + n + y) * 4);
-        } else {
-#pragma unroll
-          for (int y = 0; y < 16; ++y) o[n + y] += t[y];
+            for (int y = 0; y < 4; ++y)
+              x[y] = band ? fmaf(t[y], up, x[y]) : x[y] * lds_f(base + M::fall + (ib * N + n + y) * 4);
+            tc_st4(out + n, x);
+          }
+          tc_wait_st();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) w.arrive(kFixDone);
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        w.arrive(kSumEmpty + tb);
-        w.arrive(kInfoEmpty + ib);
-      }
-      ++it;
+      if (lane == 0) w.arrive(kInfoEmpty + ib);
     }
   }
 
-  // Writes a part's results and clears the sums.
-  __device__ __forceinline__ void finish(const Part& q, bool lost) {
-    const int h = q.hr / L.p.rt, pass0 = q.hr % L.p.rt * N;
-    const int nrows = q.s.bad ? 0 : q.s.nq * L.per;
-    const bool whole = q.first == 0 && q.count == q.s.tiles, active = q.active();
-    const long long slot = 2ll * blockIdx.x + (q.first == 0 && q.later ? 1 : 0);
-    if (q.s.bad && q.hr == 0 && tid == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
-    if (active) w.wait(kEndFull, n_parts);
-    lost = lost || w.dead || q.s.bad;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int row = pass0 + n;
-      if (row < L.rows) {
-        const long long orow = (static_cast<long long>(q.b) * a.nq + row / L.per) * a.heads + h * L.per + row % L.per;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + orow * kD + element;
+  // Writes a part's results; `nans`: rows whose sums a NaN belongs to.
+  __device__ __forceinline__ void finish(const Part& q, bool lost, unsigned long long nans) {
+    const int nrows = q.flags & Part::kBad ? 0 : q.nq * L.per, ob = n_parts % Tmem<N>::kOuts;
+    const bool whole = q.flags & Part::kWhole, active = q.active();
+    const uint32_t rows = base + M::rows;
+    if ((q.flags & Part::kBad) && q.head == 0 && q.pass0 == 0 && tid == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
+    if (active) {
+      w.wait(kEndFull, n_parts);
+      w.wait(kOutFull + ob, n_parts / Tmem<N>::kOuts);
+      tc_fence_after();
+    }
+    // a thread per row: where it goes (in halves of a part, or -1) and its factor
+    if (tid < N) {
+      const int row = q.pass0 + tid;
+      long long at = -1;
+      float f = 0.f;
+      if (row < L.rows && (row < nrows || q.first == 0)) {
+        const long long orow = (static_cast<long long>(q.b) * a.nq + row / L.per) * a.heads + q.head * L.per + row % L.per;
         float l = 0.f, m = 0.f;
-        if (active) {
+        if (active && row < nrows) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) l += lds_f(base + M::ends + (u * N + n) * 4);
-          m = lds_f(base + M::ends + (4 * N + n) * 4);
+          for (int u = 0; u < 4; ++u) l += lds_f(base + M::ends + (u * N + tid) * 4);
+          m = lds_f(base + M::ends + (4 * N + tid) * 4);
         }
-        if (row >= nrows) l = 0.f;  // a padded query's row
-        if (lost) l = __int_as_float(0x7FC00000);
-        if (row >= nrows ? q.first == 0 : whole) {
-          *out = static_cast<__nv_bfloat16>(l == 0.f ? 0.f : o[n] / l);
-          if (a.lse && tid == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + (log2f(l) - kFast)) * 0.69314718055994531f;
-        } else if (row < nrows) {
+        if (lost || w.dead || (q.flags & Part::kBad)) l = __int_as_float(0x7FC00000);
+        if (whole || row >= nrows) {
+          at = orow;
+          f = l == 0.f ? 0.f : 1.f / l;
+          if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + (log2f(l) - kFast)) * 0.69314718055994531f;
+        } else {
           // (parts are kept 2^kTop up)
-          const long long at = slot * N + n;
-          L.o[at * kD + element] = o[n] * (1 << (kTop - kFast));
-          if (tid == 0) L.ml[at] = make_float2(m, l * (1 << (kTop - kFast)));
+          at = (2ll * blockIdx.x + (q.first == 0 && (q.flags & Part::kLater) ? 1 : 0)) * N + tid;
+          f = 1 << (kTop - kFast);
+          L.ml[at] = make_float2(m, l * f);
         }
       }
-      o[n] = 0.f;
+      sts64(rows + tid * 16, make_uint2(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32)));
+      sts64(rows + tid * 16 + 8, make_uint2(__float_as_uint(f), whole || row >= nrows));
     }
+    group_sync(kSync);
+#pragma unroll 1
+    for (int n0 = 0; n0 < N; n0 += 4) {
+      float o[4] = {};
+      if (active) {
+        tc_ld4(tmem + Tmem<N>::outs + ob * N + n0, o);
+        tc_wait_ld4(o);
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint4 r = lds128(rows + (n0 + y) * 16);
+        const long long at = static_cast<long long>(r.x | static_cast<unsigned long long>(r.y) << 32);
+        const float f = __uint_as_float(r.z), x = nans >> (n0 + y) & 1 ? __int_as_float(0x7FC00000) : o[y];
+        const float z = f == 0.f ? 0.f : x * f;
+        if (at >= 0) {
+          if (r.w) static_cast<__nv_bfloat16*>(a.out)[at * kD + element] = static_cast<__nv_bfloat16>(z);
+          else L.o[at * kD + element] = z;
+        }
+      }
+    }
+    tc_fence_before();
+    group_sync(kSync);  // the rows' table is read before the next part's is written
     if (active) {
-      __syncwarp();
-      if (lane == 0) w.arrive(kEndEmpty);
+      if (lane == 0) {
+        w.arrive(kEndEmpty);
+        w.arrive(kOutEmpty + ob);
+      }
       ++n_parts;
     }
   }
 };
 
 template <int N>
-__device__ __forceinline__ void value_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, uint32_t tmem,
-                                           Waiter w, int warp, int lane) {
+__device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int warp, int lane) {
   constexpr int S = Smem<N>::kStages;
   Values<N> v(L, base, tmem, w, warp, lane);
-  Parts parts(L.a, list);
+  Ring<N> parts(base, v.w);
   Part p, prev = {};
-  int st = 0, tile = 0, prev_pos0 = 0;
+  p.count = 0;
+  int st = 0, tile = 0, k = 0;
   uint32_t phase = 0;
-  // a tile's products are added while the next one's are computed
-  bool pending = false, ends = false, lost = false, prev_lost = false;
-  while (parts.next(p)) {
-    if (!p.active()) {
-      if (pending) {
-        v.gather(prev, prev_pos0);
-        v.finish(prev, prev_lost);
-        pending = false;
-      }
-      v.finish(p, false);
-      continue;
+  // values go one tile ahead of the weights
+  bool more = true, pending = false, first = false, ends = false, lost = false, prev_lost = false;
+  unsigned long long nans = 0, prev_nans = 0;
+#pragma unroll 1
+  while (more || pending) {
+    if (more && k == p.count) {
+      more = parts.next(p, lane);
+      k = 0;
+      lost = false;
+      nans = 0;
     }
-    const int lo_last = row_lo(L.a, p.s.len, p.s.nq - 1), hi_first = row_hi(L.a, p.s.len, 0);
-    lost = false;
-    for (int k = 0; k < p.count; ++k, ++tile) {
-      const int pos0 = (p.s.tile0 + p.first + k) * kTile;
-      uint32_t found[4];
+    const bool have = more && p.active();
+    if (have) {
+      const int pos0 = (p.tile0 + p.first + k) * kTile;
+      const bool edge = pos0 < row_lo(L.a, p.len, p.nq - 1) || pos0 + kTile > row_hi(L.a, p.len, 0);
       v.w.wait(kFull + st, phase);
       lost |= lds32(base + Smem<N>::words + 16 + st * 4) != 0;
-      v.unpack(st, tile & 1, tile, pos0, pos0 < lo_last || pos0 + kTile > hi_first, p.s, found);
+      nans |= v.unpack(st, tile & 1, tile, pos0, edge, p);
       if (++st == S) st = 0, phase ^= 1;
-      if (pending) {
-        v.gather(prev, prev_pos0);
-        if (ends) v.finish(prev, prev_lost);
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) v.nans[x] = found[x];
-      pending = true;
-      ends = k == p.count - 1;
-      prev = p;
-      prev_pos0 = pos0;
-      prev_lost = lost;
+      ++tile;
     }
-  }
-  if (pending) {
-    v.gather(prev, prev_pos0);
-    v.finish(prev, prev_lost);
+    // (a part without tiles, whose count is one, has only its results: zeros, or
+    // NaN for bad lengths)
+    if (pending && prev.active()) v.follow(first);
+    if (pending && ends) v.finish(prev, prev_lost, prev_nans);
+    pending = more;
+    if (more) {
+      first = k == 0;
+      ++k;
+      ends = k == p.count;
+      prev = p;
+      prev_lost = lost;
+      prev_nans = nans;
+    }
   }
   if (v.w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
@@ -928,17 +1030,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(smem) + 1023) & ~1023u, words = base + Smem<N>::words;
   if (tid < kBars) {
+    // how many warps (or commits) arrive
     int count = 1;
     if (tid >= kEmpty && tid < kKeysFull) count = 8;
     if ((tid >= kKeysFull && tid < kKeysEmpty) || (tid >= kScoresEmpty && tid < kWeightsEmpty) ||
-        (tid >= kValuesFull && tid < kValuesEmpty) || (tid >= kSumEmpty && tid < kQueryFull) || tid >= kEndFull)
+        (tid >= kValuesFull && tid < kValuesEmpty) || (tid >= kOutEmpty && tid < kQueryFull) || tid == kEndFull ||
+        tid == kEndEmpty || tid == kFixDone)
       count = 4;
-    if (tid >= kQueryFull && tid < kQueryEmpty) count = 2;
     if (tid >= kQueryEmpty && tid < kEndFull) count = 5;
-    if (tid == kDone) count = 1;
+    if (tid >= kPartEmpty) count = 15;
     bar_init(base + tid * 8, count);
   }
   if (tid < kMaxStages) sts32(words + 16 + tid * 4, 0);
+  if (tid == 0) sts32(words + 8, 0);
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(words + 12) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -951,30 +1055,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
   const uint32_t tmem = lds32(words + 12);
   Waiter w;
   w.bars = base;
-  // 128 x (192 + 96 + 152 + 72) registers: the 512 x 128 of the launch
+  // 128 x (184 + 96 + 120 + 112) registers: the 512 x 128 of the launch
   if (warp < 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    weight_role<N>(L, list, base, tmem, w, warp, lane);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    weight_role<N>(L, base, tmem, w, warp, lane);
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    key_role<N>(L, list, base, tmem, w, warp - 4, lane);
+    key_role<N>(L, base, tmem, w, warp - 4, lane);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    value_role<N>(L, list, base, tmem, w, warp - 8, lane);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    value_role<N>(L, base, tmem, w, warp - 8, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 12) {
-      copy_role<N>(L, list, base, w, lane);
-    } else if (warp == 13) {
-      if (lane == 0) matrix_role<N>(L, list, base, tmem, w);
-      __syncwarp();
-    } else {
-      if (warp == 14 && lane == 0) {
-        const long long me = blockIdx.x;
-        L.desc[me] = me * list.quota < list.units ? list.parts(list.find(L.a, me * list.quota), me) : make_int4(0, 0, 0, 0);
-      }
-      query_role<N>(L, list, base, w, warp - 14, lane);
-    }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    if (warp == 12) copy_role<N>(L, base, w, lane);
+    else if (warp == 13) matrix_role<N>(L, base, tmem, w, lane);
+    else if (warp == 14) query_role<N>(L, base, w, lane);
+    else plan_role<N>(L, list, base, w, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -1001,7 +1097,6 @@ cudaError_t launch_attention_tc(const AttnLaunch& L, int sms, cudaStream_t strea
     case 32: return launch_n<32>(L, sms, stream);
     case 48: return launch_n<48>(L, sms, stream);
     case 64: return launch_n<64>(L, sms, stream);
-    case 80: return launch_n<80>(L, sms, stream);
   }
   return cudaErrorInvalidValue;
 }
