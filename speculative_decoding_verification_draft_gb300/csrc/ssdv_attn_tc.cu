@@ -82,12 +82,13 @@ enum : int {
 // Shared memory after the head, for N rows.
 template <int N>
 struct Smem {
-  static constexpr int kOperand = N * 256;  // N rows x 128 fp16, 128-byte swizzled halves
+  static constexpr int kQueries = N * 256;      // N rows x 128 fp16, in 128-byte swizzled halves
+  static constexpr int kWeights = kTile * 128;  // 128 tokens x 64 fp16, 128-byte swizzled
   static constexpr int query = kHead;
-  static constexpr int weight = query + 2 * kOperand;
-  static constexpr int table = weight + 2 * kOperand;   // [2] scales of the values: 8 blocks x 4 x 8 groups x 16 bytes
+  static constexpr int weight = query + 2 * kQueries;
+  static constexpr int table = weight + 2 * kWeights;   // [2] the values' scales and offsets: 8 pairs x 8 blocks x 8 groups
   static constexpr int nans = table + 2 * 4096;         // [2][8 blocks][8 groups][2] bytes
-  static constexpr int fr = nans + 2 * 128;             // [N] factor and reference of the fast weights
+  static constexpr int fr = nans + 2 * 128;             // [N / 2] two rows' factors, then references
   static constexpr int maxima = fr + 8 * N;             // [N]
   static constexpr int tops = maxima + 4 * N;           // [4][N]
   static constexpr int fall = tops + 16 * N;            // [2][N]
@@ -164,11 +165,10 @@ __device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&v)[16]) {
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t at, const float (&x)[16]) {
-  uint32_t v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(x[i]);
-  tc_st16(at, v);
+__device__ __forceinline__ void tc_st8(uint32_t at, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 // D [128 x N] in tensor memory (+)= A [128 x 16] in tensor memory, B [N x 16] in shared memory.
 __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, bool leader) {
@@ -178,9 +178,10 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
-// fp16 x fp16 -> fp32, both operands contraction-major, M = 128.
-__device__ __forceinline__ constexpr uint32_t tc_idesc(int n) {
-  return (1u << 4) | (static_cast<uint32_t>(n / 8) << 17) | ((128u / 16) << 24);
+// fp16 x fp16 -> fp32, M = 128, A contraction-major; B so (rows of 64 of the
+// contraction) or row-major (64 rows at each of the contraction).
+__device__ __forceinline__ constexpr uint32_t tc_idesc(int n, bool row_major) {
+  return (1u << 4) | (row_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n / 8) << 17) | ((128u / 16) << 24);
 }
 // An operand of 128-byte rows, 128-byte swizzle: 8-row groups lie 1024 bytes apart.
 __device__ __forceinline__ uint64_t tc_operand(uint32_t at) {
@@ -219,6 +220,21 @@ __device__ __forceinline__ uint32_t lds16(uint32_t p) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
   return v;
 }
+// (x, y) = (x, y) * (f.x, f.y) + (f.z, f.w), and (x, y) += (a, b): two fp32 operations at once.
+__device__ __forceinline__ void fma_pair(float& x, float& y, const uint4& f) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w));
+}
+__device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
 // The larger of all lanes' numbers (NaN aside).
 __device__ __forceinline__ float warp_max(float x) {
   float y;
@@ -233,6 +249,14 @@ struct Waiter {
   bool dead = false;
   __device__ __forceinline__ void wait(int bar, uint32_t phase) {
     if (!dead && !bar_wait(bars + bar * 8, phase & 1)) dead = true;
+  }
+  // For warps that run ahead: they sleep between tries.
+  __device__ __forceinline__ void nap(int bar, uint32_t phase) {
+    for (int i = 0; i < (1 << 22) && !dead; ++i) {
+      if (bar_test(bars + bar * 8, phase & 1)) return;
+      __nanosleep(200);
+    }
+    dead = true;
   }
   __device__ __forceinline__ void arrive(int bar) { bar_arrive(bars + bar * 8); }
 };
@@ -281,7 +305,7 @@ __device__ __forceinline__ void plan_role(const AttnLaunch& L, const List<kTile>
   for (int n = 0;; ++n) {
     const int slot = n % kRing, count = left ? min(left, at.s.tiles - at.tile) : 0;
     const bool end = left == 0;
-    w.wait(kPartEmpty + slot, (n / kRing) ^ 1);
+    w.nap(kPartEmpty + slot, (n / kRing) ^ 1);
     if (lane == 0) {
       const uint32_t to = base + Smem<N>::parts + slot * 64;
       const int flags = (later ? Part::kLater : 0) | (at.tile == 0 && count == at.s.tiles ? Part::kWhole : 0) |
@@ -352,7 +376,7 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, uint32_t base, Wa
       }
       const bool want_next = seen(k + 1);
       const int page_next = want_next ? table[col] : 0;
-      w.wait(kEmpty + st, phase);
+      w.nap(kEmpty + st, phase);
       const uint32_t bar = w.bars + (kFull + st) * 8;
       if (lane == 0) {
         sts32(base + Smem<N>::words + 16 + st * 4, lacks);
@@ -386,7 +410,7 @@ __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, W
   while (parts.next(p, lane)) {
     if (!p.active()) continue;
     const int qb = n_parts & 1, nrows = p.nq * L.per;
-    w.wait(kQueryEmpty + qb, (n_parts >> 1) ^ 1);
+    w.nap(kQueryEmpty + qb, (n_parts >> 1) ^ 1);
     const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + p.b * a.qs[0] + p.head * L.per * a.qs[2] + lane * 4;
     int i = p.pass0 / L.per, g = p.pass0 % L.per;  // the row's query token and head
 #pragma unroll 1
@@ -417,7 +441,7 @@ __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, W
         int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
         ex = max(-100, min(ex, 127));
         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), a.scale_log2);
-        sts64(base + Smem<N>::query + qb * Smem<N>::kOperand + operand_byte<N>(k0 + k, lane * 4),
+        sts64(base + Smem<N>::query + qb * Smem<N>::kQueries + operand_byte<N>(k0 + k, lane * 4),
               make_uint2(half2_bits(__floats2half2_rn(x[k][0] * up, x[k][1] * up)),
                          half2_bits(__floats2half2_rn(x[k][2] * up, x[k][3] * up))));
         if (lane == 0)
@@ -438,14 +462,16 @@ __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, W
 template <int N>
 __device__ __forceinline__ void matrix_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int lane) {
   const bool leader = lane == 0;
-  // D (+)= A B over 128 of the contraction: A 8 columns, B 32 bytes a step
-  const auto product = [&](uint32_t d, uint32_t a, uint32_t b, bool add) {
+  // D (+)= A B over 128 of the contraction: A 8 columns a step, B 32 bytes
+  // (queries) or 16 rows (weights)
+  const auto product = [&](uint32_t d, uint32_t a, uint32_t b, bool weights, bool add) {
     // (a broadcast is what tells the compiler that the warp agrees on a number)
     d = __shfl_sync(~0u, d, 0), a = __shfl_sync(~0u, a, 0), b = __shfl_sync(~0u, b, 0);
     const uint64_t operand = tc_operand(b);
 #pragma unroll
     for (int s = 0; s < 8; ++s)
-      tc_mma(d, a + s * 8, operand + (s >> 2) * (N * 8) + (s & 3) * 2, tc_idesc(N), s > 0 || add, leader);
+      tc_mma(d, a + s * 8, operand + (weights ? s * 128 : (s >> 2) * (N * 8) + (s & 3) * 2), tc_idesc(N, weights),
+             s > 0 || add, leader);
   };
   Ring<N> parts(base, w);
   Part p;
@@ -469,7 +495,7 @@ __device__ __forceinline__ void matrix_role(const AttnLaunch& L, uint32_t base, 
       tc_fence_after();
       if (!w.dead) {
         product(tmem + Tmem<N>::scores + sb * N, tmem + Tmem<N>::keys + sb * 64,
-                base + Smem<N>::query + qb * Smem<N>::kOperand, false);
+                base + Smem<N>::query + qb * Smem<N>::kQueries, false, false);
         tc_commit(w.bars + (kScoresFull + sb) * 8, leader);
         tc_commit(w.bars + (kKeysEmpty + sb) * 8, leader);
         if (last_tile) tc_commit(w.bars + (kQueryEmpty + qb) * 8, leader);
@@ -497,7 +523,7 @@ __device__ __forceinline__ void matrix_role(const AttnLaunch& L, uint32_t base, 
         tc_fence_after();
         if (!w.dead) {
           product(band ? tmem + Tmem<N>::band : out, tmem + Tmem<N>::values + vb * 64,
-                  base + Smem<N>::weight + pb * Smem<N>::kOperand, band == 0 && !is_first);
+                  base + Smem<N>::weight + pb * Smem<N>::kWeights, true, band == 0 && !is_first);
           tc_commit(w.bars + (kWeightsEmpty + pb) * 8, leader);
           if (band) {
             tc_commit(w.bars + kFixFull * 8, leader);
@@ -584,10 +610,13 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
   using M = Smem<N>;
   constexpr int kSync = 1;
   const int tid = warp * 32 + lane;
-  const int token = ((lane & 3) + 4 * (warp >> 1)) * kKvBlock + (((lane >> 2) & 1) | ((lane >> 3) << 1) | ((warp & 1) << 3));
-  uint32_t to[8];  // where the thread's column of the weights lies in rows 0..7
-#pragma unroll
-  for (int r = 0; r < 8; ++r) to[r] = base + M::weight + operand_byte<N>(r, token);
+  const int blk = (lane & 3) + 4 * (warp >> 1), t = ((lane >> 2) & 1) | ((lane >> 3) << 1) | ((warp & 1) << 3);
+  const int token = blk * kKvBlock + t;
+  // In the products' contraction pair p of block b comes at 16 p + 2 b: eight
+  // neighbouring lanes then write to different banks.
+  const int place = (t >> 1) * 16 + blk * 2 + (t & 1);
+  const auto fr_at = [&](int n) { return base + M::fr + (n >> 1) * 16 + (n & 1) * 4; };
+  const uint32_t to = base + M::weight + place * 128, turn = (place & 7) << 4;
   Ring<N> parts(base, w);
   Part p;
   int n_parts = 0, tile = 0, it = 0;
@@ -597,7 +626,8 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
     w.wait(kQueryFull + qb, n_parts >> 1);
     if (tid < N) {
       // an infinite reference makes the first tile set it
-      sts64(base + M::fr + tid * 8, make_uint2(lds32(base + M::factors + (qb * N + tid) * 4), 0x7F800000u));
+      sts32(fr_at(tid), lds32(base + M::factors + (qb * N + tid) * 4));
+      sts32(fr_at(tid) + 8, 0x7F800000u);
       sts_f(base + M::maxima + tid * 4, -INFINITY);
     }
     group_sync(kSync);
@@ -613,10 +643,11 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
       int2 seen = make_int2(0, N);  // rows that see the token
       if (edge) seen = rows_seeing<N>(L, p, pos0 + token);
       const uint32_t scores = tmem + (static_cast<uint32_t>(warp * 32) << 16) + Tmem<N>::scores + sb * N;
-      const auto put = [&](int n0, int n, uint32_t pair) {
-        const uint32_t at = (it & 1) * M::kOperand + n0 * 128 + (n >> 3) * 1024;
-        sts16(to[n & 7] + at, pair);
-        sts16(to[(n + 1) & 7] + at, pair >> 16);
+      const auto put = [&](int n, const float* x) {  // rows n .. n + 7
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = half2_bits(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
+        sts128(to + (it & 1) * M::kWeights + ((n << 1) ^ turn), make_uint4(v[0], v[1], v[2], v[3]));
       };
       w.wait(kScoresFull + sb, tile >> 1);
       tc_fence_after();
@@ -633,9 +664,8 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
         tc_wait_ld<N>(u);
 #pragma unroll
         for (int n = 0; n < N; n += 2) {
-          const uint4 fr = lds128(base + M::fr + n * 8);
-          u[n] = fmaf(u[n], __uint_as_float(fr.x), __uint_as_float(fr.y));
-          u[n + 1] = fmaf(u[n + 1], __uint_as_float(fr.z), __uint_as_float(fr.w));
+          const uint4 fr = lds128(base + M::fr + n * 8);  // factors, then references of two rows
+          fma_pair(u[n], u[n + 1], fr);
         }
         if (edge) {
 #pragma unroll
@@ -684,11 +714,11 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
           float top = -INFINITY;
 #pragma unroll
           for (int x = 0; x < 4; ++x) top = fmaxf(top, lds_f(base + M::tops + (x * N + tid) * 4));
-          const float f = lds_f(base + M::fr + tid * 8), old = lds_f(base + M::maxima + tid * 4);
+          const float f = lds_f(fr_at(tid)), old = lds_f(base + M::maxima + tid * 4);
           if (top != -INFINITY) top *= f;
           const float m = fmaxf(old, top);
           sts_f(base + M::maxima + tid * 4, m);
-          sts_f(base + M::fr + tid * 8 + 4, m == -INFINITY ? INFINITY : kFast - m);
+          sts_f(fr_at(tid) + 8, m == -INFINITY ? INFINITY : kFast - m);
           sts_f(base + M::fall + ((it & 1) * N + tid) * 4, old == -INFINITY ? 0.f : ex2(old - m));
         }
         group_sync(kSync);
@@ -699,8 +729,8 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
 #pragma unroll
       for (int n = 0; n < N; n += 2) {
         u[n] = ex2(u[n]), u[n + 1] = ex2(u[n + 1]);
-        l[n] += u[n], l[n + 1] += u[n + 1];
-        put(0, n, half2_bits(__floats2half2_rn(u[n], u[n + 1])));
+        add_pair(l[n], l[n + 1], u[n], u[n + 1]);
+        if (n % 8 == 6) put(n - 6, u + n - 6);
       }
 #pragma unroll 1
       for (int band = 0;; ++band) {
@@ -726,8 +756,8 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
           tc_wait_ld<16>(s);
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            const float2 fr = lds_f2(base + M::fr + (n0 + n) * 8);
-            s[n] = !edge || (n0 + n >= seen.x && n0 + n < seen.y) ? ex2(fmaf(s[n], fr.x, fr.y)) : 0.f;
+            const uint32_t fr = fr_at(n0 + n);
+            s[n] = !edge || (n0 + n >= seen.x && n0 + n < seen.y) ? ex2(fmaf(s[n], lds_f(fr), lds_f(fr + 8))) : 0.f;
           }
 #pragma unroll 1
           for (int x = 0; x <= band; ++x)
@@ -735,7 +765,7 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
             for (int n = 0; n < 16; ++n)
               s[n] = fabsf(s[n]) < kSmallest ? (s[n] - __half2float(__float2half_rn(s[n]))) * kBandUp : 0.f;
 #pragma unroll
-          for (int n = 0; n < 16; n += 2) put(n0, n, half2_bits(__floats2half2_rn(s[n], s[n + 1])));
+          for (int n = 0; n < 16; n += 8) put(n0 + n, s + n);
         }
       }
     }
@@ -817,33 +847,33 @@ struct Values {
       asm volatile("st.shared.u8 [%0], %1;" ::"r"(base + M::nans + vb * 128 + blk * 16 + group * 2 + half), "r"(mask) : "memory");
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t word = k ? sv.y : sv.x;
-      const uint32_t s0 = __byte_perm(word, 0, 0x4140) << 7, s1 = __byte_perm(word, 0, 0x4342) << 7;
-      sts128(table + blk * 512 + half * 256 + k * 128 + group * 16,
-             make_uint4(s0, mul2(s0, kMinus24), s1, mul2(s1, kMinus264)));
+    for (int k = 0; k < 4; ++k) {  // pairs 4 half + k
+      const uint32_t scale = __byte_perm(k < 2 ? sv.x : sv.y, 0, k & 1 ? 0x4342 : 0x4140) << 7;
+      sts64(table + (half * 4 + k) * 512 + (blk >> 1) * 128 + group * 16 + (blk & 1) * 8,
+            make_uint2(scale, mul2(scale, k & 1 ? kMinus264 : kMinus24)));
     }
     group_sync(kSync);
     w.wait(kValuesEmpty + vb, (tile >> 1) ^ 1);
     tc_fence_after();
 #pragma unroll 1
-    for (int two = 0; two < 4; ++two) {  // two blocks at a time
-      uint32_t v[16];
+    for (int half2 = 0; half2 < 2; ++half2) {  // a word of every block, four pairs
+      uint32_t word[kBlocks];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t from = table + (two * 2 + b) * 512 + group * 16;
-        const uint2 c = lds64(data + (two * 2 + b) * kBlockStride + kv_v_codes(kD) + tid * 8);
+      for (int b = 0; b < kBlocks; ++b) word[b] = lds32(data + b * kBlockStride + kv_v_codes(kD) + tid * 8 + half2 * 4);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t word = k ? c.y : c.x, turned = __funnelshift_r(word, word, 8);
-          const uint4 e0 = lds128(from + (2 * k) * 128), e1 = lds128(from + (2 * k + 1) * 128);
-          v[b * 8 + k * 4] = fma2(pair_hi(word, bases), e0.x, e0.y);
-          v[b * 8 + k * 4 + 1] = fma2(pair_lo(word, bases), e0.z, e0.w);
-          v[b * 8 + k * 4 + 2] = fma2(pair_hi(turned, bases), e1.x, e1.y);
-          v[b * 8 + k * 4 + 3] = fma2(pair_lo(turned, bases), e1.z, e1.w);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t v[kBlocks];
+#pragma unroll
+        for (int q = 0; q < kBlocks / 2; ++q) {
+          const uint4 e = lds128(table + (half2 * 4 + k) * 512 + q * 128 + group * 16);
+          v[2 * q] = fma2(k & 1 ? pair_lo(word[2 * q], bases) : pair_hi(word[2 * q], bases), e.x, e.y);
+          v[2 * q + 1] = fma2(k & 1 ? pair_lo(word[2 * q + 1], bases) : pair_hi(word[2 * q + 1], bases), e.z, e.w);
         }
+        tc_st8(tmem + Tmem<N>::values + vb * 64 + (half2 * 4 + k) * 8, v);
+        if (k == 1)
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) word[b] = __funnelshift_r(word[b], word[b], 8);
       }
-      tc_st16(tmem + Tmem<N>::values + vb * 64 + two * 16, v);
     }
     unsigned long long rows = 0;
     if (edge) {
