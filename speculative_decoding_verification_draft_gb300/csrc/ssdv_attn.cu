@@ -35,7 +35,7 @@ namespace {
 constexpr int kTile = 64;        // tokens per tile: four blocks
 constexpr int kBias = 15;        // weights are at most 2^kBias
 constexpr float kLowUp = 2048.f; // the second fp16 part of a weight is held this much up
-constexpr int kTcRows = 0;       // more rows than this take ssdv_attn_tc.cu (bf16, 128 elements)
+constexpr int kTcRows = 16;      // more rows than this take ssdv_attn_tc.cu (bf16, 128 elements)
 constexpr int kSmem = 226000;    // dynamic shared memory, at most
 constexpr int kWarps = 8;        // computing warps per CTA, one CTA per SM
 constexpr int kThreads = 384;    // and four more, of which one keeps the copies going

@@ -14,12 +14,13 @@
 // shared memory would cost 512 of its cycles a tile for each product, more than
 // the tile's share of the DRAM bandwidth allows.)
 //
-// Sixteen warps with one job each, joined by mbarriers:
-//   0-3   weights: scores from tensor memory, softmax, weights to shared memory
-//   4-7   keys: codes to tensor memory
-//   8-11  values: codes to tensor memory; corrections of the sums; results
-//   12    bulk copies of the tiles' blocks   13  issues the matrix instructions
-//   14    queries   15  finds the CTA's parts of the list
+// Twenty warps with one job each, joined by mbarriers:
+//   0-7   weights: scores from tensor memory, softmax, weights to shared memory
+//         (warps 0-3 the first half of the rows, 4-7 the second)
+//   8-11  keys: codes to tensor memory
+//   12-15 values: codes to tensor memory; corrections of the sums; results
+//   16    finds the CTA's parts of the list, bulk copies of the tiles' blocks
+//   17    issues the scores' matrix instructions   18  the sums'   19  queries
 // Every buffer is double, so that a tile's scores, the tile before's weights and
 // the values of both overlap.
 //
@@ -40,7 +41,7 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kBlocks = kTile / kKvBlock;
 constexpr int kD = 128;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kFast = 9, kTop = 15;
 constexpr int kMaxStages = 8;
 constexpr float kBandUp = 536870912.f;  // 2^kBand
@@ -50,7 +51,7 @@ constexpr int kRing = 8;  // parts described ahead
 constexpr int kBlockStride = kv_block_bytes(kD) + 16;
 constexpr int kStage = kBlocks * kBlockStride;
 constexpr int kHead = 1024;
-constexpr int kSmem = 227000;
+constexpr int kSmem = 226000;
 
 // Barriers, 8 bytes each from the start of shared memory.
 enum : int {
@@ -133,6 +134,11 @@ __device__ __forceinline__ void tc_ld16(uint32_t at, float* x) {
         "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
       : "r"(at));
 }
+__device__ __forceinline__ void tc_ld8(uint32_t at, float* x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+               : "r"(at));
+}
 __device__ __forceinline__ void tc_ld4(uint32_t at, float* x) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
@@ -152,11 +158,10 @@ template <int N>
 __device__ __forceinline__ void tc_wait_ld(float* x) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < N; i += 16)
+  for (int i = 0; i < N; i += 8)
     asm volatile(""
                  : "+f"(x[i]), "+f"(x[i + 1]), "+f"(x[i + 2]), "+f"(x[i + 3]), "+f"(x[i + 4]), "+f"(x[i + 5]),
-                   "+f"(x[i + 6]), "+f"(x[i + 7]), "+f"(x[i + 8]), "+f"(x[i + 9]), "+f"(x[i + 10]), "+f"(x[i + 11]),
-                   "+f"(x[i + 12]), "+f"(x[i + 13]), "+f"(x[i + 14]), "+f"(x[i + 15]));
+                   "+f"(x[i + 6]), "+f"(x[i + 7]));
 }
 __device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&v)[16]) {
   asm volatile(
@@ -195,26 +200,23 @@ __device__ __forceinline__ uint32_t operand_byte(int row, int column) {
 }
 
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+template <int kCount = 128>
+__device__ __forceinline__ void group_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kCount) : "memory");
+}
+template <int kCount>
 __device__ __forceinline__ bool group_any(int id, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "bar.red.or.pred p, %1, 128, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      "bar.red.or.pred p, %1, %3, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(id), "r"(static_cast<uint32_t>(x))
+      : "r"(id), "r"(static_cast<uint32_t>(x)), "n"(kCount)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ float2 lds_f2(uint32_t p) {
-  const uint2 v = lds64(p);
-  return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-}
 __device__ __forceinline__ float lds_f(uint32_t p) { return __uint_as_float(lds32(p)); }
 __device__ __forceinline__ void sts_f(uint32_t p, float x) { sts32(p, __float_as_uint(x)); }
-__device__ __forceinline__ void sts16(uint32_t p, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(p), "h"(static_cast<unsigned short>(v)) : "memory");
-}
 __device__ __forceinline__ uint32_t lds16(uint32_t p) {
   unsigned short v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
@@ -268,8 +270,10 @@ struct Part {
   int b, head, pass0, first, count;  // first: among the row's tiles
   int len, nq, lo, hi, tile0;        // as in Span
   int flags;
+  int inner_lo, inner_hi;            // every row sees these positions
   static constexpr int kLater = 1, kWhole = 2, kBad = 4, kEnd = 8;
   __device__ __forceinline__ bool active() const { return hi > lo; }
+  __device__ __forceinline__ bool edge(int pos0) const { return pos0 < inner_lo || pos0 + kTile > inner_hi; }
 };
 template <int N>
 struct Ring {
@@ -277,52 +281,29 @@ struct Ring {
   Waiter& w;
   int n = 0;
   __device__ __forceinline__ Ring(uint32_t base_, Waiter& w_) : base(base_), w(w_) {}
-  // The next part; false when there is none.
-  __device__ __forceinline__ bool next(Part& p, int lane) {
-    const int at = n % kRing;
-    w.wait(kPartFull + at, n / kRing);
-    const uint32_t from = base + Smem<N>::parts + at * 64;
+  __device__ __forceinline__ Part read(int k) const {
+    const uint32_t from = base + Smem<N>::parts + k % kRing * 64;
     const uint4 x = lds128(from), y = lds128(from + 16), z = lds128(from + 32);
+    Part p;
     p.b = x.x, p.head = x.y, p.pass0 = x.z, p.first = x.w;
     p.count = y.x, p.len = y.y, p.nq = y.z, p.lo = y.w;
-    p.hi = z.x, p.tile0 = z.y, p.flags = z.z;
+    p.hi = z.x, p.tile0 = z.y, p.flags = z.z, p.inner_lo = z.w;
+    p.inner_hi = static_cast<int>(lds32(from + 48));
+    return p;
+  }
+  __device__ __forceinline__ void release(int k, int lane) {
     __syncwarp();
-    if (lane == 0) w.arrive(kPartEmpty + at);
+    if (lane == 0) w.arrive(kPartEmpty + k % kRing);
+  }
+  // The next part; false when there is none.
+  __device__ __forceinline__ bool next(Part& p, int lane, bool keep = false) {
+    w.wait(kPartFull + n % kRing, n / kRing);
+    p = read(n);
+    if (!keep) release(n, lane);
     ++n;
     return !w.dead && !(p.flags & Part::kEnd);
   }
 };
-
-template <int N>
-__device__ __forceinline__ void plan_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, Waiter w, int lane) {
-  const long long u = blockIdx.x * list.quota;
-  int left = u < list.units ? static_cast<int>(min(list.units - u, list.quota)) : 0;
-  Place<kTile> at = {};
-  if (left) at = list.find(L.a, u);
-  if (lane == 0) L.desc[blockIdx.x] = left ? list.parts(at, blockIdx.x) : make_int4(0, 0, 0, 0);
-  bool later = false;
-#pragma unroll 1
-  for (int n = 0;; ++n) {
-    const int slot = n % kRing, count = left ? min(left, at.s.tiles - at.tile) : 0;
-    const bool end = left == 0;
-    w.nap(kPartEmpty + slot, (n / kRing) ^ 1);
-    if (lane == 0) {
-      const uint32_t to = base + Smem<N>::parts + slot * 64;
-      const int flags = (later ? Part::kLater : 0) | (at.tile == 0 && count == at.s.tiles ? Part::kWhole : 0) |
-                        (at.s.bad ? Part::kBad : 0) | (end ? Part::kEnd : 0);
-      sts128(to, make_uint4(at.b, at.hr / L.p.rt, at.hr % L.p.rt * N, at.tile));
-      sts128(to + 16, make_uint4(count, at.s.len, at.s.nq, at.s.lo));
-      sts128(to + 32, make_uint4(at.s.hi, at.s.tile0, flags, 0));
-      w.arrive(kPartFull + slot);
-    }
-    if (end || w.dead) break;
-    later = true;
-    left -= count;
-    at.tile += count - 1;
-    if (left) at.next(L.a, list.per_request);
-  }
-  if (w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
-}
 
 // Which rows of a pass see the token at `pos`: [x, y).
 template <int N>
@@ -336,19 +317,42 @@ __device__ __forceinline__ int2 rows_seeing(const AttnLaunch& L, const Part& p, 
   return make_int2(max(lo, 0), static_cast<int>(max(0ll, min(hi, static_cast<long long>(N)))));
 }
 
-// ---- bulk copies (warp 12): eight lanes, a block each ----
+// ---- parts and bulk copies (warp 16): eight lanes, a block each ----
 
 template <int N>
-__device__ __forceinline__ void copy_role(const AttnLaunch& L, uint32_t base, Waiter w, int lane) {
+__device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>& list, uint32_t base, Waiter w, int lane) {
   constexpr int S = Smem<N>::kStages;
   const KvAttnArgs& a = L.a;
   const int bpp = a.c.page_size / kKvBlock;
   const long long head_bytes = static_cast<long long>(bpp) * kv_block_bytes(kD), page_bytes = head_bytes * a.c.kv_heads;
-  Ring<N> parts(base, w);
-  Part p;
+  const long long unit = blockIdx.x * list.quota;
+  int left = unit < list.units ? static_cast<int>(min(list.units - unit, list.quota)) : 0;
+  Place<kTile> place = {};
+  if (left) place = list.find(a, unit);
+  if (lane == 0) L.desc[blockIdx.x] = left ? list.parts(place, blockIdx.x) : make_int4(0, 0, 0, 0);
   int st = 0;
   uint32_t phase = 1;
-  while (parts.next(p, lane)) {
+#pragma unroll 1
+  for (int n = 0;; ++n) {
+    // the next part (the last says that there are no more)
+    Part p;
+    p.b = place.b, p.head = place.hr / L.p.rt, p.pass0 = place.hr % L.p.rt * N, p.first = place.tile;
+    p.count = min(left, place.s.tiles - place.tile), p.lo = place.s.lo, p.hi = place.s.hi, p.tile0 = place.s.tile0;
+    w.nap(kPartEmpty + n % kRing, (n / kRing) ^ 1);
+    if (lane == 0) {
+      const uint32_t to = base + Smem<N>::parts + n % kRing * 64;
+      const int flags = (n ? Part::kLater : 0) | (p.first == 0 && p.count == place.s.tiles ? Part::kWhole : 0) |
+                        (place.s.bad ? Part::kBad : 0) | (left ? 0 : Part::kEnd);
+      sts128(to, make_uint4(p.b, p.head, p.pass0, p.first));
+      sts128(to + 16, make_uint4(p.count, place.s.len, place.s.nq, p.lo));
+      sts128(to + 32, make_uint4(p.hi, p.tile0, flags, row_lo(a, place.s.len, place.s.nq - 1)));
+      sts32(to + 48, row_hi(a, place.s.len, 0));
+      w.arrive(kPartFull + n % kRing);
+    }
+    if (!left || w.dead) break;
+    left -= p.count;
+    place.tile += p.count - 1;
+    if (left) place.next(a, list.per_request);
     if (!p.active()) continue;
     const int32_t* table = a.c.page_table + static_cast<long long>(p.b) * a.c.max_pages;
     const long long head = p.head * head_bytes;
@@ -399,7 +403,7 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, uint32_t base, Wa
   }
 }
 
-// ---- queries (warp 14) ----
+// ---- queries (warp 19) ----
 
 template <int N>
 __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, Waiter w, int lane) {
@@ -457,95 +461,103 @@ __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, W
   if (w.dead && lane == 0) atomicOr(a.status, 1 << SSD_ERR_CUDA);
 }
 
-// ---- matrix instructions (warp 13; one lane issues them, the warp stays together) ----
+// ---- matrix instructions (warps 17 and 18; one lane issues them, the warp stays
+// together).  An instruction of M = 128 takes 64 cycles or more however few the
+// rows, and issuing one waits for those before. ----
+
+// D (+)= A B over 128 of the contraction: A 8 columns a step, B 32 bytes (queries)
+// or 16 rows (weights).
+template <int N, bool kRowMajor>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, bool add, bool leader) {
+  // (a broadcast is what tells the compiler that the warp agrees on a number)
+  d = __shfl_sync(~0u, d, 0), a = __shfl_sync(~0u, a, 0), b = __shfl_sync(~0u, b, 0);
+  const uint64_t operand = tc_operand(b);
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    tc_mma(d, a + s * 8, operand + (kRowMajor ? s * 128 : (s >> 2) * (N * 8) + (s & 3) * 2), tc_idesc(N, kRowMajor),
+           s > 0 || add, leader);
+}
+// The warp's instructions are done before the tensor memory goes.
+__device__ __forceinline__ void drain(const AttnLaunch& L, Waiter& w, bool leader) {
+  if (w.dead && leader) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+  tc_commit(w.bars + kDone * 8, leader);
+  bar_wait(w.bars + kDone * 8, 0);
+}
 
 template <int N>
-__device__ __forceinline__ void matrix_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int lane) {
+__device__ __forceinline__ void score_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int lane) {
   const bool leader = lane == 0;
-  // D (+)= A B over 128 of the contraction: A 8 columns a step, B 32 bytes
-  // (queries) or 16 rows (weights)
-  const auto product = [&](uint32_t d, uint32_t a, uint32_t b, bool weights, bool add) {
-    // (a broadcast is what tells the compiler that the warp agrees on a number)
-    d = __shfl_sync(~0u, d, 0), a = __shfl_sync(~0u, a, 0), b = __shfl_sync(~0u, b, 0);
-    const uint64_t operand = tc_operand(b);
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-      tc_mma(d, a + s * 8, operand + (weights ? s * 128 : (s >> 2) * (N * 8) + (s & 3) * 2), tc_idesc(N, weights),
-             s > 0 || add, leader);
-  };
   Ring<N> parts(base, w);
   Part p;
-  p.count = 0;
-  int k = 0, n_parts = 0, n_outs = 0, scored = 0, tile = 0, it = 0, fixes = 0;
-  // the scores go one tile ahead: whether there is a tile to add up, and whether
-  // it is its part's first and last
-  bool more = true, have = false, is_first = false, is_last = false;
+  int n_parts = 0, tile = 0;
+  while (parts.next(p, lane)) {
+    if (!p.active()) continue;
+    const int qb = n_parts & 1;
+    w.wait(kQueryFull + qb, n_parts >> 1);
 #pragma unroll 1
-  while (more || have) {
-    while (more && k == p.count) {
-      more = parts.next(p, lane);
-      k = more && p.active() ? 0 : p.count;
-    }
-    const bool first = k == 0, last_tile = k == p.count - 1;
-    if (more) {
-      const int sb = scored & 1, qb = n_parts & 1;
-      if (first) w.wait(kQueryFull + qb, n_parts >> 1);
-      w.wait(kKeysFull + sb, scored >> 1);
-      w.wait(kScoresEmpty + sb, (scored >> 1) ^ 1);
+    for (int k = 0; k < p.count; ++k, ++tile) {
+      const int sb = tile & 1;
+      w.wait(kKeysFull + sb, tile >> 1);
+      w.wait(kScoresEmpty + sb, (tile >> 1) ^ 1);
+      if (w.dead) continue;
       tc_fence_after();
-      if (!w.dead) {
-        product(tmem + Tmem<N>::scores + sb * N, tmem + Tmem<N>::keys + sb * 64,
-                base + Smem<N>::query + qb * Smem<N>::kQueries, false, false);
-        tc_commit(w.bars + (kScoresFull + sb) * 8, leader);
-        tc_commit(w.bars + (kKeysEmpty + sb) * 8, leader);
-        if (last_tile) tc_commit(w.bars + (kQueryEmpty + qb) * 8, leader);
-      }
-      ++scored;
-      ++k;
-      n_parts += last_tile;
+      product<N, false>(tmem + Tmem<N>::scores + sb * N, tmem + Tmem<N>::keys + sb * 64,
+                        base + Smem<N>::query + qb * Smem<N>::kQueries, false, leader);
+      tc_commit(w.bars + (kScoresFull + sb) * 8, leader);
+      tc_commit(w.bars + (kKeysEmpty + sb) * 8, leader);
     }
-    if (have) {
-      const int vb = tile & 1, ob = n_outs % Tmem<N>::kOuts;
-      const uint32_t out = tmem + Tmem<N>::outs + ob * N;
+    if (!w.dead) tc_commit(w.bars + (kQueryEmpty + qb) * 8, leader);
+    ++n_parts;
+  }
+  drain(L, w, leader);
+}
+
+template <int N>
+__device__ __forceinline__ void sum_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int lane) {
+  const bool leader = lane == 0;
+  Ring<N> parts(base, w);
+  Part p;
+  int n_parts = 0, tile = 0, it = 0, fixes = 0;
+  while (parts.next(p, lane)) {
+    if (!p.active()) continue;
+    const int ob = n_parts % Tmem<N>::kOuts;
+    const uint32_t out = tmem + Tmem<N>::outs + ob * N;
+    w.wait(kOutEmpty + ob, n_parts / Tmem<N>::kOuts + 1);
+#pragma unroll 1
+    for (int k = 0; k < p.count; ++k, ++tile) {
+      const int vb = tile & 1;
       w.wait(kValuesFull + vb, tile >> 1);
-      if (is_first) w.wait(kOutEmpty + ob, n_outs / Tmem<N>::kOuts + 1);
 #pragma unroll 1
       for (bool last = false; !last; ++it) {
         const int pb = it & 1;
         w.wait(kWeightsFull + pb, it >> 1);
         const uint32_t info = __shfl_sync(~0u, lds32(base + Smem<N>::words + pb * 4), 0), band = info >> 8;
         last = w.dead || (info & kInfoLast);
-        if (!w.dead && (info & kInfoRescale)) {
+        if (w.dead) continue;
+        if (info & kInfoRescale) {
           // the sums so far are rescaled first
           tc_commit(w.bars + kFixFull * 8, leader);
           w.wait(kFixDone, fixes++);
         }
         tc_fence_after();
-        if (!w.dead) {
-          product(band ? tmem + Tmem<N>::band : out, tmem + Tmem<N>::values + vb * 64,
-                  base + Smem<N>::weight + pb * Smem<N>::kWeights, true, band == 0 && !is_first);
-          tc_commit(w.bars + (kWeightsEmpty + pb) * 8, leader);
-          if (band) {
-            tc_commit(w.bars + kFixFull * 8, leader);
-            w.wait(kFixDone, fixes++);
-            tc_fence_after();
-          }
-          if (last) tc_commit(w.bars + (kValuesEmpty + vb) * 8, leader);
-          if (last && is_last) tc_commit(w.bars + (kOutFull + ob) * 8, leader);
+        product<N, true>(band ? tmem + Tmem<N>::band : out, tmem + Tmem<N>::values + vb * 64,
+                         base + Smem<N>::weight + pb * Smem<N>::kWeights, band == 0 && k > 0, leader);
+        tc_commit(w.bars + (kWeightsEmpty + pb) * 8, leader);
+        if (band) {
+          tc_commit(w.bars + kFixFull * 8, leader);
+          w.wait(kFixDone, fixes++);
+          tc_fence_after();
         }
+        if (last) tc_commit(w.bars + (kValuesEmpty + vb) * 8, leader);
       }
-      ++tile;
-      n_outs += is_last;
     }
-    have = more;
-    is_first = first, is_last = last_tile;
+    if (!w.dead) tc_commit(w.bars + (kOutFull + ob) * 8, leader);
+    ++n_parts;
   }
-  if (w.dead && leader) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
-  tc_commit(w.bars + kDone * 8, leader);
-  bar_wait(w.bars + kDone * 8, 0);
+  drain(L, w, leader);
 }
 
-// ---- keys (warps 4-7): lane l of warp u has token (l / 4 % 2) + 2 (l / 8) + 8 (u % 2)
+// ---- keys (warps 8-11): lane l of warp u has token (l / 4 % 2) + 2 (l / 8) + 8 (u % 2)
 // of block l % 4 + 4 (u / 2) ----
 
 template <int N>
@@ -603,13 +615,15 @@ __device__ __forceinline__ void key_role(const AttnLaunch& L, uint32_t base, uin
   if (w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
 
-// ---- weights (warps 0-3): a thread has one token of the tile, in the keys' order ----
+// ---- weights (warps 0-7): a thread has one token of the tile, in the keys' order,
+// and half of the rows ----
 
 template <int N>
 __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, uint32_t tmem, Waiter w, int warp, int lane) {
   using M = Smem<N>;
-  constexpr int kSync = 1;
-  const int tid = warp * 32 + lane;
+  constexpr int kSync = 1, kThreads = 256, H = N / 2;
+  const int tid = warp * 32 + lane, r0 = warp >> 2 ? H : 0;  // its rows begin there
+  warp &= 3;
   const int blk = (lane & 3) + 4 * (warp >> 1), t = ((lane >> 2) & 1) | ((lane >> 3) << 1) | ((warp & 1) << 3);
   const int token = blk * kKvBlock + t;
   // In the products' contraction pair p of block b comes at 16 p + 2 b: eight
@@ -630,24 +644,26 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
       sts32(fr_at(tid) + 8, 0x7F800000u);
       sts_f(base + M::maxima + tid * 4, -INFINITY);
     }
-    group_sync(kSync);
-    const int lo_last = row_lo(L.a, p.len, p.nq - 1), hi_first = row_hi(L.a, p.len, 0);
-    float l[N];
+    group_sync<kThreads>(kSync);
+    float l[H];
 #pragma unroll
-    for (int n = 0; n < N; ++n) l[n] = 0.f;
+    for (int n = 0; n < H; ++n) l[n] = 0.f;
 #pragma unroll 1
     for (int k = 0; k < p.count; ++k, ++tile) {
       const int sb = tile & 1;
       const int pos0 = (p.tile0 + p.first + k) * kTile;
-      const bool edge = pos0 < lo_last || pos0 + kTile > hi_first;
-      int2 seen = make_int2(0, N);  // rows that see the token
-      if (edge) seen = rows_seeing<N>(L, p, pos0 + token);
-      const uint32_t scores = tmem + (static_cast<uint32_t>(warp * 32) << 16) + Tmem<N>::scores + sb * N;
-      const auto put = [&](int n, const float* x) {  // rows n .. n + 7
+      const bool edge = p.edge(pos0);
+      int2 seen = make_int2(0, H);  // which of its rows see the token
+      if (edge) {
+        seen = rows_seeing<N>(L, p, pos0 + token);
+        seen.x -= r0, seen.y -= r0;
+      }
+      const uint32_t scores = tmem + (static_cast<uint32_t>(warp * 32) << 16) + Tmem<N>::scores + sb * N + r0;
+      const auto put = [&](int n, const float* x) {  // its rows n .. n + 7
         uint32_t v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = half2_bits(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
-        sts128(to + (it & 1) * M::kWeights + ((n << 1) ^ turn), make_uint4(v[0], v[1], v[2], v[3]));
+        sts128(to + (it & 1) * M::kWeights + (((r0 + n) << 1) ^ turn), make_uint4(v[0], v[1], v[2], v[3]));
       };
       w.wait(kScoresFull + sb, tile >> 1);
       tc_fence_after();
@@ -655,21 +671,22 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
       w.wait(kInfoEmpty + (it & 1), (it >> 1) ^ 1);
       bool rescaled = false;
       int bands = 0;  // passes to come
-      float u[N];
+      float u[H];
 #pragma unroll 1
       for (;;) {
         float least = 0.f, most = 0.f;
 #pragma unroll
-        for (int n = 0; n < N; n += 16) tc_ld16(scores + n, u + n);
-        tc_wait_ld<N>(u);
+        for (int n = 0; n + 16 <= H; n += 16) tc_ld16(scores + n, u + n);
+        if constexpr (H % 16 != 0) tc_ld8(scores + H / 16 * 16, u + H / 16 * 16);
+        tc_wait_ld<H>(u);
 #pragma unroll
-        for (int n = 0; n < N; n += 2) {
-          const uint4 fr = lds128(base + M::fr + n * 8);  // factors, then references of two rows
+        for (int n = 0; n < H; n += 2) {
+          const uint4 fr = lds128(base + M::fr + (r0 + n) * 8);  // factors, then references of two rows
           fma_pair(u[n], u[n + 1], fr);
         }
         if (edge) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
+          for (int n = 0; n < H; ++n) {
             const bool in = n >= seen.x && n < seen.y;
             least = fminf(least, in ? u[n] : 0.f);
             u[n] = in ? u[n] : -INFINITY;
@@ -677,39 +694,39 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
           }
         } else {
 #pragma unroll
-          for (int n = 0; n < N; n += 2) {
+          for (int n = 0; n < H; n += 2) {
             least = fminf(least, fminf(u[n], u[n + 1]));
             most = fmaxf(most, fmaxf(u[n], u[n + 1]));
           }
         }
         const bool high = most > kTop, low = least < kTop - kBand;
-        if (!group_any(kSync, high || low)) break;
-        if (rescaled || !group_any(kSync, high)) {
+        if (!group_any<kThreads>(kSync, high || low)) break;
+        if (rescaled || !group_any<kThreads>(kSync, high)) {
           // below 2^-14 fp16 keeps fewer bits: what it loses goes to later passes
           const int need = low ? static_cast<int>(fminf((kTop - least) * (1.f / kBand), kBands - 1.f)) : 0;
           const int most_needed = __reduce_max_sync(~0u, need);
           if (lane == 0 && most_needed)
             atomicMax(reinterpret_cast<int*>(__cvta_shared_to_generic(base + M::words + 8)), most_needed);
-          group_sync(kSync);
+          group_sync<kThreads>(kSync);
           bands = lds32(base + M::words + 8);
-          group_sync(kSync);
+          group_sync<kThreads>(kSync);
           if (tid == 0) sts32(base + M::words + 8, 0);
           break;
         }
         // the rows' maxima follow the tile's
 #pragma unroll 1
-        for (int n0 = 0; n0 < N; n0 += 16) {
-          float s[16], keep = -INFINITY;
-          tc_ld16(scores + n0, s);
-          tc_wait_ld<16>(s);
+        for (int n0 = 0; n0 < H; n0 += 8) {
+          float s[8], keep = -INFINITY;
+          tc_ld8(scores + n0, s);
+          tc_wait_ld<8>(s);
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
+          for (int n = 0; n < 8; ++n) {
             const float top = warp_max(!edge || (n0 + n >= seen.x && n0 + n < seen.y) ? s[n] : -INFINITY);
             if (lane == n) keep = top;
           }
-          if (lane < 16) sts_f(base + M::tops + (warp * N + n0 + lane) * 4, keep);
+          if (lane < 8) sts_f(base + M::tops + (warp * N + r0 + n0 + lane) * 4, keep);
         }
-        group_sync(kSync);
+        group_sync<kThreads>(kSync);
         if (tid < N) {
           float top = -INFINITY;
 #pragma unroll
@@ -721,13 +738,13 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
           sts_f(fr_at(tid) + 8, m == -INFINITY ? INFINITY : kFast - m);
           sts_f(base + M::fall + ((it & 1) * N + tid) * 4, old == -INFINITY ? 0.f : ex2(old - m));
         }
-        group_sync(kSync);
+        group_sync<kThreads>(kSync);
 #pragma unroll
-        for (int n = 0; n < N; ++n) l[n] *= lds_f(base + M::fall + ((it & 1) * N + n) * 4);
+        for (int n = 0; n < H; ++n) l[n] *= lds_f(base + M::fall + ((it & 1) * N + r0 + n) * 4);
         rescaled = true;
       }
 #pragma unroll
-      for (int n = 0; n < N; n += 2) {
+      for (int n = 0; n < H; n += 2) {
         u[n] = ex2(u[n]), u[n + 1] = ex2(u[n + 1]);
         add_pair(l[n], l[n + 1], u[n], u[n + 1]);
         if (n % 8 == 6) put(n - 6, u + n - 6);
@@ -750,50 +767,49 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
         w.wait(kInfoEmpty + (it & 1), (it >> 1) ^ 1);
         // what the passes before lost of weights below 2^-14, kBand octaves up each time
 #pragma unroll 1
-        for (int n0 = 0; n0 < N; n0 += 16) {
-          float s[16];
-          tc_ld16(scores + n0, s);
-          tc_wait_ld<16>(s);
+        for (int n0 = 0; n0 < H; n0 += 8) {
+          float s[8];
+          tc_ld8(scores + n0, s);
+          tc_wait_ld<8>(s);
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            const uint32_t fr = fr_at(n0 + n);
+          for (int n = 0; n < 8; ++n) {
+            const uint32_t fr = fr_at(r0 + n0 + n);
             s[n] = !edge || (n0 + n >= seen.x && n0 + n < seen.y) ? ex2(fmaf(s[n], lds_f(fr), lds_f(fr + 8))) : 0.f;
           }
 #pragma unroll 1
           for (int x = 0; x <= band; ++x)
 #pragma unroll
-            for (int n = 0; n < 16; ++n)
+            for (int n = 0; n < 8; ++n)
               s[n] = fabsf(s[n]) < kSmallest ? (s[n] - __half2float(__float2half_rn(s[n]))) * kBandUp : 0.f;
-#pragma unroll
-          for (int n = 0; n < 16; n += 8) put(n0 + n, s + n);
+          put(n0, s);
         }
       }
     }
     // the part's sums over the warp's tokens: rows are exchanged, so that each
     // step halves what a lane holds
-    int width = N, row = 0;
+    int width = H, row = r0;
 #pragma unroll
     for (int bit = 16; bit; bit >>= 1) {
       if (width % 2 == 0) {
         const int half = width / 2;
         const bool upper = lane & bit;
 #pragma unroll
-        for (int n = 0; n < N / 2; ++n)
-          if (n < half) {
-            const float mine = upper ? l[n + half] : l[n], other = upper ? l[n] : l[n + half];
+        for (int n = 0; n < H; ++n)
+          if (n < half && n + half < H) {
+            const float mine = upper ? l[n + half < H ? n + half : 0] : l[n], other = upper ? l[n] : l[n + half < H ? n + half : 0];
             l[n] = mine + __shfl_xor_sync(~0u, other, bit);
           }
         row += upper ? half : 0;
         width = half;
       } else {
 #pragma unroll
-        for (int n = 0; n < N / 2; ++n)
+        for (int n = 0; n < H; ++n)
           if (n < width) l[n] += __shfl_xor_sync(~0u, l[n], bit);
       }
     }
     w.wait(kEndEmpty, n_parts ^ 1);
 #pragma unroll
-    for (int n = 0; n < N / 2; ++n)
+    for (int n = 0; n < H; ++n)
       if (n < width) sts_f(base + M::ends + (warp * N + row + n) * 4, l[n]);
     if (tid < N) sts_f(base + M::ends + (4 * N + tid) * 4, lds_f(base + M::maxima + tid * 4));
     __syncwarp();
@@ -802,12 +818,12 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
       w.arrive(kQueryEmpty + qb);
     }
     ++n_parts;
-    group_sync(kSync);  // the maxima are read before the next part clears them
+    group_sync<kThreads>(kSync);  // the maxima are read before the next part clears them
   }
   if (w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
 
-// ---- values (warps 8-11): a thread has one element of a head ----
+// ---- values (warps 12-15): a thread has one element of a head ----
 
 template <int N>
 struct Values {
@@ -1011,17 +1027,19 @@ __device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, u
   constexpr int S = Smem<N>::kStages;
   Values<N> v(L, base, tmem, w, warp, lane);
   Ring<N> parts(base, v.w);
-  Part p, prev = {};
+  Part p;
   p.count = 0;
   int st = 0, tile = 0, k = 0;
   uint32_t phase = 0;
-  // values go one tile ahead of the weights
-  bool more = true, pending = false, first = false, ends = false, lost = false, prev_lost = false;
+  // values go one tile ahead of the weights: `pending` of the tile before, whether
+  // it was its part's first and last, and what to know of that part
+  bool more = true, pending = false, first = false, ends = false, active = false, lost = false, prev_lost = false;
+  int prev = 0;
   unsigned long long nans = 0, prev_nans = 0;
 #pragma unroll 1
   while (more || pending) {
     if (more && k == p.count) {
-      more = parts.next(p, lane);
+      more = parts.next(p, lane, true);  // (kept until its results are written)
       k = 0;
       lost = false;
       nans = 0;
@@ -1029,23 +1047,28 @@ __device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, u
     const bool have = more && p.active();
     if (have) {
       const int pos0 = (p.tile0 + p.first + k) * kTile;
-      const bool edge = pos0 < row_lo(L.a, p.len, p.nq - 1) || pos0 + kTile > row_hi(L.a, p.len, 0);
       v.w.wait(kFull + st, phase);
       lost |= lds32(base + Smem<N>::words + 16 + st * 4) != 0;
-      nans |= v.unpack(st, tile & 1, tile, pos0, edge, p);
+      nans |= v.unpack(st, tile & 1, tile, pos0, p.edge(pos0), p);
       if (++st == S) st = 0, phase ^= 1;
       ++tile;
     }
-    // (a part without tiles, whose count is one, has only its results: zeros, or
-    // NaN for bad lengths)
-    if (pending && prev.active()) v.follow(first);
-    if (pending && ends) v.finish(prev, prev_lost, prev_nans);
+    if (pending) {
+      // (a part without tiles, whose count is one, has only its results: zeros, or
+      // NaN for bad lengths)
+      if (active) v.follow(first);
+      if (ends) {
+        v.finish(parts.read(prev), prev_lost, prev_nans);
+        parts.release(prev, lane);
+      }
+    }
     pending = more;
     if (more) {
       first = k == 0;
       ++k;
       ends = k == p.count;
-      prev = p;
+      active = have;
+      prev = parts.n - 1;
       prev_lost = lost;
       prev_nans = nans;
     }
@@ -1063,17 +1086,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
     // how many warps (or commits) arrive
     int count = 1;
     if (tid >= kEmpty && tid < kKeysFull) count = 8;
-    if ((tid >= kKeysFull && tid < kKeysEmpty) || (tid >= kScoresEmpty && tid < kWeightsEmpty) ||
-        (tid >= kValuesFull && tid < kValuesEmpty) || (tid >= kOutEmpty && tid < kQueryFull) || tid == kEndFull ||
-        tid == kEndEmpty || tid == kFixDone)
+    if ((tid >= kKeysFull && tid < kKeysEmpty) || (tid >= kValuesFull && tid < kValuesEmpty) ||
+        (tid >= kOutEmpty && tid < kQueryFull) || tid == kEndEmpty || tid == kFixDone)
       count = 4;
-    if (tid >= kQueryEmpty && tid < kEndFull) count = 5;
-    if (tid >= kPartEmpty) count = 15;
+    if ((tid >= kScoresEmpty && tid < kWeightsEmpty) || tid == kEndFull) count = 8;
+    if (tid >= kQueryEmpty && tid < kEndFull) count = 9;
+    if (tid == kDone) count = 2;
+    if (tid >= kPartEmpty) count = 19;
     bar_init(base + tid * 8, count);
   }
   if (tid < kMaxStages) sts32(words + 16 + tid * 4, 0);
   if (tid == 0) sts32(words + 8, 0);
-  if (warp == 13) {
+  if (warp == 17) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(words + 12) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -1085,26 +1109,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
   const uint32_t tmem = lds32(words + 12);
   Waiter w;
   w.bars = base;
-  // 128 x (184 + 96 + 120 + 112) registers: the 512 x 128 of the launch
-  if (warp < 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+  // 128 x (112 + 112 + 72 + 96 + 88) registers: the 640 x 96 of the launch
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     weight_role<N>(L, base, tmem, w, warp, lane);
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    key_role<N>(L, base, tmem, w, warp - 4, lane);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    value_role<N>(L, base, tmem, w, warp - 8, lane);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    key_role<N>(L, base, tmem, w, warp - 8, lane);
+  } else if (warp < 16) {
+    value_role<N>(L, base, tmem, w, warp - 12, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-    if (warp == 12) copy_role<N>(L, base, w, lane);
-    else if (warp == 13) matrix_role<N>(L, base, tmem, w, lane);
-    else if (warp == 14) query_role<N>(L, base, w, lane);
-    else plan_role<N>(L, list, base, w, lane);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 16) copy_role<N>(L, list, base, w, lane);
+    else if (warp == 17) score_role<N>(L, base, tmem, w, lane);
+    else if (warp == 18) sum_role<N>(L, base, tmem, w, lane);
+    else query_role<N>(L, base, w, lane);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == 17) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
