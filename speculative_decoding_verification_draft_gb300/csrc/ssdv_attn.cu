@@ -921,7 +921,7 @@ cudaError_t launch_join(const AttnLaunch& L, int sms, cudaStream_t s) {
 template <typename E, int D, int NT, int P>
 cudaError_t launch_shape(const AttnLaunch& L, int sms, cudaStream_t s) {
   const int smem = kHead + L.p.t * (L.p.s * stage_bytes(D) + (P == 2 ? L.p.g * pair_bytes(D, NT, sizeof(E) == 4) : 0));
-  cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<E, D, NT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared<kv_attention_kernel<E, D, NT, P>>(kSmem);
   if (e != cudaSuccess) return e;
   kv_attention_kernel<E, D, NT, P><<<sms, kThreads, smem, s>>>(L);
   e = cudaGetLastError();

@@ -11,6 +11,8 @@
 
 #include "ssdv_kv.cuh"
 
+#include <atomic>
+
 namespace ssdv {
 
 constexpr int kBand = 29;        // octaves below that in which fp16 keeps 11 bits
@@ -42,6 +44,18 @@ cudaError_t launch_attention_tc(const AttnLaunch& L, int sms, cudaStream_t strea
 #ifdef __CUDACC__
 
 namespace {
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device.
+template <auto kKernel>
+cudaError_t allow_shared(int bytes) {
+  static std::atomic<unsigned long long> known{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (known.load() >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) known.fetch_or(1ull << dev);
+  return e;
+}
 
 // ---- mbarriers and bulk copies ----
 

@@ -95,7 +95,7 @@ struct Smem {
   static constexpr int fall = tops + 16 * N;            // [2][N]
   static constexpr int factors = fall + 8 * N;          // [2][N]
   static constexpr int ends = factors + 8 * N;          // [4][N] sums, [N] maxima
-  static constexpr int rows = ends + 20 * N;            // [N] a finished row's place (8 bytes) and factor
+  static constexpr int rows = ends + 20 * N;            // [N] a finished row's address, factor and type
   static constexpr int parts = rows + 16 * N;           // [kRing] 64 bytes
   static constexpr int words = parts + 64 * kRing;           // info [2], bands, tensor memory address, flags [8]
   static constexpr int stages = (words + 64 + 127) / 128 * 128;
@@ -753,7 +753,7 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
       for (int band = 0;; ++band) {
         if (tid == 0)
           sts32(base + M::words + (it & 1) * 4,
-                (rescaled && band == 0 ? kInfoRescale : 0) | (band == bands ? kInfoLast : 0) | (band << 8));
+                (rescaled && band == 0 && k > 0 ? kInfoRescale : 0) | (band == bands ? kInfoLast : 0) | (band << 8));
         async_fence();
         tc_fence_before();
         __syncwarp();
@@ -914,7 +914,7 @@ struct Values {
   }
 
   // Follows a tile's weights: corrects the sums where the tile asks for it.
-  __device__ __forceinline__ void follow(bool first) {
+  __device__ __forceinline__ void follow() {
 #pragma unroll 1
     for (bool last = false; !last; ++it) {
       const int ib = it & 1;
@@ -927,21 +927,19 @@ struct Values {
         tc_fence_after();
         const uint32_t out = tmem + Tmem<N>::outs + n_parts % Tmem<N>::kOuts * N;
         const float up = band ? ex2(static_cast<float>(-kBand * band)) : 0.f;
-        if (band || !first) {
 #pragma unroll 1
-          for (int n = 0; n < N; n += 4) {
-            float x[4], t[4];
-            tc_ld4(out + n, x);
-            tc_ld4(tmem + (band ? Tmem<N>::band + n : Tmem<N>::outs), t);
-            tc_wait_ld4(x);
-            tc_wait_ld4(t);
+        for (int n = 0; n < N; n += 4) {
+          float x[4], t[4];
+          tc_ld4(out + n, x);
+          tc_ld4(tmem + (band ? Tmem<N>::band + n : Tmem<N>::outs), t);
+          tc_wait_ld4(x);
+          tc_wait_ld4(t);
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              x[y] = band ? fmaf(t[y], up, x[y]) : x[y] * lds_f(base + M::fall + (ib * N + n + y) * 4);
-            tc_st4(out + n, x);
-          }
-          tc_wait_st();
+          for (int y = 0; y < 4; ++y)
+            x[y] = band ? fmaf(t[y], up, x[y]) : x[y] * lds_f(base + M::fall + (ib * N + n + y) * 4);
+          tc_st4(out + n, x);
         }
+        tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) w.arrive(kFixDone);
@@ -962,7 +960,7 @@ struct Values {
       w.wait(kOutFull + ob, n_parts / Tmem<N>::kOuts);
       tc_fence_after();
     }
-    // a thread per row: where it goes (in halves of a part, or -1) and its factor
+    // a thread per row: where it goes, and its factor
     if (tid < N) {
       const int row = q.pass0 + tid;
       long long at = -1;
@@ -987,26 +985,30 @@ struct Values {
           L.ml[at] = make_float2(m, l * f);
         }
       }
-      sts64(rows + tid * 16, make_uint2(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32)));
-      sts64(rows + tid * 16 + 8, make_uint2(__float_as_uint(f), whole || row >= nrows));
+      const bool half = whole || row >= nrows;  // bf16 results; else fp32 sums
+      const unsigned long long to = at < 0 ? 0 : half ? reinterpret_cast<unsigned long long>(a.out) + at * (kD * 2)
+                                                      : reinterpret_cast<unsigned long long>(L.o) + at * (kD * 4);
+      sts128(rows + tid * 16, make_uint4(static_cast<uint32_t>(to), static_cast<uint32_t>(to >> 32), __float_as_uint(f), half));
     }
     group_sync(kSync);
 #pragma unroll 1
-    for (int n0 = 0; n0 < N; n0 += 4) {
-      float o[4] = {};
+    for (int n0 = 0; n0 < N; n0 += 16) {
+      float o[16] = {};
       if (active) {
-        tc_ld4(tmem + Tmem<N>::outs + ob * N + n0, o);
-        tc_wait_ld4(o);
+        tc_ld16(tmem + Tmem<N>::outs + ob * N + n0, o);
+        tc_wait_ld<16>(o);
       }
+      if (nans)
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < 16; ++y) o[y] = nans >> (n0 + y) & 1 ? __int_as_float(0x7FC00000) : o[y];
+#pragma unroll
+      for (int y = 0; y < 16; ++y) {
         const uint4 r = lds128(rows + (n0 + y) * 16);
-        const long long at = static_cast<long long>(r.x | static_cast<unsigned long long>(r.y) << 32);
-        const float f = __uint_as_float(r.z), x = nans >> (n0 + y) & 1 ? __int_as_float(0x7FC00000) : o[y];
-        const float z = f == 0.f ? 0.f : x * f;
-        if (at >= 0) {
-          if (r.w) static_cast<__nv_bfloat16*>(a.out)[at * kD + element] = static_cast<__nv_bfloat16>(z);
-          else L.o[at * kD + element] = z;
+        const unsigned long long to = r.x | static_cast<unsigned long long>(r.y) << 32;
+        const float f = __uint_as_float(r.z), z = f == 0.f ? 0.f : o[y] * f;
+        if (to) {
+          if (r.w) reinterpret_cast<__nv_bfloat16*>(to)[element] = static_cast<__nv_bfloat16>(z);
+          else reinterpret_cast<float*>(to)[element] = z;
         }
       }
     }
@@ -1032,8 +1034,8 @@ __device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, u
   int st = 0, tile = 0, k = 0;
   uint32_t phase = 0;
   // values go one tile ahead of the weights: `pending` of the tile before, whether
-  // it was its part's first and last, and what to know of that part
-  bool more = true, pending = false, first = false, ends = false, active = false, lost = false, prev_lost = false;
+  // it was its part's last, and what to know of that part
+  bool more = true, pending = false, ends = false, active = false, lost = false, prev_lost = false;
   int prev = 0;
   unsigned long long nans = 0, prev_nans = 0;
 #pragma unroll 1
@@ -1056,7 +1058,7 @@ __device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, u
     if (pending) {
       // (a part without tiles, whose count is one, has only its results: zeros, or
       // NaN for bad lengths)
-      if (active) v.follow(first);
+      if (active) v.follow();
       if (ends) {
         v.finish(parts.read(prev), prev_lost, prev_nans);
         parts.release(prev, lane);
@@ -1064,7 +1066,6 @@ __device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, u
     }
     pending = more;
     if (more) {
-      first = k == 0;
       ++k;
       ends = k == p.count;
       active = have;
@@ -1135,8 +1136,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
 
 template <int N>
 cudaError_t launch_n(const AttnLaunch& L, int sms, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(kv_attention_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Smem<N>::total);
+  const cudaError_t e = allow_shared<kv_attention_tc_kernel<N>>(Smem<N>::total);
   if (e != cudaSuccess) return e;
   kv_attention_tc_kernel<N><<<sms, kThreads, Smem<N>::total, stream>>>(L);
   return cudaGetLastError();

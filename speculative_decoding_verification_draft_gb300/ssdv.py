@@ -11,7 +11,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -426,8 +428,14 @@ def cache_check(bonus_topk: torch.Tensor, out_tokens: torch.Tensor, n_accepted: 
 
 KV_BLOCK = 16  # tokens per block of a cache page, elements per scale
 _kv_ws_cache = {}
+_HERE = contextlib.nullcontext()
+# Small calls take a few microseconds on the GPU, so the binding of the cache calls
+# packs its structures itself and asks torch as little as it can.
+_KV_CACHE = struct.Struct("PqiiiiP")  # KvCacheStruct
+_KV_STRIDES = struct.Struct("qqq")
 
 
+@functools.lru_cache(maxsize=None)
 def kv_workspace_bytes(n_q: int = 0, n_heads: int = 0, n_kv_heads: int = 0, head_dim: int = 0) -> int:
     return int(lib().ssd_kv_workspace_bytes(n_q, n_heads, n_kv_heads, head_dim))
 
@@ -451,61 +459,63 @@ def make_kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, page_size: int =
 
 
 def _kv_cache(cache: torch.Tensor, page_table: torch.Tensor, B: int):
+    """(packed ssd_kv_cache, n_kv_heads, head_dim)"""
     ptr = _dev(cache, "cache", torch.uint8)
     table = _dev(page_table, "page_table", torch.int32)
-    if cache.dim() != 4 or cache.shape[3] % 18:
+    shape, width = cache.shape, page_table.shape
+    if len(shape) != 4 or shape[3] % 18:
         raise ValueError("cache must be [n_pages, n_kv_heads, page_size / 16, 18 * head_dim] (make_kv_cache)")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table must be [{B}, max_pages], got {list(page_table.shape)}")
-    n_pages, heads, blocks, block = cache.shape
-    return KvCacheStruct(ptr, n_pages, heads, block // 18, blocks * KV_BLOCK, page_table.shape[1], table)
+    if len(width) != 2 or width[0] != B:
+        raise ValueError(f"page_table must be [{B}, max_pages], got {list(width)}")
+    n_pages, heads, blocks, block = shape
+    dim = block // 18
+    return _KV_CACHE.pack(ptr, n_pages, heads, dim, blocks * KV_BLOCK, width[1], table), heads, dim
 
 
 def _kv_counts(t: Optional[torch.Tensor], name: str, B: int):
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != B:
+    if t.shape != (B,):
         raise ValueError(f"{name} must be [{B}], got {list(t.shape)}")
     return _dev(t, name, torch.int32)
 
 
 def _kv_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int):
-    """Pointer and strides of [B, n, heads, head_dim] rows: any strides but the last."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    """Pointer and packed strides of [B, n, heads, head_dim] rows: any strides but the last."""
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dim() != 4 or t.shape[3] != dim or (heads is not None and t.shape[2] != heads):
-        raise ValueError(f"{name} must be [B, n, {heads or 'n_heads'}, {dim}], got {list(t.shape)}")
-    st = t.stride()
+    shape, st = t.shape, t.stride()
+    if len(shape) != 4 or shape[3] != dim or (heads is not None and shape[2] != heads):
+        raise ValueError(f"{name} must be [B, n, {heads or 'n_heads'}, {dim}], got {list(shape)}")
     if st[3] != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return t.data_ptr(), (ctypes.c_int64 * 3)(st[0], st[1], st[2])
+    return t.data_ptr(), _KV_STRIDES.pack(st[0], st[1], st[2])
 
 
 def _kv_stream(stream, device):
-    """(raw stream, context that makes it current): outputs and workspaces are
+    """(raw stream, context that makes it current, or None): outputs and workspaces are
     allocated on the stream that uses them."""
+    current = torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
+        return current, None
     raw = _stream(stream)
-    if stream is None or raw == torch.cuda.current_stream(device).cuda_stream:
-        return raw, contextlib.nullcontext()
+    if raw == current:
+        return raw, None
     return raw, torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                                   else torch.cuda.ExternalStream(raw, device=device))
 
 
-def _kv_workspace(need: int, device, raw: int, given: Optional[torch.Tensor]):
-    if given is not None:
-        return given
+def _kv_workspace(need: int, device, raw: int):
+    """The stream's own workspace (called with the stream current)."""
     if need == 0:
         return torch.empty(16, dtype=torch.uint8, device=device)  # the call names the bad argument
-    if torch.cuda.is_current_stream_capturing():
+    ws = _kv_ws_cache.get((device.index, raw))
+    if torch._C._cuda_isCurrentStreamCapturing():
         # a graph keeps its own workspace: the cached one may be replaced by a larger
         return torch.zeros(need, dtype=torch.uint8, device=device)
-    key = (device.index, raw)
-    ws = _kv_ws_cache.get(key)
     if ws is None or ws.numel() < need:
         ws = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        _kv_ws_cache[key] = ws
+        _kv_ws_cache[(device.index, raw)] = ws
     return ws
 
 
@@ -522,19 +532,20 @@ def kv_append(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tenso
     """ssd_kv_append: write k, v [B, n, n_kv_heads, head_dim] (bf16 or fp32, any strides but the last) at positions
     kv_len[b] .. kv_len[b] + n_new[b] - 1.  kv_len is not changed."""
     B, n = k.shape[:2]
-    c = _kv_cache(cache, page_table, B)
-    kp, ks = _kv_rows(k, "k", c.n_kv_heads, c.head_dim)
-    vp, vs = _kv_rows(v, "v", c.n_kv_heads, c.head_dim)
+    c, heads, dim = _kv_cache(cache, page_table, B)
+    kp, ks = _kv_rows(k, "k", heads, dim)
+    vp, vs = _kv_rows(v, "v", heads, dim)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must have one shape and dtype")
     lens, news = _kv_counts(kv_len, "kv_len", B), _kv_counts(n_new, "n_new", B)
     if B == 0 or n == 0:
         return
     raw, ctx = _kv_stream(stream, cache.device)
-    with ctx:
-        ws = _kv_workspace(256, cache.device, raw, workspace)
-    _check(lib().ssd_kv_append(ctypes.byref(c), lens, news, kp, ks, vp, vs, _dtype_code(k), B, n,
-                               _dev(ws, "workspace"), ws.numel(), raw))
+    ws = workspace
+    if ws is None:
+        with ctx or _HERE:
+            ws = _kv_workspace(256, cache.device, raw)
+    _check(lib().ssd_kv_append(c, lens, news, kp, ks, vp, vs, _dtype_code(k), B, n, _dev(ws, "workspace"), ws.numel(), raw))
 
 
 def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, n: int, dtype=torch.bfloat16,
@@ -542,20 +553,22 @@ def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, 
     """ssd_kv_read: (k, v) [B, n, n_kv_heads, head_dim], the values held for positions start[b] .. start[b] +
     count[b] - 1 (rows past count[b] are zero); out: a pair of tensors to write them to."""
     B = page_table.shape[0]
-    c = _kv_cache(cache, page_table, B)
+    c, heads, dim = _kv_cache(cache, page_table, B)
     starts, counts = _kv_counts(start, "start", B), _kv_counts(count, "count", B)
-    shape = (B, int(n), c.n_kv_heads, c.head_dim)
-    raw, ctx = _kv_stream(stream, cache.device)
-    with ctx:
-        k, v = out if out is not None else (torch.empty(shape, dtype=dtype, device=cache.device),
-                                            torch.empty(shape, dtype=dtype, device=cache.device))
-        ws = _kv_workspace(256, cache.device, raw, workspace)
-    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != v.dtype:
+    shape, device = (B, int(n), heads, dim), cache.device
+    raw, ctx = _kv_stream(stream, device)
+    ws = workspace
+    with ctx or _HERE:
+        k, v = out if out is not None else (torch.empty(shape, dtype=dtype, device=device),
+                                            torch.empty(shape, dtype=dtype, device=device))
+        if ws is None:
+            ws = _kv_workspace(256, device, raw)
+    if k.shape != shape or v.shape != shape or k.dtype != v.dtype:
         raise ValueError(f"out must be two tensors {list(shape)} of one dtype")
     if B == 0 or n == 0:
         return k, v
-    _check(lib().ssd_kv_read(ctypes.byref(c), starts, counts, _dtype_code(k), B, int(n), _dev(k, "out k"),
-                             _dev(v, "out v"), _dev(ws, "workspace"), ws.numel(), raw))
+    _check(lib().ssd_kv_read(c, starts, counts, _dtype_code(k), B, int(n), _dev(k, "out k"), _dev(v, "out v"),
+                             _dev(ws, "workspace"), ws.numel(), raw))
     return k, v
 
 
@@ -566,26 +579,28 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
     """ssd_kv_attention: q [B, n, n_heads, head_dim] (bf16 or fp32, any strides but the last), query i of request b at
     position kv_len[b] + i.  scale defaults to head_dim ** -0.5.  Returns out like q, contiguous, or (out, lse
     [B, n, n_heads] float32) with return_lse (or a given lse)."""
-    B, n, heads = q.shape[:3]
-    c = _kv_cache(cache, page_table, B)
-    qp, qs = _kv_rows(q, "q", None, c.head_dim)
+    shape, device = q.shape, cache.device
+    B, n, heads = shape[:3]
+    c, kv_heads, dim = _kv_cache(cache, page_table, B)
+    qp, qs = _kv_rows(q, "q", None, dim)
     lens, counts = _kv_counts(kv_len, "kv_len", B), _kv_counts(n_q, "n_q", B)
-    raw, ctx = _kv_stream(stream, cache.device)
-    with ctx:
+    raw, ctx = _kv_stream(stream, device)
+    ws = workspace
+    with ctx or _HERE:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty(shape, dtype=q.dtype, device=device)
         if lse is None and return_lse:
-            lse = torch.empty(B, n, heads, dtype=torch.float32, device=q.device)
-        if workspace is None and B and n:
-            workspace = _kv_workspace(kv_workspace_bytes(n, heads, c.n_kv_heads, c.head_dim), cache.device, raw, None)
-    if out.shape != q.shape or (lse is not None and tuple(lse.shape) != (B, n, heads)):
+            lse = torch.empty((B, n, heads), dtype=torch.float32, device=device)
+        if ws is None and B and n:
+            ws = _kv_workspace(kv_workspace_bytes(n, heads, kv_heads, dim), device, raw)
+    if out.shape != shape or (lse is not None and lse.shape != (B, n, heads)):
         raise ValueError("out must be shaped like q and lse [B, n, n_heads]")
     if B and n:
-        _check(lib().ssd_kv_attention(ctypes.byref(c), lens, counts, qp, qs, _dtype_code(q), B, n, heads,
-                                      float(scale) if scale is not None else c.head_dim ** -0.5, int(window),
-                                      int(past_only), _dev(out, "out", q.dtype),
+        _check(lib().ssd_kv_attention(c, lens, counts, qp, qs, _dtype_code(q), B, n, heads,
+                                      float(scale) if scale is not None else dim ** -0.5, int(window), int(past_only),
+                                      _dev(out, "out", q.dtype),
                                       _dev(lse, "lse", torch.float32) if lse is not None else None,
-                                      _dev(workspace, "workspace"), workspace.numel(), raw))
+                                      _dev(ws, "workspace"), ws.numel(), raw))
     return (out, lse) if lse is not None else out
 
 
