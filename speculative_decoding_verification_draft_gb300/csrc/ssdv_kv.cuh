@@ -129,10 +129,11 @@ __device__ __forceinline__ float kv_scale(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
-// max|x| / 7 to the scale byte (x without NaN).
+// max|x| / 7 to the scale byte (x without NaN).  The quotient is taken with 1/7 in
+// two terms, good to 2^-47: a tie of the scale's 4 bits comes out exactly.
 __device__ __forceinline__ uint32_t kv_scale_byte(float amax) {
-  const float f = amax / 7.0f;
-  if (f >= 240.0f) return kKvMaxScaleByte;
+  constexpr float kSeventh = 1.0f / 7.0f, kRest = static_cast<float>(1.0 / 7.0 - kSeventh);
+  const float x = fminf(amax, 1680.0f), f = fmaf(x, kSeventh, x * kRest);
   if (f < 6.103515625e-05f)  // below 2^-14: multiples of 2^-17 (64 has that ulp)
     return __float_as_uint(f + 64.0f) - __float_as_uint(64.0f);
   const uint32_t u = __float_as_uint(f);
