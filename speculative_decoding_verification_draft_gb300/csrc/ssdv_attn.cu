@@ -35,10 +35,17 @@ namespace {
 constexpr int kTile = 64;        // tokens per tile: four blocks
 constexpr int kBias = 15;        // weights are at most 2^kBias
 constexpr float kLowUp = 2048.f; // the second fp16 part of a weight is held this much up
-constexpr int kTcRows = 16;      // more rows than this take ssdv_attn_tc.cu (bf16, 128 elements)
+// More rows than this take ssdv_attn_tc.cu (bf16, 128 elements).  64 requests of 8
+// kv heads, here against there: 20 rows 51 / 60 us for 500 tokens, 188 / 169 for
+// 4000, 117 / 160 for 201 to 8003; 30 rows 64 / 58 and 241 / 180; 40 rows 93 / 64
+// and 319 / 208.
+constexpr int kTcRows = 24;
 constexpr int kSmem = 226000;    // dynamic shared memory, at most
 constexpr int kWarps = 8;        // computing warps per CTA, one CTA per SM
 constexpr int kThreads = 384;    // and four more, of which one keeps the copies going
+// Beginning and ending a row's tiles costs as much as this many (64 requests of 201
+// to 8003 tokens, 20 rows: 143 us at 0, 127 at 1, 117 at 2, 121 at 4).
+constexpr int kPartTiles = 2;
 constexpr int kMaxStages = 48;   // per CTA
 constexpr int kHead = 1024;      // before the stages: 16 bytes of barriers and a flag per stage
 
@@ -621,9 +628,10 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List<kTile>& 
   const int S = L.p.s, RT = L.p.rt, team = lane >> 2;
   const int bpp = a.c.page_size / kKvBlock;
   const long long head_bytes = static_cast<long long>(bpp) * kv_block_bytes(D), page_bytes = head_bytes * a.c.kv_heads;
-  const long long u = (static_cast<long long>(blockIdx.x) * L.p.t + team) * list.quota;
-  int left = team < L.p.t && u < list.units ? static_cast<int>(min(list.units - u, list.quota)) : 0;
-  Place<kTile> pr = {};
+  typename List<kTile>::Share share = {};
+  if (team < L.p.t) share = list.share(a, static_cast<long long>(blockIdx.x) * L.p.t + team);
+  int left = share.count;
+  Place<kTile> pr = share.at;
   int put = 0, phase = 1;     // empty stages at first
   int sub = 0, column = 0;    // this lane's block: of which page column, and where in the page
   int page = 0;
@@ -639,7 +647,6 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List<kTile>& 
     if (want) page = a.c.page_table[static_cast<long long>(pr.b) * a.c.max_pages + column];
   };
   if (left) {
-    pr = list.find(a, u);
     locate();
     fetch_page();
   }
@@ -694,18 +701,15 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
   const int team = warp / (P * G), group = warp / P % G, pw = warp % P;
   const int sync = 1 + warp / P;  // the pair's barrier
   const long long me = static_cast<long long>(blockIdx.x) * T + team;
-  const long long u_begin = me * list.quota, u_end = min(list.units, u_begin + list.quota);
+  const typename List<kTile>::Share share = list.share(a, me);
   const bool first_warp = group == 0 && pw == 0;
-  if (u_begin >= u_end) {
-    if (first_warp && lane == 0) L.desc[me] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  Place<kTile> at = list.find(a, u_begin);
-  if (first_warp && lane == 0) L.desc[me] = list.parts(at, me);
+  if (first_warp && lane == 0) L.desc[me] = list.parts(share, me);
+  if (share.count == 0) return;
+  Place<kTile> at = share.at;
   W w;
   w.place(lane, pw,
           P == 2 ? data + T * S * stage_bytes(D) + (warp / P) * pair_bytes(D, NT, W::kF32) : 0u, spans);
-  const int n_tiles = static_cast<int>(u_end - u_begin);
+  const int n_tiles = share.count;
   int take = 0, phase = 0, buf = 0;
   int done = 0;
   bool dead = false;  // a copy did not arrive in time: go through the motions, without waiting
@@ -849,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const __grid_
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   List<kTile> list;
-  list.build(a, a.c.kv_heads * L.p.rt, gridDim.x * L.p.t, scan, sums);
+  list.build(a, a.c.kv_heads * L.p.rt, gridDim.x * L.p.t, kPartTiles, scan, sums);
   // 128 x (224 + 224 + 56) registers: the 384 x 168 of the launch
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");

@@ -219,41 +219,71 @@ struct Place {
   }
 };
 
-// The CTA's view of the list: prefix sums of the requests' tiles.
+// The CTA's view of the list: prefix sums of the requests' tiles.  Beginning and
+// ending a row's tiles costs a team about as much as `extra` tiles, so that many
+// units without work come before each row's tiles, and teams share units evenly.
 template <int kTile>
 struct List {
   const long long* scan;
-  int chunk, threads, per_request;
-  long long units, quota;
-  // The place of unit u, and the first unit of its request's tiles.
-  __device__ __forceinline__ Place<kTile> find(const KvAttnArgs& a, long long u) const {
+  int chunk, threads, per_request, requests, extra;
+  long long units, quota, tiles;
+  struct Share {
+    Place<kTile> at;   // its first tile
+    int count;         // how many tiles
+    int row_unit;      // unit where it begins, from that of the row's first tile
+  };
+
+  // The first tile at or after unit u < units, and how many come before it in the list.
+  __device__ __forceinline__ Place<kTile> find(const KvAttnArgs& a, long long u, long long& rank, int& row_unit) const {
+    const auto first = [&](int t) { return (scan[t] + static_cast<long long>(extra) * t * chunk) * per_request; };
     int lo = 0, hi = threads - 1;  // last thread whose requests begin at or before u
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (scan[mid] * per_request <= u && mid * chunk < a.B) lo = mid;
+      if (mid * chunk < requests && first(mid) <= u) lo = mid;
       else hi = mid - 1;
     }
     Place<kTile> at;
     at.b = lo * chunk;
-    long long u0 = scan[lo] * per_request;
+    long long u0 = first(lo);
+    rank = scan[lo] * per_request;
     at.s = find_span<kTile>(a, at.b);
-    while (u0 + static_cast<long long>(at.s.tiles) * per_request <= u) {
-      u0 += static_cast<long long>(at.s.tiles) * per_request;
+    for (;;) {
+      const long long mine = static_cast<long long>(at.s.tiles) * per_request;
+      if (u0 + mine + static_cast<long long>(extra) * per_request > u) break;
+      u0 += mine + static_cast<long long>(extra) * per_request;
+      rank += mine;
       at.s = find_span<kTile>(a, ++at.b);
     }
     const long long k = u - u0;
-    at.hr = static_cast<int>(k / at.s.tiles);
-    at.tile = static_cast<int>(k % at.s.tiles);
+    at.hr = static_cast<int>(k / (at.s.tiles + extra));
+    row_unit = static_cast<int>(k % (at.s.tiles + extra)) - extra;
+    at.tile = max(row_unit, 0);
+    rank += static_cast<long long>(at.hr) * at.s.tiles + at.tile;
     return at;
+  }
+  // A team's tiles.
+  __device__ __forceinline__ Share share(const KvAttnArgs& a, long long me) const {
+    Share x = {};
+    const long long begin = me * quota;
+    if (begin >= units) return x;
+    long long rank, end = tiles;
+    int unused;
+    x.at = find(a, begin, rank, x.row_unit);
+    if (extra == 0) end = min(units, begin + quota);
+    else if (begin + quota < units) find(a, begin + quota, end, unused);
+    x.count = static_cast<int>(end - rank);
+    return x;
   }
 
   // All threads of the CTA; ends with a barrier.  `sums` holds a number per warp.
-  __device__ __forceinline__ void build(const KvAttnArgs& a, int heads_passes, int teams, long long* scan_, long long* sums) {
+  __device__ __forceinline__ void build(const KvAttnArgs& a, int heads_passes, int teams, int extra_, long long* scan_,
+                                        long long* sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     scan = scan_;
     threads = blockDim.x;
     chunk = (a.B + threads - 1) / threads;
     per_request = heads_passes;
+    requests = a.B;
     long long mine = 0;
 #pragma unroll 1
     for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) mine += find_span<kTile>(a, b).tiles;
@@ -272,17 +302,21 @@ struct List {
     }
     scan_[tid] = before + x - mine;
     __syncthreads();
-    units = total * per_request;
+    tiles = total * per_request;
+    // (with few tiles a team, whole tiles count for more than the beginnings do)
+    extra = static_cast<int>(min(static_cast<long long>(extra_), tiles / teams / 2));
+    units = tiles + static_cast<long long>(extra) * requests * per_request;
     quota = (units + teams - 1) / teams;
   }
   // What a team writes about the parts it begins with: the first team to begin
-  // inside a row's tiles has that row's parts joined.
-  __device__ __forceinline__ int4 parts(const Place<kTile>& at, long long me) const {
-    const long long seg = me * quota - at.tile, prev = seg / quota;
-    int4 d = make_int4(at.b, at.hr, 0, 0);
-    if (at.tile > 0 && prev == me - 1) {
-      d.z = static_cast<int>((seg + at.s.tiles - 1) / quota - prev + 1);
-      d.w = static_cast<int>(2 * prev + (seg > prev * quota ? 1 : 0));
+  // inside a row's tiles, past the first of them, has that row's parts joined.
+  __device__ __forceinline__ int4 parts(const Share& x, long long me) const {
+    if (x.count == 0) return make_int4(0, 0, 0, 0);
+    const long long seg = me * quota - x.row_unit, prev = seg / quota;
+    int4 d = make_int4(x.at.b, x.at.hr, 0, 0);
+    if (x.at.tile > 0 && prev == me - 1) {
+      d.z = static_cast<int>((seg + x.at.s.tiles - 1) / quota - prev + 1);
+      d.w = static_cast<int>(2 * prev + (seg - extra > prev * quota ? 1 : 0));
     }
     return d;
   }

@@ -45,6 +45,9 @@ constexpr int kThreads = 640;
 constexpr int kFast = 9, kTop = 15;
 constexpr int kMaxStages = 8;
 constexpr float kBandUp = 536870912.f;  // 2^kBand
+// Beginning and ending a row's tiles costs as much as this many (64 requests of 97 to
+// 4099 tokens, 40 rows: 201 us at 0, 138 at 2, 119 at 4, 114 at 6).
+constexpr int kPartTiles = 5;
 constexpr int kRing = 8;  // parts described ahead
 // Blocks lie 16 bytes past a multiple of 128 apart: the eight lanes of a phase,
 // four blocks' two tokens, then read different banks.
@@ -325,11 +328,10 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
   const KvAttnArgs& a = L.a;
   const int bpp = a.c.page_size / kKvBlock;
   const long long head_bytes = static_cast<long long>(bpp) * kv_block_bytes(kD), page_bytes = head_bytes * a.c.kv_heads;
-  const long long unit = blockIdx.x * list.quota;
-  int left = unit < list.units ? static_cast<int>(min(list.units - unit, list.quota)) : 0;
-  Place<kTile> place = {};
-  if (left) place = list.find(a, unit);
-  if (lane == 0) L.desc[blockIdx.x] = left ? list.parts(place, blockIdx.x) : make_int4(0, 0, 0, 0);
+  const List<kTile>::Share share = list.share(a, blockIdx.x);
+  int left = share.count;
+  Place<kTile> place = share.at;
+  if (lane == 0) L.desc[blockIdx.x] = list.parts(share, blockIdx.x);
   int st = 0;
   uint32_t phase = 1;
 #pragma unroll 1
@@ -703,6 +705,8 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
         if (!group_any<kThreads>(kSync, high || low)) break;
         if (rescaled || !group_any<kThreads>(kSync, high)) {
           // below 2^-14 fp16 keeps fewer bits: what it loses goes to later passes
+          bands = 1;
+          if (!group_any<kThreads>(kSync, least < kTop - 2 * kBand)) break;
           const int need = low ? static_cast<int>(fminf((kTop - least) * (1.f / kBand), kBands - 1.f)) : 0;
           const int most_needed = __reduce_max_sync(~0u, need);
           if (lane == 0 && most_needed)
@@ -766,6 +770,16 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
         w.wait(kWeightsEmpty + (it & 1), (it >> 1) ^ 1);
         w.wait(kInfoEmpty + (it & 1), (it >> 1) ^ 1);
         // what the passes before lost of weights below 2^-14, kBand octaves up each time
+        if (band == 0) {
+#pragma unroll
+          for (int n = 0; n < H; n += 8) {
+            float s[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              s[y] = u[n + y] < kSmallest ? (u[n + y] - __half2float(__float2half_rn(u[n + y]))) * kBandUp : 0.f;
+            put(n, s);
+          }
+        } else
 #pragma unroll 1
         for (int n0 = 0; n0 < H; n0 += 8) {
           float s[8];
@@ -1105,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   tc_fence_before();
   List<kTile> list;
-  list.build(L.a, L.a.c.kv_heads * L.p.rt, gridDim.x, scan, sums);
+  list.build(L.a, L.a.c.kv_heads * L.p.rt, gridDim.x, kPartTiles, scan, sums);
   tc_fence_after();
   const uint32_t tmem = lds32(words + 12);
   Waiter w;
