@@ -37,7 +37,7 @@ constexpr int kBias = 15;        // weights are at most 2^kBias
 constexpr float kLowUp = 2048.f; // the second fp16 part of a weight is held this much up
 // More rows than this take ssdv_attn_tc.cu (bf16, 128 elements).  64 requests of 8
 // kv heads, here against there: 20 rows 51 / 60 us for 500 tokens, 188 / 169 for
-// 4000, 117 / 160 for 201 to 8003; 30 rows 64 / 58 and 241 / 180; 40 rows 93 / 64
+// 4000, 117 / 135 for 201 to 8003; 30 rows 64 / 58 and 241 / 180; 40 rows 93 / 64
 // and 319 / 208.
 constexpr int kTcRows = 24;
 constexpr int kSmem = 226000;    // dynamic shared memory, at most

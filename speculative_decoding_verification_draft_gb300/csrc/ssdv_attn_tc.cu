@@ -240,11 +240,15 @@ __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
-// The larger of all lanes' numbers (NaN aside).
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
-  return y;
+// Elements e and e + 1 of a result's row at `to` (0: none), as bf16 or fp32.
+__device__ __forceinline__ void store_pair(unsigned long long to, uint32_t half, int e, float x0, float x1) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.and.b64 q, %0, 0, !p;\n\t"
+      "setp.ne.and.b64 p, %0, 0, p;\n\t"
+      "@p st.global.b32 [%1], %3;\n\t@q st.global.v2.f32 [%2], {%4, %6};\n\t}" ::"l"(to),
+      "l"(to + e * 2), "l"(to + e * 4), "r"(*reinterpret_cast<const uint32_t*>(&h)), "f"(x0), "r"(half), "f"(x1)
+      : "memory");
 }
 
 // Waits that end: once one has run out, the warp goes through the motions
@@ -410,6 +414,8 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
 template <int N>
 __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, Waiter w, int lane) {
   const KvAttnArgs& a = L.a;
+  // (strides in elements)
+  const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && ((a.qs[0] | a.qs[1] | a.qs[2]) & 7) == 0;
   Ring<N> parts(base, w);
   Part p;
   int n_parts = 0;
@@ -417,41 +423,61 @@ __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, W
     if (!p.active()) continue;
     const int qb = n_parts & 1, nrows = p.nq * L.per;
     w.nap(kQueryEmpty + qb, (n_parts >> 1) ^ 1);
-    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + p.b * a.qs[0] + p.head * L.per * a.qs[2] + lane * 4;
-    int i = p.pass0 / L.per, g = p.pass0 % L.per;  // the row's query token and head
+    const __nv_bfloat16* from =
+        static_cast<const __nv_bfloat16*>(a.q) + p.b * a.qs[0] + p.head * L.per * a.qs[2] + (lane & 15) * 8;
+    // a lane has eight elements of every other row, sixteen rows at a time
+    int i = (p.pass0 + (lane >> 4)) / L.per, g = (p.pass0 + (lane >> 4)) % L.per;  // the row's query token and head
 #pragma unroll 1
-    for (int k0 = 0; k0 < N; k0 += 8) {
-      float x[8][4];
+    for (int k0 = 0; k0 < N; k0 += 16) {
+      uint32_t x[8][4], top[4];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        uint2 v = make_uint2(0, 0);
-        if (p.pass0 + k0 + k < nrows) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (p.pass0 + k0 + 2 * k + (lane >> 4) < nrows) {
           const __nv_bfloat16* q = from + i * a.qs[1] + g * a.qs[2];
-          if ((reinterpret_cast<uintptr_t>(q) & 7) == 0) {
-            v = *reinterpret_cast<const uint2*>(q);
+          if (vec) {
+            v = __ldg(reinterpret_cast<const uint4*>(q));
           } else {
             const unsigned short* h = reinterpret_cast<const unsigned short*>(q);
-            v = make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+            v = make_uint4(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16,
+                           h[4] | static_cast<uint32_t>(h[5]) << 16, h[6] | static_cast<uint32_t>(h[7]) << 16);
           }
         }
-        if (++g == L.per) g = 0, ++i;
-        x[k][0] = __uint_as_float(v.x << 16), x[k][1] = __uint_as_float(v.x & 0xFFFF0000u);
-        x[k][2] = __uint_as_float(v.y << 16), x[k][3] = __uint_as_float(v.y & 0xFFFF0000u);
+        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+        for (g += 2; g >= L.per; g -= L.per) ++i;
+      }
+      // the rows' largest magnitudes: bits of bf16, two rows (2 k and 2 k + 1 of the lane's) to a word
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        uint32_t m[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          m[y] = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) m[y] = __vmaxu2(m[y], x[k + y][c] & 0x7FFF7FFFu);
+        }
+        top[k >> 1] = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
       }
 #pragma unroll
+      for (int bit = 8; bit; bit >>= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = __vmaxu2(top[k], __shfl_xor_sync(~0u, top[k], bit));
+#pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float top =
-            warp_max(fmaxf(fmaxf(fabsf(x[k][0]), fabsf(x[k][1])), fmaxf(fabsf(x[k][2]), fabsf(x[k][3]))));
         // as in ssdv_attn.cu: the row's largest element to [2^12, 2^13), the
         // scale's sign to the query
-        int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        int ex = static_cast<int>((k & 1 ? top[k >> 1] >> 16 : top[k >> 1] & 0xFFFFu) >> 7) - 127;
         ex = max(-100, min(ex, 127));
         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), a.scale_log2);
-        sts64(base + Smem<N>::query + qb * Smem<N>::kQueries + operand_byte<N>(k0 + k, lane * 4),
-              make_uint2(half2_bits(__floats2half2_rn(x[k][0] * up, x[k][1] * up)),
-                         half2_bits(__floats2half2_rn(x[k][2] * up, x[k][3] * up))));
-        if (lane == 0)
-          sts_f(base + Smem<N>::factors + (qb * N + k0 + k) * 4,
+        const int row = k0 + 2 * k + (lane >> 4);
+        uint32_t y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          y[c] = half2_bits(__floats2half2_rn(__uint_as_float(x[k][c] << 16) * up, __uint_as_float(x[k][c] & 0xFFFF0000u) * up));
+        sts128(base + Smem<N>::query + qb * Smem<N>::kQueries + operand_byte<N>(row, (lane & 15) * 8),
+               make_uint4(y[0], y[1], y[2], y[3]));
+        if ((lane & 15) == 0)
+          sts_f(base + Smem<N>::factors + (qb * N + row) * 4,
                 fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23));
       }
     }
@@ -641,9 +667,7 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
     const int qb = n_parts & 1;
     w.wait(kQueryFull + qb, n_parts >> 1);
     if (tid < N) {
-      // an infinite reference makes the first tile set it
       sts32(fr_at(tid), lds32(base + M::factors + (qb * N + tid) * 4));
-      sts32(fr_at(tid) + 8, 0x7F800000u);
       sts_f(base + M::maxima + tid * 4, -INFINITY);
     }
     group_sync<kThreads>(kSync);
@@ -681,10 +705,13 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
         for (int n = 0; n + 16 <= H; n += 16) tc_ld16(scores + n, u + n);
         if constexpr (H % 16 != 0) tc_ld8(scores + H / 16 * 16, u + H / 16 * 16);
         tc_wait_ld<H>(u);
+        const bool first = k == 0 && !rescaled;  // there are no references yet
+        if (!first) {
 #pragma unroll
-        for (int n = 0; n < H; n += 2) {
-          const uint4 fr = lds128(base + M::fr + (r0 + n) * 8);  // factors, then references of two rows
-          fma_pair(u[n], u[n + 1], fr);
+          for (int n = 0; n < H; n += 2) {
+            const uint4 fr = lds128(base + M::fr + (r0 + n) * 8);  // factors, then references of two rows
+            fma_pair(u[n], u[n + 1], fr);
+          }
         }
         if (edge) {
 #pragma unroll
@@ -702,8 +729,8 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
           }
         }
         const bool high = most > kTop, low = least < kTop - kBand;
-        if (!group_any<kThreads>(kSync, high || low)) break;
-        if (rescaled || !group_any<kThreads>(kSync, high)) {
+        if (!first && !group_any<kThreads>(kSync, high || low)) break;
+        if (!first && (rescaled || !group_any<kThreads>(kSync, high))) {
           // below 2^-14 fp16 keeps fewer bits: what it loses goes to later passes
           bands = 1;
           if (!group_any<kThreads>(kSync, least < kTop - 2 * kBand)) break;
@@ -720,15 +747,26 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
         // the rows' maxima follow the tile's
 #pragma unroll 1
         for (int n0 = 0; n0 < H; n0 += 8) {
-          float s[8], keep = -INFINITY;
+          float s[8];
           tc_ld8(scores + n0, s);
           tc_wait_ld<8>(s);
+          if (edge) {
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const float top = warp_max(!edge || (n0 + n >= seen.x && n0 + n < seen.y) ? s[n] : -INFINITY);
-            if (lane == n) keep = top;
+            for (int n = 0; n < 8; ++n) s[n] = n0 + n >= seen.x && n0 + n < seen.y ? s[n] : -INFINITY;
           }
-          if (lane < 8) sts_f(base + M::tops + (warp * N + r0 + n0 + lane) * 4, keep);
+          // rows are exchanged, so that each step halves what a lane holds
+#pragma unroll
+          for (int half = 4, bit = 16; half; half >>= 1, bit >>= 1) {
+            const bool upper = lane & bit;
+#pragma unroll
+            for (int n = 0; n < half; ++n) {
+              const float mine = upper ? s[n + half] : s[n], other = upper ? s[n] : s[n + half];
+              s[n] = fmaxf(mine, __shfl_xor_sync(~0u, other, bit));
+            }
+          }
+          s[0] = fmaxf(s[0], __shfl_xor_sync(~0u, s[0], 2));
+          s[0] = fmaxf(s[0], __shfl_xor_sync(~0u, s[0], 1));
+          if ((lane & 3) == 0) sts_f(base + M::tops + (warp * N + r0 + n0 + (lane >> 2)) * 4, s[0]);
         }
         group_sync<kThreads>(kSync);
         if (tid < N) {
@@ -743,8 +781,10 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
           sts_f(base + M::fall + ((it & 1) * N + tid) * 4, old == -INFINITY ? 0.f : ex2(old - m));
         }
         group_sync<kThreads>(kSync);
+        if (k > 0) {
 #pragma unroll
-        for (int n = 0; n < H; ++n) l[n] *= lds_f(base + M::fall + ((it & 1) * N + r0 + n) * 4);
+          for (int n = 0; n < H; ++n) l[n] *= lds_f(base + M::fall + ((it & 1) * N + r0 + n) * 4);
+        }
         rescaled = true;
       }
 #pragma unroll
@@ -1005,25 +1045,28 @@ struct Values {
       sts128(rows + tid * 16, make_uint4(static_cast<uint32_t>(to), static_cast<uint32_t>(to >> 32), __float_as_uint(f), half));
     }
     group_sync(kSync);
+    // Neighbouring lanes, whose elements are neighbours, exchange: each stores
+    // both elements of every other row.
+    const int odd = lane & 1;
 #pragma unroll 1
-    for (int n0 = 0; n0 < N; n0 += 16) {
-      float o[16] = {};
+    for (int n0 = 0; n0 < N; n0 += 8) {
+      float o[8] = {};
+      uint4 r[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) r[y] = lds128(rows + (n0 + 2 * y + odd) * 16);
       if (active) {
-        tc_ld16(tmem + Tmem<N>::outs + ob * N + n0, o);
-        tc_wait_ld<16>(o);
+        tc_ld8(tmem + Tmem<N>::outs + ob * N + n0, o);
+        tc_wait_ld<8>(o);
       }
       if (nans)
 #pragma unroll
-        for (int y = 0; y < 16; ++y) o[y] = nans >> (n0 + y) & 1 ? __int_as_float(0x7FC00000) : o[y];
+        for (int y = 0; y < 8; ++y) o[y] = nans >> (n0 + y) & 1 ? __int_as_float(0x7FC00000) : o[y];
 #pragma unroll
-      for (int y = 0; y < 16; ++y) {
-        const uint4 r = lds128(rows + (n0 + y) * 16);
-        const unsigned long long to = r.x | static_cast<unsigned long long>(r.y) << 32;
-        const float f = __uint_as_float(r.z), z = f == 0.f ? 0.f : o[y] * f;
-        if (to) {
-          if (r.w) reinterpret_cast<__nv_bfloat16*>(to)[element] = static_cast<__nv_bfloat16>(z);
-          else reinterpret_cast<float*>(to)[element] = z;
-        }
+      for (int y = 0; y < 4; ++y) {
+        const float got = __shfl_xor_sync(~0u, odd ? o[2 * y] : o[2 * y + 1], 1), f = __uint_as_float(r[y].z);
+        float x0 = odd ? got : o[2 * y], x1 = odd ? o[2 * y + 1] : got;
+        x0 = f == 0.f ? 0.f : x0 * f, x1 = f == 0.f ? 0.f : x1 * f;
+        store_pair(r[y].x | static_cast<unsigned long long>(r[y].y) << 32, r[y].w, element & ~1, x0, x1);
       }
     }
     tc_fence_before();
