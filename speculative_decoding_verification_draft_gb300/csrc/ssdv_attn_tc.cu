@@ -251,21 +251,52 @@ __device__ __forceinline__ void store_pair(unsigned long long to, uint32_t half,
       : "memory");
 }
 
+// Sums over lanes of kRows rows; the rows that a lane ends with begin at the row
+// returned.  Rows are exchanged, so that each step halves what a lane holds.
+template <int kRows, int kBit, int kMost>
+__device__ __forceinline__ int lane_sums(float (&l)[kMost], int lane) {
+  if constexpr (kBit == 0) {
+    return 0;
+  } else if constexpr (kRows % 2 == 0) {
+    constexpr int kHalf = kRows / 2;
+    const bool upper = lane & kBit;
+#pragma unroll
+    for (int n = 0; n < kHalf; ++n) {
+      const float mine = upper ? l[n + kHalf] : l[n], other = upper ? l[n] : l[n + kHalf];
+      l[n] = mine + __shfl_xor_sync(~0u, other, kBit);
+    }
+    return (upper ? kHalf : 0) + lane_sums<kHalf, kBit / 2>(l, lane);
+  } else {
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) l[n] += __shfl_xor_sync(~0u, l[n], kBit);
+    return lane_sums<kRows, kBit / 2>(l, lane);
+  }
+}
+
 // Waits that end: once one has run out, the warp goes through the motions
 // without waiting, so that every barrier of the CTA is still met.
 struct Waiter {
   uint32_t bars;
-  bool dead = false;
+  int tries = 1 << 24;  // of about a hundred cycles; zero once a wait has run out
+  __device__ __forceinline__ bool dead() const { return tries == 0; }
+  // (as short as it gets: there are many of them, and instruction fetches are scarce)
   __device__ __forceinline__ void wait(int bar, uint32_t phase) {
-    if (!dead && !bar_wait(bars + bar * 8, phase & 1)) dead = true;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 n;\n\tmov.b32 n, %0;\n"
+        "TRY:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "sub.s32 n, n, 1;\n\tsetp.gt.s32 p, n, 0;\n\t@p bra TRY;\n\tmov.b32 %0, 0;\nDONE:\n\t}"
+        : "+r"(tries)
+        : "r"(bars + bar * 8), "r"(phase & 1)
+        : "memory");
   }
   // For warps that run ahead: they sleep between tries.
   __device__ __forceinline__ void nap(int bar, uint32_t phase) {
-    for (int i = 0; i < (1 << 22) && !dead; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < (1 << 22) && !dead(); ++i) {
       if (bar_test(bars + bar * 8, phase & 1)) return;
       __nanosleep(200);
     }
-    dead = true;
+    tries = 0;
   }
   __device__ __forceinline__ void arrive(int bar) { bar_arrive(bars + bar * 8); }
 };
@@ -293,7 +324,7 @@ struct Ring {
     const uint4 x = lds128(from), y = lds128(from + 16), z = lds128(from + 32);
     Part p;
     p.b = x.x, p.head = x.y, p.pass0 = x.z, p.first = x.w;
-    p.count = y.x, p.len = y.y, p.nq = y.z, p.lo = y.w;
+    p.count = __shfl_sync(~0u, y.x, 0), p.len = y.y, p.nq = y.z, p.lo = y.w;
     p.hi = z.x, p.tile0 = z.y, p.flags = z.z, p.inner_lo = z.w;
     p.inner_hi = static_cast<int>(lds32(from + 48));
     return p;
@@ -308,7 +339,7 @@ struct Ring {
     p = read(n);
     if (!keep) release(n, lane);
     ++n;
-    return !w.dead && !(p.flags & Part::kEnd);
+    return __any_sync(~0u, !w.dead() && !(p.flags & Part::kEnd));
   }
 };
 
@@ -355,7 +386,7 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
       sts32(to + 48, row_hi(a, place.s.len, 0));
       w.arrive(kPartFull + n % kRing);
     }
-    if (!left || w.dead) break;
+    if (!left || w.dead()) break;
     left -= p.count;
     place.tile += p.count - 1;
     if (left) place.next(a, list.per_request);
@@ -394,13 +425,13 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
         bar_expect(bar, got * kv_block_bytes(kD));
       }
       __syncwarp();
-      if (lane < 8 && ok && !w.dead)
+      if (lane < 8 && ok && !w.dead())
         bulk_copy(base + Smem<N>::stages + st * kStage + lane * kBlockStride, a.c.pages + at, kv_block_bytes(kD), bar);
       if (++st == S) st = 0, phase ^= 1;
       want = want_next, page = page_next;
     }
   }
-  if (w.dead) {
+  if (w.dead()) {
     // copies still in flight get the same time again before the shared memory goes
     if (lane == 0) atomicOr(a.status, 1 << SSD_ERR_CUDA);
     long long since = 0;
@@ -423,61 +454,73 @@ __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, W
     if (!p.active()) continue;
     const int qb = n_parts & 1, nrows = p.nq * L.per;
     w.nap(kQueryEmpty + qb, (n_parts >> 1) ^ 1);
+    // Eight rows at a time, the next eight on their way: a lane has eight elements
+    // of every other row.
     const __nv_bfloat16* from =
         static_cast<const __nv_bfloat16*>(a.q) + p.b * a.qs[0] + p.head * L.per * a.qs[2] + (lane & 15) * 8;
-    // a lane has eight elements of every other row, sixteen rows at a time
-    int i = (p.pass0 + (lane >> 4)) / L.per, g = (p.pass0 + (lane >> 4)) % L.per;  // the row's query token and head
+    int row = lane >> 4, i = (p.pass0 + row) / L.per, g = (p.pass0 + row) - i * L.per;  // query token and head
+    uint4 next[4];
 #pragma unroll 1
-    for (int k0 = 0; k0 < N; k0 += 16) {
-      uint32_t x[8][4], top[4];
+    for (int k0 = (lane >> 4) - 8; k0 < N; k0 += 8) {
+      const uint4 x[4] = {next[0], next[1], next[2], next[3]};
+      if (row < N) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (p.pass0 + k0 + 2 * k + (lane >> 4) < nrows) {
-          const __nv_bfloat16* q = from + i * a.qs[1] + g * a.qs[2];
-          if (vec) {
-            v = __ldg(reinterpret_cast<const uint4*>(q));
-          } else {
-            const unsigned short* h = reinterpret_cast<const unsigned short*>(q);
-            v = make_uint4(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16,
-                           h[4] | static_cast<uint32_t>(h[5]) << 16, h[6] | static_cast<uint32_t>(h[7]) << 16);
+        for (int k = 0; k < 4; ++k) {
+          next[k] = make_uint4(0, 0, 0, 0);
+          if (p.pass0 + row < nrows) {
+            const __nv_bfloat16* q = from + i * a.qs[1] + g * a.qs[2];
+            if (vec) {
+              next[k] = __ldg(reinterpret_cast<const uint4*>(q));
+            } else {
+              uint4& v = next[k];
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                const uint32_t h = reinterpret_cast<const unsigned short*>(q)[c];
+                v.x = __funnelshift_r(v.x, v.y, 16), v.y = __funnelshift_r(v.y, v.z, 16);
+                v.z = __funnelshift_r(v.z, v.w, 16), v.w = __funnelshift_r(v.w, h, 16);
+              }
+            }
           }
+          row += 2;
+#pragma unroll 1
+          for (g += 2; g >= L.per; g -= L.per) ++i;
         }
-        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
-        for (g += 2; g >= L.per; g -= L.per) ++i;
       }
-      // the rows' largest magnitudes: bits of bf16, two rows (2 k and 2 k + 1 of the lane's) to a word
+      if (k0 < 0) continue;
+      // the rows' largest magnitudes: bits of bf16, two of the lane's rows to a word
+      uint32_t top[2];
 #pragma unroll
-      for (int k = 0; k < 8; k += 2) {
+      for (int k = 0; k < 2; ++k) {
         uint32_t m[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          m[y] = 0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) m[y] = __vmaxu2(m[y], x[k + y][c] & 0x7FFF7FFFu);
+          const uint4& v = x[2 * k + y];
+          m[y] = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
         }
-        top[k >> 1] = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+        top[k] = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
       }
 #pragma unroll
-      for (int bit = 8; bit; bit >>= 1)
+      for (int bit = 8; bit; bit >>= 1) {
+        top[0] = __vmaxu2(top[0], __shfl_xor_sync(~0u, top[0], bit));
+        top[1] = __vmaxu2(top[1], __shfl_xor_sync(~0u, top[1], bit));
+      }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = __vmaxu2(top[k], __shfl_xor_sync(~0u, top[k], bit));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
         // as in ssdv_attn.cu: the row's largest element to [2^12, 2^13), the
         // scale's sign to the query
         int ex = static_cast<int>((k & 1 ? top[k >> 1] >> 16 : top[k >> 1] & 0xFFFFu) >> 7) - 127;
         ex = max(-100, min(ex, 127));
         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), a.scale_log2);
-        const int row = k0 + 2 * k + (lane >> 4);
+        const int n = k0 + 2 * k;
+        const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
         uint32_t y[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          y[c] = half2_bits(__floats2half2_rn(__uint_as_float(x[k][c] << 16) * up, __uint_as_float(x[k][c] & 0xFFFF0000u) * up));
-        sts128(base + Smem<N>::query + qb * Smem<N>::kQueries + operand_byte<N>(row, (lane & 15) * 8),
+          y[c] = half2_bits(__floats2half2_rn(__uint_as_float(v[c] << 16) * up, __uint_as_float(v[c] & 0xFFFF0000u) * up));
+        sts128(base + Smem<N>::query + qb * Smem<N>::kQueries + operand_byte<N>(n, (lane & 15) * 8),
                make_uint4(y[0], y[1], y[2], y[3]));
         if ((lane & 15) == 0)
-          sts_f(base + Smem<N>::factors + (qb * N + row) * 4,
+          sts_f(base + Smem<N>::factors + (qb * N + n) * 4,
                 fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23));
       }
     }
@@ -486,7 +529,7 @@ __device__ __forceinline__ void query_role(const AttnLaunch& L, uint32_t base, W
     if (lane == 0) w.arrive(kQueryFull + qb);
     ++n_parts;
   }
-  if (w.dead && lane == 0) atomicOr(a.status, 1 << SSD_ERR_CUDA);
+  if (w.dead() && lane == 0) atomicOr(a.status, 1 << SSD_ERR_CUDA);
 }
 
 // ---- matrix instructions (warps 17 and 18; one lane issues them, the warp stays
@@ -500,14 +543,14 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, bool
   // (a broadcast is what tells the compiler that the warp agrees on a number)
   d = __shfl_sync(~0u, d, 0), a = __shfl_sync(~0u, a, 0), b = __shfl_sync(~0u, b, 0);
   const uint64_t operand = tc_operand(b);
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < 8; ++s)
     tc_mma(d, a + s * 8, operand + (kRowMajor ? s * 128 : (s >> 2) * (N * 8) + (s & 3) * 2), tc_idesc(N, kRowMajor),
            s > 0 || add, leader);
 }
 // The warp's instructions are done before the tensor memory goes.
 __device__ __forceinline__ void drain(const AttnLaunch& L, Waiter& w, bool leader) {
-  if (w.dead && leader) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+  if (w.dead() && leader) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
   tc_commit(w.bars + kDone * 8, leader);
   bar_wait(w.bars + kDone * 8, 0);
 }
@@ -527,14 +570,14 @@ __device__ __forceinline__ void score_role(const AttnLaunch& L, uint32_t base, u
       const int sb = tile & 1;
       w.wait(kKeysFull + sb, tile >> 1);
       w.wait(kScoresEmpty + sb, (tile >> 1) ^ 1);
-      if (w.dead) continue;
+      if (w.dead()) continue;
       tc_fence_after();
       product<N, false>(tmem + Tmem<N>::scores + sb * N, tmem + Tmem<N>::keys + sb * 64,
                         base + Smem<N>::query + qb * Smem<N>::kQueries, false, leader);
       tc_commit(w.bars + (kScoresFull + sb) * 8, leader);
       tc_commit(w.bars + (kKeysEmpty + sb) * 8, leader);
     }
-    if (!w.dead) tc_commit(w.bars + (kQueryEmpty + qb) * 8, leader);
+    if (!w.dead()) tc_commit(w.bars + (kQueryEmpty + qb) * 8, leader);
     ++n_parts;
   }
   drain(L, w, leader);
@@ -560,8 +603,8 @@ __device__ __forceinline__ void sum_role(const AttnLaunch& L, uint32_t base, uin
         const int pb = it & 1;
         w.wait(kWeightsFull + pb, it >> 1);
         const uint32_t info = __shfl_sync(~0u, lds32(base + Smem<N>::words + pb * 4), 0), band = info >> 8;
-        last = w.dead || (info & kInfoLast);
-        if (w.dead) continue;
+        last = w.dead() || (info & kInfoLast);
+        if (w.dead()) continue;
         if (info & kInfoRescale) {
           // the sums so far are rescaled first
           tc_commit(w.bars + kFixFull * 8, leader);
@@ -579,7 +622,7 @@ __device__ __forceinline__ void sum_role(const AttnLaunch& L, uint32_t base, uin
         if (last) tc_commit(w.bars + (kValuesEmpty + vb) * 8, leader);
       }
     }
-    if (!w.dead) tc_commit(w.bars + (kOutFull + ob) * 8, leader);
+    if (!w.dead()) tc_commit(w.bars + (kOutFull + ob) * 8, leader);
     ++n_parts;
   }
   drain(L, w, leader);
@@ -640,7 +683,7 @@ __device__ __forceinline__ void key_role(const AttnLaunch& L, uint32_t base, uin
       if (++st == S) st = 0, phase ^= 1;
     }
   }
-  if (w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+  if (w.dead() && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
 
 // ---- weights (warps 0-7): a thread has one token of the tile, in the keys' order,
@@ -839,32 +882,12 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
         }
       }
     }
-    // the part's sums over the warp's tokens: rows are exchanged, so that each
-    // step halves what a lane holds
-    int width = H, row = r0;
-#pragma unroll
-    for (int bit = 16; bit; bit >>= 1) {
-      if (width % 2 == 0) {
-        const int half = width / 2;
-        const bool upper = lane & bit;
-#pragma unroll
-        for (int n = 0; n < H; ++n)
-          if (n < half && n + half < H) {
-            const float mine = upper ? l[n + half < H ? n + half : 0] : l[n], other = upper ? l[n] : l[n + half < H ? n + half : 0];
-            l[n] = mine + __shfl_xor_sync(~0u, other, bit);
-          }
-        row += upper ? half : 0;
-        width = half;
-      } else {
-#pragma unroll
-        for (int n = 0; n < H; ++n)
-          if (n < width) l[n] += __shfl_xor_sync(~0u, l[n], bit);
-      }
-    }
+    // the part's sums over the warp's tokens
+    const int row = r0 + lane_sums<H, 16>(l, lane);
+    constexpr int kLeft = H / ((H & -H) < 32 ? (H & -H) : 32);
     w.wait(kEndEmpty, n_parts ^ 1);
 #pragma unroll
-    for (int n = 0; n < H; ++n)
-      if (n < width) sts_f(base + M::ends + (warp * N + row + n) * 4, l[n]);
+    for (int n = 0; n < kLeft; ++n) sts_f(base + M::ends + (warp * N + row + n) * 4, l[n]);
     if (tid < N) sts_f(base + M::ends + (4 * N + tid) * 4, lds_f(base + M::maxima + tid * 4));
     __syncwarp();
     if (lane == 0) {
@@ -874,7 +897,7 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
     ++n_parts;
     group_sync<kThreads>(kSync);  // the maxima are read before the next part clears them
   }
-  if (w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+  if (w.dead() && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
 
 // ---- values (warps 12-15): a thread has one element of a head ----
@@ -926,23 +949,23 @@ struct Values {
     w.wait(kValuesEmpty + vb, (tile >> 1) ^ 1);
     tc_fence_after();
 #pragma unroll 1
-    for (int half2 = 0; half2 < 2; ++half2) {  // a word of every block, four pairs
+    for (int x = 0; x < 4; ++x) {  // a word of every block, two pairs of it
       uint32_t word[kBlocks];
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) word[b] = lds32(data + b * kBlockStride + kv_v_codes(kD) + tid * 8 + half2 * 4);
+      for (int b = 0; b < kBlocks; ++b) {
+        word[b] = lds32(data + b * kBlockStride + kv_v_codes(kD) + tid * 8 + (x >> 1) * 4);
+        word[b] = __funnelshift_r(word[b], word[b], (x & 1) * 8);
+      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         uint32_t v[kBlocks];
 #pragma unroll
         for (int q = 0; q < kBlocks / 2; ++q) {
-          const uint4 e = lds128(table + (half2 * 4 + k) * 512 + q * 128 + group * 16);
-          v[2 * q] = fma2(k & 1 ? pair_lo(word[2 * q], bases) : pair_hi(word[2 * q], bases), e.x, e.y);
-          v[2 * q + 1] = fma2(k & 1 ? pair_lo(word[2 * q + 1], bases) : pair_hi(word[2 * q + 1], bases), e.z, e.w);
+          const uint4 e = lds128(table + (x * 2 + k) * 512 + q * 128 + group * 16);
+          v[2 * q] = fma2(k ? pair_lo(word[2 * q], bases) : pair_hi(word[2 * q], bases), e.x, e.y);
+          v[2 * q + 1] = fma2(k ? pair_lo(word[2 * q + 1], bases) : pair_hi(word[2 * q + 1], bases), e.z, e.w);
         }
-        tc_st8(tmem + Tmem<N>::values + vb * 64 + (half2 * 4 + k) * 8, v);
-        if (k == 1)
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b) word[b] = __funnelshift_r(word[b], word[b], 8);
+        tc_st8(tmem + Tmem<N>::values + vb * 64 + (x * 2 + k) * 8, v);
       }
     }
     unsigned long long rows = 0;
@@ -953,7 +976,7 @@ struct Values {
 #pragma unroll 1
         for (; nans; nans &= nans - 1) {
           const int2 seen = rows_seeing<N>(L, q, pos0 + b * kKvBlock + __ffs(nans) - 1);
-          for (int n = seen.x; n < seen.y; ++n) rows |= 1ull << n;
+          if (seen.x < seen.y) rows |= (~0ull >> (64 - seen.y)) & (~0ull << seen.x);
         }
       }
     }
@@ -974,7 +997,7 @@ struct Values {
       const int ib = it & 1;
       w.wait(kWeightsFull + ib, it >> 1);
       const uint32_t info = lds32(base + M::words + ib * 4);
-      last = w.dead || (info & kInfoLast);
+      last = w.dead() || (info & kInfoLast);
       const int band = info >> 8;
       if (band || (info & kInfoRescale)) {
         w.wait(kFixFull, fixes++);
@@ -1027,7 +1050,7 @@ struct Values {
           for (int u = 0; u < 4; ++u) l += lds_f(base + M::ends + (u * N + tid) * 4);
           m = lds_f(base + M::ends + (4 * N + tid) * 4);
         }
-        if (lost || w.dead || (q.flags & Part::kBad)) l = __int_as_float(0x7FC00000);
+        if (lost || w.dead() || (q.flags & Part::kBad)) l = __int_as_float(0x7FC00000);
         if (whole || row >= nrows) {
           at = orow;
           f = l == 0.f ? 0.f : 1.f / l;
@@ -1131,7 +1154,7 @@ __device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, u
       prev_nans = nans;
     }
   }
-  if (v.w.dead && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+  if (v.w.dead() && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
 
 template <int N>
