@@ -36,10 +36,10 @@ constexpr int kTile = 64;        // tokens per tile: four blocks
 constexpr int kBias = 15;        // weights are at most 2^kBias
 constexpr float kLowUp = 2048.f; // the second fp16 part of a weight is held this much up
 // More rows than this take ssdv_attn_tc.cu (bf16, 128 elements).  64 requests of 8
-// kv heads, here against there: 20 rows 51 / 60 us for 500 tokens, 188 / 169 for
-// 4000, 117 / 135 for 201 to 8003; 30 rows 64 / 58 and 241 / 180; 40 rows 93 / 64
-// and 319 / 208.
-constexpr int kTcRows = 24;
+// kv heads, here against there: 16 rows 42 / 46 us for 500 tokens, 125 / 164 for
+// 4000, 89 / 111 for 201 to 8003; 20 rows 52 / 51, 184 / 180 and 117 / 118; 40 rows
+// 93 / 56 and 319 / 172 for 500 and 4000.
+constexpr int kTcRows = 16;
 constexpr int kSmem = 226000;    // dynamic shared memory, at most
 constexpr int kWarps = 8;        // computing warps per CTA, one CTA per SM
 constexpr int kThreads = 384;    // and four more, of which one keeps the copies going
