@@ -98,8 +98,9 @@ struct Smem {
   static constexpr int fall = tops + 16 * N;            // [2][N]
   static constexpr int factors = fall + 8 * N;          // [2][N]
   static constexpr int ends = factors + 8 * N;          // [4][N] sums, [N] maxima
-  static constexpr int rows = ends + 20 * N;            // [N] a finished row's address, factor and type
-  static constexpr int parts = rows + 16 * N;           // [kRing] 64 bytes
+  static constexpr int rows = ends + 20 * N;            // [N] a finished row's factor, then which are zero
+  static constexpr int results = (rows + 4 * N + 8 + 15) / 16 * 16;  // [N][128] bf16
+  static constexpr int parts = results + 256 * N;       // [kRing] 64 bytes
   static constexpr int words = parts + 64 * kRing;           // info [2], bands, tensor memory address, flags [8]
   static constexpr int stages = (words + 64 + 127) / 128 * 128;
   static constexpr int kStages = (kSmem - stages) / kStage < kMaxStages ? (kSmem - stages) / kStage : kMaxStages;
@@ -220,6 +221,10 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
 }
 __device__ __forceinline__ float lds_f(uint32_t p) { return __uint_as_float(lds32(p)); }
 __device__ __forceinline__ void sts_f(uint32_t p, float x) { sts32(p, __float_as_uint(x)); }
+__device__ __forceinline__ int warp_of(int tid) { return tid >> 5; }
+__device__ __forceinline__ void sts16(uint32_t p, uint32_t x) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(p), "h"(static_cast<unsigned short>(x)) : "memory");
+}
 __device__ __forceinline__ uint32_t lds16(uint32_t p) {
   unsigned short v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
@@ -240,17 +245,6 @@ __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
-// Elements e and e + 1 of a result's row at `to` (0: none), as bf16 or fp32.
-__device__ __forceinline__ void store_pair(unsigned long long to, uint32_t half, int e, float x0, float x1) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.and.b64 q, %0, 0, !p;\n\t"
-      "setp.ne.and.b64 p, %0, 0, p;\n\t"
-      "@p st.global.b32 [%1], %3;\n\t@q st.global.v2.f32 [%2], {%4, %6};\n\t}" ::"l"(to),
-      "l"(to + e * 2), "l"(to + e * 4), "r"(*reinterpret_cast<const uint32_t*>(&h)), "f"(x0), "r"(half), "f"(x1)
-      : "memory");
-}
-
 // Sums over lanes of kRows rows; the rows that a lane ends with begin at the row
 // returned.  Rows are exchanged, so that each step halves what a lane holds.
 template <int kRows, int kBit, int kMost>
@@ -1030,67 +1024,93 @@ struct Values {
   __device__ __forceinline__ void finish(const Part& q, bool lost, unsigned long long nans) {
     const int nrows = q.flags & Part::kBad ? 0 : q.nq * L.per, ob = n_parts % Tmem<N>::kOuts;
     const bool whole = q.flags & Part::kWhole, active = q.active();
-    const uint32_t rows = base + M::rows;
     if ((q.flags & Part::kBad) && q.head == 0 && q.pass0 == 0 && tid == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
     if (active) {
       w.wait(kEndFull, n_parts);
       w.wait(kOutFull + ob, n_parts / Tmem<N>::kOuts);
       tc_fence_after();
     }
-    // a thread per row: where it goes, and its factor
+    // a thread per row: its factor, and where a whole row goes
+    const uint32_t factors = base + M::rows, staged = base + M::results;
+    const int live = min(nrows - q.pass0, N);  // rows that are real
+    const long long slot = (2ll * blockIdx.x + (q.first == 0 && (q.flags & Part::kLater) ? 1 : 0)) * N;
+    __nv_bfloat16* to = nullptr;
     if (tid < N) {
       const int row = q.pass0 + tid;
-      long long at = -1;
       float f = 0.f;
-      if (row < L.rows && (row < nrows || q.first == 0)) {
-        const long long orow = (static_cast<long long>(q.b) * a.nq + row / L.per) * a.heads + q.head * L.per + row % L.per;
+      if (row < L.rows && (tid < live || q.first == 0)) {
+        const int i = row / L.per;
+        const long long orow = (static_cast<long long>(q.b) * a.nq + i) * a.heads + q.head * L.per + row - i * L.per;
         float l = 0.f, m = 0.f;
-        if (active && row < nrows) {
+        if (active && tid < live) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) l += lds_f(base + M::ends + (u * N + tid) * 4);
           m = lds_f(base + M::ends + (4 * N + tid) * 4);
         }
         if (lost || w.dead() || (q.flags & Part::kBad)) l = __int_as_float(0x7FC00000);
-        if (whole || row >= nrows) {
-          at = orow;
+        if (whole || tid >= live) {
+          to = static_cast<__nv_bfloat16*>(a.out) + orow * kD;
           f = l == 0.f ? 0.f : 1.f / l;
           if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + (log2f(l) - kFast)) * 0.69314718055994531f;
         } else {
-          // (parts are kept 2^kTop up)
-          at = (2ll * blockIdx.x + (q.first == 0 && (q.flags & Part::kLater) ? 1 : 0)) * N + tid;
-          f = 1 << (kTop - kFast);
-          L.ml[at] = make_float2(m, l * f);
+          f = 1 << (kTop - kFast);  // (parts are kept 2^kTop up)
+          L.ml[slot + tid] = make_float2(m, l * f);
         }
       }
-      const bool half = whole || row >= nrows;  // bf16 results; else fp32 sums
-      const unsigned long long to = at < 0 ? 0 : half ? reinterpret_cast<unsigned long long>(a.out) + at * (kD * 2)
-                                                      : reinterpret_cast<unsigned long long>(L.o) + at * (kD * 4);
-      sts128(rows + tid * 16, make_uint4(static_cast<uint32_t>(to), static_cast<uint32_t>(to >> 32), __float_as_uint(f), half));
+      sts_f(factors + tid * 4, f);
+      const uint32_t none = __ballot_sync((tid | 31) < N ? ~0u : 0xFFFFu, f == 0.f);
+      if (lane == 0) sts32(factors + (N + warp_of(tid)) * 4, none);
+      // the copies of the part before have read what was staged
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     group_sync(kSync);
-    // Neighbouring lanes, whose elements are neighbours, exchange: each stores
-    // both elements of every other row.
-    const int odd = lane & 1;
+    unsigned long long none = lds32(factors + N * 4);  // rows whose weights are all zero
+    if constexpr (N > 32) none |= static_cast<unsigned long long>(lds32(factors + N * 4 + 4)) << 32;
 #pragma unroll 1
     for (int n0 = 0; n0 < N; n0 += 8) {
       float o[8] = {};
-      uint4 r[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) r[y] = lds128(rows + (n0 + 2 * y + odd) * 16);
       if (active) {
         tc_ld8(tmem + Tmem<N>::outs + ob * N + n0, o);
         tc_wait_ld<8>(o);
       }
-      if (nans)
+      if (none | nans) {
 #pragma unroll
-        for (int y = 0; y < 8; ++y) o[y] = nans >> (n0 + y) & 1 ? __int_as_float(0x7FC00000) : o[y];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float got = __shfl_xor_sync(~0u, odd ? o[2 * y] : o[2 * y + 1], 1), f = __uint_as_float(r[y].z);
-        float x0 = odd ? got : o[2 * y], x1 = odd ? o[2 * y + 1] : got;
-        x0 = f == 0.f ? 0.f : x0 * f, x1 = f == 0.f ? 0.f : x1 * f;
-        store_pair(r[y].x | static_cast<unsigned long long>(r[y].y) << 32, r[y].w, element & ~1, x0, x1);
+        for (int y = 0; y < 8; ++y) {
+          if (nans >> (n0 + y) & 1) o[y] = __int_as_float(0x7FC00000);
+          if (none >> (n0 + y) & 1) o[y] = 0.f;
+        }
       }
+      const uint4 fa = lds128(factors + n0 * 4), fb = lds128(factors + n0 * 4 + 16);
+      const uint32_t f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] *= __uint_as_float(f[y]);
+      if (whole) {
+#pragma unroll
+        for (int y = 0; y < 8; y += 2) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(o[y], o[y + 1]);
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(&h);
+          sts16(staged + (n0 + y) * (kD * 2) + element * 2, x);
+          sts16(staged + (n0 + y + 1) * (kD * 2) + element * 2, x >> 16);
+        }
+      } else {
+        float* part = L.o + (slot + n0) * kD + element;
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          if (n0 + y < live) part[y * kD] = o[y];
+      }
+    }
+    if (whole) {
+      async_fence();
+      group_sync(kSync);
+      if (to)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(staged + tid * (kD * 2)),
+                     "n"(kD * 2)
+                     : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    } else if (to) {
+      // rows past the request's own
+      const uint32_t x = q.flags & Part::kBad ? 0x7FC07FC0u : 0u;
+      for (int d = 0; d < kD / 8; ++d) reinterpret_cast<uint4*>(to)[d] = make_uint4(x, x, x, x);
     }
     tc_fence_before();
     group_sync(kSync);  // the rows' table is read before the next part's is written
@@ -1154,6 +1174,7 @@ __device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, u
       prev_nans = nans;
     }
   }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   if (v.w.dead() && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
 
@@ -1191,21 +1212,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
   Waiter w;
   w.bars = base;
   // 128 x (112 + 112 + 72 + 96 + 88) registers: the 640 x 96 of the launch
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-    weight_role<N>(L, base, tmem, w, warp, lane);
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    key_role<N>(L, base, tmem, w, warp - 8, lane);
-  } else if (warp < 16) {
-    value_role<N>(L, base, tmem, w, warp - 12, lane);
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 16) copy_role<N>(L, list, base, w, lane);
-    else if (warp == 17) score_role<N>(L, base, tmem, w, lane);
-    else if (warp == 18) sum_role<N>(L, base, tmem, w, lane);
-    else query_role<N>(L, base, w, lane);
-  }
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+  else if (warp < 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  else if (warp >= 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  // Their code lies in this order: the three that work all the time share the
+  // instruction cache best side by side (64 requests of 201 to 8003 tokens, 20
+  // rows: 102 us; with the values' code before the keys' 118).
+  if (warp < 8) weight_role<N>(L, base, tmem, w, warp, lane);
+  else if (warp >= 8 && warp < 12) key_role<N>(L, base, tmem, w, warp - 8, lane);
+  else if (warp >= 12 && warp < 16) value_role<N>(L, base, tmem, w, warp - 12, lane);
+  else if (warp == 18) sum_role<N>(L, base, tmem, w, lane);
+  else if (warp == 17) score_role<N>(L, base, tmem, w, lane);
+  else if (warp == 16) copy_role<N>(L, list, base, w, lane);
+  else if (warp == 19) query_role<N>(L, base, w, lane);
   tc_fence_before();
   __syncthreads();
   if (warp == 17) {
