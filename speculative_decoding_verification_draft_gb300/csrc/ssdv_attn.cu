@@ -24,6 +24,12 @@
 // with a smaller one, which real scores hardly hold, is passed over again for
 // the octaves below.  Each tile's product is added to the row's fp32 sums with
 // its own power of two, and maxima and sums of weights are in fp32.
+//
+// Measured: 128 requests of 301 to 6007 tokens, one query token, 4 query heads a
+// kv head of 128 (8 kv heads): 82 us, 3.5 TB/s, bound by the issue of instructions
+// (0.48 a cycle with two warps a scheduler) and their latency; twelve computing
+// warps of 152 registers in place of eight of 224: 82 us too, and short requests
+// slower.  32 requests, 10 rows of 256: 62 us, 1.7 TB/s, also instruction fetches.
 #include "ssdv_attn.cuh"
 
 #include <algorithm>
@@ -77,7 +83,7 @@ AttnShape attn_shape(int rows, int D, bool f32) {
   const int n8 = (rows + 7) / 8;
   a.tc = D == 128 && !f32 && rows > kTcRows;
   if (a.tc) {
-    // passes of 16 to 64 rows, as even as they come
+    // passes of 32 to 64 rows, as even as they come
     a.rt = (rows + 63) / 64;
     a.nt = ((rows + a.rt - 1) / a.rt + 15) / 16 * 2;
     a.p = a.g = a.t = a.s = 1;
@@ -945,7 +951,9 @@ cudaError_t launch_rows(const AttnLaunch& L, int sms, cudaStream_t s) {
 
 template <typename E, int D>
 cudaError_t launch_dim(const AttnLaunch& L, int sms, cudaStream_t s) {
-  return L.p.p == 1 ? launch_rows<E, D, 1, 2>(L, sms, s) : launch_rows<E, D, 2, 6>(L, sms, s);
+  if (L.p.p == 1) return launch_rows<E, D, 1, 2>(L, sms, s);
+  if constexpr (D == 128 && sizeof(E) == 2) return cudaErrorInvalidValue;  // rows for pairs go to ssdv_attn_tc.cu
+  else return launch_rows<E, D, 2, 6>(L, sms, s);
 }
 
 struct WorkLayout {

@@ -12,7 +12,10 @@
 // Both are bound by memory; what they compute per element is kept to a few
 // operations: quotients by a two-term reciprocal, the integer in the low bits of a
 // sum with 1.5 * 2^23, places in the word by one multiply-add each (append), and
-// fp16 pairs as in the attention (read).
+// fp16 pairs as in the attention (read).  Measured, 8 prompts of 701 to 4099 bf16
+// tokens, 8 heads of 128: writing 20 us for 66 MB of rows (half of the copy
+// bandwidth; one wave of loads, the table's look-up before it), reading 22 us for
+// 134 MB with the rows past a request's count (the copy bandwidth).
 #include "ssdv_kv.cuh"
 
 namespace ssdv {
@@ -263,7 +266,7 @@ __device__ __forceinline__ float2 pair_values(uint32_t word, int p, uint32_t sca
 }
 
 // wide: p is 32-byte aligned.  One store then covers whole sectors; two of 16 bytes
-// each touch every sector twice (8 prompts of 701 to 4099 tokens: 22 22 against 35 us).
+// each touch every sector twice (8 prompts of 701 to 4099 tokens: 22 against 35 us).
 __device__ __forceinline__ void store32(void* p, uint4 a, uint4 b, bool wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
