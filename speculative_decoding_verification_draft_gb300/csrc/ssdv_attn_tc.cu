@@ -31,8 +31,8 @@
 // again, kBand octaves a pass, into a sum of their own that is added with its
 // power of two.  Sums of weights and maxima are fp32.
 //
-// Measured: 256 requests of 2048 tokens, 40 rows: 372 us, 1.7 TB/s and 231 TFLOP/s
-// of the products that count, a tile of 128 tokens in 1.7 us a CTA where the matrix
+// Measured: 256 requests of 2048 tokens, 40 rows: 388 us, 1.6 TB/s and 221 TFLOP/s
+// of the products that count, a tile of 128 tokens in 1.8 us a CTA where the matrix
 // instructions alone would take 0.55 (16 of 64 cycles each).  About 1500
 // instructions a scheduler and tile issue at 0.5 a cycle: five roles fetch from one
 // instruction cache, so loops are kept short and slow paths rolled up.

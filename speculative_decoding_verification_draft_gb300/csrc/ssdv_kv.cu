@@ -13,9 +13,11 @@
 // operations: quotients by a two-term reciprocal, the integer in the low bits of a
 // sum with 1.5 * 2^23, places in the word by one multiply-add each (append), and
 // fp16 pairs as in the attention (read).  Measured, 8 prompts of 701 to 4099 bf16
-// tokens, 8 heads of 128: writing 20 us for 66 MB of rows (half of the copy
-// bandwidth; one wave of loads, the table's look-up before it), reading 22 us for
-// 134 MB with the rows past a request's count (the copy bandwidth).
+// tokens, 8 heads of 128: writing 19.5 us for 24 MB of rows (a chain of loads, the
+// lengths, the page table, the rows, and about 200 instructions a group at 0.5 a
+// cycle), reading 22 us for 134 MB with the rows past a request's count (the copy
+// bandwidth).  300 requests of up to 41 tokens, 2 heads of 256: 13 and 8.5 us (16.5
+// for writing with its loops unrolled).
 #include "ssdv_kv.cuh"
 
 namespace ssdv {
@@ -173,21 +175,29 @@ __device__ __forceinline__ Task find_task(const KvStoreArgs& a) {
 
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(KvStoreArgs a, int vec) {
-  constexpr int G = D / 16, kBatch = sizeof(E) == 2 ? 4 : 2;  // tokens loaded at a time
+  constexpr int G = D / 16, kBatch = sizeof(E) == 2 ? 2 : 1;  // tokens at a time, as many on their way
   const Task k = find_task<D>(a);
   const int lo = max(k.t0, k.half * 8), hi = k.block ? min(k.t1, k.half * 8 + 8) : 0;
   const bool values = blockIdx.y != 0;
   const long long* st = values ? a.vs : a.ks;
   const E* base = static_cast<const E*>(values ? a.v : a.k) + k.b * st[0] + k.h * st[2] + k.g * 16;
-  if (!values) {
+  Raw<E> next[kBatch];
+  const auto load = [&](int i0) {
 #pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = k.half * 8 + i0 + i;
+      if (t >= lo && t < hi) next[i].load(base + (k.first + t) * st[1], vec);
+    }
+  };
+  // (loops stay rolled: a small call runs code that is in no cache yet)
+  if (!values) {
+    load(0);
+#pragma unroll 1
     for (int i0 = 0; i0 < 8; i0 += kBatch) {
       Raw<E> x[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int t = k.half * 8 + i0 + i;
-        if (t >= lo && t < hi) x[i].load(base + (k.first + t) * st[1], vec);
-      }
+      for (int i = 0; i < kBatch; ++i) x[i] = next[i];
+      if (i0 + kBatch < 8) load(i0 + kBatch);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int t = k.half * 8 + i0 + i;
@@ -211,26 +221,26 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(KvStoreArgs a, int 
     return;
   }
   uint32_t word[16] = {}, keep = 0xFFFFFFFFu;
-#pragma unroll
-  for (int i0 = 8 - kBatch; i0 >= 0; i0 -= kBatch) {  // tokens 4 to 7 first: theirs are turned
+  load(4);
+#pragma unroll 1
+  for (int n = 0; n < 8; n += kBatch) {
+    const int i0 = (n + 4) & 7;  // tokens 4 to 7 first: theirs are turned
     Raw<E> x[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int t = k.half * 8 + i0 + i;
-      if (t >= lo && t < hi) x[i].load(base + (k.first + t) * st[1], vec);
-    }
+    for (int i = 0; i < kBatch; ++i) x[i] = next[i];
+    if (n + kBatch < 8) load((i0 + kBatch) & 7);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int t = k.half * 8 + i0 + i;
       if (t < lo || t >= hi) continue;
       uint32_t u[16];
-      const uint32_t byte = quantise(x[i], u);
+      const uint32_t byte = quantise(x[i], u), unit = entry_unit(i0 + i);
 #pragma unroll
-      for (int d = 0; d < 16; ++d) word[d] += (u[d] - kMagicBits) * entry_unit(i0 + i);
+      for (int d = 0; d < 16; ++d) word[d] += (u[d] - kMagicBits) * unit;
       keep &= ~kv_place(15u, i0 + i);
       k.block[kv_v_scales(D) + k.g * kKvBlock + t] = static_cast<uint8_t>(byte);
     }
-    if (i0 == 4) {
+    if (n + kBatch == 4) {
 #pragma unroll
       for (int d = 0; d < 16; ++d) word[d] = turn(word[d]);
     }
