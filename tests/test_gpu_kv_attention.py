@@ -280,3 +280,29 @@ def test_pool_past_32_bits(ssdv):
     q, q64 = kc.rows((1, 2, 16, D), BF16, 3)
     out, lse = ssdv.kv_attention(p.cache, p.table, kc.ints(lens), q, return_lse=True)
     compare(p, q, q64, kh, vh, lens, np.full(1, 2), BF16, out, lse)
+
+
+def test_query_strides_of_many_rows(ssdv):
+    B, n, Hkv, G, D = 2, 5, 2, 8, 128
+    lens = np.array([33, 300])
+    p = kc.Pool(ssdv, B, Hkv, D, 16, 310)
+    kh, vh = fill(p, lens, lens + n)
+    q, q64 = kc.rows((B, n, Hkv * G, D), BF16, 3)
+    odd = torch.zeros(q.numel() + 1, dtype=BF16, device="cuda")[1:].view(q.shape).copy_(q)
+    wide = q.new_zeros(B, n, 3, Hkv * G, D)
+    wide[:, :, 1] = q
+    padded = q.new_zeros(B, n, Hkv * G, D + 4)[..., :D].copy_(q)
+    first = q.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    for form in (odd, wide[:, :, 1], padded, first):
+        out, lse = ssdv.kv_attention(p.cache, p.table, kc.ints(lens), form, return_lse=True)
+        compare(p, q, q64, kh, vh, lens, np.full(B, n), BF16, out, lse)
+
+
+@pytest.mark.parametrize("n,G,past_only", [(1, 4, False), (5, 8, False), (5, 13, True), (4, 6, True)])
+def test_uneven_shares(ssdv, n, G, past_only):
+    # many beginnings of rows next to long ones: shares that hold only beginnings, rows split at every place
+    rng = np.random.default_rng(n)
+    lens = np.concatenate([np.zeros(40, int), rng.integers(1, 4, 60), rng.integers(1, 700, 180), [3001, 1, 0, 1999]])
+    rng.shuffle(lens)
+    n_q = rng.integers(0, n + 1, lens.size)
+    check(ssdv, lens.size, 2, G, 128, 32, BF16, n, lens, n_q=n_q, past_only=past_only)
