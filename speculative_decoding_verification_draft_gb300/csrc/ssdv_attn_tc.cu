@@ -52,8 +52,9 @@ constexpr int kFast = 9, kTop = 15;
 constexpr int kMaxStages = 8;
 constexpr float kBandUp = 536870912.f;  // 2^kBand
 // Beginning and ending a row's tiles costs as much as this many (64 requests of 97 to
-// 4099 tokens, 40 rows: 201 us at 0, 138 at 2, 119 at 4, 114 at 6).
-constexpr int kPartTiles = 5;
+// 4099 tokens, 40 rows: 201 us at 0 and 138 at 2 in an earlier form; now 90 at 3, 85
+// at 4, 86 at 5, and 512 requests of up to 36 rows 96, 94 and 97).
+constexpr int kPartTiles = 4;
 constexpr int kRing = 8;  // parts described ahead
 // Blocks lie 16 bytes past a multiple of 128 apart: the eight lanes of a phase,
 // four blocks' two tokens, then read different banks.
