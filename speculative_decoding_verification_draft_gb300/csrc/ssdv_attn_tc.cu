@@ -352,7 +352,7 @@ __device__ __forceinline__ int2 rows_seeing(const AttnLaunch& L, const Part& p, 
   // query i sees it if i >= pos - len (its own key included) and i < pos - len + window
   const int i = pos - p.len;
   const int lo = a.past_only || i <= 0 ? 0 : i * L.per - p.pass0;
-  const long long hi = a.window ? static_cast<long long>(i + a.window) * L.per - p.pass0 : N;
+  const long long hi = a.window ? (static_cast<long long>(i) + a.window) * L.per - p.pass0 : N;
   return make_int2(max(lo, 0), static_cast<int>(max(0ll, min(hi, static_cast<long long>(N)))));
 }
 
