@@ -581,6 +581,9 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
     [B, n, n_heads] float32) with return_lse (or a given lse)."""
     shape, device = q.shape, cache.device
     B, n, heads = shape[:3]
+    window = int(window)
+    if not -1 << 31 <= window < 1 << 31:
+        raise ValueError(f"window={window} is no 32-bit number")
     c, kv_heads, dim = _kv_cache(cache, page_table, B)
     qp, qs = _kv_rows(q, "q", None, dim)
     lens, counts = _kv_counts(kv_len, "kv_len", B), _kv_counts(n_q, "n_q", B)
@@ -597,7 +600,7 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
         raise ValueError("out must be shaped like q and lse [B, n, n_heads]")
     if B and n:
         _check(lib().ssd_kv_attention(c, lens, counts, qp, qs, _dtype_code(q), B, n, heads,
-                                      float(scale) if scale is not None else dim ** -0.5, int(window), int(past_only),
+                                      float(scale) if scale is not None else dim ** -0.5, window, int(past_only),
                                       _dev(out, "out", q.dtype),
                                       _dev(lse, "lse", torch.float32) if lse is not None else None,
                                       _dev(ws, "workspace"), ws.numel(), raw))
