@@ -395,8 +395,9 @@ typedef struct {
 size_t ssd_kv_page_bytes(int n_kv_heads, int head_dim, int page_size);
 
 /* Workspace of the calls below (0 for a bad shape): a status word, read by
- * ssd_read_status, and the attention's partial results.  n_q = 0 gives what
- * ssd_kv_append and ssd_kv_read need.  Zero it once (ssd_workspace_init). */
+ * ssd_read_status, and the attention's partial results.  It serves attention
+ * calls of n = 1 to n_q; n_q = 0 gives what ssd_kv_append and ssd_kv_read need.
+ * Zero it once (ssd_workspace_init). */
 size_t ssd_kv_workspace_bytes(int n_q, int n_heads, int n_kv_heads, int head_dim);
 
 /* Write n_new[b] new tokens of each request at positions kv_len[b] ..

@@ -915,7 +915,11 @@ size_t ssd_kv_workspace_bytes(int n_q, int n_heads, int n_kv_heads, int head_dim
   if (n_q < 0 || n_q > SSD_MAX_GAMMA + 1 || n_kv_heads < 1 || n_heads < n_kv_heads || n_heads % n_kv_heads ||
       n_heads / n_kv_heads > kMaxHeadsPerKv || !kv_dim_valid(head_dim))
     return 0;
-  return kKvWorkOffset + kv_attention_work_bytes(n_q * (n_heads / n_kv_heads), head_dim);
+  // fewer rows may be spread over more teams and need more: the largest of all calls up to n_q
+  size_t most = 0;
+  for (int n = 1; n <= n_q; ++n)
+    most = std::max(most, kv_attention_work_bytes(n * (n_heads / n_kv_heads), head_dim));
+  return kKvWorkOffset + most;
 }
 
 ssd_status ssd_kv_append(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_new, const void* k,
