@@ -427,6 +427,7 @@ def cache_check(bonus_topk: torch.Tensor, out_tokens: torch.Tensor, n_accepted: 
 
 
 KV_BLOCK = 16  # tokens per block of a cache page, elements per scale
+_KV_STATUS = 16  # bytes of a workspace that hold the status word
 _kv_ws_cache = {}
 _HERE = contextlib.nullcontext()
 # Small calls take a few microseconds on the GPU, so the binding of the cache calls
@@ -514,7 +515,9 @@ def _kv_workspace(need: int, device, raw: int):
         # a graph keeps its own workspace: the cached one may be replaced by a larger
         return torch.zeros(need, dtype=torch.uint8, device=device)
     if ws is None or ws.numel() < need:
-        ws = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        old, ws = ws, torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        if old is not None:  # errors that nobody has read yet
+            ws[:_KV_STATUS].copy_(old[:_KV_STATUS])
         _kv_ws_cache[(device.index, raw)] = ws
     return ws
 
