@@ -451,6 +451,11 @@ ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, co
  * since the last read. */
 ssd_status ssd_read_status(void* workspace, size_t ws_bytes, int* status, void* stream);
 
+/* *id gets the number of the stream capture (CUDA graph) that `stream` is in,
+ * 0 if it is in none.  Calls captured in one sequence may share a workspace;
+ * two graphs that may run at the same time need two. */
+ssd_status ssd_stream_capture_id(void* stream, uint64_t* id);
+
 /* Static text for a status code. */
 const char* ssd_status_str(ssd_status status);
 

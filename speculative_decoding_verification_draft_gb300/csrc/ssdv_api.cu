@@ -832,6 +832,18 @@ ssd_status ssd_read_status(void* workspace, size_t ws_bytes, int* status, void* 
   return SSD_OK;
 }
 
+ssd_status ssd_stream_capture_id(void* stream, uint64_t* id) {
+  g_last_error.clear();
+  if (!id) return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  *id = 0;
+  cudaStreamCaptureStatus state = cudaStreamCaptureStatusNone;
+  unsigned long long n = 0;
+  const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &state, &n);
+  if (e != cudaSuccess) return cuda_fail(e, "capture query");
+  if (state != cudaStreamCaptureStatusNone) *id = n;
+  return SSD_OK;
+}
+
 const char* ssd_status_str(ssd_status status) {
   switch (status) {
     case SSD_OK: return "SSD_OK";

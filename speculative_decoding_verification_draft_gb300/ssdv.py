@@ -80,6 +80,7 @@ def _declare(lib):
     lib.ssd_kv_read.argtypes = [P, P, P, I, I, I, P, P, P, SZ, P]
     lib.ssd_kv_attention.argtypes = [P, P, P, P, P, I, I, I, I, F, I, I, P, P, P, SZ, P]
     lib.ssd_read_status.argtypes = [P, SZ, P, P]
+    lib.ssd_stream_capture_id.argtypes = [P, P]
     lib.ssd_debug_uniforms.argtypes = [U64, I, I, P, P]
     lib.ssd_status_str.argtypes = [I]
     lib.ssd_status_str.restype = ctypes.c_char_p
@@ -89,7 +90,7 @@ def _declare(lib):
                  "ssd_verify_ragged", "ssd_verify_ragged_pipelined", "ssd_saguaro_prespec", "ssd_debug_rowstats",
                  "ssd_debug_saguaro_stats", "ssd_read_status",
                  "ssd_verify_saguaro", "ssd_cache_check", "ssd_verify_saguaro_draft", "ssd_verify_top_p",
-                 "ssd_kv_append", "ssd_kv_read", "ssd_kv_attention", "ssd_debug_uniforms"):
+                 "ssd_kv_append", "ssd_kv_read", "ssd_kv_attention", "ssd_stream_capture_id", "ssd_debug_uniforms"):
         getattr(lib, name).restype = I
     return lib
 
@@ -428,7 +429,8 @@ def cache_check(bonus_topk: torch.Tensor, out_tokens: torch.Tensor, n_accepted: 
 
 KV_BLOCK = 16  # tokens per block of a cache page, elements per scale
 _KV_STATUS = 16  # bytes of a workspace that hold the status word
-_kv_ws_cache = {}
+_kv_ws_cache = {}  # (device, stream): 0 and the stream's workspace
+_kv_graph_ws = {}  # (device, stream): the last capture and its workspace
 _HERE = contextlib.nullcontext()
 # Small calls take a few microseconds on the GPU, so the binding of the cache calls
 # packs its structures itself and asks torch as little as it can.
@@ -506,28 +508,45 @@ def _kv_stream(stream, device):
                                   else torch.cuda.ExternalStream(raw, device=device))
 
 
+def _capture_id(raw: int) -> int:
+    """The number of the capture that a stream is in, 0 if it is in none."""
+    n = ctypes.c_uint64(0)
+    _check(lib().ssd_stream_capture_id(raw, ctypes.byref(n)))
+    return n.value
+
+
 def _kv_workspace(need: int, device, raw: int):
-    """The stream's own workspace (called with the stream current)."""
+    """The stream's own workspace (called with the stream current).  The calls of a
+    capture share one of their own, which the graph keeps: the stream's may be
+    replaced by a larger one, and a graph may run beside the stream."""
     if need == 0:
         return torch.empty(16, dtype=torch.uint8, device=device)  # the call names the bad argument
-    ws = _kv_ws_cache.get((device.index, raw))
-    if torch._C._cuda_isCurrentStreamCapturing():
-        # a graph keeps its own workspace: the cached one may be replaced by a larger
-        return torch.zeros(need, dtype=torch.uint8, device=device)
+    capture = _capture_id(raw) if torch._C._cuda_isCurrentStreamCapturing() else 0
+    cache = _kv_graph_ws if capture else _kv_ws_cache
+    of, ws = cache.get((device.index, raw), (0, None))
+    if of != capture:
+        ws = None
     if ws is None or ws.numel() < need:
-        old, ws = ws, torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        if old is not None:  # errors that nobody has read yet
-            ws[:_KV_STATUS].copy_(old[:_KV_STATUS])
-        _kv_ws_cache[(device.index, raw)] = ws
+        old, ws = ws, torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        # of a workspace only the status word is read before it is written
+        if old is None:
+            ws[:_KV_STATUS].zero_()
+        else:
+            ws[:_KV_STATUS].copy_(old[:_KV_STATUS])  # errors that nobody has read yet
+        cache[(device.index, raw)] = (capture, ws)
     return ws
 
 
 def kv_workspace(device=None, stream=None) -> Optional[torch.Tensor]:
     """The workspace that the kv_ calls without one use on this stream (None before
-    the first), for read_status."""
+    the first), for read_status.  Inside a capture it is the one of the calls
+    captured so far: kept, it tells the errors of the graph's last replay."""
     device = torch.device(device if device is not None else "cuda")
     index = device.index if device.index is not None else torch.cuda.current_device()
-    return _kv_ws_cache.get((index, _stream(stream)))
+    raw = _stream(stream)
+    capture = _capture_id(raw)
+    of, ws = (_kv_graph_ws if capture else _kv_ws_cache).get((index, raw), (0, None))
+    return ws if of == capture else None
 
 
 def kv_append(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, k: torch.Tensor, v: torch.Tensor,

@@ -25,3 +25,7 @@ def test_fewer_queries_than_it_was_made_for(lib, head_dim, n_q, per):  # noqa: F
             status = lib.ssd_kv_attention(cache(head_dim=head_dim), P, None, P, ST, dtype, 2, n, 2 * per, 0.1, 0, 0,
                                           ctypes.c_void_p(4104), None, P, size, None)
             assert ssdv.STATUS_NAMES[status] == "SSD_ERR_ALIGN", (n, dtype)
+
+
+def test_capture_id_arguments(lib):  # noqa: F811
+    assert ssdv.STATUS_NAMES[lib.ssd_stream_capture_id(None, None)] == "SSD_ERR_NULL"
