@@ -439,8 +439,9 @@ ssd_status ssd_kv_read(const ssd_kv_cache* cache, const int32_t* start, const in
  * Rows that see nothing, and rows past n_q[b], have out = 0 and lse = -inf.
  * What lies in masked places, NaN included, changes nothing.  1 <= n <=
  * SSD_MAX_GAMMA + 1, n_heads / n_kv_heads at most 128.  A request with a bad
- * length, or one that visits a bad page, has NaN outputs (ssd_kv_read: the rows
- * on that page; ssd_kv_append writes nothing for them) and sets a status bit. */
+ * length or count has NaN outputs, one that visits a bad page NaN for its n_q[b]
+ * queries (ssd_kv_read: for the rows on that page; ssd_kv_append writes nothing
+ * for them), and both set a status bit. */
 ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_q, const void* q,
                             const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
                             int window, int past_only, void* out, float* out_lse, void* workspace, size_t ws_bytes,

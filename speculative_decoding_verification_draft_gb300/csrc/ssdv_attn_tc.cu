@@ -1054,7 +1054,8 @@ struct Values {
           for (int u = 0; u < 4; ++u) l += lds_f(base + M::ends + (u * N + tid) * 4);
           m = lds_f(base + M::ends + (4 * N + tid) * 4);
         }
-        if (lost || w.dead() || (q.flags & Part::kBad)) l = __int_as_float(0x7FC00000);
+        // (a bad page is the queries' own rows' loss, bad lengths are every row's)
+        if ((q.flags & Part::kBad) || (tid < live && (lost || w.dead()))) l = __int_as_float(0x7FC00000);
         if (whole || tid >= live) {
           to = static_cast<__nv_bfloat16*>(a.out) + orow * kD;
           f = l == 0.f ? 0.f : 1.f / l;
