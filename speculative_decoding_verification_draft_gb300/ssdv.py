@@ -461,10 +461,18 @@ def make_kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, page_size: int =
                        device=device or "cuda")
 
 
+def _kv_dev(t: torch.Tensor, name: str, dtype, index: int) -> int:
+    """_dev of a tensor that has to be on the cache's device."""
+    ptr = _dev(t, name, dtype)
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on the cache's device, cuda:{index}, not on {t.device}")
+    return ptr
+
+
 def _kv_cache(cache: torch.Tensor, page_table: torch.Tensor, B: int):
     """(packed ssd_kv_cache, n_kv_heads, head_dim)"""
     ptr = _dev(cache, "cache", torch.uint8)
-    table = _dev(page_table, "page_table", torch.int32)
+    table = _kv_dev(page_table, "page_table", torch.int32, cache.get_device())
     shape, width = cache.shape, page_table.shape
     if len(shape) != 4 or shape[3] % 18:
         raise ValueError("cache must be [n_pages, n_kv_heads, page_size / 16, 18 * head_dim] (make_kv_cache)")
@@ -475,18 +483,20 @@ def _kv_cache(cache: torch.Tensor, page_table: torch.Tensor, B: int):
     return _KV_CACHE.pack(ptr, n_pages, heads, dim, blocks * KV_BLOCK, width[1], table), heads, dim
 
 
-def _kv_counts(t: Optional[torch.Tensor], name: str, B: int):
+def _kv_counts(t: Optional[torch.Tensor], name: str, B: int, index: int):
     if t is None:
         return None
     if t.shape != (B,):
         raise ValueError(f"{name} must be [{B}], got {list(t.shape)}")
-    return _dev(t, name, torch.int32)
+    return _kv_dev(t, name, torch.int32, index)
 
 
-def _kv_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int):
+def _kv_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, index: int):
     """Pointer and packed strides of [B, n, heads, head_dim] rows: any strides but the last."""
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on the cache's device, cuda:{index}, not on {t.device}")
     shape, st = t.shape, t.stride()
     if len(shape) != 4 or shape[3] != dim or (heads is not None and shape[2] != heads):
         raise ValueError(f"{name} must be [B, n, {heads or 'n_heads'}, {dim}], got {list(shape)}")
@@ -497,7 +507,11 @@ def _kv_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int):
 
 def _kv_stream(stream, device):
     """(raw stream, context that makes it current, or None): outputs and workspaces are
-    allocated on the stream that uses them."""
+    allocated on the stream that uses them.  The launch goes to the current device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {device}, which is not the current device")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"the cache is on {device}, the stream on {stream.device}")
     current = torch._C._cuda_getCurrentRawStream(device.index)
     if stream is None:
         return current, None
@@ -555,11 +569,12 @@ def kv_append(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tenso
     kv_len[b] .. kv_len[b] + n_new[b] - 1.  kv_len is not changed."""
     B, n = k.shape[:2]
     c, heads, dim = _kv_cache(cache, page_table, B)
-    kp, ks = _kv_rows(k, "k", heads, dim)
-    vp, vs = _kv_rows(v, "v", heads, dim)
+    index = cache.get_device()
+    kp, ks = _kv_rows(k, "k", heads, dim, index)
+    vp, vs = _kv_rows(v, "v", heads, dim, index)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must have one shape and dtype")
-    lens, news = _kv_counts(kv_len, "kv_len", B), _kv_counts(n_new, "n_new", B)
+    lens, news = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_new, "n_new", B, index)
     if B == 0 or n == 0:
         return
     raw, ctx = _kv_stream(stream, cache.device)
@@ -567,7 +582,8 @@ def kv_append(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tenso
     if ws is None:
         with ctx or _HERE:
             ws = _kv_workspace(256, cache.device, raw)
-    _check(lib().ssd_kv_append(c, lens, news, kp, ks, vp, vs, _dtype_code(k), B, n, _dev(ws, "workspace"), ws.numel(), raw))
+    _check(lib().ssd_kv_append(c, lens, news, kp, ks, vp, vs, _dtype_code(k), B, n, _kv_dev(ws, "workspace", None, index),
+                               ws.numel(), raw))
 
 
 def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, n: int, dtype=torch.bfloat16,
@@ -576,8 +592,8 @@ def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, 
     count[b] - 1 (rows past count[b] are zero); out: a pair of tensors to write them to."""
     B = page_table.shape[0]
     c, heads, dim = _kv_cache(cache, page_table, B)
-    starts, counts = _kv_counts(start, "start", B), _kv_counts(count, "count", B)
-    shape, device = (B, int(n), heads, dim), cache.device
+    shape, device, index = (B, int(n), heads, dim), cache.device, cache.get_device()
+    starts, counts = _kv_counts(start, "start", B, index), _kv_counts(count, "count", B, index)
     raw, ctx = _kv_stream(stream, device)
     ws = workspace
     with ctx or _HERE:
@@ -589,8 +605,8 @@ def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, 
         raise ValueError(f"out must be two tensors {list(shape)} of one dtype")
     if B == 0 or n == 0:
         return k, v
-    _check(lib().ssd_kv_read(c, starts, counts, _dtype_code(k), B, int(n), _dev(k, "out k"), _dev(v, "out v"),
-                             _dev(ws, "workspace"), ws.numel(), raw))
+    _check(lib().ssd_kv_read(c, starts, counts, _dtype_code(k), B, int(n), _kv_dev(k, "out k", None, index),
+                             _kv_dev(v, "out v", None, index), _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
     return k, v
 
 
@@ -607,8 +623,9 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
     if not -1 << 31 <= window < 1 << 31:
         raise ValueError(f"window={window} is no 32-bit number")
     c, kv_heads, dim = _kv_cache(cache, page_table, B)
-    qp, qs = _kv_rows(q, "q", None, dim)
-    lens, counts = _kv_counts(kv_len, "kv_len", B), _kv_counts(n_q, "n_q", B)
+    index = cache.get_device()
+    qp, qs = _kv_rows(q, "q", None, dim, index)
+    lens, counts = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_q, "n_q", B, index)
     raw, ctx = _kv_stream(stream, device)
     ws = workspace
     with ctx or _HERE:
@@ -623,9 +640,9 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
     if B and n:
         _check(lib().ssd_kv_attention(c, lens, counts, qp, qs, _dtype_code(q), B, n, heads,
                                       float(scale) if scale is not None else dim ** -0.5, window, int(past_only),
-                                      _dev(out, "out", q.dtype),
-                                      _dev(lse, "lse", torch.float32) if lse is not None else None,
-                                      _dev(ws, "workspace"), ws.numel(), raw))
+                                      _kv_dev(out, "out", q.dtype, index),
+                                      _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None,
+                                      _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
     return (out, lse) if lse is not None else out
 
 
