@@ -377,9 +377,10 @@ ssd_status ssd_debug_uniforms(uint64_t seed, int B, int W, float* out, void* str
  *
  * Pages: a pool of n_pages pages of page_size tokens (a multiple of 16) holds
  * for each kv head blocks of 16 tokens of 18 * head_dim bytes.  Request b's
- * token at position t lives in page page_table[b, t / page_size].  Requests may
- * share pages that no call writes.  The order of bytes inside a block is the
- * library's own: only ssd_kv_append writes it.
+ * token at position t lives in page page_table[b, t / page_size], max_pages *
+ * page_size at most 2^30.  Requests may share pages that no call writes.  The
+ * order of bytes inside a block is the library's own: only ssd_kv_append writes
+ * it.  Calls of more than 2^30 tokens a request are refused.
  * --------------------------------------------------------------------------- */
 typedef struct {
   void* pages;               /* n_pages * ssd_kv_page_bytes(...) bytes, 16-byte aligned */

@@ -887,7 +887,8 @@ ssd_status kv_check(const ssd_kv_cache* c, const int32_t* len, const int32_t* co
                 static_cast<long long>(c->n_pages), c->n_kv_heads, c->head_dim, c->page_size, c->max_pages);
   if (static_cast<long long>(c->max_pages) * c->page_size > (1 << 30))
     return fail(SSD_ERR_SHAPE, "max_pages * page_size above 2^30 tokens");
-  if (B < 1 || n < 1) return fail(SSD_ERR_SHAPE, "bad shape B=%d n=%d", B, n);
+  // (no request has more than 2^30 positions)
+  if (B < 1 || n < 1 || n > (1 << 30)) return fail(SSD_ERR_SHAPE, "bad shape B=%d n=%d", B, n);
   if (!aligned_to(c->pages, 16) || !aligned_to(c->page_table, 4) || !aligned_to(len, 4) ||
       (count && !aligned_to(count, 4)) || !aligned_to(workspace, 16))
     return fail(SSD_ERR_ALIGN, "pages and workspace need 16-byte alignment, int32 arrays 4-byte");
