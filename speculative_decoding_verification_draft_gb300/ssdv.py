@@ -112,12 +112,12 @@ def _check(status: int):
         raise SsdError(status, lib().ssd_last_error().decode())
 
 
-def _dtype_code(t: torch.Tensor) -> int:
+def _dtype_code(t: torch.Tensor, name: str = "logits") -> int:
     if t.dtype == torch.bfloat16:
         return SSD_BF16
     if t.dtype == torch.float32:
         return SSD_F32
-    raise TypeError(f"logits must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
@@ -582,8 +582,8 @@ def kv_append(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tenso
     if ws is None:
         with ctx or _HERE:
             ws = _kv_workspace(256, cache.device, raw)
-    _check(lib().ssd_kv_append(c, lens, news, kp, ks, vp, vs, _dtype_code(k), B, n, _kv_dev(ws, "workspace", None, index),
-                               ws.numel(), raw))
+    _check(lib().ssd_kv_append(c, lens, news, kp, ks, vp, vs, _dtype_code(k, "k and v"), B, n,
+                               _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
 
 
 def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, n: int, dtype=torch.bfloat16,
@@ -605,7 +605,7 @@ def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, 
         raise ValueError(f"out must be two tensors {list(shape)} of one dtype")
     if B == 0 or n == 0:
         return k, v
-    _check(lib().ssd_kv_read(c, starts, counts, _dtype_code(k), B, int(n), _kv_dev(k, "out k", None, index),
+    _check(lib().ssd_kv_read(c, starts, counts, _dtype_code(k, "outputs"), B, int(n), _kv_dev(k, "out k", None, index),
                              _kv_dev(v, "out v", None, index), _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
     return k, v
 
@@ -638,7 +638,7 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
     if out.shape != shape or (lse is not None and lse.shape != (B, n, heads)):
         raise ValueError("out must be shaped like q and lse [B, n, n_heads]")
     if B and n:
-        _check(lib().ssd_kv_attention(c, lens, counts, qp, qs, _dtype_code(q), B, n, heads,
+        _check(lib().ssd_kv_attention(c, lens, counts, qp, qs, _dtype_code(q, "q"), B, n, heads,
                                       float(scale) if scale is not None else dim ** -0.5, window, int(past_only),
                                       _kv_dev(out, "out", q.dtype, index),
                                       _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None,

@@ -72,3 +72,10 @@ def test_a_stream_of_another_device(lib, first_device, monkeypatch):
     t = arguments()
     with pytest.raises(ValueError, match="the stream on cuda:1"):
         ssdv.kv_append(t["cache"], t["table"], t["lens"], t["x"], t["y"], workspace=t["ws"], stream=Stream())
+
+
+@pytest.mark.parametrize("call,what", [("append", "k and v"), ("read", "outputs"), ("attention", "q")])
+def test_types_are_refused_by_name(monkeypatch, first_device, call, what):
+    monkeypatch.setattr(ssdv, "lib", lambda: type("Library", (), {"__getattr__": lambda self, function: None})())
+    with pytest.raises(TypeError, match=f"^{what} must be bfloat16 or float32, got torch.float16"):
+        calls(arguments(dtype=torch.float16))[call]()
