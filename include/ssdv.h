@@ -432,7 +432,7 @@ ssd_status ssd_kv_read(const ssd_kv_cache* cache, const int32_t* start, const in
  *             != 0: only those below kv_len[b] (the new tokens' own keys are
  *             attended to elsewhere and joined by out_lse)
  *   n_q       device [B], or NULL: n of every request
- *   scale     factor of q.k (finite)
+ *   scale     factor of q.k; scale * log2(e) has to be finite in fp32
  *   window    > 0: only the last `window` positions up to the query's own
  *   out       [B, n, n_heads, head_dim], q's type, contiguous, 16-byte aligned
  *   out_lse   [B, n, n_heads] fp32 or NULL: log sum exp(scale q.k)

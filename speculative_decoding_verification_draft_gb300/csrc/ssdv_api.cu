@@ -988,7 +988,8 @@ ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, co
                             int window, int past_only, void* out, float* out_lse, void* workspace, size_t ws_bytes,
                             void* stream) {
   g_last_error.clear();
-  if (!(fabsf(scale) <= 3.0e38f)) return fail(SSD_ERR_SHAPE, "scale is not finite");
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return fail(SSD_ERR_SHAPE, "scale=%g is not finite or above 2.3e38", scale);
   if (window < 0) return fail(SSD_ERR_SHAPE, "window=%d is negative", window);
   ssd_status st = kv_check(cache, kv_len, n_q, dtype, B, n, workspace, ws_bytes, 0);
   if (st != SSD_OK) return st;
@@ -1012,7 +1013,7 @@ ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, co
   a.nq = n;
   a.heads = n_heads;
   a.q = q;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.window = window;
   a.past_only = past_only != 0;
   a.out = out;
