@@ -463,10 +463,12 @@ def make_kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, page_size: int =
 
 def _kv_dev(t: torch.Tensor, name: str, dtype, index: int) -> int:
     """_dev of a tensor that has to be on the cache's device."""
-    ptr = _dev(t, name, dtype)
-    if t.get_device() != index:
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
+        _dev(t, name)
         raise ValueError(f"{name} must live on the cache's device, cuda:{index}, not on {t.device}")
-    return ptr
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
 
 
 def _kv_cache(cache: torch.Tensor, page_table: torch.Tensor, B: int):
@@ -493,9 +495,9 @@ def _kv_counts(t: Optional[torch.Tensor], name: str, B: int, index: int):
 
 def _kv_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, index: int):
     """Pointer and packed strides of [B, n, heads, head_dim] rows: any strides but the last."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
     if t.get_device() != index:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must live on a CUDA device")
         raise ValueError(f"{name} must live on the cache's device, cuda:{index}, not on {t.device}")
     shape, st = t.shape, t.stride()
     if len(shape) != 4 or shape[3] != dim or (heads is not None and shape[2] != heads):
@@ -508,13 +510,14 @@ def _kv_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, index: 
 def _kv_stream(stream, device):
     """(raw stream, context that makes it current, or None): outputs and workspaces are
     allocated on the stream that uses them.  The launch goes to the current device."""
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on {device}, which is not the current device")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"the cache is on {device}, the stream on {stream.device}")
-    current = torch._C._cuda_getCurrentRawStream(device.index)
+    current = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
         return current, None
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"the cache is on {device}, the stream on {stream.device}")
     raw = _stream(stream)
     if raw == current:
         return raw, None

@@ -33,7 +33,7 @@ def test_windows_of_more_than_32_bits(lib, window):
 @pytest.fixture
 def first_device(monkeypatch):
     """cuda:0 is current, its current stream is 0 and in no capture."""
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
 
