@@ -21,15 +21,16 @@
 // of the row's largest element; fp32: as two fp16 parts).  Weights are rounded
 // to fp16 for the second product (fp32 outputs: two parts), 2^15 at the largest
 // of the row in the tile, so that they keep 11 bits down to 2^-29 of it; a tile
-// with a smaller one, which real scores hardly hold, is passed over again for
-// the octaves below.  Each tile's product is added to the row's fp32 sums with
+// with a smaller one is passed over again for the octaves below (128 requests, one
+// query token: 82 us where no tile is, 176 with scores spread four times as far).
+// Each tile's product is added to the row's fp32 sums with
 // its own power of two, and maxima and sums of weights are in fp32.
 //
 // Measured: 128 requests of 301 to 6007 tokens, one query token, 4 query heads a
-// kv head of 128 (8 kv heads): 82 us, 3.5 TB/s, bound by the issue of instructions
-// (0.48 a cycle with two warps a scheduler) and their latency; twelve computing
-// warps of 152 registers in place of eight of 224: 82 us too, and short requests
-// slower.  32 requests, 10 rows of 256: 62 us, 1.7 TB/s, also instruction fetches.
+// kv head of 128 (8 kv heads): 80 us, 3.6 TB/s, bound by the latency of a tile's
+// steps (two warps a scheduler issue 0.48 a cycle); twelve computing warps of 152
+// registers in place of eight of 224: the same, and short requests slower.  32
+// requests, 10 rows of 256: 60 us, 1.8 TB/s, also instruction fetches.
 #include "ssdv_attn.cuh"
 
 #include <algorithm>
