@@ -1,14 +1,13 @@
-"""What the status word of the cache calls' own workspaces tells, and which rows a bad page touches."""
-import numpy as np
+"""What the status word of the cache calls' own workspaces tells."""
 import pytest
 import torch
 
 import kv_common as kc
-from test_gpu_kv_attention import fill, ssdv  # noqa: F401
+from test_gpu_kv_attention import ssdv  # noqa: F401
 
 pytestmark = pytest.mark.gpu
-BF16, F32 = torch.bfloat16, torch.float32
-LENGTH, PAGE = 13, 12
+BF16 = torch.bfloat16
+LENGTH = 13
 
 
 @pytest.mark.parametrize("on_a_stream", [False, True])
