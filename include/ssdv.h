@@ -84,7 +84,8 @@ typedef enum {
   SSD_ERR_GAMMA = 10,      /* (device) a per-request gamma above gamma_max       */
   SSD_ERR_DRAW = 11,       /* (device) a draw found no token of positive weight  */
   SSD_ERR_PAGE = 12,       /* (device) a page number outside [0, n_pages)        */
-  SSD_ERR_LENGTH = 13      /* (device) a length or count out of range            */
+  SSD_ERR_LENGTH = 13,     /* (device) a length or count out of range            */
+  SSD_ERR_POOL = 14        /* (device) too few free pages for a request          */
 } ssd_status;
 
 typedef enum { SSD_BF16 = 0, SSD_F32 = 1 } ssd_dtype;
@@ -447,6 +448,83 @@ ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, co
                             const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
                             int window, int past_only, void* out, float* out_lse, void* workspace, size_t ws_bytes,
                             void* stream);
+
+/* ---------------------------------------------------------------------------
+ * What a round needs around the cache: pages for the new tokens, and their keys
+ * and queries normed and rotated.
+ * --------------------------------------------------------------------------- */
+
+/* Pages for the tokens of a round.  After the call request b holds
+ *   max(n_shared[b], ceil((kv_len[b] + n_new[b]) / page_size))
+ * pages, in the first columns of its row of the page table.  Pages that it held
+ * beyond that are put onto the stack of free pages, in the order of requests and
+ * columns (kv_len = n_new = 0 gives all back); then the pages that requests lack
+ * are taken from the top of the stack in the same order.  A request is served if
+ * the pages wanted by it and those before it do not exceed those on the stack;
+ * one that is not keeps what it had, and the status says SSD_ERR_POOL.
+ *
+ *   page_table  device [B, max_pages]; n_held [B]: pages that each row holds
+ *   free_pages  device [n_pages], n_free [1]: the stack's first n_free entries
+ *               are free pages
+ *   kv_len      device [B]; n_new [B] or NULL (n of every request), at most n
+ *   n_shared    device [B] or NULL (none): the first columns of a row, counted
+ *               in n_held, that belong to others: they are never taken or given
+ *   out_*       the new state: the same four arrays (in place), or others, which
+ *               leave the state before the call as it was
+ *   slots       device [B, n] int64 or NULL: page * page_size + place in the page of
+ *               each new token, -1 past n_new[b] and for a request not served
+ *   workspace   >= ssd_kv_plan_workspace_bytes(B) bytes, zeroed once
+ *
+ * Cells of the table that are given back, and entries of the stack that are
+ * taken, become -1.  A request with a length or count out of range (or more than
+ * max_pages * page_size tokens) keeps what it had, has slots -1 and sets
+ * SSD_ERR_LENGTH; a stack with n_free outside [0, n_pages], or on which more than
+ * n_pages would lie, is left as it is with all the rest (SSD_ERR_PAGE).  Page
+ * numbers themselves are not looked at. */
+ssd_status ssd_kv_plan(const int32_t* page_table, const int32_t* n_held, const int32_t* free_pages,
+                       const int32_t* n_free, int B, int max_pages, int n_pages, int page_size, const int32_t* kv_len,
+                       const int32_t* n_new, int n, const int32_t* n_shared, int32_t* out_table, int32_t* out_held,
+                       int32_t* out_free, int32_t* out_n_free, int64_t* slots, void* workspace, size_t ws_bytes,
+                       void* stream);
+size_t ssd_kv_plan_workspace_bytes(int B);
+
+/* Norms of queries and keys for each head, and their rotation by position, in
+ * one pass.  For a row x of a head at position p = kv_len[b] + i:
+ *   y = x * w / sqrt(mean(x^2) + eps)                     (w NULL: y = x)
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t), t = p * inv_freq[j]
+ * for the pairs (a, b) = (j, j + rot_dim / 2), or (2 j, 2 j + 1) if interleaved,
+ * j < rot_dim / 2; elements from rot_dim on are not rotated.
+ *
+ *   q, k      [B, n, n_heads, head_dim] and [B, n, n_kv_heads, head_dim] bf16 or
+ *             fp32, strides as for ssd_kv_append; k may be NULL (n_kv_heads 0)
+ *   kv_len    device [B]; n_new [B] or NULL: n tokens of every request
+ *   q_weight, k_weight  device fp32 [head_dim], 16-byte aligned, or NULL: no norm
+ *   inv_freq  device fp32 [rot_dim / 2]; rot_dim a multiple of 16 up to head_dim, 0:
+ *             no rotation.  Angles are exact to 2^-24 of themselves and
+ *             p * 2^-63 half-turns (|inv_freq| up to 2^26)
+ *   out_q, out_k  of the inputs' shapes and type with strides of their own; the
+ *             inputs themselves (in place, same strides) or memory apart from them
+ *   workspace >= 256 bytes, zeroed once: its status word
+ *
+ * Rows past n_new[b] are not read and become zero.  A request with a negative
+ * length, a count outside [0, n] or positions above 2^30 has NaN rows and sets
+ * SSD_ERR_LENGTH. */
+ssd_status ssd_qk_norm_rope(const void* q, const int64_t q_strides[3], const void* k, const int64_t k_strides[3],
+                            ssd_dtype dtype, const int32_t* kv_len, const int32_t* n_new, int B, int n, int n_heads,
+                            int n_kv_heads, int head_dim, const float* q_weight, const float* k_weight, float eps,
+                            const float* inv_freq, int rot_dim, int interleaved, void* out_q,
+                            const int64_t out_q_strides[3], void* out_k, const int64_t out_k_strides[3],
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* ssd_kv_attention with a window (> 0) whose queries also see the first n_sinks
+ * positions, as far as the window has left them behind: the query at position p
+ * sees the positions t <= p (t < kv_len[b] with past_only) with t > p - window or
+ * t < n_sinks.  Without a window all positions are visible anyway.  n_sinks >= 0;
+ * everything else is as for ssd_kv_attention. */
+ssd_status ssd_kv_attention_sinks(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_q, const void* q,
+                                  const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
+                                  int window, int n_sinks, int past_only, void* out, float* out_lse, void* workspace,
+                                  size_t ws_bytes, void* stream);
 
 /* Read and clear the device status word of a workspace.  Synchronises
  * `stream`.  *status gets SSD_OK or the lowest-numbered device error seen

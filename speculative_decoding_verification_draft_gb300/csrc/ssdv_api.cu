@@ -17,6 +17,7 @@
 #include "ssdv_device.cuh"
 #include "ssdv_internal.h"
 #include "ssdv_kv.cuh"
+#include "ssdv_round.cuh"
 
 namespace ssdv {
 
@@ -859,6 +860,7 @@ const char* ssd_status_str(ssd_status status) {
     case SSD_ERR_GAMMA: return "SSD_ERR_GAMMA: a per-request gamma above gamma_max";
     case SSD_ERR_PAGE: return "SSD_ERR_PAGE: a page number outside the pool";
     case SSD_ERR_LENGTH: return "SSD_ERR_LENGTH: a length or count out of range";
+    case SSD_ERR_POOL: return "SSD_ERR_POOL: too few free pages for a request";
     case SSD_ERR_DRAW: return "SSD_ERR_DRAW: a draw found no token of positive weight";
   }
   return "unknown ssd_status";
@@ -899,6 +901,12 @@ ssd_status kv_check(const ssd_kv_cache* c, const int32_t* len, const int32_t* co
 KvCacheArgs kv_cache_args(const ssd_kv_cache* c) {
   return {static_cast<uint8_t*>(c->pages), static_cast<long long>(c->n_pages), c->n_kv_heads, c->page_size,
           c->max_pages, c->page_table};
+}
+
+// Whether two int32 arrays of n elements overlap without being one.
+bool partly(const int32_t* x, const int32_t* y, size_t n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a != b && a < b + 4 * n && b < a + 4 * n;
 }
 
 // Strides in elements; vec: every head's row starts on a 16-byte boundary.
@@ -987,10 +995,18 @@ ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, co
                             const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
                             int window, int past_only, void* out, float* out_lse, void* workspace, size_t ws_bytes,
                             void* stream) {
+  return ssd_kv_attention_sinks(cache, kv_len, n_q, q, q_strides, dtype, B, n, n_heads, scale, window, 0, past_only, out,
+                                out_lse, workspace, ws_bytes, stream);
+}
+
+ssd_status ssd_kv_attention_sinks(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_q, const void* q,
+                                  const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
+                                  int window, int n_sinks, int past_only, void* out, float* out_lse, void* workspace,
+                                  size_t ws_bytes, void* stream) {
   g_last_error.clear();
   const float scale_log2 = scale * 1.4426950408889634f;
   if (!std::isfinite(scale_log2)) return fail(SSD_ERR_SHAPE, "scale=%g is not finite or above 2.3e38", scale);
-  if (window < 0) return fail(SSD_ERR_SHAPE, "window=%d is negative", window);
+  if (window < 0 || n_sinks < 0) return fail(SSD_ERR_SHAPE, "window=%d or n_sinks=%d is negative", window, n_sinks);
   ssd_status st = kv_check(cache, kv_len, n_q, dtype, B, n, workspace, ws_bytes, 0);
   if (st != SSD_OK) return st;
   if (!q || !q_strides || !out) return fail(SSD_ERR_NULL, "a required pointer is NULL");
@@ -1015,6 +1031,7 @@ ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, co
   a.q = q;
   a.scale_log2 = scale_log2;
   a.window = window;
+  a.sinks = window ? n_sinks : 0;
   a.past_only = past_only != 0;
   a.out = out;
   a.lse = out_lse;
@@ -1022,6 +1039,118 @@ ssd_status ssd_kv_attention(const ssd_kv_cache* cache, const int32_t* kv_len, co
   a.work = static_cast<uint8_t*>(workspace) + kKvWorkOffset;
   const cudaError_t e = launch_kv_attention(a, cache->head_dim, esize_of(dtype), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SSD_OK : cuda_fail(e, "cache attention launch");
+}
+
+size_t ssd_kv_plan_workspace_bytes(int B) {
+  return B < 1 ? 0 : kKvWorkOffset + (static_cast<size_t>(B) + 1) * sizeof(int4);
+}
+
+ssd_status ssd_kv_plan(const int32_t* page_table, const int32_t* n_held, const int32_t* free_pages,
+                       const int32_t* n_free, int B, int max_pages, int n_pages, int page_size, const int32_t* kv_len,
+                       const int32_t* n_new, int n, const int32_t* n_shared, int32_t* out_table, int32_t* out_held,
+                       int32_t* out_free, int32_t* out_n_free, int64_t* slots, void* workspace, size_t ws_bytes,
+                       void* stream) {
+  g_last_error.clear();
+  if (!page_table || !n_held || !free_pages || !n_free || !kv_len || !out_table || !out_held || !out_free ||
+      !out_n_free || !workspace)
+    return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  if (B < 1 || max_pages < 1 || n_pages < 1 || page_size < kKvBlock || page_size % kKvBlock || n < 0 || n > (1 << 30))
+    return fail(SSD_ERR_SHAPE, "bad shape B=%d max_pages=%d n_pages=%d page_size=%d n=%d", B, max_pages, n_pages,
+                page_size, n);
+  if (static_cast<long long>(max_pages) * page_size > (1 << 30))
+    return fail(SSD_ERR_SHAPE, "max_pages * page_size above 2^30 tokens");
+  for (const void* p : {static_cast<const void*>(page_table), static_cast<const void*>(n_held),
+                        static_cast<const void*>(free_pages), static_cast<const void*>(n_free),
+                        static_cast<const void*>(kv_len), static_cast<const void*>(n_new),
+                        static_cast<const void*>(n_shared), static_cast<const void*>(out_table),
+                        static_cast<const void*>(out_held), static_cast<const void*>(out_free),
+                        static_cast<const void*>(out_n_free)})
+    if (!aligned_to(p, 4)) return fail(SSD_ERR_ALIGN, "int32 arrays need 4-byte alignment");
+  if (!aligned_to(slots, 8) || !aligned_to(workspace, 16))
+    return fail(SSD_ERR_ALIGN, "slots need 8-byte alignment, the workspace 16-byte");
+  const size_t need = ssd_kv_plan_workspace_bytes(B);
+  if (ws_bytes < need) return fail(SSD_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", ws_bytes, need);
+  const size_t cells = static_cast<size_t>(B) * max_pages;
+  if (partly(page_table, out_table, cells) || partly(n_held, out_held, B) || partly(free_pages, out_free, n_pages))
+    return fail(SSD_ERR_SHAPE, "an output lies partly over its input");
+  KvPlanArgs a = {};
+  a.table = page_table;
+  a.held = n_held;
+  a.free = free_pages;
+  a.n_free = n_free;
+  a.len = kv_len;
+  a.n_new = n_new;
+  a.shared = n_shared;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.n_pages = n_pages;
+  a.page_size = page_size;
+  a.n = n;
+  a.out_table = out_table;
+  a.out_held = out_held;
+  a.out_free = out_free;
+  a.out_n_free = out_n_free;
+  a.slots = n ? slots : nullptr;
+  a.status = static_cast<int32_t*>(workspace);
+  a.work = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + kKvWorkOffset);
+  const cudaError_t e = launch_kv_plan(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SSD_OK : cuda_fail(e, "page plan launch");
+}
+
+ssd_status ssd_qk_norm_rope(const void* q, const int64_t q_strides[3], const void* k, const int64_t k_strides[3],
+                            ssd_dtype dtype, const int32_t* kv_len, const int32_t* n_new, int B, int n, int n_heads,
+                            int n_kv_heads, int head_dim, const float* q_weight, const float* k_weight, float eps,
+                            const float* inv_freq, int rot_dim, int interleaved, void* out_q,
+                            const int64_t out_q_strides[3], void* out_k, const int64_t out_k_strides[3],
+                            void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  const int es = esize_of(dtype);
+  if (es == 0) return fail(SSD_ERR_DTYPE, "unknown dtype %d", static_cast<int>(dtype));
+  if (!q || !q_strides || !out_q || !out_q_strides || !kv_len || !workspace || (rot_dim > 0 && !inv_freq) ||
+      (n_kv_heads > 0 && (!k || !k_strides || !out_k || !out_k_strides)))
+    return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  if (B < 1 || n < 1 || n > (1 << 30) || n_heads < 1 || n_heads > 65535 || n_kv_heads < 0 || n_kv_heads > 65535 ||
+      !kv_dim_valid(head_dim))
+    return fail(SSD_ERR_SHAPE, "bad shape B=%d n=%d n_heads=%d n_kv_heads=%d head_dim=%d", B, n, n_heads, n_kv_heads,
+                head_dim);
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
+    return fail(SSD_ERR_SHAPE, "rot_dim=%d is no multiple of 16 up to %d", rot_dim, head_dim);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SSD_ERR_SHAPE, "eps=%g is negative or not finite", eps);
+  if (static_cast<double>(B) * n * ((n_heads + n_kv_heads) / 8 + 1) >= 2147483648.0)
+    return fail(SSD_ERR_SHAPE, "grid too large");
+  if (!aligned_to(kv_len, 4) || !aligned_to(n_new, 4) || !aligned_to(q_weight, 16) || !aligned_to(k_weight, 16) ||
+      !aligned_to(inv_freq, 4) || !aligned_to(workspace, 16))
+    return fail(SSD_ERR_ALIGN, "weights and workspace need 16-byte alignment, the other arrays 4-byte");
+  if (ws_bytes < kKvWorkOffset)
+    return fail(SSD_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", ws_bytes, kKvWorkOffset);
+  RopeArgs a = {};
+  bool vec = true;
+  ssd_status st = kv_strides(q, q_strides, es, a.qs, &vec);
+  if (st == SSD_OK) st = kv_strides(out_q, out_q_strides, es, a.oqs, &vec);
+  if (st == SSD_OK && n_kv_heads) st = kv_strides(k, k_strides, es, a.ks, &vec);
+  if (st == SSD_OK && n_kv_heads) st = kv_strides(out_k, out_k_strides, es, a.oks, &vec);
+  if (st != SSD_OK) return st;
+  for (int i = 0; i < 3; ++i)
+    if ((q == out_q && a.qs[i] != a.oqs[i]) || (n_kv_heads && k == out_k && a.ks[i] != a.oks[i]))
+      return fail(SSD_ERR_SHAPE, "in place, the strides have to be the input's");
+  a.q = q;
+  a.k = k;
+  a.out_q = out_q;
+  a.out_k = out_k;
+  a.len = kv_len;
+  a.n_new = n_new;
+  a.B = B;
+  a.n = n;
+  a.heads = n_heads;
+  a.kv_heads = n_kv_heads;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.freq = inv_freq;
+  a.eps = eps;
+  a.rot = rot_dim;
+  a.status = static_cast<int32_t*>(workspace);
+  const cudaError_t e = launch_rope(a, head_dim, es, interleaved != 0, vec, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SSD_OK : cuda_fail(e, "norm and rotation launch");
 }
 
 }  // extern "C"

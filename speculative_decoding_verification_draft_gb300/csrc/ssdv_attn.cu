@@ -215,7 +215,7 @@ __device__ __forceinline__ void load_queries(const AttnLaunch& L, Rows<E, D, NT,
   __syncwarp();  // the rows before are done with shared memory
   for (int k = lane; k < NT * 8; k += 32) {
     const int i = (row0 + k) / L.per;
-    span[k] = make_int2(row_lo(L.a, sp.len, i), min(row_hi(L.a, sp.len, i), sp.hi));
+    span[k] = make_int2(row_lo(L.a, sp, i), min(row_hi(L.a, sp.len, i), sp.hi));
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -284,8 +284,9 @@ __device__ __forceinline__ void load_queries(const AttnLaunch& L, Rows<E, D, NT,
 // `edge`: some row does not see some token.  Returns the further bands (bits)
 // that a first pass, band 0, leaves to be done.
 template <typename E, int D, int NT, int P, int NA>
-__device__ __forceinline__ uint32_t tile_step(Rows<E, D, NT, P>& w, uint32_t base, int pos0, bool edge, int lo_seen,
-                                              int hi_seen, int lane, int sync, int buf, int band) {
+__device__ __forceinline__ uint32_t tile_step(const KvAttnArgs& a, Rows<E, D, NT, P>& w, uint32_t base, int pos0,
+                                              bool edge, int lo_seen, int hi_seen, int lane, int sync, int buf,
+                                              int band) {
   using W = Rows<E, D, NT, P>;
   const int r = lane >> 2, c = lane & 3;
   float s[W::kJ][NA][4];
@@ -382,7 +383,7 @@ __device__ __forceinline__ uint32_t tile_step(Rows<E, D, NT, P>& w, uint32_t bas
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const int pos = pos0 + (r >> 1) * kKvBlock + 4 * (w.pw * W::kJ + j) + (r & 1) + 2 * y;
-            if (pos < seen.x || pos >= seen.y) s[j][nt][2 * y + x] = -INFINITY;
+            if (!in_span(a, seen.x, seen.y, pos)) s[j][nt][2 * y + x] = -INFINITY;
           }
       }
     }
@@ -544,7 +545,7 @@ __device__ __forceinline__ uint32_t tile_step(Rows<E, D, NT, P>& w, uint32_t bas
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const uint32_t byte = (sc[k >> 2] >> ((k & 3) * 8)) & 0xFFu;
-        const bool seen = first + k >= lo_seen && first + k < hi_seen;
+        const bool seen = in_span(a, lo_seen, hi_seen, first + k);
         if (seen && byte == kKvNanByte) nans |= 1u << k;
         if (!seen || byte == kKvNanByte) sc[k >> 2] &= ~(0xFFu << ((k & 3) * 8));
       }
@@ -614,7 +615,8 @@ __device__ __forceinline__ uint32_t tile_step(Rows<E, D, NT, P>& w, uint32_t bas
           for (int x = 0; x < 2; ++x) {
             const int2 seen = w.span[nt * 8 + 2 * c + x];
             const int from = max(0, min(seen.x - first, 16)), to = max(0, min(seen.y - first, 16));
-            if (there & ((1u << to) - 1u) & ~((1u << from) - 1u))
+            const int sinks = max(0, min(a.sinks - first, 16));
+            if (there & ((1u << to) - 1u) & (~((1u << from) - 1u) | ((1u << sinks) - 1u)))
 #pragma unroll
               for (int ii = 0; ii < kMost; ++ii) {
                 w.o[gg * kMost + ii][nt][x] = __int_as_float(0x7FC00000);
@@ -644,13 +646,13 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List<kTile>& 
   int page = 0;
   bool want = false;          // the next tile has this lane's block
   const auto locate = [&]() {
-    const int pb = (pr.s.tile0 + pr.tile) * (kTile / kKvBlock) + (lane & 3);
+    const int pb = pr.s.tile(pr.tile) * (kTile / kKvBlock) + (lane & 3);
     column = pb / bpp;
     sub = pb % bpp;
   };
   const auto fetch_page = [&]() {
-    const int pos = (pr.s.tile0 + pr.tile) * kTile + (lane & 3) * kKvBlock;
-    want = pos < pr.s.hi && pos + kKvBlock > pr.s.lo;
+    const int pos = pr.s.tile(pr.tile) * kTile + (lane & 3) * kKvBlock;
+    want = pr.s.any && pos < pr.s.hi && (pos + kKvBlock > pr.s.lo || pos < a.sinks);
     if (want) page = a.c.page_table[static_cast<long long>(pr.b) * a.c.max_pages + column];
   };
   if (left) {
@@ -685,7 +687,7 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List<kTile>& 
       if (++put == S) put = 0, phase ^= 1;
       if (--left) {
         pr.next(a, list.per_request);
-        if (pr.tile == 0 || bpp < 4) {
+        if (pr.tile == 0 || pr.tile == pr.s.ahead || bpp < 4) {
           locate();
         } else if ((sub += 4) >= bpp) {
           sub -= bpp;
@@ -729,8 +731,8 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
     const int n8 = max(0, (min(nrows - pass0, L.rows_pass) + 7) / 8);
     const int row0 = pass0 + group * n8 / G * 8;
     const int own = (group + 1) * n8 / G - group * n8 / G;
-    const int active = sp.hi > sp.lo ? own : 0;
-    const int lo_last = row_lo(a, sp.len, sp.nq - 1), hi_first = row_hi(a, sp.len, 0);
+    const int active = sp.any ? own : 0;
+    const int lo_last = row_lo(a, sp, sp.nq - 1), hi_first = row_hi(a, sp.len, 0);
     bool bad = sp.bad;
     load_queries<E, D, NT, P>(L, w, b, h, row0, nrows, sp, spans, lane, sync);
     for (int k = 0; k < count; ++k, ++done) {
@@ -738,16 +740,16 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
       if (!dead && !bar_wait(bar, phase)) dead = true;
       bad |= flags[team * S + take] != 0;
       const uint32_t tile = data + (team * S + take) * stage_bytes(D);
-      const int pos0 = (sp.tile0 + first + k) * kTile;
-      const bool edge = pos0 < lo_last || pos0 + kTile > hi_first;
+      const int pos0 = sp.tile(first + k) * kTile;
+      const bool edge = (pos0 < lo_last && pos0 + kTile > a.sinks) || pos0 + kTile > hi_first;
       for (uint32_t todo = active ? 1 : 0; todo;) {
         const int band = __ffs(todo) - 1;
         todo &= todo - 1;
         constexpr int kHalf = (NT + 1) / 2;
         if (kHalf < NT && active <= kHalf)
-          todo |= tile_step<E, D, NT, P, kHalf>(w, tile, pos0, edge, sp.lo, sp.hi, lane, sync, buf, band);
+          todo |= tile_step<E, D, NT, P, kHalf>(a, w, tile, pos0, edge, sp.lo, sp.hi, lane, sync, buf, band);
         else
-          todo |= tile_step<E, D, NT, P, NT>(w, tile, pos0, edge, sp.lo, sp.hi, lane, sync, buf, band);
+          todo |= tile_step<E, D, NT, P, NT>(a, w, tile, pos0, edge, sp.lo, sp.hi, lane, sync, buf, band);
         buf ^= 1;
       }
       __syncwarp();
@@ -790,7 +792,7 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
         if (nt >= own || row >= nrows) continue;  // (a padded query's row went along with its tile)
         float l = w.l[nt][x];
         if (bad) l = __int_as_float(0x7FC00000);
-        if (whole) {
+        if (whole && !a.own_ml) {
           const int i = row / L.per;
           const long long orow = (static_cast<long long>(b) * a.nq + i) * a.heads + h * L.per + row % L.per;
           const float inv = 1.f / l;
@@ -811,19 +813,20 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
           if (a.lse && r == 0 && pw == 0)
             a.lse[orow] = l == 0.f ? -INFINITY : (w.m[nt][x] + (log2f(l) - kBias)) * 0.69314718055994531f;
         } else {
-          const long long at_row = slot * L.rows_pass + (row - pass0);
-          float4* o = reinterpret_cast<float4*>(L.o + at_row * D + d0);
+          const long long at_row =
+              whole ? (static_cast<long long>(b) * a.c.kv_heads + h) * L.rows + row : slot * L.rows_pass + (row - pass0);
+          float4* o = reinterpret_cast<float4*>((whole ? a.own_o : L.o) + at_row * D + d0);
 #pragma unroll
           for (int v = 0; v < kOwn / 4; ++v)
             o[v] = make_float4(w.o[2 * v][nt][x], w.o[2 * v][nt][2 + x], w.o[2 * v + 1][nt][x], w.o[2 * v + 1][nt][2 + x]);
-          if (r == 0 && pw == 0) L.ml[at_row] = make_float2(w.m[nt][x], l);
+          if (r == 0 && pw == 0) (whole ? a.own_ml : L.ml)[at_row] = make_float2(w.m[nt][x], l);
         }
       }
     if (first == 0) {
       // rows past the request's own (all of them if its lengths are bad)
       if (sp.bad && at.hr == 0 && first_warp && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
       const float none = sp.bad ? __int_as_float(0x7FC00000) : 0.f;
-      const int end = min(pass0 + L.rows_pass, L.rows);
+      const int end = a.own_ml ? 0 : min(pass0 + L.rows_pass, L.rows);
       for (int row = max(pass0, nrows) + group * P + pw; row < end; row += G * P) {
         const long long orow = (static_cast<long long>(b) * a.nq + row / L.per) * a.heads + h * L.per + row % L.per;
         for (int d = lane; d < D; d += 32) static_cast<E*>(a.out)[orow * D + d] = static_cast<E>(none);
@@ -906,6 +909,14 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnLaunch L) {
     }
   }
   const int i = row / L.per, h = d.y / RT;
+  if (L.a.own_ml) {
+    const long long at = (static_cast<long long>(d.x) * L.a.c.kv_heads + h) * L.rows + row;
+    if (lane == 0) L.a.own_ml[at] = make_float2(ref, l);
+#pragma unroll
+    for (int v = 0; v < kPer / 2; ++v)
+      reinterpret_cast<float2*>(L.a.own_o + at * D + lane * kPer)[v] = make_float2(y[2 * v], y[2 * v + 1]);
+    return;
+  }
   const long long orow = (static_cast<long long>(d.x) * L.a.nq + i) * L.a.heads + h * L.per + row % L.per;
   const float inv = 1.f / l;
   E* out = static_cast<E*>(L.a.out) + orow * D + lane * kPer;

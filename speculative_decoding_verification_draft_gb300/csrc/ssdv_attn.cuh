@@ -175,9 +175,15 @@ __device__ __forceinline__ void sts64(uint32_t p, uint2 v) {
 // What a request's rows see together, and its tiles.
 struct Span {
   int len, nq;     // query rows i < nq are real
-  int lo, hi;      // positions some row sees
-  int tile0, tiles;  // at least one tile, so that some team writes the outputs
-  bool bad;
+  int lo, hi;      // positions some row sees, beside those below a.sinks
+  // Tile t is tile0 + t of the sequence for t < ahead and t - ahead after that: the
+  // tiles of sinks come last, so that their large scores do not become the
+  // reference of a window's small ones.  At least one tile, so that some team
+  // writes the outputs.
+  int tile0, ahead, tiles;
+  int first;
+  bool bad, any;   // any: some row sees something
+  __device__ __forceinline__ int tile(int t) const { return t < ahead ? tile0 + t : t - ahead; }
 };
 template <int kTile>
 __device__ __forceinline__ Span find_span(const KvAttnArgs& a, int b) {
@@ -187,21 +193,35 @@ __device__ __forceinline__ Span find_span(const KvAttnArgs& a, int b) {
   s.bad = s.len < 0 || s.nq < 0 || s.nq > a.nq ||
           static_cast<long long>(s.len) + (a.past_only ? 0 : s.nq) >
               static_cast<long long>(a.c.max_pages) * a.c.page_size;
-  s.lo = s.hi = s.tile0 = 0;
-  s.tiles = 1;
-  if (s.bad || s.nq == 0) return s;
-  s.hi = a.past_only ? s.len : s.len + s.nq;
-  s.lo = a.window ? max(0, s.len + 1 - a.window) : 0;
-  if (s.lo >= s.hi) {
-    s.lo = s.hi = 0;
-    return s;
+  s.lo = s.hi = s.tile0 = s.first = 0;
+  s.tiles = s.ahead = 1;
+  s.any = false;
+  if (a.first) {
+    s.first = a.first[b];
+    s.bad |= s.first < 0 || s.first > s.len;
   }
-  s.tile0 = s.lo / kTile;
-  s.tiles = (s.hi + kTile - 1) / kTile - s.tile0;
+  if (s.bad || s.nq == 0) return s;
+  const int hi = a.past_only ? s.len : s.len + s.nq;
+  const int lo = min(a.window ? max(0, s.len + 1 - a.window) : s.first, hi);
+  const int sink_tiles = (min(a.sinks, lo) + kTile - 1) / kTile;
+  const int tile0 = max(lo / kTile, sink_tiles), ahead = max((hi + kTile - 1) / kTile - tile0, 0);
+  // (a window that lies behind the past holds nothing, whatever tile it ends in)
+  const int seen = lo < hi ? ahead : 0;
+  if (seen + sink_tiles == 0) return s;
+  s.any = true;
+  s.lo = lo;
+  s.hi = hi;
+  s.tile0 = tile0;
+  s.ahead = seen;
+  s.tiles = seen + sink_tiles;
   return s;
 }
-__device__ __forceinline__ int row_lo(const KvAttnArgs& a, int len, int i) {
-  return a.window ? max(0, len + i + 1 - a.window) : 0;
+__device__ __forceinline__ int row_lo(const KvAttnArgs& a, const Span& s, int i) {
+  return a.window ? max(0, s.len + i + 1 - a.window) : s.first;
+}
+// Whether some row sees a position of a request.
+__device__ __forceinline__ bool in_span(const KvAttnArgs& a, int lo, int hi, int pos) {
+  return pos < hi && (pos >= lo || pos < a.sinks);
 }
 __device__ __forceinline__ int row_hi(const KvAttnArgs& a, int len, int i) { return a.past_only ? len : len + i + 1; }
 

@@ -311,12 +311,17 @@ struct Waiter {
 // and describes them in a ring in shared memory.
 struct Part {
   int b, head, pass0, first, count;  // first: among the row's tiles
-  int len, nq, lo, hi, tile0;        // as in Span
+  int len, nq, lo, hi, tile0, ahead; // as in Span
   int flags;
   int inner_lo, inner_hi;            // every row sees these positions
-  static constexpr int kLater = 1, kWhole = 2, kBad = 4, kEnd = 8;
-  __device__ __forceinline__ bool active() const { return hi > lo; }
-  __device__ __forceinline__ bool edge(int pos0) const { return pos0 < inner_lo || pos0 + kTile > inner_hi; }
+  static constexpr int kLater = 1, kWhole = 2, kBad = 4, kEnd = 8, kActive = 16;
+  __device__ __forceinline__ bool active() const { return flags & kActive; }
+  __device__ __forceinline__ int pos0(int k) const {
+    return (first + k < ahead ? tile0 + first + k : first + k - ahead) * kTile;
+  }
+  __device__ __forceinline__ bool edge(int pos0, int sinks) const {
+    return (pos0 < inner_lo && pos0 + kTile > sinks) || pos0 + kTile > inner_hi;
+  }
 };
 template <int N>
 struct Ring {
@@ -331,7 +336,8 @@ struct Ring {
     p.b = x.x, p.head = x.y, p.pass0 = x.z, p.first = x.w;
     p.count = __shfl_sync(~0u, y.x, 0), p.len = y.y, p.nq = y.z, p.lo = y.w;
     p.hi = z.x, p.tile0 = z.y, p.flags = z.z, p.inner_lo = z.w;
-    p.inner_hi = static_cast<int>(lds32(from + 48));
+    const uint2 v = lds64(from + 48);
+    p.inner_hi = v.x, p.ahead = v.y;
     return p;
   }
   __device__ __forceinline__ void release(int k, int lane) {
@@ -352,11 +358,12 @@ struct Ring {
 template <int N>
 __device__ __forceinline__ int2 rows_seeing(const AttnLaunch& L, const Part& p, int pos) {
   const KvAttnArgs& a = L.a;
-  if (pos < p.lo || pos >= p.hi) return make_int2(0, 0);
-  // query i sees it if i >= pos - len (its own key included) and i < pos - len + window
+  if (!in_span(a, p.lo, p.hi, pos)) return make_int2(0, 0);
+  // query i sees it if i >= pos - len (its own key included) and i < pos - len + window,
+  // or if it is a sink
   const int i = pos - p.len;
   const int lo = a.past_only || i <= 0 ? 0 : i * L.per - p.pass0;
-  const long long hi = a.window ? (static_cast<long long>(i) + a.window) * L.per - p.pass0 : N;
+  const long long hi = a.window && pos >= a.sinks ? (static_cast<long long>(i) + a.window) * L.per - p.pass0 : N;
   return make_int2(max(lo, 0), static_cast<int>(max(0ll, min(hi, static_cast<long long>(N)))));
 }
 
@@ -380,32 +387,34 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
     Part p;
     p.b = place.b, p.head = place.hr / L.p.rt, p.pass0 = place.hr % L.p.rt * N, p.first = place.tile;
     p.count = min(left, place.s.tiles - place.tile), p.lo = place.s.lo, p.hi = place.s.hi, p.tile0 = place.s.tile0;
+    p.ahead = place.s.ahead;
     w.nap(kPartEmpty + n % kRing, (n / kRing) ^ 1);
     if (lane == 0) {
       const uint32_t to = base + Smem<N>::parts + n % kRing * 64;
       const int flags = (n ? Part::kLater : 0) | (p.first == 0 && p.count == place.s.tiles ? Part::kWhole : 0) |
-                        (place.s.bad ? Part::kBad : 0) | (left ? 0 : Part::kEnd);
+                        (place.s.bad ? Part::kBad : 0) | (left ? 0 : Part::kEnd) | (place.s.any ? Part::kActive : 0);
       sts128(to, make_uint4(p.b, p.head, p.pass0, p.first));
       sts128(to + 16, make_uint4(p.count, place.s.len, place.s.nq, p.lo));
-      sts128(to + 32, make_uint4(p.hi, p.tile0, flags, row_lo(a, place.s.len, place.s.nq - 1)));
-      sts32(to + 48, row_hi(a, place.s.len, 0));
+      sts128(to + 32, make_uint4(p.hi, p.tile0, flags, row_lo(a, place.s, place.s.nq - 1)));
+      sts64(to + 48, make_uint2(row_hi(a, place.s.len, 0), p.ahead));
       w.arrive(kPartFull + n % kRing);
     }
     if (!left || w.dead()) break;
+    const bool any = place.s.any;
     left -= p.count;
     place.tile += p.count - 1;
     if (left) place.next(a, list.per_request);
-    if (!p.active()) continue;
+    if (!any) continue;
     const int32_t* table = a.c.page_table + static_cast<long long>(p.b) * a.c.max_pages;
     const long long head = p.head * head_bytes;
     const auto seen = [&](int k) {
-      const int pos = (p.tile0 + p.first + k) * kTile + (lane & 7) * kKvBlock;
-      return k < p.count && pos < p.hi && pos + kKvBlock > p.lo;
+      const int pos = p.pos0(k) + (lane & 7) * kKvBlock;
+      return k < p.count && pos < p.hi && (pos + kKvBlock > p.lo || pos < a.sinks);
     };
     // the lane's block: its page's column of the table, and its place in the page;
     // page numbers are read a tile ahead
-    int col = ((p.tile0 + p.first) * kBlocks + (lane & 7)) / bpp;
-    int sub = ((p.tile0 + p.first) * kBlocks + (lane & 7)) - col * bpp;
+    int col = (p.pos0(0) / kKvBlock + (lane & 7)) / bpp;
+    int sub = (p.pos0(0) / kKvBlock + (lane & 7)) - col * bpp;
     bool want = seen(0);
     int page = want ? table[col] : 0;
 #pragma unroll 1
@@ -415,7 +424,10 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
       const bool lacks = (__ballot_sync(~0u, want && !ok) & 0xFFu) != 0;
       const long long at = page * page_bytes + head + static_cast<long long>(sub) * kv_block_bytes(kD);
       sub += kBlocks;
-      if (sub >= bpp) {
+      if (p.first + k + 1 == p.ahead) {  // on to the sinks
+        col = (lane & 7) / bpp;
+        sub = (lane & 7) - col * bpp;
+      } else if (sub >= bpp) {
         const int q = bpp >= kBlocks ? 1 : sub / bpp;
         col += q;
         sub -= q * bpp;
@@ -725,8 +737,8 @@ __device__ __forceinline__ void weight_role(const AttnLaunch& L, uint32_t base, 
 #pragma unroll 1
     for (int k = 0; k < p.count; ++k, ++tile) {
       const int sb = tile & 1;
-      const int pos0 = (p.tile0 + p.first + k) * kTile;
-      const bool edge = p.edge(pos0);
+      const int pos0 = p.pos0(k);
+      const bool edge = p.edge(pos0, L.a.sinks);
       int2 seen = make_int2(0, H);  // which of its rows see the token
       if (edge) {
         seen = rows_seeing<N>(L, p, pos0 + token);
@@ -937,7 +949,7 @@ struct Values {
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
         const uint32_t byte = static_cast<uint32_t>(bytes >> (k * 8)) & 0xFFu;
-        const bool seen = first + k >= q.lo && first + k < q.hi;
+        const bool seen = in_span(a, q.lo, q.hi, first + k);
         if (seen && byte == kKvNanByte) mask |= 1u << k;
         if (!seen || byte == kKvNanByte) bytes &= ~(0xFFull << (k * 8));
       }
@@ -1034,7 +1046,7 @@ struct Values {
   // Writes a part's results; `nans`: rows whose sums a NaN belongs to.
   __device__ __forceinline__ void finish(const Part& q, bool lost, unsigned long long nans) {
     const int nrows = q.flags & Part::kBad ? 0 : q.nq * L.per, ob = n_parts % Tmem<N>::kOuts;
-    const bool whole = q.flags & Part::kWhole, active = q.active();
+    const bool whole = q.flags & Part::kWhole, active = q.active(), direct = whole && !a.own_ml;
     if ((q.flags & Part::kBad) && q.head == 0 && q.pass0 == 0 && tid == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
     if (active) {
       w.wait(kEndFull, n_parts);
@@ -1044,6 +1056,7 @@ struct Values {
     // a thread per row: its factor, and where a whole row goes
     const uint32_t factors = base + M::rows, staged = base + M::results;
     const int live = min(nrows - q.pass0, N);  // rows that are real
+    const long long own = (static_cast<long long>(q.b) * a.c.kv_heads + q.head) * L.rows + q.pass0;
     const long long slot = (2ll * blockIdx.x + (q.first == 0 && (q.flags & Part::kLater) ? 1 : 0)) * N;
     __nv_bfloat16* to = nullptr;
     if (tid < N) {
@@ -1060,7 +1073,10 @@ struct Values {
         }
         // (a bad page is the queries' own rows' loss, bad lengths are every row's)
         if ((q.flags & Part::kBad) || (tid < live && (lost || w.dead()))) l = __int_as_float(0x7FC00000);
-        if (whole || tid >= live) {
+        if (a.own_ml && (whole || tid >= live)) {
+          f = 1 << (kTop - kFast);
+          if (tid < live) a.own_ml[own + tid] = make_float2(m, l * f);
+        } else if (whole || tid >= live) {
           to = static_cast<__nv_bfloat16*>(a.out) + orow * kD;
           f = l == 0.f ? 0.f : 1.f / l;
           if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + (log2f(l) - kFast)) * 0.69314718055994531f;
@@ -1096,7 +1112,7 @@ struct Values {
       const uint32_t f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
 #pragma unroll
       for (int y = 0; y < 8; ++y) o[y] *= __uint_as_float(f[y]);
-      if (whole) {
+      if (direct) {
 #pragma unroll
         for (int y = 0; y < 8; y += 2) {
           const __nv_bfloat162 h = __floats2bfloat162_rn(o[y], o[y + 1]);
@@ -1105,13 +1121,13 @@ struct Values {
           sts16(staged + (n0 + y + 1) * (kD * 2) + element * 2, x >> 16);
         }
       } else {
-        float* part = L.o + (slot + n0) * kD + element;
+        float* part = (whole ? a.own_o + (own + n0) * kD : L.o + (slot + n0) * kD) + element;
 #pragma unroll
         for (int y = 0; y < 8; ++y)
           if (n0 + y < live) part[y * kD] = o[y];
       }
     }
-    if (whole) {
+    if (direct) {
       async_fence();
       group_sync(kSync);
       if (to)
@@ -1160,10 +1176,10 @@ __device__ __forceinline__ void value_role(const AttnLaunch& L, uint32_t base, u
     }
     const bool have = more && p.active();
     if (have) {
-      const int pos0 = (p.tile0 + p.first + k) * kTile;
+      const int pos0 = p.pos0(k);
       v.w.wait(kFull + st, phase);
       lost |= lds32(base + Smem<N>::words + 16 + st * 4) != 0;
-      nans |= v.unpack(st, tile & 1, tile, pos0, p.edge(pos0), p);
+      nans |= v.unpack(st, tile & 1, tile, pos0, p.edge(pos0, L.a.sinks), p);
       if (++st == S) st = 0, phase ^= 1;
       ++tile;
     }

@@ -82,9 +82,13 @@ struct KvAttnArgs {
   long long qs[3];        // element strides of request, token, head
   float scale_log2;       // scale * log2(e)
   int window;             // 0: none
+  int sinks;              // with a window: the first positions stay visible (0: none)
   int past_only;
+  const int32_t* first;   // [B] or null: positions below first[b] are left out (without sinks)
   void* out;              // [B, nq, heads, D]
   float* lse;             // [B, nq, heads] or null
+  float2* own_ml;         // in place of out and lse, or null: [B, kv_heads, nq * heads / kv_heads] maximum and sum
+  float* own_o;           // and [.., D] sums of the rows that are real, as parts keep them
   int32_t* status;
   uint8_t* work;          // partial results
 };

@@ -1,0 +1,222 @@
+// ssdv_plan.cu -- page tables, held pages and slots from the requests' lengths.
+//
+// Request b is to hold h_b = max(shared_b, ceil((len_b + new_b) / page_size))
+// pages.  What it holds beyond that goes onto the stack of free pages, in the
+// order of requests and columns; then what requests lack is taken from the
+// stack's top in the same order, from all that want pages while the running sum
+// of wants stays within the stack.  With G_b and W_b the sums of pages given and
+// wanted by the requests before b, the k-th page that b gives lands at place
+// n_free + G_b + k, and the k-th that it takes lies at n_free + G - 1 - W_b - k: two
+// prefix sums over the batch, and every page has its place.
+//
+// One CTA does the sums and moves pages (a round moves few); the rest, copies of
+// the tables and the slots, is spread over the GPU when it is large.
+#include "ssdv_round.cuh"
+
+#include <algorithm>
+
+#include "ssdv.h"
+
+namespace ssdv {
+
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kChunk = 256;  // cells of a row, or slots, that a warp takes at a time
+// Cells up to which the one CTA also copies and writes slots; above, a second
+// kernel does (four CTAs an SM).
+constexpr long long kAlone = 32768;
+
+struct Want {
+  int held, hold;
+  bool bad;
+};
+__device__ __forceinline__ Want look(const KvPlanArgs& a, int b) {
+  Want w;
+  const int len = a.len[b], add = a.n_new ? a.n_new[b] : a.n, shared = a.shared ? a.shared[b] : 0;
+  w.held = a.held[b];
+  const long long end = static_cast<long long>(len) + add;
+  w.bad = len < 0 || add < 0 || add > a.n || end > static_cast<long long>(a.max_pages) * a.page_size || w.held < 0 ||
+          w.held > a.max_pages || shared < 0 || shared > w.held;
+  w.hold = w.bad ? w.held : max(shared, static_cast<int>((end + a.page_size - 1) / a.page_size));
+  return w;
+}
+
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+// Inclusive sum over the CTA; total gets the sum of all.
+__device__ __forceinline__ long long block_scan(long long x, long long* sums, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = warp_scan(x, lane);
+  __syncthreads();
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  const long long s = warp_scan(sums[lane], lane);
+  total = __shfl_sync(~0u, s, 31);
+  const long long before = __shfl_sync(~0u, s, max(warp - 1, 0));
+  return x + (warp ? before : 0);
+}
+
+// What is left once pages have moved: cells that did not change, the stack's
+// rest, and the slots, by `warps` warps.
+__device__ __forceinline__ void finish(const KvPlanArgs& a, long long me, long long warps, int lane) {
+  const int4 head = a.work[0];  // free pages before, on the stack at its highest, after
+  const int4* plan = a.work + 1;
+  if (a.out_free != a.free) {
+    const int keep = min(head.x, head.z);
+    for (long long i = me * 32 + lane; i < a.n_pages; i += warps * 32)
+      if (i < keep || i >= head.y) a.out_free[i] = a.free[i];
+  }
+  if (a.out_table != a.table) {
+    const int per = (a.max_pages + kChunk - 1) / kChunk;
+    for (long long u = me; u < static_cast<long long>(a.B) * per; u += warps) {
+      const int b = static_cast<int>(u / per), c0 = static_cast<int>(u % per) * kChunk;
+      const int4 p = plan[b];
+      const long long row = static_cast<long long>(b) * a.max_pages;
+      const int lo = min(p.x, p.y), hi = max(p.x, p.y), end = min(c0 + kChunk, a.max_pages);
+#pragma unroll 4
+      for (int c = c0 + lane; c < end; c += 32)
+        if (c < lo || c >= hi) a.out_table[row + c] = a.table[row + c];
+    }
+  }
+  if (a.slots) {
+    const int per = (a.n + kChunk - 1) / kChunk;
+    for (long long u = me; u < static_cast<long long>(a.B) * per; u += warps) {
+      const int b = static_cast<int>(u / per), i0 = static_cast<int>(u % per) * kChunk;
+      const int4 p = plan[b];
+      const long long row = static_cast<long long>(b) * a.max_pages;
+      const int len = a.len[b], add = p.w ? (a.n_new ? a.n_new[b] : a.n) : 0, end = min(i0 + kChunk, a.n);
+      int64_t* out = a.slots + static_cast<long long>(b) * a.n;
+#pragma unroll 4
+      for (int i = i0 + lane; i < end; i += 32) {
+        long long slot = -1;
+        if (i < add) {
+          const unsigned pos = len + i, col = pos / static_cast<unsigned>(a.page_size);
+          // columns taken in this call are in the new table already
+          const int page = (col >= static_cast<unsigned>(p.x) ? a.out_table : a.table)[row + col];
+          if (page >= 0) slot = static_cast<long long>(page) * a.page_size + (pos - col * a.page_size);
+        }
+        out[i] = slot;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant__ KvPlanArgs a, bool alone) {
+  __shared__ long long sums[kWarps];
+  __shared__ unsigned long long taken;
+  __shared__ int errors;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    taken = 0;
+    errors = 0;
+  }
+  const int n_free = a.n_free[0];
+  // pages given back by all
+  long long given = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    long long mine = 0, sum;
+    if (b0 + tid < a.B) {
+      const Want w = look(a, b0 + tid);
+      mine = max(w.held - w.hold, 0);
+    }
+    block_scan(mine, sums, sum);
+    given += sum;
+  }
+  const long long total = n_free + given;
+  const bool broken = n_free < 0 || n_free > a.n_pages || total > a.n_pages;
+  // each request's place among those that give and those that take
+  int4* plan = a.work + 1;
+  long long gives = 0, wants = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    Want w = {0, 0, false};
+    if (b < a.B) w = look(a, b);
+    const int give = max(w.held - w.hold, 0), want = max(w.hold - w.held, 0);
+    long long sum_gives, sum_wants;
+    const long long g = gives + block_scan(give, sums, sum_gives), t = wants + block_scan(want, sums, sum_wants);
+    gives += sum_gives;
+    wants += sum_wants;
+    if (b < a.B) {
+      const bool served = !w.bad && !broken && (want == 0 || t <= total);
+      const int after = served ? w.hold : w.held;
+      plan[b] = w.bad ? make_int4(0, 0, 0, 0)
+                      : make_int4(w.held, after, static_cast<int>(give ? g - give : t - want), served);
+      a.out_held[b] = after;
+      if (served && want) atomicMax(&taken, static_cast<unsigned long long>(t));
+      if (w.bad) atomicOr(&errors, 1 << SSD_ERR_LENGTH);
+      else if (!served && !broken) atomicOr(&errors, 1 << SSD_ERR_POOL);
+    }
+  }
+  __syncthreads();
+  const int left = broken ? n_free : static_cast<int>(total - static_cast<long long>(taken));
+  if (tid == 0) {
+    a.out_n_free[0] = left;
+    // (a broken stack is copied as it is)
+    a.work[0] = broken ? make_int4(0, 0, 0, 0) : make_int4(n_free, static_cast<int>(total), left, 0);
+    if (broken) atomicOr(&errors, 1 << SSD_ERR_PAGE);
+    if (errors) atomicOr(a.status, errors);
+  }
+  // pages that come back, then pages that go: a warp looks at 32 requests at a time
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int b0 = warp * 32; b0 < a.B; b0 += kThreads) {
+      const int4 p = b0 + lane < a.B ? plan[b0 + lane] : make_int4(0, 0, 0, 0);
+      unsigned todo = __ballot_sync(~0u, pass == 0 ? p.y < p.x : p.y > p.x);
+      while (todo) {
+        const int l = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int held = __shfl_sync(~0u, p.x, l), after = __shfl_sync(~0u, p.y, l), rank = __shfl_sync(~0u, p.z, l);
+        const long long row = static_cast<long long>(b0 + l) * a.max_pages;
+        if (pass == 0) {
+          for (int c = after + lane; c < held; c += 32) {
+            a.out_free[n_free + rank + c - after] = a.table[row + c];
+            a.out_table[row + c] = -1;
+          }
+        } else {
+          for (int c = held + lane; c < after; c += 32) {
+            const int at = static_cast<int>(total) - 1 - (rank + c - held);
+            a.out_table[row + c] = at >= n_free ? a.out_free[at] : a.free[at];
+            a.out_free[at] = -1;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (alone) finish(a, warp, kWarps, lane);
+}
+
+__global__ void __launch_bounds__(256) kv_plan_finish_kernel(const __grid_constant__ KvPlanArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  finish(a, static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5), static_cast<long long>(gridDim.x) * 8,
+         threadIdx.x & 31);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
+  long long cells = a.slots ? static_cast<long long>(a.B) * a.n : 0;
+  if (a.out_table != a.table) cells += static_cast<long long>(a.B) * a.max_pages;
+  if (a.out_free != a.free) cells += a.n_pages;
+  const bool alone = cells <= kAlone;
+  kv_plan_kernel<<<1, kThreads, 0, stream>>>(a, alone);
+  cudaError_t e = cudaGetLastError();
+  if (alone || e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((cells + 8 * kChunk - 1) / (8 * kChunk), 608)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_plan_finish_kernel, a);
+}
+
+}  // namespace ssdv

@@ -31,6 +31,7 @@ STATUS_NAMES = {
     0: "SSD_OK", 1: "SSD_ERR_NULL", 2: "SSD_ERR_SHAPE", 3: "SSD_ERR_DTYPE", 4: "SSD_ERR_ALIGN",
     5: "SSD_ERR_TOKEN_RANGE", 6: "SSD_ERR_TEMPERATURE", 7: "SSD_ERR_CUDA", 8: "SSD_ERR_UNSUPPORTED",
     9: "SSD_ERR_WORKSPACE", 10: "SSD_ERR_GAMMA", 11: "SSD_ERR_DRAW", 12: "SSD_ERR_PAGE", 13: "SSD_ERR_LENGTH",
+    14: "SSD_ERR_POOL",
 }
 
 
@@ -79,6 +80,11 @@ def _declare(lib):
     lib.ssd_kv_append.argtypes = [P, P, P, P, P, P, P, I, I, I, P, SZ, P]
     lib.ssd_kv_read.argtypes = [P, P, P, I, I, I, P, P, P, SZ, P]
     lib.ssd_kv_attention.argtypes = [P, P, P, P, P, I, I, I, I, F, I, I, P, P, P, SZ, P]
+    lib.ssd_kv_attention_sinks.argtypes = [P, P, P, P, P, I, I, I, I, F, I, I, I, P, P, P, SZ, P]
+    lib.ssd_kv_plan.argtypes = [P, P, P, P, I, I, I, I, P, P, I, P, P, P, P, P, P, P, SZ, P]
+    lib.ssd_kv_plan_workspace_bytes.argtypes = [I]
+    lib.ssd_kv_plan_workspace_bytes.restype = SZ
+    lib.ssd_qk_norm_rope.argtypes = [P, P, P, P, I, P, P, I, I, I, I, I, P, P, F, P, I, I, P, P, P, P, P, SZ, P]
     lib.ssd_read_status.argtypes = [P, SZ, P, P]
     lib.ssd_stream_capture_id.argtypes = [P, P]
     lib.ssd_debug_uniforms.argtypes = [U64, I, I, P, P]
@@ -90,7 +96,8 @@ def _declare(lib):
                  "ssd_verify_ragged", "ssd_verify_ragged_pipelined", "ssd_saguaro_prespec", "ssd_debug_rowstats",
                  "ssd_debug_saguaro_stats", "ssd_read_status",
                  "ssd_verify_saguaro", "ssd_cache_check", "ssd_verify_saguaro_draft", "ssd_verify_top_p",
-                 "ssd_kv_append", "ssd_kv_read", "ssd_kv_attention", "ssd_stream_capture_id", "ssd_debug_uniforms"):
+                 "ssd_kv_append", "ssd_kv_read", "ssd_kv_attention", "ssd_kv_attention_sinks", "ssd_kv_plan", "ssd_qk_norm_rope",
+                 "ssd_stream_capture_id", "ssd_debug_uniforms"):
         getattr(lib, name).restype = I
     return lib
 
@@ -616,15 +623,18 @@ def kv_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, 
 def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q: torch.Tensor,
                  n_q: Optional[torch.Tensor] = None, scale: Optional[float] = None, window: int = 0,
                  past_only: bool = False, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                 return_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+                 return_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None, sinks: int = 0):
     """ssd_kv_attention: q [B, n, n_heads, head_dim] (bf16 or fp32, any strides but the last), query i of request b at
-    position kv_len[b] + i.  scale defaults to head_dim ** -0.5.  Returns out like q, contiguous, or (out, lse
+    position kv_len[b] + i.  scale defaults to head_dim ** -0.5.  With a window the first `sinks` positions stay visible
+    (ssd_kv_attention_sinks).  Returns out like q, contiguous, or (out, lse
     [B, n, n_heads] float32) with return_lse (or a given lse)."""
     shape, device = q.shape, cache.device
     B, n, heads = shape[:3]
-    window = int(window)
+    window, sinks = int(window), int(sinks)
     if not -1 << 31 <= window < 1 << 31:
         raise ValueError(f"window={window} is no 32-bit number")
+    if not -1 << 31 <= sinks < 1 << 31:
+        raise ValueError(f"sinks={sinks} is no 32-bit number")
     c, kv_heads, dim = _kv_cache(cache, page_table, B)
     index = cache.get_device()
     qp, qs = _kv_rows(q, "q", None, dim, index)
@@ -641,12 +651,115 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
     if out.shape != shape or (lse is not None and lse.shape != (B, n, heads)):
         raise ValueError("out must be shaped like q and lse [B, n, n_heads]")
     if B and n:
-        _check(lib().ssd_kv_attention(c, lens, counts, qp, qs, _dtype_code(q, "q"), B, n, heads,
-                                      float(scale) if scale is not None else dim ** -0.5, window, int(past_only),
-                                      _kv_dev(out, "out", q.dtype, index),
-                                      _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None,
-                                      _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
+        _check(lib().ssd_kv_attention_sinks(c, lens, counts, qp, qs, _dtype_code(q, "q"), B, n, heads,
+                                            float(scale) if scale is not None else dim ** -0.5, window, sinks,
+                                            int(past_only), _kv_dev(out, "out", q.dtype, index),
+                                            _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None,
+                                            _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
     return (out, lse) if lse is not None else out
+
+
+def make_kv_pool(n_pages: int, device=None):
+    """(free_pages [n_pages], n_free [1]) int32: a stack on which all pages of a pool are free, page 0 on top."""
+    if not 1 <= n_pages < 1 << 31:
+        raise ValueError(f"no pool of {n_pages} pages")
+    device = device or "cuda"
+    return (torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device),
+            torch.full((1,), n_pages, dtype=torch.int32, device=device))
+
+
+def kv_plan(page_table: torch.Tensor, n_held: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor,
+            kv_len: torch.Tensor, n: int, page_size: int, n_new: Optional[torch.Tensor] = None,
+            n_shared: Optional[torch.Tensor] = None, out=None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """ssd_kv_plan: pages for the tokens kv_len[b] .. kv_len[b] + n_new[b] - 1 (n of every request without n_new).
+    Returns (page_table, n_held, free_pages, n_free, slots [B, n] int64), new tensors or those of `out`, four tensors
+    that may be the inputs (in place)."""
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [B, max_pages], got {list(page_table.shape)}")
+    B, width = page_table.shape
+    n, device, index = int(n), page_table.device, page_table.get_device()
+    state = (page_table, n_held, free_pages, n_free)
+    ins = [_dev(page_table, "page_table", torch.int32), _kv_counts(n_held, "n_held", B, index),
+           _kv_dev(free_pages, "free_pages", torch.int32, index), _kv_counts(n_free, "n_free", 1, index)]
+    if free_pages.dim() != 1:
+        raise ValueError(f"free_pages must be [n_pages], got {list(free_pages.shape)}")
+    lens, news = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_new, "n_new", B, index)
+    shared = _kv_counts(n_shared, "n_shared", B, index)
+    raw, ctx = _kv_stream(stream, device)
+    ws = workspace
+    with ctx or _HERE:
+        if out is None:
+            out = [torch.empty(t.shape, dtype=torch.int32, device=device) for t in state]
+        slots = torch.empty((B, max(n, 0)), dtype=torch.int64, device=device)
+        if ws is None and B:
+            ws = _kv_workspace(_kv_plan_bytes(B), device, raw)
+    if len(out) != 4 or any(o.shape != t.shape for o, t in zip(out, state)):
+        raise ValueError("out must be four tensors shaped like page_table, n_held, free_pages and n_free")
+    outs = [_kv_dev(o, "out", torch.int32, index) for o in out]
+    if B:
+        _check(lib().ssd_kv_plan(*ins, B, width, free_pages.shape[0], int(page_size), lens, news, n, shared, *outs,
+                                 slots.data_ptr() if n > 0 else None, _kv_dev(ws, "workspace", None, index),
+                                 ws.numel(), raw))
+    elif out[2] is not free_pages or out[3] is not n_free:
+        with ctx or _HERE:  # no request: the stack is what it was
+            out[2].copy_(free_pages)
+            out[3].copy_(n_free)
+    return (*out, slots)
+
+
+@functools.lru_cache(maxsize=None)
+def _kv_plan_bytes(B: int) -> int:
+    return int(lib().ssd_kv_plan_workspace_bytes(B))
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], kv_len: torch.Tensor,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 inv_freq: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                 n_new: Optional[torch.Tensor] = None, out=None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """ssd_qk_norm_rope: q [B, n, n_heads, head_dim] and k [B, n, n_kv_heads, head_dim] or None (bf16 or fp32, any
+    strides but the last) normed for each head with the fp32 weights [head_dim] and rotated by their positions
+    kv_len[b] + i with inv_freq [rot_dim / 2] (fp32).  out: a pair of tensors, the inputs themselves among others.
+    Returns (q, k)."""
+    if q.dim() != 4 or not q.is_cuda:
+        raise ValueError("q must be [B, n, n_heads, head_dim] on a CUDA device")
+    (B, n, heads, dim), device, index = q.shape, q.device, q.get_device()
+    qp, qs = _kv_rows(q, "q", None, dim, index)
+    kp = ks = None
+    kv_heads = 0
+    if k is not None:
+        kp, ks = _kv_rows(k, "k", None, dim, index)
+        kv_heads = k.shape[2]
+        if k.shape[:2] != q.shape[:2] or k.dtype != q.dtype:
+            raise ValueError("q and k must have one dtype and the same requests and tokens")
+    code = _dtype_code(q, "q and k")
+    weights = [None if w is None else _kv_dev(w, name, torch.float32, index)
+               for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
+    for w in (q_weight, k_weight):
+        if w is not None and w.shape != (dim,):
+            raise ValueError(f"weights must be [{dim}], got {list(w.shape)}")
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError(f"inv_freq must be [rot_dim / 2], got {list(inv_freq.shape)}")
+        rot = 2 * inv_freq.shape[0]
+    freq = _kv_dev(inv_freq, "inv_freq", torch.float32, index) if rot else None
+    lens, news = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_new, "n_new", B, index)
+    raw, ctx = _kv_stream(stream, device)
+    ws = workspace
+    with ctx or _HERE:
+        oq, ok = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=device),
+                                              None if k is None else torch.empty(k.shape, dtype=q.dtype, device=device))
+        if ws is None:
+            ws = _kv_workspace(256, device, raw)
+    oqp, oqs = _kv_rows(oq, "out q", heads, dim, index)
+    okp, oks = (None, None) if k is None else _kv_rows(ok, "out k", kv_heads, dim, index)
+    if oq.shape != q.shape or oq.dtype != q.dtype or (k is not None and (ok.shape != k.shape or ok.dtype != q.dtype)):
+        raise ValueError("out must be tensors like q and k")
+    if B and n:
+        _check(lib().ssd_qk_norm_rope(qp, qs, kp, ks, code, lens, news, B, n, heads, kv_heads, dim, *weights, float(eps),
+                                      freq, rot, int(interleaved), oqp, oqs, okp, oks,
+                                      _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
+    return oq, ok
 
 
 def debug_rowstats(target, draft, draft_tokens, temperature, seed, workspace=None, stream=None):
