@@ -526,6 +526,29 @@ ssd_status ssd_kv_attention_sinks(const ssd_kv_cache* cache, const int32_t* kv_l
                                   int window, int n_sinks, int past_only, void* out, float* out_lse, void* workspace,
                                   size_t ws_bytes, void* stream);
 
+/* ssd_kv_attention for requests that share prefixes, each read once for all of
+ * its group: requests group_start[g] .. group_start[g + 1] - 1 hold the same keys
+ * and values at positions below shared_len[g] (many samples of one prompt, a
+ * system prompt, a document).  They are read through the page table's row of the
+ * group's first request, everything else through each request's own; whether the
+ * pages are the same or copies does not matter.
+ *
+ *   group_start  device [G + 1], from 0 to B, not falling; shared_len device [G],
+ *                at most kv_len of every request of the group.  1 <= G <= 65535
+ *   workspace    >= ssd_kv_shared_workspace_bytes(...) for the call's own shape;
+ *                its status word is all that has to be zeroed
+ *
+ * out, out_lse, rows that see nothing and rows past n_q[b] as for
+ * ssd_kv_attention; positions below shared_len[g] are seen by all queries of the
+ * group.  There is no window.  A bad shared_len makes its requests' outputs NaN, a
+ * bad group_start those of all, and both set SSD_ERR_LENGTH; a bad page of the
+ * prefix is the loss of the whole group. */
+ssd_status ssd_kv_attention_shared(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_q, const void* q,
+                                   const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
+                                   const int32_t* group_start, const int32_t* shared_len, int G, int past_only,
+                                   void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream);
+size_t ssd_kv_shared_workspace_bytes(int B, int n, int n_heads, int n_kv_heads, int head_dim, int G);
+
 /* Read and clear the device status word of a workspace.  Synchronises
  * `stream`.  *status gets SSD_OK or the lowest-numbered device error seen
  * since the last read. */

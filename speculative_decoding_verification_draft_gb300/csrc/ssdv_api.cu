@@ -921,6 +921,45 @@ ssd_status kv_strides(const void* p, const int64_t* st, int es, long long* out, 
   return SSD_OK;
 }
 
+// What the attention calls share; need(): bytes of the call's workspace, 0 for a bad shape.
+template <typename Need>
+ssd_status attention_args(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_q, const void* q,
+                          const int64_t* q_strides, ssd_dtype dtype, int B, int n, int n_heads, float scale,
+                          int past_only, void* out, float* out_lse, void* workspace, size_t ws_bytes, Need need_of,
+                          KvAttnArgs* a) {
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return fail(SSD_ERR_SHAPE, "scale=%g is not finite or above 2.3e38", scale);
+  ssd_status st = kv_check(cache, kv_len, n_q, dtype, B, n, workspace, ws_bytes, 0);
+  if (st != SSD_OK) return st;
+  if (!q || !q_strides || !out) return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  const size_t need = B > 65535 ? 0 : need_of();
+  if (need == 0)
+    return fail(SSD_ERR_SHAPE, "bad shape B=%d n=%d n_heads=%d n_kv_heads=%d", B, n, n_heads, cache->n_kv_heads);
+  // a team's tiles are counted in 32 bits
+  if (static_cast<double>(B) * n_heads * n * (cache->max_pages * (cache->page_size / kKvBlock) / 4 + 1) >= 274877906944.0)
+    return fail(SSD_ERR_SHAPE, "B * n * n_heads * max_pages too large");
+  if (ws_bytes < need) return fail(SSD_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", ws_bytes, need);
+  if (!aligned_to(out, 16) || (out_lse && !aligned_to(out_lse, 4)))
+    return fail(SSD_ERR_ALIGN, "out needs 16-byte alignment, out_lse 4-byte");
+  bool vec = true;
+  st = kv_strides(q, q_strides, esize_of(dtype), a->qs, &vec);
+  if (st != SSD_OK) return st;
+  a->c = kv_cache_args(cache);
+  a->kv_len = kv_len;
+  a->n_q = n_q;
+  a->B = B;
+  a->nq = n;
+  a->heads = n_heads;
+  a->q = q;
+  a->scale_log2 = scale_log2;
+  a->past_only = past_only != 0;
+  a->out = out;
+  a->lse = out_lse;
+  a->status = static_cast<int32_t*>(workspace);
+  a->work = static_cast<uint8_t*>(workspace) + kKvWorkOffset;
+  return SSD_OK;
+}
+
 }  // namespace
 }  // namespace ssdv
 
@@ -1004,41 +1043,42 @@ ssd_status ssd_kv_attention_sinks(const ssd_kv_cache* cache, const int32_t* kv_l
                                   int window, int n_sinks, int past_only, void* out, float* out_lse, void* workspace,
                                   size_t ws_bytes, void* stream) {
   g_last_error.clear();
-  const float scale_log2 = scale * 1.4426950408889634f;
-  if (!std::isfinite(scale_log2)) return fail(SSD_ERR_SHAPE, "scale=%g is not finite or above 2.3e38", scale);
-  if (window < 0 || n_sinks < 0) return fail(SSD_ERR_SHAPE, "window=%d or n_sinks=%d is negative", window, n_sinks);
-  ssd_status st = kv_check(cache, kv_len, n_q, dtype, B, n, workspace, ws_bytes, 0);
-  if (st != SSD_OK) return st;
-  if (!q || !q_strides || !out) return fail(SSD_ERR_NULL, "a required pointer is NULL");
-  const size_t need = ssd_kv_workspace_bytes(n, n_heads, cache->n_kv_heads, cache->head_dim);
-  if (need == 0 || B > 65535)
-    return fail(SSD_ERR_SHAPE, "bad shape B=%d n=%d n_heads=%d n_kv_heads=%d", B, n, n_heads, cache->n_kv_heads);
-  if (static_cast<double>(B) * n_heads * n * (cache->max_pages * (cache->page_size / kKvBlock) / 4 + 1) >= 274877906944.0)
-    return fail(SSD_ERR_SHAPE, "B * n * n_heads * max_pages too large");  // a team's tiles are counted in 32 bits
-  if (ws_bytes < need) return fail(SSD_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", ws_bytes, need);
-  if (!aligned_to(out, 16) || (out_lse && !aligned_to(out_lse, 4)))
-    return fail(SSD_ERR_ALIGN, "out needs 16-byte alignment, out_lse 4-byte");
   KvAttnArgs a = {};
-  bool vec = true;
-  st = kv_strides(q, q_strides, esize_of(dtype), a.qs, &vec);
-  if (st != SSD_OK) return st;
-  a.c = kv_cache_args(cache);
-  a.kv_len = kv_len;
-  a.n_q = n_q;
-  a.B = B;
-  a.nq = n;
-  a.heads = n_heads;
-  a.q = q;
-  a.scale_log2 = scale_log2;
+  if (window < 0 || n_sinks < 0) return fail(SSD_ERR_SHAPE, "window=%d or n_sinks=%d is negative", window, n_sinks);
   a.window = window;
   a.sinks = window ? n_sinks : 0;
-  a.past_only = past_only != 0;
-  a.out = out;
-  a.lse = out_lse;
-  a.status = static_cast<int32_t*>(workspace);
-  a.work = static_cast<uint8_t*>(workspace) + kKvWorkOffset;
+  const ssd_status st =
+      attention_args(cache, kv_len, n_q, q, q_strides, dtype, B, n, n_heads, scale, past_only, out, out_lse, workspace,
+                     ws_bytes, [&] { return ssd_kv_workspace_bytes(n, n_heads, cache->n_kv_heads, cache->head_dim); }, &a);
+  if (st != SSD_OK) return st;
   const cudaError_t e = launch_kv_attention(a, cache->head_dim, esize_of(dtype), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SSD_OK : cuda_fail(e, "cache attention launch");
+}
+
+size_t ssd_kv_shared_workspace_bytes(int B, int n, int n_heads, int n_kv_heads, int head_dim, int G) {
+  if (B < 1 || B > 65535 || n < 1 || G < 1 || G > 65535 ||
+      ssd_kv_workspace_bytes(n, n_heads, n_kv_heads, head_dim) == 0)
+    return 0;
+  return kKvWorkOffset + kv_shared_work_bytes(B, n, n_heads, n_kv_heads, head_dim, G);
+}
+
+ssd_status ssd_kv_attention_shared(const ssd_kv_cache* cache, const int32_t* kv_len, const int32_t* n_q, const void* q,
+                                   const int64_t q_strides[3], ssd_dtype dtype, int B, int n, int n_heads, float scale,
+                                   const int32_t* group_start, const int32_t* shared_len, int G, int past_only,
+                                   void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  if (!group_start || !shared_len) return fail(SSD_ERR_NULL, "a required pointer is NULL");
+  if (G < 1 || G > 65535) return fail(SSD_ERR_SHAPE, "G=%d is not in 1..65535", G);
+  if (!aligned_to(group_start, 4) || !aligned_to(shared_len, 4))
+    return fail(SSD_ERR_ALIGN, "group_start and shared_len need 4-byte alignment");
+  KvAttnArgs a = {};
+  const ssd_status st = attention_args(
+      cache, kv_len, n_q, q, q_strides, dtype, B, n, n_heads, scale, past_only, out, out_lse, workspace, ws_bytes,
+      [&] { return ssd_kv_shared_workspace_bytes(B, n, n_heads, cache->n_kv_heads, cache->head_dim, G); }, &a);
+  if (st != SSD_OK) return st;
+  const cudaError_t e = launch_kv_shared(a, group_start, shared_len, G, cache->head_dim, esize_of(dtype),
+                                         static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SSD_OK : cuda_fail(e, "shared attention launch");
 }
 
 size_t ssd_kv_plan_workspace_bytes(int B) {

@@ -94,6 +94,10 @@ struct KvAttnArgs {
 };
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int D, int esize, cudaStream_t stream);
 size_t kv_attention_work_bytes(int rows, int D);
+// The same for groups of requests that share a prefix (ssdv_shared.cu).
+cudaError_t launch_kv_shared(const KvAttnArgs& a, const int32_t* group_start, const int32_t* shared_len, int G, int D,
+                             int esize, cudaStream_t stream);
+size_t kv_shared_work_bytes(int B, int nq, int heads, int kv_heads, int D, int G);
 
 #ifdef __CUDACC__
 

@@ -1,0 +1,429 @@
+// ssdv_shared.cu -- attention for groups of requests that share a prefix, in any
+// type and head size, and the kernel that joins the parts of a row.
+//
+// A CTA of four warps has 64 rows of a row block, 16 a warp.  For each tile of 64
+// tokens it unpacks keys (by token) and values (by element) to fp16 in shared
+// memory, where they are exact, and multiplies with m16n8k16 instructions: scores
+// with queries from shared memory (fp32: two fp16 parts), then weights, which stay in
+// the registers that the scores came in (fp32: two fp16 parts).  Weights are
+// 2^(x - m + 15) with m the row's maximum so far, so fp16 keeps 11 bits down to 2^-29
+// of the largest and a multiple of 2^-40 of it below; maxima, sums of weights and of
+// values are fp32.
+#include "ssdv_shared.cuh"
+
+#include <algorithm>
+
+namespace ssdv {
+
+namespace {
+
+constexpr int kRows = 64, kTokens = 64, kThreads = 128;
+constexpr int kBias = 15;
+constexpr int kPad = 8;  // halves between rows: eight rows' 16 bytes lie in different banks
+constexpr int kTeamsPerSm = 2;
+
+template <int D, int kParts>
+struct Tile {
+  static constexpr int kRow = D + kPad, kCol = kTokens + kPad;
+  static constexpr int q = 0, k = q + kParts * kRows * kRow * 2, v = k + kTokens * kRow * 2;
+  static constexpr int factors = v + D * kCol * 2, total = factors + kRows * 4;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&x)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(at));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Queries to shared memory, a power of two up (the row's largest element in [2^12,
+// 2^13), the scale's sign on them), and what their scores are to be multiplied by.
+template <typename E, int D, int kParts>
+__device__ __forceinline__ void load_queries(const SharedLaunch& L, const SharedPart& p, uint32_t smem, int warp, int lane) {
+  using T = Tile<D, kParts>;
+  constexpr int kEach = D / 32;
+  for (int row = warp * 16; row < warp * 16 + 16; ++row) {
+    const SharedRow at(L, p, row);
+    float x[kEach], top = 0.f;
+    const E* q = static_cast<const E*>(L.a.q) + at.b * L.a.qs[0] + at.i * L.a.qs[1] + at.head * L.a.qs[2] + lane * kEach;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      x[e] = at.real ? static_cast<float>(q[e]) : 0.f;
+      top = fmaxf(top, fabsf(x[e]));
+    }
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    ex = max(-100, min(ex, 127));
+    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), L.a.scale_log2);
+#pragma unroll
+    for (int e = 0; e < kEach; e += 2) {
+      const float y0 = x[e] * up, y1 = x[e + 1] * up;
+      const __half2 hi = __floats2half2_rn(y0, y1);
+      const uint32_t to = smem + T::q + (row * T::kRow + lane * kEach + e) * 2;
+      sts32(to, half2_bits(hi));
+      if constexpr (kParts == 2) {
+        const float2 back = __half22float2(hi);
+        sts32(to + kRows * T::kRow * 2, half2_bits(__floats2half2_rn(y0 - back.x, y1 - back.y)));
+      }
+    }
+    if (lane == 0)
+      sts32(smem + T::factors + row * 4,
+            __float_as_uint(fabsf(L.a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23)));
+  }
+}
+
+// Four pairs of values of a word: codes to n s.
+__device__ __forceinline__ uint4 unpack_word(uint32_t w, const Bases& b, const uint32_t (&s)[4], const uint32_t (&o)[4]) {
+  const uint32_t u = __funnelshift_r(w, w, 8);
+  return make_uint4(fma2(pair_hi(w, b), s[0], o[0]), fma2(pair_lo(w, b), s[1], o[1]), fma2(pair_hi(u, b), s[2], o[2]),
+                    fma2(pair_lo(u, b), s[3], o[3]));
+}
+
+template <int D, int kParts>
+__device__ __forceinline__ void unpack_tile(uint32_t smem, const uint8_t* const (&blocks)[4], int pos0, int len,
+                                            const Bases& bases, int tid) {
+  using T = Tile<D, kParts>;
+  // keys: 32 elements of a token at a time
+  for (int x = tid; x < kTokens * (D / 32); x += kThreads) {
+    const int part = x % (D / 32), token = x / (D / 32), t = token & 15;
+    const uint8_t* block = blocks[token >> 4];
+    uint4 c = make_uint4(0, 0, 0, 0);
+    uint32_t sb[2] = {0, 0};
+    if (block) {
+      c = *reinterpret_cast<const uint4*>(block + k_word_offset<D>(t, part * 4));
+      sb[0] = block[k_scale_offset<D>(t, part * 2)];
+      sb[1] = block[k_scale_offset<D>(t, part * 2 + 1)];
+    }
+    const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t s = __byte_perm(sb[i >> 1], 0, 0x4040) << 7;
+      const uint32_t hi = mul2(s, kMinus24), lo = mul2(s, kMinus264);
+      const uint32_t ss[4] = {s, s, s, s}, oo[4] = {hi, lo, hi, lo};
+      sts128(smem + T::k + (token * T::kRow + part * 32 + i * 8) * 2, unpack_word(words[i], bases, ss, oo));
+    }
+  }
+  // values: an element of a block's 16 tokens at a time
+  for (int x = tid; x < 4 * D; x += kThreads) {
+    const int d = x % D, blk = x / D;
+    const uint8_t* block = blocks[blk];
+    uint2 c = make_uint2(0, 0);
+    uint4 sb = make_uint4(0, 0, 0, 0);
+    if (block) {
+      c = *reinterpret_cast<const uint2*>(block + v_word_offset<D>(d, 0));
+      sb = *reinterpret_cast<const uint4*>(block + kv_v_scales(D) + (d >> 4) * 16);
+    }
+    uint32_t scales[4] = {sb.x, sb.y, sb.z, sb.w};
+    const int seen = len - pos0 - blk * 16;  // tokens of the block that count: the others become zero
+    if (seen < 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i >= seen) scales[i >> 2] &= ~(0xFFu << (i & 3) * 8);
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t ss[4], oo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ss[i] = __byte_perm(scales[half * 2 + (i >> 1)], 0, i & 1 ? 0x4342 : 0x4140) << 7;
+        oo[i] = mul2(ss[i], i & 1 ? kMinus264 : kMinus24);
+      }
+      sts128(smem + T::v + (d * T::kCol + blk * 16 + half * 8) * 2, unpack_word(half ? c.y : c.x, bases, ss, oo));
+    }
+  }
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) shared_kernel(const __grid_constant__ SharedLaunch L) {
+  constexpr int kParts = sizeof(E) == 4 ? 2 : 1;
+  using T = Tile<D, kParts>;
+  extern __shared__ __align__(16) uint8_t bytes[];
+  __shared__ long long scan[kThreads], sums[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t smem = smem_u32(bytes);
+  const KvCacheArgs& c = L.a.c;
+  const Bases bases = make_bases();
+  GroupList list(L);
+  list.build(scan, sums);
+  const long long end = min((blockIdx.x + 1) * list.quota, list.total);
+  for (long long u = blockIdx.x * list.quota; u < end;) {
+    const SharedPart p = list.part(u, end);
+    u += p.count;
+    __syncthreads();
+    load_queries<E, D, kParts>(L, p, smem, warp, lane);
+    __syncthreads();
+    float f[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) f[x] = __uint_as_float(lds32(smem + T::factors + (warp * 16 + (lane >> 2) + 8 * x) * 4));
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    bool bad = false;
+    const int bpp = c.page_size / kKvBlock;
+    const int32_t* table = c.page_table + static_cast<long long>(p.b0) * c.max_pages;
+    for (int t = p.t0; t < p.t0 + p.count; ++t) {
+      const int pos0 = t * kTokens;
+      const uint8_t* blocks[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        blocks[k] = nullptr;
+        if (pos0 + k * kKvBlock < p.len) {
+          const int at = t * 4 + k, page = table[at / bpp];
+          if (page >= 0 && page < c.n_pages)
+            blocks[k] = c.pages + ((static_cast<long long>(page) * c.kv_heads + p.h) * bpp + at % bpp) * kv_block_bytes(D);
+          else bad = true;
+        }
+      }
+      __syncthreads();  // the tile before has been read
+      unpack_tile<D, kParts>(smem, blocks, pos0, p.len, bases, tid);
+      __syncthreads();
+      float s[8][4];
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t q[kParts][4];
+#pragma unroll
+        for (int x = 0; x < kParts; ++x)
+          ldsm4(q[x], smem + T::q + ((x * kRows + warp * 16 + (lane & 15)) * T::kRow + k * 16 + (lane >> 4) * 8) * 2);
+#pragma unroll
+        for (int n = 0; n < 8; n += 2) {
+          uint32_t b[4];  // tokens 8 n .. 8 n + 15, both halves of the 16 elements
+          ldsm4(b, smem + T::k + ((n * 8 + (lane & 7) + (lane >> 4) * 8) * T::kRow + k * 16 + ((lane >> 3) & 1) * 8) * 2);
+#pragma unroll
+          for (int x = 0; x < kParts; ++x) {
+            mma(s[n], q[x], b[0], b[1]);
+            mma(s[n + 1], q[x], b[2], b[3]);
+          }
+        }
+      }
+      if (pos0 + kTokens > p.len) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (pos0 + n * 8 + (lane & 3) * 2 + (e & 1) >= p.len) s[n][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) top = fmaxf(top, fmaxf(s[n][2 * x], s[n][2 * x + 1]));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const float now = fmaxf(m[x], top * f[x]);  // (some token of a tile is always seen, f >= 0)
+        const float fall = ex2(m[x] - now);
+        m[x] = now;
+        l[x] *= fall;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][2 * x] *= fall;
+          o[n][2 * x + 1] *= fall;
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 2 * x; e < 2 * x + 2; ++e) {
+            // (a factor of zero makes no number of a masked score)
+            s[n][e] = s[n][e] == -INFINITY ? 0.f : ex2(fmaf(s[n][e], f[x], kBias - now));
+            l[x] += s[n][e];
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // 16 tokens
+        uint32_t w[kParts][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float a = s[2 * k + (x >> 1)][2 * (x & 1)], b = s[2 * k + (x >> 1)][2 * (x & 1) + 1];
+          const __half2 hi = __floats2half2_rn(a, b);
+          w[0][x] = half2_bits(hi);
+          if constexpr (kParts == 2) {
+            const float2 back = __half22float2(hi);
+            w[1][x] = half2_bits(__floats2half2_rn(a - back.x, b - back.y));
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; n += 2) {
+          uint32_t b[4];  // elements 8 n .. 8 n + 15
+          ldsm4(b, smem + T::v + ((n * 8 + (lane & 7) + (lane >> 4) * 8) * T::kCol + k * 16 + ((lane >> 3) & 1) * 8) * 2);
+#pragma unroll
+          for (int x = 0; x < kParts; ++x) {
+            mma(o[n], w[x], b[0], b[1]);
+            mma(o[n + 1], w[x], b[2], b[3]);
+          }
+        }
+      }
+    }
+    if (bad && tid == 0) atomicOr(L.a.status, 1 << SSD_ERR_PAGE);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(~0u, l[x], 1);
+      l[x] += __shfl_xor_sync(~0u, l[x], 2);
+      const int row = warp * 16 + (lane >> 2) + 8 * x;
+      if (row >= p.n_rows) continue;
+      const long long at = p.row0 + row + static_cast<long long>(blockIdx.x) * kRows;
+      if ((lane & 3) == 0) L.ml[at] = make_float2(m[x], bad ? __int_as_float(0x7FC00000) : l[x]);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(L.o + at * D + n * 8 + (lane & 3) * 2) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
+    }
+  }
+}
+
+// Joins a row's own part and its parts of the prefix, in order: a warp a row.
+template <typename E, int D>
+__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ SharedLaunch L) {
+  constexpr int kPer = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const KvAttnArgs& a = L.a;
+  const int lane = threadIdx.x & 31;
+  const long long orow = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // (request, query, query head)
+  if (orow >= static_cast<long long>(a.B) * a.nq * a.heads) return;
+  const int head = static_cast<int>(orow % a.heads), i = static_cast<int>(orow / a.heads % a.nq);
+  const int b = static_cast<int>(orow / a.heads / a.nq), h = head / L.per, k = i * L.per + head - h * L.per;
+  const Span s = find_span<kTokens>(a, b);
+  float m = -INFINITY, l = 0.f, y[kPer] = {};
+  if (s.bad) {
+    l = __int_as_float(0x7FC00000);
+    if (i == 0 && head == 0 && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
+  } else if (i < s.nq) {
+    const int g = L.group_of[b], b0 = L.group_start[g], n = (s.first + L.tile - 1) / L.tile;
+    const long long rows = static_cast<long long>(L.group_start[g + 1] - b0) * L.rows;
+    const long long r = static_cast<long long>(b - b0) * L.rows + k, nb = (rows + L.R - 1) / L.R;
+    const long long quota = L.head[0], u0 = L.unit0[g] + (h * nb + r / L.R) * n;
+    const long long c0 = u0 / quota, c1 = n ? (u0 + n - 1) / quota : c0 - 1;  // teams
+    const long long at = static_cast<long long>(b0) * L.rows * a.c.kv_heads + h * rows + r;
+    const long long own = (static_cast<long long>(b) * a.c.kv_heads + h) * L.rows + k;
+    const auto sums = [&](long long c) { return c < c0 ? a.own_ml[own] : L.ml[at + c * L.R]; };  // c0 - 1: its own
+    for (long long c = c0 - 1 + lane; c <= c1; c += 32) {
+      const float2 x = sums(c);
+      if (x.y != 0.f) m = fmaxf(m, x.x);
+    }
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (long long c = c0 - 1; c <= c1; ++c) {
+      const float2 x = sums(c);
+      const float f = x.y == 0.f ? 0.f : ex2(x.x - ref);
+      l += x.y * f;
+      const float* o = (c < c0 ? a.own_o + own * D : L.o + (at + c * L.R) * D) + lane * kPer;
+      if (x.y == 0.f) continue;
+#pragma unroll
+      for (int v = 0; v < kPer / 2; ++v) {
+        const float2 z = reinterpret_cast<const float2*>(o)[v];
+        y[2 * v] += z.x * f;
+        y[2 * v + 1] += z.y * f;
+      }
+    }
+  }
+  const float inv = 1.f / l;
+  E* out = static_cast<E*>(a.out) + orow * D + lane * kPer;
+#pragma unroll
+  for (int v = 0; v < kPer; ++v) out[v] = static_cast<E>(l == 0.f ? 0.f : y[v] * inv);
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + (log2f(l) - kBias)) * 0.69314718055994531f;
+}
+
+template <typename E, int D>
+cudaError_t launch_dim(const SharedLaunch& L, cudaStream_t stream) {
+  using T = Tile<D, sizeof(E) == 4 ? 2 : 1>;
+  cudaError_t e = allow_shared<shared_kernel<E, D>>(T::total);
+  if (e != cudaSuccess) return e;
+  shared_kernel<E, D><<<L.teams, kThreads, T::total, stream>>>(L);
+  return cudaGetLastError();
+}
+
+template <typename E, int D>
+cudaError_t launch_join(const SharedLaunch& L, cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(L.a.B) * L.a.nq * L.a.heads + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_join_kernel<E, D>, L);
+}
+
+template <typename E>
+cudaError_t launch_type(const SharedLaunch& L, int D, cudaStream_t stream, bool join) {
+  if (D == 64) return join ? launch_join<E, 64>(L, stream) : launch_dim<E, 64>(L, stream);
+  if (D == 128) return join ? launch_join<E, 128>(L, stream) : launch_dim<E, 128>(L, stream);
+  return join ? launch_join<E, 256>(L, stream) : launch_dim<E, 256>(L, stream);
+}
+
+struct SharedWork {
+  size_t unit0, first, group_of, own_ml, own_o, ml, o, attn, total;
+};
+SharedWork shared_work(long long B, int nq, int heads, int kv_heads, int D, int G, const SharedShape& s) {
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = static_cast<size_t>(B) * nq * heads, parts = rows + static_cast<size_t>(s.teams) * s.R;
+  SharedWork w;
+  w.unit0 = 256;
+  w.first = w.unit0 + up(static_cast<size_t>(G) * 8);
+  w.group_of = w.first + up(static_cast<size_t>(B) * 4);
+  w.own_ml = w.group_of + up(static_cast<size_t>(B) * 4);
+  w.own_o = w.own_ml + up(rows * 8);
+  w.ml = w.own_o + up(rows * D * 4);
+  w.o = w.ml + up(parts * 8);
+  w.attn = w.o + up(parts * D * 4);
+  w.total = w.attn + kv_attention_work_bytes(nq * (heads / kv_heads), D);
+  return w;
+}
+
+}  // namespace
+
+SharedShape shared_shape(int D, int esize, int sms) {
+  return {kRows, kTokens, sms * kTeamsPerSm, false};
+}
+
+size_t kv_shared_work_bytes(int B, int nq, int heads, int kv_heads, int D, int G) {
+  size_t most = 0;
+  for (int esize = 2; esize <= 4; esize += 2)
+    most = std::max(most, shared_work(B, nq, heads, kv_heads, D, G, shared_shape(D, esize, kMaxSms)).total);
+  return most;
+}
+
+cudaError_t launch_kv_shared(const KvAttnArgs& a, const int32_t* group_start, const int32_t* shared_len, int G, int D,
+                             int esize, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const SharedShape s = shared_shape(D, esize, std::min(sms, kMaxSms));
+  const SharedWork w = shared_work(a.B, a.nq, a.heads, a.c.kv_heads, D, G, s);
+  SharedLaunch L;
+  L.a = a;
+  L.group_start = group_start;
+  L.shared_len = shared_len;
+  L.G = G;
+  L.per = a.heads / a.c.kv_heads;
+  L.rows = a.nq * L.per;
+  L.R = s.R;
+  L.tile = s.tile;
+  L.teams = s.teams;
+  L.head = reinterpret_cast<long long*>(a.work);
+  L.unit0 = reinterpret_cast<long long*>(a.work + w.unit0);
+  L.first = reinterpret_cast<int32_t*>(a.work + w.first);
+  L.group_of = reinterpret_cast<int32_t*>(a.work + w.group_of);
+  L.a.own_ml = reinterpret_cast<float2*>(a.work + w.own_ml);
+  L.a.own_o = reinterpret_cast<float*>(a.work + w.own_o);
+  L.ml = reinterpret_cast<float2*>(a.work + w.ml);
+  L.o = reinterpret_cast<float*>(a.work + w.o);
+  L.a.first = L.first;
+  L.a.work = a.work + w.attn;
+  e = esize == 2 ? launch_type<__nv_bfloat16>(L, D, stream, false) : launch_type<float>(L, D, stream, false);
+  if (e == cudaSuccess) e = launch_kv_attention(L.a, D, esize, stream);
+  if (e != cudaSuccess) return e;
+  return esize == 2 ? launch_type<__nv_bfloat16>(L, D, stream, true) : launch_type<float>(L, D, stream, true);
+}
+
+}  // namespace ssdv

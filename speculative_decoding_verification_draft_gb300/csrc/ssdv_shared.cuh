@@ -1,0 +1,171 @@
+// ssdv_shared.cuh -- attention for groups of requests that share a prefix: what
+// its kernels share.
+//
+// The prefix of a group is attended to by the rows of all its requests together,
+// R rows at a time: a row block (group, kv head, R rows) meets the prefix's tiles one
+// after another, and all tiles of all row blocks form one list that is cut into
+// equal shares, one a team.  A row block that is cut leaves one part a team, a row's
+// maximum, sum of weights and sums of values.  Row r of the list of all rows (by
+// group, kv head, request, query, query head) has its part of team c at place
+// r + c R: parts of one row block lie R apart, and those of one team as their rows
+// do, so no two meet.  Each request's own tokens go through the kernels of
+// ssdv_attn.cu from position first[b] on, and a last kernel joins a row's parts in
+// the teams' order.
+#pragma once
+
+#include "ssdv_attn.cuh"
+
+namespace ssdv {
+
+struct SharedLaunch {
+  KvAttnArgs a;                // first, own_ml and own_o set
+  const int32_t* group_start;  // [G + 1]
+  const int32_t* shared_len;   // [G]
+  int G;
+  int per, rows;               // query heads per kv head; rows of a request and kv head
+  int R, tile, teams;          // rows of a row block, tokens of a tile
+  // workspace
+  long long* head;             // [0]: tiles a team
+  long long* unit0;            // [G]: tiles in the list before a group's
+  int32_t* first;              // [B]: tokens of the request's prefix, -1 if its group is bad
+  int32_t* group_of;           // [B]
+  float2* ml;                  // [rows of all + teams * R]
+  float* o;                    // and [.., D]
+};
+
+struct SharedShape {
+  int R, tile, teams;
+  bool tc;
+};
+SharedShape shared_shape(int D, int esize, int sms);
+cudaError_t launch_shared_tc(const SharedLaunch& L, int D, cudaStream_t stream);
+
+#ifdef __CUDACC__
+
+namespace {
+
+// A team's stretch of one row block's tiles.
+struct SharedPart {
+  int g, h, block;        // group, kv head, row block
+  int b0, n_rows;         // first request; rows in the block
+  int len, t0, count;     // tokens of the prefix, first tile, tiles
+  long long row0;         // the block's first row in the list of all rows
+};
+
+struct GroupList {
+  const SharedLaunch& L;
+  const long long* scan;
+  int chunk, threads;
+  long long total, quota;
+  __device__ __forceinline__ GroupList(const SharedLaunch& L_) : L(L_) {}
+
+  __device__ __forceinline__ int length(int g) const {
+    const int n = L.shared_len[g];
+    return n < 0 || n > static_cast<long long>(L.a.c.max_pages) * L.a.c.page_size ? 0 : n;
+  }
+  __device__ __forceinline__ long long group_rows(int g) const {
+    return static_cast<long long>(L.group_start[g + 1] - L.group_start[g]) * L.rows;
+  }
+  __device__ __forceinline__ int blocks(int g) const { return static_cast<int>((group_rows(g) + L.R - 1) / L.R); }
+  __device__ __forceinline__ int tiles(int g) const { return static_cast<int>((length(g) + L.tile - 1ll) / L.tile); }
+  __device__ __forceinline__ long long units(int g) const {
+    return static_cast<long long>(L.a.c.kv_heads) * blocks(g) * tiles(g);
+  }
+
+  // All threads of the CTA; ends with a barrier.  `sums` holds a number per warp.
+  __device__ __forceinline__ void build(long long* scan_, long long* sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    threads = blockDim.x;
+    scan = scan_;
+    chunk = (L.G + threads - 1) / threads;
+    const int g0 = min(tid * chunk, L.G), g1 = min(g0 + chunk, L.G);
+    bool broken = false;
+    for (int g = g0; g < g1; ++g)
+      broken |= L.group_start[g] > L.group_start[g + 1] || (g == 0 && L.group_start[g] != 0) ||
+                (g == L.G - 1 && L.group_start[g + 1] != L.a.B);
+    broken = __syncthreads_or(broken);
+    long long mine = 0;
+    if (!broken)
+      for (int g = g0; g < g1; ++g) mine += units(g);
+    long long x = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+    for (int v = 0; v < threads / 32; ++v) {
+      if (v < warp) before += sums[v];
+      total += sums[v];
+    }
+    scan_[tid] = before + x - mine;
+    quota = max((total + L.teams - 1) / L.teams, 1ll);
+    // what the kernels after this one need to know
+    if (blockIdx.x == 0) {
+      if (tid == 0) L.head[0] = quota;
+      long long u = before + x - mine;
+      for (int g = g0; g < g1; ++g) {
+        L.unit0[g] = u;
+        if (!broken) u += units(g);
+      }
+    }
+    for (int b = blockIdx.x * threads + tid; b < L.a.B; b += gridDim.x * threads) {
+      int lo = 0, hi = L.G - 1;  // the last group that begins at or before b
+      while (!broken && lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (L.group_start[mid] <= b) lo = mid;
+        else hi = mid - 1;
+      }
+      const int n = L.shared_len[lo];
+      L.group_of[b] = lo;
+      L.first[b] = broken || n < 0 || n != length(lo) ? -1 : n;
+    }
+    __syncthreads();
+  }
+  // The part that begins with unit u < end of the list, and goes on to `end` at most.
+  __device__ __forceinline__ SharedPart part(long long u, long long end) const {
+    int lo = 0, hi = threads - 1;  // last thread whose groups begin at or before u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (mid * chunk < L.G && scan[mid] <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    SharedPart p;
+    p.g = lo * chunk;
+    long long u0 = scan[lo];
+    while (u0 + units(p.g) <= u) u0 += units(p.g++);
+    const int n = tiles(p.g), nb = blocks(p.g);
+    const long long k = u - u0, rb = k / n, rows = group_rows(p.g);
+    p.h = static_cast<int>(rb / nb);
+    p.block = static_cast<int>(rb - static_cast<long long>(p.h) * nb);
+    p.len = length(p.g);
+    p.t0 = static_cast<int>(k - rb * n);
+    p.count = static_cast<int>(min(static_cast<long long>(n - p.t0), end - u));
+    p.b0 = L.group_start[p.g];
+    p.n_rows = static_cast<int>(min(static_cast<long long>(L.R), rows - static_cast<long long>(p.block) * L.R));
+    p.row0 = static_cast<long long>(p.b0) * L.rows * L.a.c.kv_heads + p.h * rows + static_cast<long long>(p.block) * L.R;
+    return p;
+  }
+};
+
+// Where a row block's row is: request, query, query head; whether it is real.
+struct SharedRow {
+  int b, i, head;
+  bool real;
+  __device__ __forceinline__ SharedRow(const SharedLaunch& L, const SharedPart& p, int row) {
+    const long long r = static_cast<long long>(p.block) * L.R + row;
+    b = p.b0 + static_cast<int>(r / L.rows);
+    const int k = static_cast<int>(r % L.rows);
+    i = k / L.per;
+    head = p.h * L.per + k - i * L.per;
+    real = row < p.n_rows && i < (L.a.n_q ? L.a.n_q[b] : L.a.nq);
+  }
+};
+
+}  // namespace
+
+#endif  // __CUDACC__
+
+}  // namespace ssdv

@@ -81,6 +81,9 @@ def _declare(lib):
     lib.ssd_kv_read.argtypes = [P, P, P, I, I, I, P, P, P, SZ, P]
     lib.ssd_kv_attention.argtypes = [P, P, P, P, P, I, I, I, I, F, I, I, P, P, P, SZ, P]
     lib.ssd_kv_attention_sinks.argtypes = [P, P, P, P, P, I, I, I, I, F, I, I, I, P, P, P, SZ, P]
+    lib.ssd_kv_attention_shared.argtypes = [P, P, P, P, P, I, I, I, I, F, P, P, I, I, P, P, P, SZ, P]
+    lib.ssd_kv_shared_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.ssd_kv_shared_workspace_bytes.restype = SZ
     lib.ssd_kv_plan.argtypes = [P, P, P, P, I, I, I, I, P, P, I, P, P, P, P, P, P, P, SZ, P]
     lib.ssd_kv_plan_workspace_bytes.argtypes = [I]
     lib.ssd_kv_plan_workspace_bytes.restype = SZ
@@ -96,7 +99,8 @@ def _declare(lib):
                  "ssd_verify_ragged", "ssd_verify_ragged_pipelined", "ssd_saguaro_prespec", "ssd_debug_rowstats",
                  "ssd_debug_saguaro_stats", "ssd_read_status",
                  "ssd_verify_saguaro", "ssd_cache_check", "ssd_verify_saguaro_draft", "ssd_verify_top_p",
-                 "ssd_kv_append", "ssd_kv_read", "ssd_kv_attention", "ssd_kv_attention_sinks", "ssd_kv_plan", "ssd_qk_norm_rope",
+                 "ssd_kv_append", "ssd_kv_read", "ssd_kv_attention", "ssd_kv_attention_sinks",
+                 "ssd_kv_attention_shared", "ssd_kv_plan", "ssd_qk_norm_rope",
                  "ssd_stream_capture_id", "ssd_debug_uniforms"):
         getattr(lib, name).restype = I
     return lib
@@ -656,6 +660,51 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
                                             int(past_only), _kv_dev(out, "out", q.dtype, index),
                                             _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None,
                                             _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
+    return (out, lse) if lse is not None else out
+
+
+@functools.lru_cache(maxsize=None)
+def kv_shared_workspace_bytes(B: int, n: int, n_heads: int, n_kv_heads: int, head_dim: int, groups: int) -> int:
+    return int(lib().ssd_kv_shared_workspace_bytes(B, n, n_heads, n_kv_heads, head_dim, groups))
+
+
+def kv_attention_shared(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, q: torch.Tensor,
+                        group_start: torch.Tensor, shared_len: torch.Tensor, n_q: Optional[torch.Tensor] = None,
+                        scale: Optional[float] = None, past_only: bool = False, out: Optional[torch.Tensor] = None,
+                        lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """ssd_kv_attention_shared: kv_attention for requests group_start[g] .. group_start[g + 1] - 1 (int32 [groups + 1])
+    that hold the same keys and values at positions below shared_len[g] (int32 [groups]), read once for the group."""
+    shape, device = q.shape, cache.device
+    if len(shape) != 4:
+        raise ValueError(f"q must be [B, n, n_heads, head_dim], got {list(shape)}")
+    B, n, heads = shape[:3]
+    c, kv_heads, dim = _kv_cache(cache, page_table, B)
+    index = cache.get_device()
+    qp, qs = _kv_rows(q, "q", None, dim, index)
+    lens, counts = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_q, "n_q", B, index)
+    if shared_len.dim() != 1 or shared_len.shape[0] < 1:
+        raise ValueError(f"shared_len must be [groups], got {list(shared_len.shape)}")
+    groups = shared_len.shape[0]
+    starts = _kv_counts(group_start, "group_start", groups + 1, index)
+    shared = _kv_counts(shared_len, "shared_len", groups, index)
+    raw, ctx = _kv_stream(stream, device)
+    ws = workspace
+    with ctx or _HERE:
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=device)
+        if lse is None and return_lse:
+            lse = torch.empty((B, n, heads), dtype=torch.float32, device=device)
+        if ws is None and B and n:
+            ws = _kv_workspace(kv_shared_workspace_bytes(B, n, heads, kv_heads, dim, groups), device, raw)
+    if out.shape != shape or (lse is not None and lse.shape != (B, n, heads)):
+        raise ValueError("out must be shaped like q and lse [B, n, n_heads]")
+    if B and n:
+        _check(lib().ssd_kv_attention_shared(c, lens, counts, qp, qs, _dtype_code(q, "q"), B, n, heads,
+                                             float(scale) if scale is not None else dim ** -0.5, starts, shared, groups,
+                                             int(past_only), _kv_dev(out, "out", q.dtype, index),
+                                             _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None,
+                                             _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
     return (out, lse) if lse is not None else out
 
 

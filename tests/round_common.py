@@ -70,11 +70,12 @@ def rope_bound(y, size, dtype):
 
 def attend(q, k, v, seen, scale):
     """One request: q [n, H, D], k and v [T, Hkv, D] as held; seen(i): the positions that query i sees.
-    (out, lse, mag, spread, count) as kv_common.attention gives them."""
+    (out, lse, mag, spread, count) as kv_common.attention gives them, and the sums of |v| over what is seen."""
     n, H, D = q.shape
     G = H // k.shape[1]
     out, mag = np.zeros((n, H, D)), np.zeros((n, H, D))
     lse, spread, count = np.full((n, H), -np.inf), np.zeros((n, H)), np.zeros((n, H))
+    every = np.zeros((n, H, D))
     for i in range(n):
         at = seen(i)
         if len(at) == 0:
@@ -89,4 +90,14 @@ def attend(q, k, v, seen, scale):
             mag[i, h] = (p @ np.abs(vv)) / z
             spread[i, h] = abs(scale) * (np.abs(kk) @ np.abs(q[i, h])).max()
             count[i, h] = len(at)
-    return out, lse, mag, spread, count
+            every[i, h] = np.abs(vv).sum(0)
+    return (out, lse, mag, spread, count), every
+
+
+def small_weights(every, dtype):
+    """What rounding weights to fp16 adds to kv_common.bounds where the kernels keep no more than one pass of them.  A
+    weight is 2^(x - m + 15) with m at least the row's largest score so far (fp32: two parts), or 2^(x - m + 9) with m
+    at most six octaves below it (bf16 on the tensor cores).  Below 2^-14 fp16 numbers are multiples of 2^-24, so a
+    weight is off by 2^-25 at most, which is 2^-40 or 2^-34 of the row's largest weight and no more of the sum of
+    weights; each token's error comes with its |v|."""
+    return every * (2.0 ** -40 if dtype == torch.float32 else 2.0 ** -34)

@@ -28,7 +28,7 @@ def compare(p, q64, kh, vh, lens, n_q, dtype, out, lse, window, sinks, past_only
     scale = p.D ** -0.5 if scale is None else scale
     out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
     for b in range(p.B):
-        ref = rc.attend(q64[b], kh[b], vh[b],
+        ref, _ = rc.attend(q64[b], kh[b], vh[b],
                         lambda i: visible(int(lens[b]), i, window, sinks, past_only) if i < n_q[b] else np.arange(0), scale)
         tol, ltol = kc.bounds(*ref, p.D, dtype)
         gone = ref[4] == 0
@@ -138,7 +138,7 @@ def test_nan_between_sinks_and_window(ssdv, D, G, n, dtype):
     assert torch.isnan(out[1, 0]).all()
     clean_v[1, only] = 0
     kh, vh = kc.held(clean_k), kc.held(clean_v)
-    ref = rc.attend(q64[1], kh[1], vh[1], lambda i: visible(int(lens[1]), i, window, sinks, False), D ** -0.5)
+    ref, _ = rc.attend(q64[1], kh[1], vh[1], lambda i: visible(int(lens[1]), i, window, sinks, False), D ** -0.5)
     out[1, 0] = torch.from_numpy(ref[0][0]).to(out)  # (its NaN is right)
     compare(p, q64, kh, vh, lens, np.full(B, n), dtype, out, lse, window, sinks)
     v[2, 3] = float("nan")  # a sink

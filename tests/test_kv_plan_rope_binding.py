@@ -93,3 +93,32 @@ def test_sinks_arguments(lib):
         return lib.ssd_kv_attention_sinks(c, P, None, P, ST, 0, 2, 3, 8, 0.1, window, sinks, 0, P, None, P, 16, None)
 
     assert att(-1, 0) == SHAPE and att(0, -1) == SHAPE and att(64, -(1 << 31)) == SHAPE and att(64, 4) == WORKSPACE
+
+
+def test_shared_arguments(lib):
+    def cache(**kw):
+        args = dict(pages=4096, n_pages=8, n_kv_heads=2, head_dim=128, page_size=64, max_pages=4, page_table=4096)
+        args.update(kw)
+        return ctypes.byref(ssdv.KvCacheStruct(**args))
+
+    def att(c=None, lens=P, nq=None, q=P, qs=ST, dt=0, B=2, n=3, heads=8, scale=0.1, start=P, shared=P, G=2, out=P, lse=None,
+            ws=P, size=1 << 40):
+        return lib.ssd_kv_attention_shared(c or cache(), lens, nq, q, qs, dt, B, n, heads, scale, start, shared, G, 0, out, lse,
+                                           ws, size, None)
+
+    neg = (ctypes.c_int64 * 3)(-1024, 128, 128)
+    for kw in (dict(lens=None), dict(q=None), dict(qs=None), dict(out=None), dict(ws=None), dict(start=None), dict(shared=None),
+               dict(c=cache(pages=None)), dict(c=cache(page_table=None))):
+        assert att(**kw) == NULL, kw
+    for kw in (dict(B=0), dict(B=65536), dict(n=0), dict(n=33), dict(heads=7), dict(heads=512), dict(G=0), dict(G=65536),
+               dict(scale=float("inf")), dict(scale=float("nan")), dict(scale=3e38), dict(qs=neg), dict(c=cache(head_dim=96)),
+               dict(c=cache(page_size=24))):
+        assert att(**kw) == SHAPE, kw
+    for kw in (dict(lens=ODD), dict(nq=ODD), dict(q=ODD), dict(start=ODD), dict(shared=ODD), dict(out=ODD), dict(lse=ODD),
+               dict(ws=ODD)):
+        assert att(**kw) == ALIGN, kw
+    need = lib.ssd_kv_shared_workspace_bytes(2, 3, 8, 2, 128, 2)
+    assert need > 256 and att(size=need - 1) == WORKSPACE and att(dt=3) == DTYPE
+    for bad in ((0, 3, 8, 2, 128, 2), (65536, 3, 8, 2, 128, 2), (2, 0, 8, 2, 128, 2), (2, 33, 8, 2, 128, 2), (2, 3, 7, 2, 128, 2),
+                (2, 3, 8, 2, 96, 2), (2, 3, 8, 2, 128, 0), (2, 3, 8, 2, 128, 65536)):
+        assert lib.ssd_kv_shared_workspace_bytes(*bad) == 0, bad
