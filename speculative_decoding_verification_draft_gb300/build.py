@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libssdv.so")
 SOURCES = ["ssdv_api.cu", "ssdv_verify.cu", "ssdv_saguaro.cu", "ssdv_topp.cu",
            "ssdv_kv.cu", "ssdv_attn.cu", "ssdv_attn_tc.cu", "ssdv_plan.cu", "ssdv_rope.cu",
-           "ssdv_shared.cu"]
+           "ssdv_attn_more.cu", "ssdv_attn_tc_more.cu", "ssdv_shared.cu", "ssdv_shared_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -51,7 +51,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
-                     "--expt-relaxed-constexpr"] + list(extra_flags)
+                     "--expt-relaxed-constexpr", "--split-compile=0"] + list(extra_flags)
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")

@@ -615,7 +615,7 @@ __device__ __forceinline__ uint32_t tile_step(const KvAttnArgs& a, Rows<E, D, NT
           for (int x = 0; x < 2; ++x) {
             const int2 seen = w.span[nt * 8 + 2 * c + x];
             const int from = max(0, min(seen.x - first, 16)), to = max(0, min(seen.y - first, 16));
-            const int sinks = max(0, min(a.sinks - first, 16));
+            const int sinks = max(0, min(sinks_of(a) - first, 16));
             if (there & ((1u << to) - 1u) & (~((1u << from) - 1u) | ((1u << sinks) - 1u)))
 #pragma unroll
               for (int ii = 0; ii < kMost; ++ii) {
@@ -652,7 +652,7 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List<kTile>& 
   };
   const auto fetch_page = [&]() {
     const int pos = pr.s.tile(pr.tile) * kTile + (lane & 3) * kKvBlock;
-    want = pr.s.any && pos < pr.s.hi && (pos + kKvBlock > pr.s.lo || pos < a.sinks);
+    want = pr.s.any() && pos < pr.s.hi && (pos + kKvBlock > pr.s.lo || (kMore && pos < a.sinks));
     if (want) page = a.c.page_table[static_cast<long long>(pr.b) * a.c.max_pages + column];
   };
   if (left) {
@@ -687,7 +687,7 @@ __device__ __forceinline__ void produce(const AttnLaunch& L, const List<kTile>& 
       if (++put == S) put = 0, phase ^= 1;
       if (--left) {
         pr.next(a, list.per_request);
-        if (pr.tile == 0 || pr.tile == pr.s.ahead || bpp < 4) {
+        if (pr.tile == 0 || (kMore && pr.tile == pr.s.ahead) || bpp < 4) {
           locate();
         } else if ((sub += 4) >= bpp) {
           sub -= bpp;
@@ -731,7 +731,7 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
     const int n8 = max(0, (min(nrows - pass0, L.rows_pass) + 7) / 8);
     const int row0 = pass0 + group * n8 / G * 8;
     const int own = (group + 1) * n8 / G - group * n8 / G;
-    const int active = sp.any ? own : 0;
+    const int active = sp.any() ? own : 0;
     const int lo_last = row_lo(a, sp, sp.nq - 1), hi_first = row_hi(a, sp.len, 0);
     bool bad = sp.bad;
     load_queries<E, D, NT, P>(L, w, b, h, row0, nrows, sp, spans, lane, sync);
@@ -741,7 +741,7 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
       bad |= flags[team * S + take] != 0;
       const uint32_t tile = data + (team * S + take) * stage_bytes(D);
       const int pos0 = sp.tile(first + k) * kTile;
-      const bool edge = (pos0 < lo_last && pos0 + kTile > a.sinks) || pos0 + kTile > hi_first;
+      const bool edge = (pos0 < lo_last && (!kMore || pos0 + kTile > a.sinks)) || pos0 + kTile > hi_first;
       for (uint32_t todo = active ? 1 : 0; todo;) {
         const int band = __ffs(todo) - 1;
         todo &= todo - 1;
@@ -792,7 +792,7 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
         if (nt >= own || row >= nrows) continue;  // (a padded query's row went along with its tile)
         float l = w.l[nt][x];
         if (bad) l = __int_as_float(0x7FC00000);
-        if (whole && !a.own_ml) {
+        if (whole && !own_sums(a)) {
           const int i = row / L.per;
           const long long orow = (static_cast<long long>(b) * a.nq + i) * a.heads + h * L.per + row % L.per;
           const float inv = 1.f / l;
@@ -814,19 +814,19 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
             a.lse[orow] = l == 0.f ? -INFINITY : (w.m[nt][x] + (log2f(l) - kBias)) * 0.69314718055994531f;
         } else {
           const long long at_row =
-              whole ? (static_cast<long long>(b) * a.c.kv_heads + h) * L.rows + row : slot * L.rows_pass + (row - pass0);
-          float4* o = reinterpret_cast<float4*>((whole ? a.own_o : L.o) + at_row * D + d0);
+              kMore && whole ? (static_cast<long long>(b) * a.c.kv_heads + h) * L.rows + row : slot * L.rows_pass + (row - pass0);
+          float4* o = reinterpret_cast<float4*>((kMore && whole ? a.own_o : L.o) + at_row * D + d0);
 #pragma unroll
           for (int v = 0; v < kOwn / 4; ++v)
             o[v] = make_float4(w.o[2 * v][nt][x], w.o[2 * v][nt][2 + x], w.o[2 * v + 1][nt][x], w.o[2 * v + 1][nt][2 + x]);
-          if (r == 0 && pw == 0) (whole ? a.own_ml : L.ml)[at_row] = make_float2(w.m[nt][x], l);
+          if (r == 0 && pw == 0) (kMore && whole ? a.own_ml : L.ml)[at_row] = make_float2(w.m[nt][x], l);
         }
       }
     if (first == 0) {
       // rows past the request's own (all of them if its lengths are bad)
       if (sp.bad && at.hr == 0 && first_warp && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
       const float none = sp.bad ? __int_as_float(0x7FC00000) : 0.f;
-      const int end = a.own_ml ? 0 : min(pass0 + L.rows_pass, L.rows);
+      const int end = own_sums(a) ? 0 : min(pass0 + L.rows_pass, L.rows);
       for (int row = max(pass0, nrows) + group * P + pw; row < end; row += G * P) {
         const long long orow = (static_cast<long long>(b) * a.nq + row / L.per) * a.heads + h * L.per + row % L.per;
         for (int d = lane; d < D; d += 32) static_cast<E*>(a.out)[orow * D + d] = static_cast<E>(none);
@@ -909,7 +909,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnLaunch L) {
     }
   }
   const int i = row / L.per, h = d.y / RT;
-  if (L.a.own_ml) {
+  if (own_sums(L.a)) {
     const long long at = (static_cast<long long>(d.x) * L.a.c.kv_heads + h) * L.rows + row;
     if (lane == 0) L.a.own_ml[at] = make_float2(ref, l);
 #pragma unroll
@@ -983,11 +983,16 @@ WorkLayout work_layout(const AttnShape& p, int D) {
 
 }  // namespace
 
+#if SSDV_ATTN_MORE
+cudaError_t launch_attention_more(const KvAttnArgs& a, int D, int esize, cudaStream_t stream) {
+#else
 size_t kv_attention_work_bytes(int rows, int D) {
   return std::max(work_layout(attn_shape(rows, D, false), D).total, work_layout(attn_shape(rows, D, true), D).total);
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int D, int esize, cudaStream_t stream) {
+  if (a.sinks || a.first || a.own_ml) return launch_attention_more(a, D, esize, stream);
+#endif
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1004,7 +1009,7 @@ cudaError_t launch_kv_attention(const KvAttnArgs& a, int D, int esize, cudaStrea
   L.ml = reinterpret_cast<float2*>(a.work + w.ml);
   L.o = reinterpret_cast<float*>(a.work + w.o);
   if (L.p.tc) {
-    e = launch_attention_tc(L, sms, stream);
+    e = kMore ? launch_attention_tc_more(L, sms, stream) : launch_attention_tc(L, sms, stream);
     return e == cudaSuccess ? launch_join<__nv_bfloat16, 128>(L, sms, stream) : e;
   }
   if (esize == 2) {

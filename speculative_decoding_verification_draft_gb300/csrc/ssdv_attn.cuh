@@ -13,8 +13,17 @@
 
 #include <atomic>
 
+// The attention kernels are compiled twice: without (0) and with (1) sinks, first
+// positions and sums in place of outputs.  They are bound by instruction fetches and
+// latency, and what those cost would be paid by all calls (64 requests of 201 to 8003
+// tokens, 20 rows: 100 us without, 110 with; 2 of 131072: 172 and 210).
+#ifndef SSDV_ATTN_MORE
+#define SSDV_ATTN_MORE 0
+#endif
+
 namespace ssdv {
 
+constexpr bool kMore = SSDV_ATTN_MORE;
 constexpr int kBand = 29;        // octaves below that in which fp16 keeps 11 bits
 constexpr int kBands = 5;        // passes a tile may take; weights below 2^-141 of its largest are dropped
 constexpr float kSmallest = 6.103515625e-05f;  // 2^(kBias - kBand)
@@ -40,6 +49,8 @@ struct AttnLaunch {
 };
 
 cudaError_t launch_attention_tc(const AttnLaunch& L, int sms, cudaStream_t stream);
+cudaError_t launch_attention_tc_more(const AttnLaunch& L, int sms, cudaStream_t stream);
+cudaError_t launch_attention_more(const KvAttnArgs& a, int D, int esize, cudaStream_t stream);
 
 #ifdef __CUDACC__
 
@@ -182,9 +193,15 @@ struct Span {
   // writes the outputs.
   int tile0, ahead, tiles;
   int first;
-  bool bad, any;   // any: some row sees something
-  __device__ __forceinline__ int tile(int t) const { return t < ahead ? tile0 + t : t - ahead; }
+  bool bad, some;
+  __device__ __forceinline__ int tile(int t) const { return !kMore || t < ahead ? tile0 + t : t - ahead; }
+  __device__ __forceinline__ bool any() const { return kMore ? some : hi > lo; }  // some row sees something
 };
+__device__ __forceinline__ int sinks_of(const KvAttnArgs& a) { return kMore ? a.sinks : 0; }
+__device__ __forceinline__ bool own_sums(const KvAttnArgs& a) { return kMore && a.own_ml; }
+__device__ __forceinline__ int row_lo(const KvAttnArgs& a, const Span& s, int i) {
+  return a.window ? max(0, s.len + i + 1 - a.window) : kMore ? s.first : 0;
+}
 template <int kTile>
 __device__ __forceinline__ Span find_span(const KvAttnArgs& a, int b) {
   Span s;
@@ -195,20 +212,20 @@ __device__ __forceinline__ Span find_span(const KvAttnArgs& a, int b) {
               static_cast<long long>(a.c.max_pages) * a.c.page_size;
   s.lo = s.hi = s.tile0 = s.first = 0;
   s.tiles = s.ahead = 1;
-  s.any = false;
-  if (a.first) {
+  s.some = false;
+  if (kMore && a.first) {
     s.first = a.first[b];
     s.bad |= s.first < 0 || s.first > s.len;
   }
   if (s.bad || s.nq == 0) return s;
   const int hi = a.past_only ? s.len : s.len + s.nq;
-  const int lo = min(a.window ? max(0, s.len + 1 - a.window) : s.first, hi);
-  const int sink_tiles = (min(a.sinks, lo) + kTile - 1) / kTile;
+  const int lo = min(row_lo(a, s, 0), hi);
+  const int sink_tiles = (min(sinks_of(a), lo) + kTile - 1) / kTile;
   const int tile0 = max(lo / kTile, sink_tiles), ahead = max((hi + kTile - 1) / kTile - tile0, 0);
   // (a window that lies behind the past holds nothing, whatever tile it ends in)
   const int seen = lo < hi ? ahead : 0;
   if (seen + sink_tiles == 0) return s;
-  s.any = true;
+  s.some = true;
   s.lo = lo;
   s.hi = hi;
   s.tile0 = tile0;
@@ -216,12 +233,9 @@ __device__ __forceinline__ Span find_span(const KvAttnArgs& a, int b) {
   s.tiles = seen + sink_tiles;
   return s;
 }
-__device__ __forceinline__ int row_lo(const KvAttnArgs& a, const Span& s, int i) {
-  return a.window ? max(0, s.len + i + 1 - a.window) : s.first;
-}
 // Whether some row sees a position of a request.
 __device__ __forceinline__ bool in_span(const KvAttnArgs& a, int lo, int hi, int pos) {
-  return pos < hi && (pos >= lo || pos < a.sinks);
+  return pos < hi && (pos >= lo || (kMore && pos < a.sinks));
 }
 __device__ __forceinline__ int row_hi(const KvAttnArgs& a, int len, int i) { return a.past_only ? len : len + i + 1; }
 

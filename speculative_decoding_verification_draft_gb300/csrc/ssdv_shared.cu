@@ -382,6 +382,7 @@ SharedWork shared_work(long long B, int nq, int heads, int kv_heads, int D, int 
 }  // namespace
 
 SharedShape shared_shape(int D, int esize, int sms) {
+  if (esize == 2 && D != 256) return {256, 128, sms, true};
   return {kRows, kTokens, sms * kTeamsPerSm, false};
 }
 
@@ -420,7 +421,8 @@ cudaError_t launch_kv_shared(const KvAttnArgs& a, const int32_t* group_start, co
   L.o = reinterpret_cast<float*>(a.work + w.o);
   L.a.first = L.first;
   L.a.work = a.work + w.attn;
-  e = esize == 2 ? launch_type<__nv_bfloat16>(L, D, stream, false) : launch_type<float>(L, D, stream, false);
+  if (s.tc) e = launch_shared_tc(L, D, stream);
+  else e = esize == 2 ? launch_type<__nv_bfloat16>(L, D, stream, false) : launch_type<float>(L, D, stream, false);
   if (e == cudaSuccess) e = launch_kv_attention(L.a, D, esize, stream);
   if (e != cudaSuccess) return e;
   return esize == 2 ? launch_type<__nv_bfloat16>(L, D, stream, true) : launch_type<float>(L, D, stream, true);

@@ -13,6 +13,7 @@
 // the teams' order.
 #pragma once
 
+#define SSDV_ATTN_MORE 1
 #include "ssdv_attn.cuh"
 
 namespace ssdv {

@@ -1,0 +1,581 @@
+// ssdv_shared_tc.cu -- attention over a shared prefix on the fifth-generation tensor
+// cores: bf16 queries, 64 or 128 elements a head.
+//
+// Rows are the M side here (a group has hundreds of them): 256 rows of a row block,
+// two tiles of 128, meet tiles of 128 tokens.
+//   S [128 rows x 128 tokens]    = Q K^T     both operands in shared memory
+//   O [128 rows x D elements]   += P V       P in tensor memory, where S was
+// Keys and values are unpacked once for all 256 rows, to fp16, where n s is exact.
+//
+// Twenty warps:
+//   0-3, 4-7   weights of the first and the second 128 rows, a thread a row: maximum,
+//              2^x, sum, weights back to tensor memory, corrections, results
+//   8-11       keys: a token a thread, from global memory to a shared operand
+//   12-15      values: two elements of some blocks a thread, likewise
+//   16, 17     issue the matrix instructions of the first and the second 128 rows
+//   18         finds the CTA's parts of the list
+// The two tiles of rows take turns: while one's weights are computed the other's
+// products run.
+//
+// Weights are fp16, 2^(x - m + 9), with m the row's maximum when it was last moved:
+// it moves once a score lies more than six octaves above, so sums are corrected a few
+// times a row and not once a tile.  fp16 keeps 11 bits down to 2^-14, 23 octaves
+// below m, and multiples of 2^-24 below that, 2^-34 of the row's largest weight at
+// most; outputs are bf16.  Maxima, sums of weights and of values are fp32.
+#include "ssdv_shared.cuh"
+#include "ssdv_tc.cuh"
+
+namespace ssdv {
+
+namespace {
+
+constexpr int kTile = 128, kM = 128, kThreads = 640;
+constexpr int kFast = 9, kTop = 15;
+
+enum : int {
+  kKeysFull = 0,     // [2] keys unpacked               -> matrix
+  kKeysEmpty = 2,    // [2] both tiles' scores computed -> keys
+  kValuesFull = 4,   // [2] values unpacked             -> matrix
+  kValuesEmpty = 6,  // [2] both tiles' products        -> values
+  kQueryFull = 8,    // [2 tiles of rows] queries written    -> matrix
+  kScoresFull = 10,  // [2] scores computed                  -> weights
+  kWeightsFull = 12, // [2] weights written, sums corrected  -> matrix
+  kOutFull = 14,     // [2] a tile's products added          -> matrix, and the last -> weights
+  kDone = 16,        // all matrix instructions are done
+  kPartFull = 17,    // [kRing] a part is described          -> all
+  kPartEmpty = 21,   // [kRing] all have read it             -> plan
+  kBars = 25
+};
+constexpr int kRing = 4, kReaders = 18, kPartsAt = 256;
+
+template <int D>
+struct Smem {
+  static constexpr int kOperand = kTile * D * 2;  // 128 rows or tokens x D, or D x 128
+  static constexpr int tmem = 200, query = 1024, keys = query + 2 * kOperand, values = keys + 2 * kOperand;
+  static constexpr int total = values + 2 * kOperand + 1024;  // operands begin at a multiple of 1024
+};
+constexpr int kScoresAt = 0, kOutAt = 2 * kTile;  // columns of tensor memory, a tile of rows after the other
+
+__device__ __forceinline__ void tc_ld32(uint32_t at, float (&x)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
+      "%31}, [%32];"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]),
+        "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]),
+        "=f"(x[17]), "=f"(x[18]), "=f"(x[19]), "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]),
+        "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
+      : "r"(at));
+}
+// D [128 x N] in tensor memory (+)= A [128 x 16] B [N x 16], both in shared memory.
+__device__ __forceinline__ void tc_mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, bool leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+
+// A role's view of the CTA.  Parts are found by one warp (64-bit divisions, searches)
+// and described in a ring in shared memory.
+struct Roles {
+  const SharedLaunch& L;
+  uint32_t base, tmem;
+  Waiter w;
+  int n = 0;
+  // The CTA's next part, false when there is none.
+  __device__ __forceinline__ bool next(SharedPart& p, int lane) {
+    w.wait(kPartFull + n % kRing, n / kRing);
+    const uint32_t from = base + kPartsAt + n % kRing * 64;
+    const uint4 x = lds128(from), y = lds128(from + 16);
+    const uint2 z = lds64(from + 32);
+    p.h = x.x, p.block = x.y, p.b0 = x.z, p.n_rows = x.w;
+    p.len = y.x, p.t0 = y.y, p.count = __shfl_sync(~0u, y.z, 0);
+    p.row0 = z.x | static_cast<long long>(z.y) << 32;
+    __syncwarp();
+    if (lane == 0) w.arrive(kPartEmpty + n % kRing);
+    ++n;
+    return __any_sync(~0u, !w.dead() && p.count > 0);
+  }
+};
+__device__ __forceinline__ void part_role(const SharedLaunch& L, const GroupList& list, uint32_t base, Waiter w, int lane) {
+  long long u = blockIdx.x * list.quota;
+  const long long end = min(u + list.quota, list.total);
+#pragma unroll 1
+  for (int n = 0; !w.dead(); ++n) {
+    SharedPart p = {};
+    if (u < end) p = list.part(u, end);
+    u += p.count;
+    w.nap(kPartEmpty + n % kRing, (n / kRing) ^ 1);
+    if (lane == 0) {
+      const uint32_t to = base + kPartsAt + n % kRing * 64;
+      sts128(to, make_uint4(p.h, p.block, p.b0, p.n_rows));
+      sts128(to + 16, make_uint4(p.len, p.t0, p.count, 0));
+      sts64(to + 32, make_uint2(static_cast<uint32_t>(p.row0), static_cast<uint32_t>(p.row0 >> 32)));
+      w.arrive(kPartFull + n % kRing);
+    }
+    if (p.count == 0) break;
+  }
+  if (w.dead() && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+}
+
+// Where a block of the prefix lies.
+struct Blocks {
+  const KvCacheArgs& c;
+  const int32_t* table;
+  int bpp, len, block_bytes;
+  long long head;
+  __device__ __forceinline__ Blocks(const SharedLaunch& L, const SharedPart& p, int block_bytes_)
+      : c(L.a.c), table(L.a.c.page_table + static_cast<long long>(p.b0) * L.a.c.max_pages),
+        bpp(L.a.c.page_size / kKvBlock), len(p.len), block_bytes(block_bytes_), head(p.h) {}
+  // Block `at` of the sequence: its page (0 if there is no such block).
+  __device__ __forceinline__ int page(int at) const { return at * kKvBlock < len ? table[at / bpp] : 0; }
+  __device__ __forceinline__ bool good(int page) const { return page >= 0 && page < c.n_pages; }
+  // Null behind the prefix and on a bad page.
+  __device__ __forceinline__ const uint8_t* find(int at, int page) const {
+    if (at * kKvBlock >= len || !good(page)) return nullptr;
+    return c.pages + ((page * static_cast<long long>(c.kv_heads) + head) * bpp + at % bpp) * block_bytes;
+  }
+};
+
+// ---- keys ----
+
+template <int D>
+__device__ __forceinline__ void key_role(Roles r, int tid) {
+  constexpr int kWords = D / 32, kGroups = D / 16;  // 16 bytes of codes; scales
+  const int lane = tid & 31, t = tid & 15, blk = tid >> 4;
+  const Bases bases = make_bases();
+  const uint32_t to = r.base + Smem<D>::keys + tid * 128;
+  SharedPart p;
+  int it = 0;
+  while (r.next(p, lane)) {
+    const Blocks blocks(r.L, p, kv_block_bytes(D));
+    uint4 c[kWords];
+    uint32_t s[kGroups / 2];  // two groups' scales each
+    const uint8_t* from;
+    const auto load = [&](int i) {  // 32 elements
+      c[i] = from ? __ldg(reinterpret_cast<const uint4*>(from + k_word_offset<D>(t, i * 4))) : make_uint4(0, 0, 0, 0);
+      if constexpr (D == 64) {
+        s[i] = from ? from[k_scale_offset<D>(t, 2 * i)] | from[k_scale_offset<D>(t, 2 * i + 1)] << 8 : 0xFFFFu;
+      } else {
+        s[i] = from ? *reinterpret_cast<const unsigned short*>(from + k_scale_offset<D>(t, 2 * i)) : 0xFFFFu;
+      }
+    };
+    int at = p.t0 * 8 + blk, page = blocks.page(at);
+    bool bad = !blocks.good(page);
+    from = blocks.find(at, page);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) load(i);
+    page = p.count > 1 ? blocks.page(at + 8) : 0;
+#pragma unroll 1
+    for (int k = 0; k < p.count; ++k, ++it) {
+      at += 8;
+      const bool more = k + 1 < p.count;
+      if (more) {
+        from = blocks.find(at, page);
+        bad |= !blocks.good(page);
+        page = k + 2 < p.count ? blocks.page(at + 8) : 0;
+      }
+      const int st = it & 1;
+      r.w.wait(kKeysEmpty + st, (it >> 1) ^ 1);
+      const uint32_t row = to + st * Smem<D>::kOperand;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t words[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        const uint32_t sb = s[i];
+        // what is behind the prefix may be anything: its scores are not used
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t x = __byte_perm(sb, 0, g ? 0x4141 : 0x4040) << 7;
+          const uint32_t x24 = mul2(x, kMinus24), x264 = mul2(x, kMinus264);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t v = words[g * 2 + y], u = __funnelshift_r(v, v, 8);
+            const int chunk = i * 4 + g * 2 + y;  // of 8 elements
+            sts128(row + (chunk >> 3) * (kTile * 128) + (((chunk & 7) ^ (tid & 7)) << 4),
+                   make_uint4(fma2(pair_hi(v, bases), x, x24), fma2(pair_lo(v, bases), x, x264),
+                              fma2(pair_hi(u, bases), x, x24), fma2(pair_lo(u, bases), x, x264)));
+          }
+        }
+        if (more) load(i);
+      }
+      async_fence();
+      __syncwarp();
+      if (lane == 0) r.w.arrive(kKeysFull + st);
+    }
+    if (bad) atomicOr(r.L.a.status, 1 << SSD_ERR_PAGE);
+  }
+  if (r.w.dead() && lane == 0) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
+}
+
+// ---- values: lane l has elements (2 i, 2 i + 1) of row g of the codes' order, i = l %
+// (D / 16), and half of the lanes take them the other way round, so that eight
+// neighbours write to different banks ----
+
+template <int D>
+__device__ __forceinline__ void value_role(Roles r, int tid) {
+  constexpr int kI = D / 16, kB = D / 32;  // blocks a thread
+  const int lane = tid & 31, warp = tid >> 5, i = lane & (kI - 1), swap = (lane >> 2) & 1;
+  const int g = lane / kI + (D == 128 ? 4 * (warp & 1) : 0), b0 = (D == 128 ? warp >> 1 : warp) * kB;
+  const int d0 = g * (D / 8) + 2 * i;
+  const Bases bases = make_bases();
+  const uint32_t to = r.base + Smem<D>::values;
+  SharedPart p;
+  int it = 0;
+  while (r.next(p, lane)) {
+    const Blocks blocks(r.L, p, kv_block_bytes(D));
+    uint4 c[kB], s[kB];
+    int page[kB];
+    const auto load = [&](int b, const uint8_t* from) {
+      c[b] = from ? __ldg(reinterpret_cast<const uint4*>(from + v_word_offset<D>(d0, 0))) : make_uint4(0, 0, 0, 0);
+      s[b] = from ? __ldg(reinterpret_cast<const uint4*>(from + kv_v_scales(D) + (d0 >> 4) * 16)) : make_uint4(0, 0, 0, 0);
+    };
+    int at = p.t0 * 8 + b0;
+#pragma unroll
+    for (int b = 0; b < kB; ++b) page[b] = blocks.page(at + b);
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      load(b, blocks.find(at + b, page[b]));
+      page[b] = p.count > 1 ? blocks.page(at + 8 + b) : 0;
+    }
+#pragma unroll 1
+    for (int k = 0; k < p.count; ++k, ++it) {
+      at += 8;
+      const int st = it & 1, pos0 = (p.t0 + k) * kTile;
+      const bool edge = pos0 + kTile > p.len;
+      r.w.wait(kValuesEmpty + st, (it >> 1) ^ 1);
+      const uint32_t operand = to + st * Smem<D>::kOperand;
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        uint32_t sb[4] = {s[b].x, s[b].y, s[b].z, s[b].w};
+        if (edge) {
+          // tokens behind the prefix: zero
+          const int seen = p.len - pos0 - (b0 + b) * 16;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            sb[x] = seen >= 4 * x + 4 ? sb[x] : seen <= 4 * x ? 0u : sb[x] & ((1u << (seen - 4 * x) * 8) - 1u);
+        }
+        const uint4 code = c[b];
+        if (k + 1 < p.count) {
+          load(b, blocks.find(at + b, page[b]));
+          page[b] = k + 2 < p.count ? blocks.page(at + 8 + b) : 0;
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // 8 tokens
+          uint32_t x[4], o[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            x[y] = __byte_perm(sb[half * 2 + (y >> 1)], 0, y & 1 ? 0x4342 : 0x4140) << 7;
+            o[y] = mul2(x[y], y & 1 ? kMinus264 : kMinus24);
+          }
+          const int chunk = (b0 + b) * 2 + half;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = d0 + (e ^ swap);
+            const uint32_t v = half ? (e ^ swap ? code.w : code.y) : (e ^ swap ? code.z : code.x);
+            const uint32_t u = __funnelshift_r(v, v, 8);
+            sts128(operand + (chunk >> 3) * (D * 128) + d * 128 + (((chunk & 7) ^ (d & 7)) << 4),
+                   make_uint4(fma2(pair_hi(v, bases), x[0], o[0]), fma2(pair_lo(v, bases), x[1], o[1]),
+                              fma2(pair_hi(u, bases), x[2], o[2]), fma2(pair_lo(u, bases), x[3], o[3])));
+          }
+        }
+      }
+      async_fence();
+      __syncwarp();
+      if (lane == 0) r.w.arrive(kValuesFull + st);
+    }
+  }
+  if (r.w.dead() && lane == 0) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
+}
+
+// ---- matrix instructions of a tile of rows (one lane issues them) ----
+
+template <int D>
+__device__ __forceinline__ void matrix_role(Roles r, int tile, int lane) {
+  const bool leader = lane == 0;
+  const uint32_t scores = r.tmem + kScoresAt + tile * kTile, out = r.tmem + kOutAt + tile * D;
+  const uint64_t query = tc_operand(r.base + Smem<D>::query + tile * Smem<D>::kOperand);
+  const uint64_t keys = tc_operand(r.base + Smem<D>::keys), values = tc_operand(r.base + Smem<D>::values);
+  Waiter& w = r.w;
+  const auto score = [&](int st) {
+#pragma unroll 1
+    for (int s = 0; s < D / 16; ++s) {
+      const int at = (s >> 2) * (kTile * 128 / 16) + (s & 3) * 2;
+      tc_mma_shared(scores, query + at, keys + st * (Smem<D>::kOperand / 16) + at, tc_idesc(kTile, false), s > 0, leader);
+    }
+    tc_commit(w.bars + (kScoresFull + tile) * 8, leader);
+    tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
+  };
+  SharedPart p;
+  int it = 0, mine = 0, parts = 0;
+  while (r.next(p, lane)) {
+    if (tile && p.n_rows <= kM) {
+      // nothing to do with this part's tiles but to let them go
+#pragma unroll 1
+      for (int k = 0; k < p.count; ++k, ++it) {
+        w.wait(kKeysFull + (it & 1), it >> 1);
+        if (leader) w.arrive(kKeysEmpty + (it & 1));
+        w.wait(kValuesFull + (it & 1), it >> 1);
+        if (leader) w.arrive(kValuesEmpty + (it & 1));
+      }
+      continue;
+    }
+    w.wait(kQueryFull + tile, parts++);
+    w.wait(kKeysFull + (it & 1), it >> 1);
+    tc_fence_after();
+    if (!w.dead()) score(it & 1);
+#pragma unroll 1
+    for (int k = 0; k < p.count; ++k, ++it, ++mine) {
+      const int st = it & 1;
+      w.wait(kValuesFull + st, it >> 1);
+      w.wait(kWeightsFull + tile, mine);
+      if (w.dead()) continue;
+      tc_fence_after();
+#pragma unroll 1
+      for (int s = 0; s < kTile / 16; ++s)
+        tc_mma(out, scores + s * 8, values + st * (Smem<D>::kOperand / 16) + (s >> 2) * (D * 128 / 16) + (s & 3) * 2,
+               tc_idesc(D, false), k > 0 || s > 0, leader);
+      tc_commit(w.bars + (kOutFull + tile) * 8, leader);
+      tc_commit(w.bars + (kValuesEmpty + st) * 8, leader);
+      if (k + 1 < p.count) {
+        w.wait(kKeysFull + (st ^ 1), (it + 1) >> 1);
+        // the scores go where the weights are: these have to be read
+        w.wait(kOutFull + tile, mine);
+        tc_fence_after();
+        if (!w.dead()) score(st ^ 1);
+      }
+    }
+  }
+  if (w.dead() && leader) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
+  tc_commit(w.bars + kDone * 8, leader);
+  bar_wait(w.bars + kDone * 8, 0);
+}
+
+// ---- weights: a thread a row ----
+
+template <int D>
+__device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
+  const SharedLaunch& L = r.L;
+  const int lane = tid & 31;
+  const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
+  const uint32_t scores = r.tmem + lanes + kScoresAt + tile * kTile, out = r.tmem + lanes + kOutAt + tile * D;
+  const uint32_t query = r.base + Smem<D>::query + tile * Smem<D>::kOperand + tid * 128;
+  const bool vec =
+      (reinterpret_cast<uintptr_t>(L.a.q) & 15) == 0 && ((L.a.qs[0] | L.a.qs[1] | L.a.qs[2]) & 7) == 0;  // (in elements)
+  Waiter& w = r.w;
+  SharedPart p;
+  int mine = 0;
+  while (r.next(p, lane)) {
+    if (tile && p.n_rows <= kM) continue;
+    const int row = tile * kM + tid;
+    float f;
+    {
+      // the query as fp16, a power of two up: its largest element to [2^12, 2^13), the
+      // scale's sign on it (exact down to 2^-26 of the largest)
+      const SharedRow at(L, p, row);
+      const unsigned short* q =
+          static_cast<const unsigned short*>(L.a.q) + at.b * L.a.qs[0] + at.i * L.a.qs[1] + at.head * L.a.qs[2];
+      const auto load = [&](int c) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (at.real) {
+          if (vec) {
+            v = __ldg(reinterpret_cast<const uint4*>(q) + c);
+          } else {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t h = q[c * 8 + e];
+              v.x = __funnelshift_r(v.x, v.y, 16), v.y = __funnelshift_r(v.y, v.z, 16);
+              v.z = __funnelshift_r(v.z, v.w, 16), v.w = __funnelshift_r(v.w, h, 16);
+            }
+          }
+        }
+        return v;
+      };
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 v = load(c);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+      }
+      int ex = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127;
+      ex = max(-100, min(ex, 127));
+      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), L.a.scale_log2);
+      f = fabsf(L.a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23);
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 v = load(c);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y[e] = half2_bits(__floats2half2_rn(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up));
+        sts128(query + (c >> 3) * (kM * 128) + (((c & 7) ^ (tid & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+      }
+    }
+    async_fence();
+    __syncwarp();
+    if (lane == 0) w.arrive(kQueryFull + tile);
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < p.count; ++k, ++mine) {
+      const int seen = p.len - (p.t0 + k) * kTile;  // tokens of the tile
+      w.wait(kScoresFull + tile, mine);
+      tc_fence_after();
+      float x[2][32];
+      float top = -INFINITY;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        tc_ld32(scores + half * 64, x[0]);
+        tc_ld32(scores + half * 64 + 32, x[1]);
+        tc_wait_ld<32>(x[0]);
+        tc_wait_ld<32>(x[1]);
+        if (seen < kTile) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] = half * 64 + i < seen ? x[i >> 5][i & 31] : -INFINITY;
+        }
+        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          a = fmaxf(a, fmaxf(x[0][i], x[0][i + 1]));
+          b = fmaxf(b, fmaxf(x[1][i], x[1][i + 1]));
+        }
+        top = fmaxf(top, fmaxf(a, b));
+      }
+      top *= f;  // (f >= 0, and some token of a tile is always seen)
+      if (__any_sync(~0u, !(top <= m + (kTop - kFast)))) {
+        const float now = fmaxf(m, top), fall = ex2(m - now);
+        // (the products of the tiles before are done: these scores came after them)
+        if (k > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            tc_ld32(out + c * 32, x[0]);
+            tc_wait_ld<32>(x[0]);
+            uint32_t y[2][16];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i >> 4][i & 15] = __float_as_uint(x[0][i] * fall);
+            tc_st16(out + c * 32, y[0]);
+            tc_st16(out + c * 32 + 16, y[1]);
+          }
+          l *= fall;
+        }
+        m = now;
+      }
+      const float ref = kFast - m;
+      tc_ld32(scores, x[0]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float (&y)[32] = x[c & 1];
+        tc_wait_ld<32>(y);
+        if (c < 3) tc_ld32(scores + (c + 1) * 32, x[(c + 1) & 1]);
+        uint32_t h[16];
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          fma_pair(y[i], y[i + 1], make_uint4(__float_as_uint(f), __float_as_uint(f), __float_as_uint(ref), __float_as_uint(ref)));
+          y[i] = ex2(y[i]);
+          y[i + 1] = ex2(y[i + 1]);
+          if (seen < kTile) {
+            if (c * 32 + i >= seen) y[i] = 0.f;
+            if (c * 32 + i + 1 >= seen) y[i + 1] = 0.f;
+          }
+          add_pair(a, b, y[i], y[i + 1]);
+          h[i >> 1] = half2_bits(__floats2half2_rn(y[i], y[i + 1]));
+        }
+        l += a + b;
+        tc_st16(scores + c * 16, h);  // (where scores that have been read were)
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) w.arrive(kWeightsFull + tile);
+    }
+    // this part's sums
+    w.wait(kOutFull + tile, mine - 1);
+    tc_fence_after();
+    const bool real = row < p.n_rows;
+    const long long at = p.row0 + row + static_cast<long long>(blockIdx.x) * (2 * kM);
+    constexpr float kUp = 1 << (kTop - kFast);  // (parts are kept 2^15 up)
+    if (real) L.ml[at] = make_float2(m, w.dead() ? __int_as_float(0x7FC00000) : l * kUp);
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      float x[32];
+      tc_ld32(out + c * 32, x);
+      tc_wait_ld<32>(x);
+      if (real) {
+        float4* o = reinterpret_cast<float4*>(L.o + at * D + c * 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          o[i] = make_float4(x[4 * i] * kUp, x[4 * i + 1] * kUp, x[4 * i + 2] * kUp, x[4 * i + 3] * kUp);
+      }
+    }
+    tc_fence_before();
+  }
+  if (w.dead() && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedLaunch L) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ long long scan[kThreads], sums[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_u32(smem) + 1023) & ~1023u;
+  if (tid < kBars) {
+    // how many warps (or commits) arrive
+    int count = 1;
+    if ((tid >= kKeysFull && tid < kKeysEmpty) || (tid >= kValuesFull && tid < kValuesEmpty) ||
+        (tid >= kQueryFull && tid < kScoresFull) || (tid >= kWeightsFull && tid < kOutFull))
+      count = 4;
+    if (tid >= kPartEmpty) count = kReaders;
+    if ((tid >= kKeysEmpty && tid < kValuesFull) || (tid >= kValuesEmpty && tid < kQueryFull) || tid == kDone) count = 2;
+    bar_init(base + tid * 8, count);
+  }
+  if (warp == 16) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + Smem<D>::tmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  tc_fence_before();
+  GroupList list(L);
+  list.build(scan, sums);
+  tc_fence_after();
+  Roles r = {L, base, lds32(base + Smem<D>::tmem), {}};
+  r.w.bars = base;
+  // 128 x (128 + 128 + 80 + 88 + 48) registers: within the 640 x 96 of the launch
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    weight_role<D>(r, warp >> 2, tid & 127);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    key_role<D>(r, tid & 127);
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    value_role<D>(r, tid & 127);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp < 18) matrix_role<D>(r, warp - 16, lane);
+    else if (warp == 18) part_role(L, list, base, r.w, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(lds32(base + Smem<D>::tmem)));
+  }
+}
+
+template <int D>
+cudaError_t launch_dim(const SharedLaunch& L, cudaStream_t stream) {
+  const cudaError_t e = allow_shared<shared_tc_kernel<D>>(Smem<D>::total);
+  if (e != cudaSuccess) return e;
+  shared_tc_kernel<D><<<L.teams, kThreads, Smem<D>::total, stream>>>(L);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_shared_tc(const SharedLaunch& L, int D, cudaStream_t stream) {
+  return D == 64 ? launch_dim<64>(L, stream) : launch_dim<128>(L, stream);
+}
+
+}  // namespace ssdv
