@@ -210,14 +210,29 @@ __device__ __forceinline__ Span find_span(const KvAttnArgs& a, int b) {
   s.bad = s.len < 0 || s.nq < 0 || s.nq > a.nq ||
           static_cast<long long>(s.len) + (a.past_only ? 0 : s.nq) >
               static_cast<long long>(a.c.max_pages) * a.c.page_size;
-  s.lo = s.hi = s.tile0 = s.first = 0;
-  s.tiles = s.ahead = 1;
-  s.some = false;
+  s.lo = s.hi = s.tile0 = 0;
+  s.tiles = 1;
+  if (kMore) {
+    s.first = 0;
+    s.ahead = 1;
+    s.some = false;
+  }
   if (kMore && a.first) {
     s.first = a.first[b];
     s.bad |= s.first < 0 || s.first > s.len;
   }
   if (s.bad || s.nq == 0) return s;
+  if constexpr (!kMore) {
+    s.hi = a.past_only ? s.len : s.len + s.nq;
+    s.lo = a.window ? max(0, s.len + 1 - a.window) : 0;
+    if (s.lo >= s.hi) {
+      s.lo = s.hi = 0;
+      return s;
+    }
+    s.tile0 = s.lo / kTile;
+    s.tiles = (s.hi + kTile - 1) / kTile - s.tile0;
+    return s;
+  }
   const int hi = a.past_only ? s.len : s.len + s.nq;
   const int lo = min(row_lo(a, s, 0), hi);
   const int sink_tiles = (min(sinks_of(a), lo) + kTile - 1) / kTile;
