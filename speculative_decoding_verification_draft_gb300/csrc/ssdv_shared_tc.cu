@@ -17,11 +17,13 @@
 // The two tiles of rows take turns: while one's weights are computed the other's
 // products run.
 //
-// Weights are fp16, 2^(x - m + 9), with m the row's maximum when it was last moved:
-// it moves once a score lies more than six octaves above, so sums are corrected a few
-// times a row and not once a tile.  fp16 keeps 11 bits down to 2^-14, 23 octaves
-// below m, and multiples of 2^-24 below that, 2^-34 of the row's largest weight at
-// most; outputs are bf16.  Maxima, sums of weights and of values are fp32.
+// Weights are fp16, 2^(x - m + 8), with m the row's maximum when it was last moved:
+// first taken from a part's first tile, it moves when a tile's weights add up to more
+// than fp16 holds, so most tiles are passed over once, without a maximum, and sums are
+// corrected a few times a row.  fp16 keeps 11 bits down to 2^-14, 22 octaves below m,
+// and multiples of 2^-24 below that; an error of half of one is 2^-33 of the row's
+// largest weight at most.  Outputs are bf16.  Maxima, sums of weights and of values are
+// fp32.
 #include "ssdv_shared.cuh"
 #include "ssdv_tc.cuh"
 
@@ -30,7 +32,7 @@ namespace ssdv {
 namespace {
 
 constexpr int kTile = 128, kM = 128, kThreads = 640;
-constexpr int kFast = 9, kTop = 15;
+constexpr int kFast = 8, kTop = 15;
 
 enum : int {
   kKeysFull = 0,     // [2] keys unpacked               -> matrix
@@ -44,14 +46,17 @@ enum : int {
   kDone = 16,        // all matrix instructions are done
   kPartFull = 17,    // [kRing] a part is described          -> all
   kPartEmpty = 21,   // [kRing] all have read it             -> plan
-  kBars = 25
+  kPlaceFull = 25,   // [kPlaces] a tile's blocks are found  -> keys, values
+  kPlaceEmpty = 33,  // [kPlaces] both have read them        -> plan
+  kBars = 41
 };
-constexpr int kRing = 4, kReaders = 18, kPartsAt = 256;
+constexpr int kRing = 4, kReaders = 18, kPlaces = 8;
+constexpr int kTmemAt = 384, kPartsAt = 512, kPlacesAt = 768;  // bytes; a part 64, a tile's eight blocks 64
 
 template <int D>
 struct Smem {
   static constexpr int kOperand = kTile * D * 2;  // 128 rows or tokens x D, or D x 128
-  static constexpr int tmem = 200, query = 1024, keys = query + 2 * kOperand, values = keys + 2 * kOperand;
+  static constexpr int query = 2048, keys = query + 2 * kOperand, values = keys + 2 * kOperand;
   static constexpr int total = values + 2 * kOperand + 1024;  // operands begin at a multiple of 1024
 };
 constexpr int kScoresAt = 0, kOutAt = 2 * kTile;  // columns of tensor memory, a tile of rows after the other
@@ -98,9 +103,14 @@ struct Roles {
     return __any_sync(~0u, !w.dead() && p.count > 0);
   }
 };
-__device__ __forceinline__ void part_role(const SharedLaunch& L, const GroupList& list, uint32_t base, Waiter w, int lane) {
+__device__ __forceinline__ void part_role(const SharedLaunch& L, const GroupList& list, uint32_t base, Waiter w, int lane,
+                                          int block_bytes) {
+  const KvCacheArgs& c = L.a.c;
+  const int bpp = c.page_size / kKvBlock;
   long long u = blockIdx.x * list.quota;
   const long long end = min(u + list.quota, list.total);
+  int it = 0;
+  bool bad = false;
 #pragma unroll 1
   for (int n = 0; !w.dead(); ++n) {
     SharedPart p = {};
@@ -115,84 +125,97 @@ __device__ __forceinline__ void part_role(const SharedLaunch& L, const GroupList
       w.arrive(kPartFull + n % kRing);
     }
     if (p.count == 0) break;
+    // where the tiles' blocks lie (null behind the prefix and on a bad page): eight
+    // lanes, a block each, pages a tile ahead
+    const int32_t* table = c.page_table + static_cast<long long>(p.b0) * c.max_pages;
+    int at = p.t0 * 8 + (lane & 7), col = at / bpp, sub = at - col * bpp;
+    const auto page_of = [&]() { return at * kKvBlock < p.len ? table[col] : -1; };
+    int page = page_of();
+#pragma unroll 1
+    for (int k = 0; k < p.count; ++k, ++it) {
+      const bool there = at * kKvBlock < p.len, ok = there && page >= 0 && page < c.n_pages;
+      bad |= there && !ok;
+      const uint8_t* from =
+          ok ? c.pages + ((static_cast<long long>(page) * c.kv_heads + p.h) * bpp + sub) * block_bytes : nullptr;
+      at += 8, sub += 8;
+      if (sub >= bpp) {
+        const int q = bpp >= 8 ? 1 : sub / bpp;
+        col += q;
+        sub -= q * bpp;
+      }
+      if (k + 1 < p.count) page = page_of();
+      const int slot = it % kPlaces;
+      w.nap(kPlaceEmpty + slot, (it / kPlaces) ^ 1);
+      if (lane < 8) {
+        const unsigned long long v = reinterpret_cast<unsigned long long>(from);
+        sts64(base + kPlacesAt + slot * 64 + lane * 8, make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32)));
+      }
+      __syncwarp();
+      if (lane == 0) w.arrive(kPlaceFull + slot);
+    }
   }
+  if (bad) atomicOr(L.a.status, 1 << SSD_ERR_PAGE);
   if (w.dead() && lane == 0) atomicOr(L.a.status, 1 << SSD_ERR_CUDA);
 }
 
-// Where a block of the prefix lies.
-struct Blocks {
-  const KvCacheArgs& c;
-  const int32_t* table;
-  int bpp, len, block_bytes;
-  long long head;
-  __device__ __forceinline__ Blocks(const SharedLaunch& L, const SharedPart& p, int block_bytes_)
-      : c(L.a.c), table(L.a.c.page_table + static_cast<long long>(p.b0) * L.a.c.max_pages),
-        bpp(L.a.c.page_size / kKvBlock), len(p.len), block_bytes(block_bytes_), head(p.h) {}
-  // Block `at` of the sequence: its page (0 if there is no such block).
-  __device__ __forceinline__ int page(int at) const { return at * kKvBlock < len ? table[at / bpp] : 0; }
-  __device__ __forceinline__ bool good(int page) const { return page >= 0 && page < c.n_pages; }
-  // Null behind the prefix and on a bad page.
-  __device__ __forceinline__ const uint8_t* find(int at, int page) const {
-    if (at * kKvBlock >= len || !good(page)) return nullptr;
-    return c.pages + ((page * static_cast<long long>(c.kv_heads) + head) * bpp + at % bpp) * block_bytes;
-  }
-};
+__device__ __forceinline__ const uint8_t* pointer(uint32_t lo, uint32_t hi) {
+  return reinterpret_cast<const uint8_t*>(lo | static_cast<unsigned long long>(hi) << 32);
+}
 
 // ---- keys ----
 
 template <int D>
 __device__ __forceinline__ void key_role(Roles r, int tid) {
-  constexpr int kWords = D / 32, kGroups = D / 16;  // 16 bytes of codes; scales
+  constexpr int kWords = D / 32;  // 16 bytes of codes
   const int lane = tid & 31, t = tid & 15, blk = tid >> 4;
   const Bases bases = make_bases();
-  const uint32_t to = r.base + Smem<D>::keys + tid * 128;
+  // chunk c of 8 elements of row `tid` lies at c ^ (tid & 7) of its 128 bytes
+  const uint32_t to = r.base + Smem<D>::keys + tid * 128 + ((tid & 7) << 4);
+  uint4 c[kWords];
+  uint32_t s[kWords];  // two groups' scales each
+  const uint8_t* from;
+  const auto find = [&](int it) {
+    const int slot = it % kPlaces;
+    r.w.wait(kPlaceFull + slot, it / kPlaces);
+    const uint2 v = lds64(r.base + kPlacesAt + slot * 64 + blk * 8);
+    from = pointer(v.x, v.y);
+    __syncwarp();
+    if (lane == 0) r.w.arrive(kPlaceEmpty + slot);
+  };
+  const auto load = [&](int i) {  // 32 elements; NaN where there is no block
+    c[i] = from ? __ldg(reinterpret_cast<const uint4*>(from + k_word_offset<D>(t, i * 4))) : make_uint4(0, 0, 0, 0);
+    if constexpr (D == 64) {
+      s[i] = from ? __ldg(from + k_scale_offset<D>(t, 2 * i)) | __ldg(from + k_scale_offset<D>(t, 2 * i + 1)) << 8 : 0xFFFFu;
+    } else {
+      s[i] = from ? __ldg(reinterpret_cast<const unsigned short*>(from + k_scale_offset<D>(t, 2 * i))) : 0xFFFFu;
+    }
+  };
   SharedPart p;
   int it = 0;
   while (r.next(p, lane)) {
-    const Blocks blocks(r.L, p, kv_block_bytes(D));
-    uint4 c[kWords];
-    uint32_t s[kGroups / 2];  // two groups' scales each
-    const uint8_t* from;
-    const auto load = [&](int i) {  // 32 elements
-      c[i] = from ? __ldg(reinterpret_cast<const uint4*>(from + k_word_offset<D>(t, i * 4))) : make_uint4(0, 0, 0, 0);
-      if constexpr (D == 64) {
-        s[i] = from ? from[k_scale_offset<D>(t, 2 * i)] | from[k_scale_offset<D>(t, 2 * i + 1)] << 8 : 0xFFFFu;
-      } else {
-        s[i] = from ? *reinterpret_cast<const unsigned short*>(from + k_scale_offset<D>(t, 2 * i)) : 0xFFFFu;
-      }
-    };
-    int at = p.t0 * 8 + blk, page = blocks.page(at);
-    bool bad = !blocks.good(page);
-    from = blocks.find(at, page);
+    find(it);
 #pragma unroll
     for (int i = 0; i < kWords; ++i) load(i);
-    page = p.count > 1 ? blocks.page(at + 8) : 0;
 #pragma unroll 1
     for (int k = 0; k < p.count; ++k, ++it) {
-      at += 8;
       const bool more = k + 1 < p.count;
-      if (more) {
-        from = blocks.find(at, page);
-        bad |= !blocks.good(page);
-        page = k + 2 < p.count ? blocks.page(at + 8) : 0;
-      }
+      if (more) find(it + 1);
       const int st = it & 1;
       r.w.wait(kKeysEmpty + st, (it >> 1) ^ 1);
       const uint32_t row = to + st * Smem<D>::kOperand;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const uint32_t words[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-        const uint32_t sb = s[i];
         // what is behind the prefix may be anything: its scores are not used
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const uint32_t x = __byte_perm(sb, 0, g ? 0x4141 : 0x4040) << 7;
+          const uint32_t x = __byte_perm(s[i], 0, g ? 0x4141 : 0x4040) << 7;
           const uint32_t x24 = mul2(x, kMinus24), x264 = mul2(x, kMinus264);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t v = words[g * 2 + y], u = __funnelshift_r(v, v, 8);
             const int chunk = i * 4 + g * 2 + y;  // of 8 elements
-            sts128(row + (chunk >> 3) * (kTile * 128) + (((chunk & 7) ^ (tid & 7)) << 4),
+            sts128((row ^ ((chunk & 7) << 4)) + (chunk >> 3) * (kTile * 128),
                    make_uint4(fma2(pair_hi(v, bases), x, x24), fma2(pair_lo(v, bases), x, x264),
                               fma2(pair_hi(u, bases), x, x24), fma2(pair_lo(u, bases), x, x264)));
           }
@@ -203,7 +226,6 @@ __device__ __forceinline__ void key_role(Roles r, int tid) {
       __syncwarp();
       if (lane == 0) r.w.arrive(kKeysFull + st);
     }
-    if (bad) atomicOr(r.L.a.status, 1 << SSD_ERR_PAGE);
   }
   if (r.w.dead() && lane == 0) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
 }
@@ -219,47 +241,62 @@ __device__ __forceinline__ void value_role(Roles r, int tid) {
   const int g = lane / kI + (D == 128 ? 4 * (warp & 1) : 0), b0 = (D == 128 ? warp >> 1 : warp) * kB;
   const int d0 = g * (D / 8) + 2 * i;
   const Bases bases = make_bases();
-  const uint32_t to = r.base + Smem<D>::values;
+  // chunk c of 8 tokens of row d lies at c ^ (d & 7) of its 128 bytes
+  uint32_t to[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int d = d0 + (e ^ swap);
+    to[e] = (r.base + Smem<D>::values + d * 128 + ((d & 7) << 4)) ^ ((b0 & 3) << 5);
+    if (b0 & 4) to[e] += D * 128;
+  }
+  uint4 c[kB], s[kB];
+  uint32_t at[2 * kB];  // where the next tile's blocks are
+  const auto find = [&](int it) {
+    const int slot = it % kPlaces;
+    r.w.wait(kPlaceFull + slot, it / kPlaces);
+#pragma unroll
+    for (int b = 0; b < kB; b += 2) {
+      const uint4 v = lds128(r.base + kPlacesAt + slot * 64 + (b0 + b) * 8);
+      at[2 * b] = v.x, at[2 * b + 1] = v.y, at[2 * b + 2] = v.z, at[2 * b + 3] = v.w;
+    }
+    __syncwarp();
+    if (lane == 0) r.w.arrive(kPlaceEmpty + slot);
+  };
+  const auto load = [&](int b) {
+    const uint8_t* from = pointer(at[2 * b], at[2 * b + 1]);
+    c[b] = from ? __ldg(reinterpret_cast<const uint4*>(from + v_word_offset<D>(d0, 0))) : make_uint4(0, 0, 0, 0);
+    s[b] = from ? __ldg(reinterpret_cast<const uint4*>(from + kv_v_scales(D) + (d0 >> 4) * 16)) : make_uint4(0, 0, 0, 0);
+  };
   SharedPart p;
   int it = 0;
   while (r.next(p, lane)) {
-    const Blocks blocks(r.L, p, kv_block_bytes(D));
-    uint4 c[kB], s[kB];
-    int page[kB];
-    const auto load = [&](int b, const uint8_t* from) {
-      c[b] = from ? __ldg(reinterpret_cast<const uint4*>(from + v_word_offset<D>(d0, 0))) : make_uint4(0, 0, 0, 0);
-      s[b] = from ? __ldg(reinterpret_cast<const uint4*>(from + kv_v_scales(D) + (d0 >> 4) * 16)) : make_uint4(0, 0, 0, 0);
-    };
-    int at = p.t0 * 8 + b0;
+    find(it);
 #pragma unroll
-    for (int b = 0; b < kB; ++b) page[b] = blocks.page(at + b);
-#pragma unroll
-    for (int b = 0; b < kB; ++b) {
-      load(b, blocks.find(at + b, page[b]));
-      page[b] = p.count > 1 ? blocks.page(at + 8 + b) : 0;
-    }
+    for (int b = 0; b < kB; ++b) load(b);
 #pragma unroll 1
     for (int k = 0; k < p.count; ++k, ++it) {
-      at += 8;
       const int st = it & 1, pos0 = (p.t0 + k) * kTile;
-      const bool edge = pos0 + kTile > p.len;
+      const bool more = k + 1 < p.count;
+      if (more) find(it + 1);
+      if (pos0 + kTile > p.len) {
+        // tokens behind the prefix: zero
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+          const int seen = p.len - pos0 - (b0 + b) * 16;
+          const auto keep = [&](uint32_t v, int x) {
+            return seen >= 4 * x + 4 ? v : seen <= 4 * x ? 0u : v & ((1u << (seen - 4 * x) * 8) - 1u);
+          };
+          s[b] = make_uint4(keep(s[b].x, 0), keep(s[b].y, 1), keep(s[b].z, 2), keep(s[b].w, 3));
+        }
+      }
       r.w.wait(kValuesEmpty + st, (it >> 1) ^ 1);
-      const uint32_t operand = to + st * Smem<D>::kOperand;
 #pragma unroll
       for (int b = 0; b < kB; ++b) {
-        uint32_t sb[4] = {s[b].x, s[b].y, s[b].z, s[b].w};
-        if (edge) {
-          // tokens behind the prefix: zero
-          const int seen = p.len - pos0 - (b0 + b) * 16;
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            sb[x] = seen >= 4 * x + 4 ? sb[x] : seen <= 4 * x ? 0u : sb[x] & ((1u << (seen - 4 * x) * 8) - 1u);
-        }
+        const uint32_t sb[4] = {s[b].x, s[b].y, s[b].z, s[b].w};
         const uint4 code = c[b];
-        if (k + 1 < p.count) {
-          load(b, blocks.find(at + b, page[b]));
-          page[b] = k + 2 < p.count ? blocks.page(at + 8 + b) : 0;
-        }
+        if (more) load(b);
+        const uint32_t first[2] = {swap ? code.z : code.x, swap ? code.x : code.z};
+        const uint32_t second[2] = {swap ? code.w : code.y, swap ? code.y : code.w};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // 8 tokens
           uint32_t x[4], o[4];
@@ -268,13 +305,10 @@ __device__ __forceinline__ void value_role(Roles r, int tid) {
             x[y] = __byte_perm(sb[half * 2 + (y >> 1)], 0, y & 1 ? 0x4342 : 0x4140) << 7;
             o[y] = mul2(x[y], y & 1 ? kMinus264 : kMinus24);
           }
-          const int chunk = (b0 + b) * 2 + half;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int d = d0 + (e ^ swap);
-            const uint32_t v = half ? (e ^ swap ? code.w : code.y) : (e ^ swap ? code.z : code.x);
-            const uint32_t u = __funnelshift_r(v, v, 8);
-            sts128(operand + (chunk >> 3) * (D * 128) + d * 128 + (((chunk & 7) ^ (d & 7)) << 4),
+            const uint32_t v = half ? second[e] : first[e], u = __funnelshift_r(v, v, 8);
+            sts128((to[e] ^ ((b * 2 + half) << 4)) + st * Smem<D>::kOperand,
                    make_uint4(fma2(pair_hi(v, bases), x[0], o[0]), fma2(pair_lo(v, bases), x[1], o[1]),
                               fma2(pair_hi(u, bases), x[2], o[2]), fma2(pair_lo(u, bases), x[3], o[3])));
           }
@@ -423,67 +457,78 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
       w.wait(kScoresFull + tile, mine);
       tc_fence_after();
       float x[2][32];
-      float top = -INFINITY;
+      bool done = false;
+      if (k > 0 && seen >= kTile) {
+        // with the reference as it is: no weight is too large for fp16 if their sum is not
+        uint32_t h[4][16];
+        float sum = 0.f;
+        const uint32_t fb = __float_as_uint(f), rb = __float_as_uint(kFast - m);
+        tc_ld32(scores, x[0]);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        tc_ld32(scores + half * 64, x[0]);
-        tc_ld32(scores + half * 64 + 32, x[1]);
-        tc_wait_ld<32>(x[0]);
-        tc_wait_ld<32>(x[1]);
-        if (seen < kTile) {
+        for (int c = 0; c < 4; ++c) {
+          float (&y)[32] = x[c & 1];
+          tc_wait_ld<32>(y);
+          if (c < 3) tc_ld32(scores + (c + 1) * 32, x[(c + 1) & 1]);
+          float a = 0.f, b = 0.f;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] = half * 64 + i < seen ? x[i >> 5][i & 31] : -INFINITY;
+          for (int i = 0; i < 32; i += 2) {
+            fma_pair(y[i], y[i + 1], make_uint4(fb, fb, rb, rb));
+            y[i] = ex2(y[i]);
+            y[i + 1] = ex2(y[i + 1]);
+            add_pair(a, b, y[i], y[i + 1]);
+            h[c][i >> 1] = half2_bits(__floats2half2_rn(y[i], y[i + 1]));
+          }
+          sum += a + b;
         }
-        float a = -INFINITY, b = -INFINITY;
+        done = __all_sync(~0u, sum <= 65504.f);
+        if (done) {
+          l += sum;
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          a = fmaxf(a, fmaxf(x[0][i], x[0][i + 1]));
-          b = fmaxf(b, fmaxf(x[1][i], x[1][i + 1]));
+          for (int c = 0; c < 4; ++c) tc_st16(scores + c * 16, h[c]);
         }
-        top = fmaxf(top, fmaxf(a, b));
       }
-      top *= f;  // (f >= 0, and some token of a tile is always seen)
-      if (__any_sync(~0u, !(top <= m + (kTop - kFast)))) {
-        const float now = fmaxf(m, top), fall = ex2(m - now);
-        // (the products of the tiles before are done: these scores came after them)
+      if (!done) {
+        // the reference becomes the row's maximum, the sums so far follow
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tc_ld32(scores + c * 32, x[0]);
+          tc_wait_ld<32>(x[0]);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, c * 32 + i < seen ? x[0][i] : -INFINITY);
+        }
+        const float now = fmaxf(m, top * f), fall = ex2(m - now);  // (f >= 0)
         if (k > 0) {
+          // (the products of the tiles before are done: these scores came after them)
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            float y[16];
+            uint32_t z[16];
+            tc_ld16(out + c * 16, y);
+            tc_wait_ld<16>(y);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            tc_ld32(out + c * 32, x[0]);
-            tc_wait_ld<32>(x[0]);
-            uint32_t y[2][16];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i >> 4][i & 15] = __float_as_uint(x[0][i] * fall);
-            tc_st16(out + c * 32, y[0]);
-            tc_st16(out + c * 32 + 16, y[1]);
+            for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(y[i] * fall);
+            tc_st16(out + c * 16, z);
           }
           l *= fall;
         }
         m = now;
-      }
-      const float ref = kFast - m;
-      tc_ld32(scores, x[0]);
+        const float ref = kFast - m;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tc_ld32(scores + c * 32, x[0]);
+          tc_wait_ld<32>(x[0]);
+          uint32_t h[16];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float (&y)[32] = x[c & 1];
-        tc_wait_ld<32>(y);
-        if (c < 3) tc_ld32(scores + (c + 1) * 32, x[(c + 1) & 1]);
-        uint32_t h[16];
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          fma_pair(y[i], y[i + 1], make_uint4(__float_as_uint(f), __float_as_uint(f), __float_as_uint(ref), __float_as_uint(ref)));
-          y[i] = ex2(y[i]);
-          y[i + 1] = ex2(y[i + 1]);
-          if (seen < kTile) {
-            if (c * 32 + i >= seen) y[i] = 0.f;
-            if (c * 32 + i + 1 >= seen) y[i + 1] = 0.f;
+          for (int i = 0; i < 32; ++i) {
+            // (a factor of zero makes no number of what is behind the prefix)
+            x[0][i] = c * 32 + i < seen ? ex2(fmaf(x[0][i], f, ref)) : 0.f;
+            l += x[0][i];
           }
-          add_pair(a, b, y[i], y[i + 1]);
-          h[i >> 1] = half2_bits(__floats2half2_rn(y[i], y[i + 1]));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) h[i] = half2_bits(__floats2half2_rn(x[0][2 * i], x[0][2 * i + 1]));
+          tc_st16(scores + c * 16, h);  // (where scores that have been read were)
         }
-        l += a + b;
-        tc_st16(scores + c * 16, h);  // (where scores that have been read were)
       }
       tc_wait_st();
       tc_fence_before();
@@ -526,12 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if ((tid >= kKeysFull && tid < kKeysEmpty) || (tid >= kValuesFull && tid < kValuesEmpty) ||
         (tid >= kQueryFull && tid < kScoresFull) || (tid >= kWeightsFull && tid < kOutFull))
       count = 4;
-    if (tid >= kPartEmpty) count = kReaders;
+    if (tid >= kPartEmpty && tid < kPlaceFull) count = kReaders;
+    if (tid >= kPlaceEmpty) count = 8;
     if ((tid >= kKeysEmpty && tid < kValuesFull) || (tid >= kValuesEmpty && tid < kQueryFull) || tid == kDone) count = 2;
     bar_init(base + tid * 8, count);
   }
   if (warp == 16) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + Smem<D>::tmem) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + kTmemAt) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -539,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   GroupList list(L);
   list.build(scan, sums);
   tc_fence_after();
-  Roles r = {L, base, lds32(base + Smem<D>::tmem), {}};
+  Roles r = {L, base, lds32(base + kTmemAt), {}};
   r.w.bars = base;
   // 128 x (128 + 128 + 80 + 88 + 48) registers: within the 640 x 96 of the launch
   if (warp < 8) {
@@ -554,13 +600,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp < 18) matrix_role<D>(r, warp - 16, lane);
-    else if (warp == 18) part_role(L, list, base, r.w, lane);
+    else if (warp == 18) part_role(L, list, base, r.w, lane, kv_block_bytes(D));
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 16) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(lds32(base + Smem<D>::tmem)));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(lds32(base + kTmemAt)));
   }
 }
 
