@@ -2,8 +2,8 @@
 // cores: bf16 queries, 64 or 128 elements a head.
 //
 // Rows are the M side here (a group has hundreds of them): 256 rows of a row block,
-// two tiles of 128, meet tiles of 128 tokens.
-//   S [128 rows x 128 tokens]    = Q K^T     both operands in shared memory
+// two tiles of 128, meet tiles of 128 tokens, scored in halves.
+//   S [128 rows x 64 tokens]     = Q K^T     both operands in shared memory
 //   O [128 rows x D elements]   += P V       P in tensor memory, where S was
 // Keys and values are unpacked once for all 256 rows, to fp16, where n s is exact.
 //
@@ -14,14 +14,14 @@
 //   12-15      values: two elements of some blocks a thread, likewise
 //   16, 17     issue the matrix instructions of the first and the second 128 rows
 //   18         finds the CTA's parts of the list
-// The two tiles of rows take turns: while one's weights are computed the other's
-// products run.
+// Scores of two halves are kept for each tile of rows, so that one half's weights are
+// computed while the products of the other run.
 //
-// Weights are fp16, 2^(x - m + 8), with m the row's maximum when it was last moved:
+// Weights are fp16, 2^(x - m + 9), with m the row's maximum when it was last moved:
 // first taken from a part's first tile, it moves when a tile's weights add up to more
 // than fp16 holds, so most tiles are passed over once, without a maximum, and sums are
-// corrected a few times a row.  fp16 keeps 11 bits down to 2^-14, 22 octaves below m,
-// and multiples of 2^-24 below that; an error of half of one is 2^-33 of the row's
+// corrected a few times a row.  fp16 keeps 11 bits down to 2^-14, 23 octaves below m,
+// and multiples of 2^-24 below that; an error of half of one is 2^-34 of the row's
 // largest weight at most.  Outputs are bf16.  Maxima, sums of weights and of values are
 // fp32.
 #include "ssdv_shared.cuh"
@@ -32,23 +32,24 @@ namespace ssdv {
 namespace {
 
 constexpr int kTile = 128, kM = 128, kThreads = 640;
-constexpr int kFast = 8, kTop = 15;
+constexpr int kHalf = 64;  // tokens that are scored at a time
+constexpr int kFast = 9, kTop = 15;
 
 enum : int {
-  kKeysFull = 0,     // [2] keys unpacked               -> matrix
-  kKeysEmpty = 2,    // [2] both tiles' scores computed -> keys
-  kValuesFull = 4,   // [2] values unpacked             -> matrix
-  kValuesEmpty = 6,  // [2] both tiles' products        -> values
-  kQueryFull = 8,    // [2 tiles of rows] queries written    -> matrix
-  kScoresFull = 10,  // [2] scores computed                  -> weights
-  kWeightsFull = 12, // [2] weights written, sums corrected  -> matrix
-  kOutFull = 14,     // [2] a tile's products added          -> matrix, and the last -> weights
-  kDone = 16,        // all matrix instructions are done
-  kPartFull = 17,    // [kRing] a part is described          -> all
-  kPartEmpty = 21,   // [kRing] all have read it             -> plan
-  kPlaceFull = 25,   // [kPlaces] a tile's blocks are found  -> keys, values
-  kPlaceEmpty = 33,  // [kPlaces] both have read them        -> plan
-  kBars = 41
+  kKeysFull = 0,      // [2] keys unpacked               -> matrix
+  kKeysEmpty = 2,     // [2] both tiles' scores computed -> keys
+  kValuesFull = 4,    // [2] values unpacked             -> matrix
+  kValuesEmpty = 6,   // [2] both tiles' products        -> values
+  kQueryFull = 8,     // [2 tiles of rows] queries written       -> matrix
+  kScoresFull = 10,   // [2][2] half a tile's scores computed    -> weights
+  kWeightsFull = 14,  // [2][2] weights written, sums corrected  -> matrix
+  kOutFull = 18,      // [2] half a tile's products added        -> matrix, weights
+  kDone = 20,         // all matrix instructions are done
+  kPartFull = 21,     // [kRing] a part is described          -> all
+  kPartEmpty = 25,    // [kRing] all have read it             -> plan
+  kPlaceFull = 29,    // [kPlaces] a tile's blocks are found  -> keys, values
+  kPlaceEmpty = 37,   // [kPlaces] both have read them        -> plan
+  kBars = 45
 };
 constexpr int kRing = 4, kReaders = 18, kPlaces = 8;
 constexpr int kTmemAt = 384, kPartsAt = 512, kPlacesAt = 768;  // bytes; a part 64, a tile's eight blocks 64
@@ -59,7 +60,8 @@ struct Smem {
   static constexpr int query = 2048, keys = query + 2 * kOperand, values = keys + 2 * kOperand;
   static constexpr int total = values + 2 * kOperand + 1024;  // operands begin at a multiple of 1024
 };
-constexpr int kScoresAt = 0, kOutAt = 2 * kTile;  // columns of tensor memory, a tile of rows after the other
+// Columns of tensor memory: scores of two half tiles for each tile of rows, then sums.
+constexpr int kScoresAt = 0, kOutAt = 4 * kHalf;
 
 __device__ __forceinline__ void tc_ld32(uint32_t at, float (&x)[32]) {
   asm volatile(
@@ -327,18 +329,22 @@ __device__ __forceinline__ void value_role(Roles r, int tid) {
 template <int D>
 __device__ __forceinline__ void matrix_role(Roles r, int tile, int lane) {
   const bool leader = lane == 0;
-  const uint32_t scores = r.tmem + kScoresAt + tile * kTile, out = r.tmem + kOutAt + tile * D;
+  const uint32_t scores = r.tmem + kScoresAt + tile * 2 * kHalf, out = r.tmem + kOutAt + tile * D;
   const uint64_t query = tc_operand(r.base + Smem<D>::query + tile * Smem<D>::kOperand);
   const uint64_t keys = tc_operand(r.base + Smem<D>::keys), values = tc_operand(r.base + Smem<D>::values);
   Waiter& w = r.w;
-  const auto score = [&](int st) {
+  // scores of half h of the tile in stage st
+  const auto score = [&](int st, int h) {
+    if (w.dead()) return;
+    tc_fence_after();
 #pragma unroll 1
     for (int s = 0; s < D / 16; ++s) {
       const int at = (s >> 2) * (kTile * 128 / 16) + (s & 3) * 2;
-      tc_mma_shared(scores, query + at, keys + st * (Smem<D>::kOperand / 16) + at, tc_idesc(kTile, false), s > 0, leader);
+      tc_mma_shared(scores + h * kHalf, query + at, keys + st * (Smem<D>::kOperand / 16) + h * (kHalf * 128 / 16) + at,
+                    tc_idesc(kHalf, false), s > 0, leader);
     }
-    tc_commit(w.bars + (kScoresFull + tile) * 8, leader);
-    tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
+    tc_commit(w.bars + (kScoresFull + tile * 2 + h) * 8, leader);
+    if (h) tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
   };
   SharedPart p;
   int it = 0, mine = 0, parts = 0;
@@ -356,27 +362,29 @@ __device__ __forceinline__ void matrix_role(Roles r, int tile, int lane) {
     }
     w.wait(kQueryFull + tile, parts++);
     w.wait(kKeysFull + (it & 1), it >> 1);
-    tc_fence_after();
-    if (!w.dead()) score(it & 1);
+    score(it & 1, 0);
+    score(it & 1, 1);
 #pragma unroll 1
     for (int k = 0; k < p.count; ++k, ++it, ++mine) {
       const int st = it & 1;
       w.wait(kValuesFull + st, it >> 1);
-      w.wait(kWeightsFull + tile, mine);
-      if (w.dead()) continue;
-      tc_fence_after();
 #pragma unroll 1
-      for (int s = 0; s < kTile / 16; ++s)
-        tc_mma(out, scores + s * 8, values + st * (Smem<D>::kOperand / 16) + (s >> 2) * (D * 128 / 16) + (s & 3) * 2,
-               tc_idesc(D, false), k > 0 || s > 0, leader);
-      tc_commit(w.bars + (kOutFull + tile) * 8, leader);
-      tc_commit(w.bars + (kValuesEmpty + st) * 8, leader);
-      if (k + 1 < p.count) {
-        w.wait(kKeysFull + (st ^ 1), (it + 1) >> 1);
-        // the scores go where the weights are: these have to be read
-        w.wait(kOutFull + tile, mine);
+      for (int h = 0; h < 2; ++h) {
+        w.wait(kWeightsFull + tile * 2 + h, mine);
+        if (w.dead()) continue;
         tc_fence_after();
-        if (!w.dead()) score(st ^ 1);
+#pragma unroll 1
+        for (int s = 0; s < kHalf / 16; ++s)
+          tc_mma(out, scores + h * kHalf + s * 8, values + st * (Smem<D>::kOperand / 16) + h * (D * 128 / 16) + s * 2,
+                 tc_idesc(D, false), k > 0 || h > 0 || s > 0, leader);
+        tc_commit(w.bars + (kOutFull + tile) * 8, leader);
+        if (h) tc_commit(w.bars + (kValuesEmpty + st) * 8, leader);
+        if (k + 1 < p.count) {
+          // the next tile's scores go where the weights are: these have to be read
+          if (h == 0) w.wait(kKeysFull + (st ^ 1), (it + 1) >> 1);
+          w.wait(kOutFull + tile, h);
+          score(st ^ 1, h);
+        }
       }
     }
   }
@@ -392,7 +400,7 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
   const SharedLaunch& L = r.L;
   const int lane = tid & 31;
   const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
-  const uint32_t scores = r.tmem + lanes + kScoresAt + tile * kTile, out = r.tmem + lanes + kOutAt + tile * D;
+  const uint32_t both = r.tmem + lanes + kScoresAt + tile * 2 * kHalf, out = r.tmem + lanes + kOutAt + tile * D;
   const uint32_t query = r.base + Smem<D>::query + tile * Smem<D>::kOperand + tid * 128;
   const bool vec =
       (reinterpret_cast<uintptr_t>(L.a.q) & 15) == 0 && ((L.a.qs[0] | L.a.qs[1] | L.a.qs[2]) & 7) == 0;  // (in elements)
@@ -452,54 +460,58 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
     if (lane == 0) w.arrive(kQueryFull + tile);
     float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-    for (int k = 0; k < p.count; ++k, ++mine) {
-      const int seen = p.len - (p.t0 + k) * kTile;  // tokens of the tile
-      w.wait(kScoresFull + tile, mine);
+    for (int k = 0; k < 2 * p.count; ++k, ++mine) {
+      const int h = k & 1;
+      const int seen = p.len - p.t0 * kTile - k * kHalf;  // tokens of the half tile
+      const uint32_t scores = both + h * kHalf;
+      w.wait(kScoresFull + tile * 2 + h, mine >> 1);
       tc_fence_after();
       float x[2][32];
       bool done = false;
-      if (k > 0 && seen >= kTile) {
+      if (k > 0 && seen >= kHalf) {
         // with the reference as it is: no weight is too large for fp16 if their sum is not
-        uint32_t h[4][16];
-        float sum = 0.f;
+        uint32_t y[2][16];
+        float sum[2];
         const uint32_t fb = __float_as_uint(f), rb = __float_as_uint(kFast - m);
         tc_ld32(scores, x[0]);
+        tc_ld32(scores + 32, x[1]);
+        tc_wait_ld<32>(x[0]);
+        tc_wait_ld<32>(x[1]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float (&y)[32] = x[c & 1];
-          tc_wait_ld<32>(y);
-          if (c < 3) tc_ld32(scores + (c + 1) * 32, x[(c + 1) & 1]);
+        for (int c = 0; c < 2; ++c) {
           float a = 0.f, b = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            fma_pair(y[i], y[i + 1], make_uint4(fb, fb, rb, rb));
-            y[i] = ex2(y[i]);
-            y[i + 1] = ex2(y[i + 1]);
-            add_pair(a, b, y[i], y[i + 1]);
-            h[c][i >> 1] = half2_bits(__floats2half2_rn(y[i], y[i + 1]));
+            fma_pair(x[c][i], x[c][i + 1], make_uint4(fb, fb, rb, rb));
+            x[c][i] = ex2(x[c][i]);
+            x[c][i + 1] = ex2(x[c][i + 1]);
+            add_pair(a, b, x[c][i], x[c][i + 1]);
+            y[c][i >> 1] = half2_bits(__floats2half2_rn(x[c][i], x[c][i + 1]));
           }
-          sum += a + b;
+          sum[c] = a + b;
         }
-        done = __all_sync(~0u, sum <= 65504.f);
+        sum[0] += sum[1];
+        done = __all_sync(~0u, sum[0] <= 65504.f);
         if (done) {
-          l += sum;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc_st16(scores + c * 16, h[c]);
+          l += sum[0];
+          tc_st16(scores, y[0]);
+          tc_st16(scores + 16, y[1]);
         }
       }
       if (!done) {
         // the reference becomes the row's maximum, the sums so far follow
         float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           tc_ld32(scores + c * 32, x[0]);
           tc_wait_ld<32>(x[0]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) top = fmaxf(top, c * 32 + i < seen ? x[0][i] : -INFINITY);
         }
-        const float now = fmaxf(m, top * f), fall = ex2(m - now);  // (f >= 0)
+        const float now = top == -INFINITY ? m : fmaxf(m, top * f), fall = ex2(m - now);  // (f >= 0)
         if (k > 0) {
-          // (the products of the tiles before are done: these scores came after them)
+          w.wait(kOutFull + tile, mine - 1);
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             float y[16];
@@ -515,10 +527,10 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
         m = now;
         const float ref = kFast - m;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           tc_ld32(scores + c * 32, x[0]);
           tc_wait_ld<32>(x[0]);
-          uint32_t h[16];
+          uint32_t y[16];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             // (a factor of zero makes no number of what is behind the prefix)
@@ -526,16 +538,18 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
             l += x[0][i];
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = half2_bits(__floats2half2_rn(x[0][2 * i], x[0][2 * i + 1]));
-          tc_st16(scores + c * 16, h);  // (where scores that have been read were)
+          for (int i = 0; i < 16; ++i) y[i] = half2_bits(__floats2half2_rn(x[0][2 * i], x[0][2 * i + 1]));
+          tc_st16(scores + c * 16, y);  // (where scores that have been read were)
         }
       }
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) w.arrive(kWeightsFull + tile);
+      if (lane == 0) w.arrive(kWeightsFull + tile * 2 + h);
     }
-    // this part's sums
+    // this part's sums (nobody has waited for the half before the last yet, and a phase
+    // can only be waited for once the one before it is over)
+    w.wait(kOutFull + tile, mine - 2);
     w.wait(kOutFull + tile, mine - 1);
     tc_fence_after();
     const bool real = row < p.n_rows;

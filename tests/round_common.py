@@ -96,8 +96,8 @@ def attend(q, k, v, seen, scale):
 
 def small_weights(every, dtype):
     """What rounding weights to fp16 adds to kv_common.bounds where the kernels keep no more than one pass of them.  A
-    weight is 2^(x - m + 15) with m at least the row's largest score so far (fp32: two parts), or 2^(x - m + 8) with m at
+    weight is 2^(x - m + 15) with m at least the row's largest score so far (fp32: two parts), or 2^(x - m + 9) with m at
     or below it (bf16 on the tensor cores).  Below 2^-14 fp16 numbers are multiples of 2^-24, so a
-    weight is off by 2^-25 at most, which is 2^-40 or 2^-33 of the row's largest weight and no more of the sum of
+    weight is off by 2^-25 at most, which is 2^-40 or 2^-34 of the row's largest weight and no more of the sum of
     weights; each token's error comes with its |v|."""
-    return every * (2.0 ** -40 if dtype == torch.float32 else 2.0 ** -33)
+    return every * (2.0 ** -40 if dtype == torch.float32 else 2.0 ** -34)
