@@ -4,7 +4,7 @@
 // Rows are the M side here (a group has hundreds of them): 256 rows of a row block,
 // two tiles of 128, meet tiles of 128 tokens, scored in halves.
 //   S [128 rows x 64 tokens]     = Q K^T     both operands in shared memory
-//   O [128 rows x D elements]   += P V       P in tensor memory, where S was
+//   O [128 rows x D elements]   += P V       P in tensor memory
 // Keys and values are unpacked once for all 256 rows, to fp16, where n s is exact.
 //
 // Twenty warps:
@@ -14,8 +14,9 @@
 //   12-15      values: two elements of some blocks a thread, likewise
 //   16, 17     issue the matrix instructions of the first and the second 128 rows
 //   18         finds the CTA's parts of the list
-// Scores of two halves are kept for each tile of rows, so that one half's weights are
-// computed while the products of the other run.
+// Scores go to registers as soon as they are there, so the next half's are computed
+// while this half's weights are; weights of two halves are kept, so that no matrix
+// instruction waits for another's end.
 //
 // Weights are fp16, 2^(x - m + 9), with m the row's maximum when it was last moved:
 // first taken from a part's first tile, it moves when a tile's weights add up to more
@@ -41,15 +42,16 @@ enum : int {
   kValuesFull = 4,    // [2] values unpacked             -> matrix
   kValuesEmpty = 6,   // [2] both tiles' products        -> values
   kQueryFull = 8,     // [2 tiles of rows] queries written       -> matrix
-  kScoresFull = 10,   // [2][2] half a tile's scores computed    -> weights
+  kScoresFull = 10,   // [2] half a tile's scores computed       -> weights
+  kScoresRead = 12,   // [2] and in registers                    -> matrix
   kWeightsFull = 14,  // [2][2] weights written, sums corrected  -> matrix
-  kOutFull = 18,      // [2] half a tile's products added        -> matrix, weights
-  kDone = 20,         // all matrix instructions are done
-  kPartFull = 21,     // [kRing] a part is described          -> all
-  kPartEmpty = 25,    // [kRing] all have read it             -> plan
-  kPlaceFull = 29,    // [kPlaces] a tile's blocks are found  -> keys, values
-  kPlaceEmpty = 37,   // [kPlaces] both have read them        -> plan
-  kBars = 45
+  kOutFull = 18,      // [2][2] half a tile's products added     -> weights
+  kDone = 22,         // all matrix instructions are done
+  kPartFull = 23,     // [kRing] a part is described          -> all
+  kPartEmpty = 27,    // [kRing] all have read it             -> plan
+  kPlaceFull = 31,    // [kPlaces] a tile's blocks are found  -> keys, values
+  kPlaceEmpty = 39,   // [kPlaces] both have read them        -> plan
+  kBars = 47
 };
 constexpr int kRing = 4, kReaders = 18, kPlaces = 8;
 constexpr int kTmemAt = 384, kPartsAt = 512, kPlacesAt = 768;  // bytes; a part 64, a tile's eight blocks 64
@@ -60,8 +62,9 @@ struct Smem {
   static constexpr int query = 2048, keys = query + 2 * kOperand, values = keys + 2 * kOperand;
   static constexpr int total = values + 2 * kOperand + 1024;  // operands begin at a multiple of 1024
 };
-// Columns of tensor memory: scores of two half tiles for each tile of rows, then sums.
-constexpr int kScoresAt = 0, kOutAt = 4 * kHalf;
+// Columns of tensor memory: each tile of rows' scores of half a tile, weights of two
+// halves (two fp16 a column), sums.
+constexpr int kScoresAt = 0, kWeightsAt = 2 * kHalf, kOutAt = 4 * kHalf;
 
 __device__ __forceinline__ void tc_ld32(uint32_t at, float (&x)[32]) {
   asm volatile(
@@ -329,7 +332,8 @@ __device__ __forceinline__ void value_role(Roles r, int tid) {
 template <int D>
 __device__ __forceinline__ void matrix_role(Roles r, int tile, int lane) {
   const bool leader = lane == 0;
-  const uint32_t scores = r.tmem + kScoresAt + tile * 2 * kHalf, out = r.tmem + kOutAt + tile * D;
+  const uint32_t scores = r.tmem + kScoresAt + tile * kHalf, weights = r.tmem + kWeightsAt + tile * kHalf;
+  const uint32_t out = r.tmem + kOutAt + tile * D;
   const uint64_t query = tc_operand(r.base + Smem<D>::query + tile * Smem<D>::kOperand);
   const uint64_t keys = tc_operand(r.base + Smem<D>::keys), values = tc_operand(r.base + Smem<D>::values);
   Waiter& w = r.w;
@@ -340,10 +344,10 @@ __device__ __forceinline__ void matrix_role(Roles r, int tile, int lane) {
 #pragma unroll 1
     for (int s = 0; s < D / 16; ++s) {
       const int at = (s >> 2) * (kTile * 128 / 16) + (s & 3) * 2;
-      tc_mma_shared(scores + h * kHalf, query + at, keys + st * (Smem<D>::kOperand / 16) + h * (kHalf * 128 / 16) + at,
+      tc_mma_shared(scores, query + at, keys + st * (Smem<D>::kOperand / 16) + h * (kHalf * 128 / 16) + at,
                     tc_idesc(kHalf, false), s > 0, leader);
     }
-    tc_commit(w.bars + (kScoresFull + tile * 2 + h) * 8, leader);
+    tc_commit(w.bars + (kScoresFull + tile) * 8, leader);
     if (h) tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
   };
   SharedPart p;
@@ -363,29 +367,26 @@ __device__ __forceinline__ void matrix_role(Roles r, int tile, int lane) {
     w.wait(kQueryFull + tile, parts++);
     w.wait(kKeysFull + (it & 1), it >> 1);
     score(it & 1, 0);
-    score(it & 1, 1);
 #pragma unroll 1
-    for (int k = 0; k < p.count; ++k, ++it, ++mine) {
-      const int st = it & 1;
-      w.wait(kValuesFull + st, it >> 1);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        w.wait(kWeightsFull + tile * 2 + h, mine);
-        if (w.dead()) continue;
+    for (int k = 0; k < 2 * p.count; ++k, ++mine) {
+      const int h = k & 1, st = it & 1;
+      // the next half's scores, once these have been read
+      if (h && k + 1 < 2 * p.count) w.wait(kKeysFull + (st ^ 1), (it + 1) >> 1);
+      w.wait(kScoresRead + tile, mine);
+      if (k + 1 < 2 * p.count) score(h ? st ^ 1 : st, h ^ 1);
+      if (h == 0) w.wait(kValuesFull + st, it >> 1);
+      w.wait(kWeightsFull + tile * 2 + h, mine >> 1);
+      if (!w.dead()) {
         tc_fence_after();
 #pragma unroll 1
         for (int s = 0; s < kHalf / 16; ++s)
-          tc_mma(out, scores + h * kHalf + s * 8, values + st * (Smem<D>::kOperand / 16) + h * (D * 128 / 16) + s * 2,
-                 tc_idesc(D, false), k > 0 || h > 0 || s > 0, leader);
-        tc_commit(w.bars + (kOutFull + tile) * 8, leader);
+          tc_mma(out, weights + h * (kHalf / 2) + s * 8,
+                 values + st * (Smem<D>::kOperand / 16) + h * (D * 128 / 16) + s * 2, tc_idesc(D, false), k > 0 || s > 0,
+                 leader);
+        tc_commit(w.bars + (kOutFull + tile * 2 + h) * 8, leader);
         if (h) tc_commit(w.bars + (kValuesEmpty + st) * 8, leader);
-        if (k + 1 < p.count) {
-          // the next tile's scores go where the weights are: these have to be read
-          if (h == 0) w.wait(kKeysFull + (st ^ 1), (it + 1) >> 1);
-          w.wait(kOutFull + tile, h);
-          score(st ^ 1, h);
-        }
       }
+      it += h;
     }
   }
   if (w.dead() && leader) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
@@ -400,7 +401,8 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
   const SharedLaunch& L = r.L;
   const int lane = tid & 31;
   const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
-  const uint32_t both = r.tmem + lanes + kScoresAt + tile * 2 * kHalf, out = r.tmem + lanes + kOutAt + tile * D;
+  const uint32_t scores = r.tmem + lanes + kScoresAt + tile * kHalf;
+  const uint32_t weights = r.tmem + lanes + kWeightsAt + tile * kHalf, out = r.tmem + lanes + kOutAt + tile * D;
   const uint32_t query = r.base + Smem<D>::query + tile * Smem<D>::kOperand + tid * 128;
   const bool vec =
       (reinterpret_cast<uintptr_t>(L.a.q) & 15) == 0 && ((L.a.qs[0] | L.a.qs[1] | L.a.qs[2]) & 7) == 0;  // (in elements)
@@ -443,7 +445,8 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
       int ex = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127;
       ex = max(-100, min(ex, 127));
       const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), L.a.scale_log2);
-      f = fabsf(L.a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23);
+      // (not zero, which would make a NaN of what is behind the prefix)
+      f = fmaxf(fabsf(L.a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23), 1e-37f);
 #pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
         const uint4 v = load(c);
@@ -463,94 +466,81 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
     for (int k = 0; k < 2 * p.count; ++k, ++mine) {
       const int h = k & 1;
       const int seen = p.len - p.t0 * kTile - k * kHalf;  // tokens of the half tile
-      const uint32_t scores = both + h * kHalf;
-      w.wait(kScoresFull + tile * 2 + h, mine >> 1);
+      w.wait(kScoresFull + tile, mine);
       tc_fence_after();
       float x[2][32];
-      bool done = false;
-      if (k > 0 && seen >= kHalf) {
-        // with the reference as it is: no weight is too large for fp16 if their sum is not
-        uint32_t y[2][16];
-        float sum[2];
+      tc_ld32(scores, x[0]);
+      tc_ld32(scores + 32, x[1]);
+      tc_wait_ld<32>(x[0]);
+      tc_wait_ld<32>(x[1]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) w.arrive(kScoresRead + tile);
+      if (seen < kHalf) {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) x[i >> 5][i & 31] = i < seen ? x[i >> 5][i & 31] : -INFINITY;
+      }
+      uint32_t y[2][16];
+      float sum;
+      // First with the reference as it is: no weight is too large for fp16 if their sum is
+      // not.  Else the reference becomes the row's maximum, and the sums so far follow.
+#pragma unroll 1
+      for (bool move = k == 0;; move = true) {
+        if (move) {
+          float top = x[0][0], top1 = x[1][0];
+#pragma unroll
+          for (int i = 1; i < 32; ++i) top = fmaxf(top, x[0][i]), top1 = fmaxf(top1, x[1][i]);
+          top = fmaxf(top, top1);
+          const float now = top == -INFINITY ? m : fmaxf(m, top * f), fall = ex2(m - now);
+          if (k > 0) {
+            w.wait(kOutFull + tile * 2 + (h ^ 1), (mine - 1) >> 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+              float o[8];
+              uint32_t z[8];
+              tc_ld8(out + c * 8, o);
+              tc_wait_ld<8>(o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(o[i] * fall);
+              tc_st8(out + c * 8, z);
+            }
+            l *= fall;
+          }
+          m = now;
+        }
         const uint32_t fb = __float_as_uint(f), rb = __float_as_uint(kFast - m);
-        tc_ld32(scores, x[0]);
-        tc_ld32(scores + 32, x[1]);
-        tc_wait_ld<32>(x[0]);
-        tc_wait_ld<32>(x[1]);
+        float part[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float a = 0.f, b = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            fma_pair(x[c][i], x[c][i + 1], make_uint4(fb, fb, rb, rb));
-            x[c][i] = ex2(x[c][i]);
-            x[c][i + 1] = ex2(x[c][i + 1]);
-            add_pair(a, b, x[c][i], x[c][i + 1]);
-            y[c][i >> 1] = half2_bits(__floats2half2_rn(x[c][i], x[c][i + 1]));
+            float e0 = x[c][i], e1 = x[c][i + 1];
+            fma_pair(e0, e1, make_uint4(fb, fb, rb, rb));
+            e0 = ex2(e0), e1 = ex2(e1);
+            add_pair(a, b, e0, e1);
+            y[c][i >> 1] = half2_bits(__floats2half2_rn(e0, e1));
           }
-          sum[c] = a + b;
+          part[c] = a + b;
         }
-        sum[0] += sum[1];
-        done = __all_sync(~0u, sum[0] <= 65504.f);
-        if (done) {
-          l += sum[0];
-          tc_st16(scores, y[0]);
-          tc_st16(scores + 16, y[1]);
-        }
+        sum = part[0] + part[1];
+        if (move || __all_sync(~0u, sum <= 65504.f)) break;
       }
-      if (!done) {
-        // the reference becomes the row's maximum, the sums so far follow
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          tc_ld32(scores + c * 32, x[0]);
-          tc_wait_ld<32>(x[0]);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, c * 32 + i < seen ? x[0][i] : -INFINITY);
-        }
-        const float now = top == -INFINITY ? m : fmaxf(m, top * f), fall = ex2(m - now);  // (f >= 0)
-        if (k > 0) {
-          w.wait(kOutFull + tile, mine - 1);
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            float y[16];
-            uint32_t z[16];
-            tc_ld16(out + c * 16, y);
-            tc_wait_ld<16>(y);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(y[i] * fall);
-            tc_st16(out + c * 16, z);
-          }
-          l *= fall;
-        }
-        m = now;
-        const float ref = kFast - m;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          tc_ld32(scores + c * 32, x[0]);
-          tc_wait_ld<32>(x[0]);
-          uint32_t y[16];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            // (a factor of zero makes no number of what is behind the prefix)
-            x[0][i] = c * 32 + i < seen ? ex2(fmaf(x[0][i], f, ref)) : 0.f;
-            l += x[0][i];
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = half2_bits(__floats2half2_rn(x[0][2 * i], x[0][2 * i + 1]));
-          tc_st16(scores + c * 16, y);  // (where scores that have been read were)
-        }
-      }
+      l += sum;
+      // (the half before the last's weights have been read)
+      w.wait(kOutFull + tile * 2 + h, (mine >> 1) ^ 1);
+      tc_fence_after();
+      tc_st16(weights + h * (kHalf / 2), y[0]);
+      tc_st16(weights + h * (kHalf / 2) + 16, y[1]);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) w.arrive(kWeightsFull + tile * 2 + h);
     }
-    // this part's sums (nobody has waited for the half before the last yet, and a phase
-    // can only be waited for once the one before it is over)
-    w.wait(kOutFull + tile, mine - 2);
-    w.wait(kOutFull + tile, mine - 1);
+    // this part's sums
+    w.wait(kOutFull + tile * 2, (mine - 2) >> 1);
+    w.wait(kOutFull + tile * 2 + 1, (mine - 1) >> 1);
     tc_fence_after();
     const bool real = row < p.n_rows;
     const long long at = p.row0 + row + static_cast<long long>(blockIdx.x) * (2 * kM);
@@ -583,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     // how many warps (or commits) arrive
     int count = 1;
     if ((tid >= kKeysFull && tid < kKeysEmpty) || (tid >= kValuesFull && tid < kValuesEmpty) ||
-        (tid >= kQueryFull && tid < kScoresFull) || (tid >= kWeightsFull && tid < kOutFull))
+        (tid >= kQueryFull && tid < kScoresFull) || (tid >= kScoresRead && tid < kOutFull))
       count = 4;
     if (tid >= kPartEmpty && tid < kPlaceFull) count = kReaders;
     if (tid >= kPlaceEmpty) count = 8;
