@@ -382,7 +382,7 @@ SharedWork shared_work(long long B, int nq, int heads, int kv_heads, int D, int 
 }  // namespace
 
 SharedShape shared_shape(int D, int esize, int sms) {
-  if (esize == 2 && D != 256) return {256, 128, sms, true};
+  if (esize == 2 && D != 256) return {128, 128, sms, true};
   return {kRows, kTokens, sms * kTeamsPerSm, false};
 }
 

@@ -1,22 +1,24 @@
 // ssdv_shared_tc.cu -- attention over a shared prefix on the fifth-generation tensor
 // cores: bf16 queries, 64 or 128 elements a head.
 //
-// Rows are the M side here (a group has hundreds of them): 256 rows of a row block,
-// two tiles of 128, meet tiles of 128 tokens, scored in halves.
-//   S [128 rows x 64 tokens]     = Q K^T     both operands in shared memory
+// Rows are the M side here (a group has hundreds of them): 128 rows of a row block
+// meet tiles of 128 tokens.
+//   S [128 rows x 128 tokens]    = Q K^T     both operands in shared memory
 //   O [128 rows x D elements]   += P V       P in tensor memory
-// Keys and values are unpacked once for all 256 rows, to fp16, where n s is exact.
+// Keys and values are unpacked to fp16, where n s is exact.
 //
 // Twenty warps:
-//   0-3, 4-7   weights of the first and the second 128 rows, a thread a row: maximum,
-//              2^x, sum, weights back to tensor memory, corrections, results
-//   8-11       keys: a token a thread, from global memory to a shared operand
-//   12-15      values: two elements of some blocks a thread, likewise
-//   16, 17     issue the matrix instructions of the first and the second 128 rows
-//   18         finds the CTA's parts of the list
-// Scores go to registers as soon as they are there, so the next half's are computed
-// while this half's weights are; weights of two halves are kept, so that no matrix
-// instruction waits for another's end.
+//   0-7    weights: a thread has a row and half of a tile's tokens (0-3 the first half,
+//          4-7 the second): 2^x, sum, weights to tensor memory, corrections, results
+//   8-11   keys: a token a thread, from global memory to a shared operand
+//   12-15  values: two elements of some blocks a thread, likewise
+//   16     issues the matrix instructions
+//   17     finds the CTA's parts of the list and the tiles' blocks
+// Scores and weights are double, so that a tile's weights are computed while the
+// products of the tiles beside it run: the matrix instructions of M = 128 take 62
+// cycles each however few the columns (and 81 with weights from tensor memory), 1150
+// a tile, and a handshake from one to the other takes 450 cycles, which one tile at a
+// time would wait for four times.
 //
 // Weights are fp16, 2^(x - m + 9), with m the row's maximum when it was last moved:
 // first taken from a part's first tile, it moves when a tile's weights add up to more
@@ -33,38 +35,40 @@ namespace ssdv {
 namespace {
 
 constexpr int kTile = 128, kM = 128, kThreads = 640;
-constexpr int kHalf = 64;  // tokens that are scored at a time
+constexpr int kHalf = 64;  // tokens of a tile that a thread has
 constexpr int kFast = 9, kTop = 15;
+constexpr int kKeyStages = 3, kValueStages = 2;
+constexpr int kRing = 4, kReaders = 17, kPlaces = 8;
 
 enum : int {
-  kKeysFull = 0,      // [2] keys unpacked               -> matrix
-  kKeysEmpty = 2,     // [2] both tiles' scores computed -> keys
-  kValuesFull = 4,    // [2] values unpacked             -> matrix
-  kValuesEmpty = 6,   // [2] both tiles' products        -> values
-  kQueryFull = 8,     // [2 tiles of rows] queries written       -> matrix
-  kScoresFull = 10,   // [2] half a tile's scores computed       -> weights
-  kScoresRead = 12,   // [2] and in registers                    -> matrix
-  kWeightsFull = 14,  // [2][2] weights written, sums corrected  -> matrix
-  kOutFull = 18,      // [2][2] half a tile's products added     -> weights
-  kDone = 22,         // all matrix instructions are done
-  kPartFull = 23,     // [kRing] a part is described          -> all
-  kPartEmpty = 27,    // [kRing] all have read it             -> plan
-  kPlaceFull = 31,    // [kPlaces] a tile's blocks are found  -> keys, values
-  kPlaceEmpty = 39,   // [kPlaces] both have read them        -> plan
-  kBars = 47
+  kKeysFull = 0,       // [kKeyStages] keys unpacked      -> matrix
+  kKeysEmpty = 3,      // [kKeyStages] scores computed    -> keys
+  kValuesFull = 6,     // [2] values unpacked             -> matrix
+  kValuesEmpty = 8,    // [2] products added              -> values
+  kScoresFull = 10,    // [2] scores computed             -> weights
+  kScoresRead = 12,    // [2] and in registers            -> matrix
+  kWeightsFull = 14,   // [2] weights written, sums corrected  -> matrix
+  kOutFull = 16,       // [2] a tile's products added     -> weights
+  kQueryFull = 18,     // queries written                 -> matrix
+  kDone = 19,          // all matrix instructions are done
+  kPartFull = 20,      // [kRing] a part is described          -> all
+  kPartEmpty = 24,     // [kRing] all have read it             -> plan
+  kPlaceFull = 28,     // [kPlaces] a tile's blocks are found  -> keys, values
+  kPlaceEmpty = 36,    // [kPlaces] both have read them        -> plan
+  kBars = 44
 };
-constexpr int kRing = 4, kReaders = 18, kPlaces = 8;
-constexpr int kTmemAt = 384, kPartsAt = 512, kPlacesAt = 768;  // bytes; a part 64, a tile's eight blocks 64
+// Bytes of shared memory: a part 64, a tile's eight blocks 64, rows' factors, their
+// maxima in each half of a tile.
+constexpr int kTmemAt = 384, kPartsAt = 512, kPlacesAt = 768, kFactorsAt = 1280, kTopsAt = 2048;
 
 template <int D>
 struct Smem {
   static constexpr int kOperand = kTile * D * 2;  // 128 rows or tokens x D, or D x 128
-  static constexpr int query = 2048, keys = query + 2 * kOperand, values = keys + 2 * kOperand;
-  static constexpr int total = values + 2 * kOperand + 1024;  // operands begin at a multiple of 1024
+  static constexpr int query = 3072, keys = query + kOperand, values = keys + kKeyStages * kOperand;
+  static constexpr int total = values + kValueStages * kOperand + 1024;  // operands begin at a multiple of 1024
 };
-// Columns of tensor memory: each tile of rows' scores of half a tile, weights of two
-// halves (two fp16 a column), sums.
-constexpr int kScoresAt = 0, kWeightsAt = 2 * kHalf, kOutAt = 4 * kHalf;
+// Columns of tensor memory: scores of two tiles, their weights (two fp16 a column), sums.
+constexpr int kScoresAt = 0, kWeightsAt = 2 * kTile, kOutAt = 3 * kTile;
 
 __device__ __forceinline__ void tc_ld32(uint32_t at, float (&x)[32]) {
   asm volatile(
@@ -86,6 +90,11 @@ __device__ __forceinline__ void tc_mma_shared(uint32_t d, uint64_t a, uint64_t b
       : "memory");
 }
 
+// What the roles know of a part: request and place among its rows of the first row.
+struct Stretch {
+  int h, b, k0, n_rows, len, t0, count;
+  long long row0;
+};
 // A role's view of the CTA.  Parts are found by one warp (64-bit divisions, searches)
 // and described in a ring in shared memory.
 struct Roles {
@@ -94,12 +103,12 @@ struct Roles {
   Waiter w;
   int n = 0;
   // The CTA's next part, false when there is none.
-  __device__ __forceinline__ bool next(SharedPart& p, int lane) {
+  __device__ __forceinline__ bool next(Stretch& p, int lane) {
     w.wait(kPartFull + n % kRing, n / kRing);
     const uint32_t from = base + kPartsAt + n % kRing * 64;
     const uint4 x = lds128(from), y = lds128(from + 16);
     const uint2 z = lds64(from + 32);
-    p.h = x.x, p.block = x.y, p.b0 = x.z, p.n_rows = x.w;
+    p.h = x.x, p.k0 = x.y, p.b = x.z, p.n_rows = x.w;
     p.len = y.x, p.t0 = y.y, p.count = __shfl_sync(~0u, y.z, 0);
     p.row0 = z.x | static_cast<long long>(z.y) << 32;
     __syncwarp();
@@ -124,39 +133,40 @@ __device__ __forceinline__ void part_role(const SharedLaunch& L, const GroupList
     w.nap(kPartEmpty + n % kRing, (n / kRing) ^ 1);
     if (lane == 0) {
       const uint32_t to = base + kPartsAt + n % kRing * 64;
-      sts128(to, make_uint4(p.h, p.block, p.b0, p.n_rows));
+      const long long first = static_cast<long long>(p.block) * L.R;
+      const int b = p.count ? static_cast<int>(first / L.rows) : 0;
+      sts128(to, make_uint4(p.h, static_cast<int>(first - static_cast<long long>(b) * L.rows), p.b0 + b, p.n_rows));
       sts128(to + 16, make_uint4(p.len, p.t0, p.count, 0));
       sts64(to + 32, make_uint2(static_cast<uint32_t>(p.row0), static_cast<uint32_t>(p.row0 >> 32)));
       w.arrive(kPartFull + n % kRing);
     }
     if (p.count == 0) break;
-    // where the tiles' blocks lie (null behind the prefix and on a bad page): eight
-    // lanes, a block each, pages a tile ahead
+    // where the tiles' blocks lie (null behind the prefix and on a bad page): four tiles
+    // at a time, a block a lane, the next four's pages on their way
     const int32_t* table = c.page_table + static_cast<long long>(p.b0) * c.max_pages;
-    int at = p.t0 * 8 + (lane & 7), col = at / bpp, sub = at - col * bpp;
-    const auto page_of = [&]() { return at * kKvBlock < p.len ? table[col] : -1; };
-    int page = page_of();
+    const int first = p.t0 * 8, blocks = min((p.len + kKvBlock - 1) / kKvBlock, (p.t0 + p.count) * 8);
+    const auto page_of = [&](int at) { return at < blocks ? table[at / bpp] : 0; };
+    int page = page_of(first + lane);
 #pragma unroll 1
-    for (int k = 0; k < p.count; ++k, ++it) {
-      const bool there = at * kKvBlock < p.len, ok = there && page >= 0 && page < c.n_pages;
-      bad |= there && !ok;
-      const uint8_t* from =
-          ok ? c.pages + ((static_cast<long long>(page) * c.kv_heads + p.h) * bpp + sub) * block_bytes : nullptr;
-      at += 8, sub += 8;
-      if (sub >= bpp) {
-        const int q = bpp >= 8 ? 1 : sub / bpp;
-        col += q;
-        sub -= q * bpp;
+    for (int k0 = 0; k0 < p.count; k0 += 4) {
+      const int at = first + k0 * 8 + lane, next = page_of(at + 32);
+      const bool ok = at < blocks && page >= 0 && page < c.n_pages;
+      bad |= at < blocks && !ok;
+      const unsigned long long from =
+          ok ? reinterpret_cast<unsigned long long>(c.pages) +
+                   ((static_cast<long long>(page) * c.kv_heads + p.h) * bpp + at % bpp) * block_bytes
+             : 0ull;
+      page = next;
+#pragma unroll 1
+      for (int t = 0; t < 4 && k0 + t < p.count; ++t, ++it) {
+        const int slot = it % kPlaces;
+        w.nap(kPlaceEmpty + slot, (it / kPlaces) ^ 1);
+        if (lane >> 3 == t)
+          sts64(base + kPlacesAt + slot * 64 + (lane & 7) * 8,
+                make_uint2(static_cast<uint32_t>(from), static_cast<uint32_t>(from >> 32)));
+        __syncwarp();
+        if (lane == 0) w.arrive(kPlaceFull + slot);
       }
-      if (k + 1 < p.count) page = page_of();
-      const int slot = it % kPlaces;
-      w.nap(kPlaceEmpty + slot, (it / kPlaces) ^ 1);
-      if (lane < 8) {
-        const unsigned long long v = reinterpret_cast<unsigned long long>(from);
-        sts64(base + kPlacesAt + slot * 64 + lane * 8, make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32)));
-      }
-      __syncwarp();
-      if (lane == 0) w.arrive(kPlaceFull + slot);
     }
   }
   if (bad) atomicOr(L.a.status, 1 << SSD_ERR_PAGE);
@@ -195,8 +205,9 @@ __device__ __forceinline__ void key_role(Roles r, int tid) {
       s[i] = from ? __ldg(reinterpret_cast<const unsigned short*>(from + k_scale_offset<D>(t, 2 * i))) : 0xFFFFu;
     }
   };
-  SharedPart p;
-  int it = 0;
+  Stretch p;
+  int it = 0, st = 0;
+  uint32_t phase = 1;
   while (r.next(p, lane)) {
     find(it);
 #pragma unroll
@@ -205,8 +216,7 @@ __device__ __forceinline__ void key_role(Roles r, int tid) {
     for (int k = 0; k < p.count; ++k, ++it) {
       const bool more = k + 1 < p.count;
       if (more) find(it + 1);
-      const int st = it & 1;
-      r.w.wait(kKeysEmpty + st, (it >> 1) ^ 1);
+      r.w.wait(kKeysEmpty + st, phase);
       const uint32_t row = to + st * Smem<D>::kOperand;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
@@ -230,6 +240,7 @@ __device__ __forceinline__ void key_role(Roles r, int tid) {
       async_fence();
       __syncwarp();
       if (lane == 0) r.w.arrive(kKeysFull + st);
+      if (++st == kKeyStages) st = 0, phase ^= 1;
     }
   }
   if (r.w.dead() && lane == 0) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
@@ -272,7 +283,7 @@ __device__ __forceinline__ void value_role(Roles r, int tid) {
     c[b] = from ? __ldg(reinterpret_cast<const uint4*>(from + v_word_offset<D>(d0, 0))) : make_uint4(0, 0, 0, 0);
     s[b] = from ? __ldg(reinterpret_cast<const uint4*>(from + kv_v_scales(D) + (d0 >> 4) * 16)) : make_uint4(0, 0, 0, 0);
   };
-  SharedPart p;
+  Stretch p;
   int it = 0;
   while (r.next(p, lane)) {
     find(it);
@@ -327,66 +338,61 @@ __device__ __forceinline__ void value_role(Roles r, int tid) {
   if (r.w.dead() && lane == 0) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
 }
 
-// ---- matrix instructions of a tile of rows (one lane issues them) ----
+// ---- matrix instructions (one lane issues them) ----
+
+// A number that all lanes have, and that the compiler knows they do: operands that may
+// differ between lanes make an instruction's issue take 240 cycles.
+__device__ __forceinline__ uint32_t agreed(uint32_t x) { return __shfl_sync(~0u, x, 0); }
 
 template <int D>
-__device__ __forceinline__ void matrix_role(Roles r, int tile, int lane) {
+__device__ __forceinline__ void matrix_role(Roles r, int lane) {
   const bool leader = lane == 0;
-  const uint32_t scores = r.tmem + kScoresAt + tile * kHalf, weights = r.tmem + kWeightsAt + tile * kHalf;
-  const uint32_t out = r.tmem + kOutAt + tile * D;
-  const uint64_t query = tc_operand(r.base + Smem<D>::query + tile * Smem<D>::kOperand);
-  const uint64_t keys = tc_operand(r.base + Smem<D>::keys), values = tc_operand(r.base + Smem<D>::values);
+  const uint32_t base = r.base, tmem = r.tmem;
   Waiter& w = r.w;
-  // scores of half h of the tile in stage st
-  const auto score = [&](int st, int h) {
+  int st = 0;
+  uint32_t phase = 0;
+  // scores of the CTA's tile `it`
+  const auto score = [&](int it) {
+    const int b = it & 1;
+    w.wait(kKeysFull + st, phase);
+    w.wait(kScoresRead + b, (it >> 1) ^ 1);
     if (w.dead()) return;
     tc_fence_after();
-#pragma unroll 1
+    const uint32_t to = agreed(tmem + kScoresAt + b * kTile);
+    const uint64_t query = tc_operand(agreed(base + Smem<D>::query));
+    const uint64_t keys = tc_operand(agreed(base + Smem<D>::keys + st * Smem<D>::kOperand));
+#pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       const int at = (s >> 2) * (kTile * 128 / 16) + (s & 3) * 2;
-      tc_mma_shared(scores, query + at, keys + st * (Smem<D>::kOperand / 16) + h * (kHalf * 128 / 16) + at,
-                    tc_idesc(kHalf, false), s > 0, leader);
+      tc_mma_shared(to, query + at, keys + at, tc_idesc(kTile, false), s > 0, leader);
     }
-    tc_commit(w.bars + (kScoresFull + tile) * 8, leader);
-    if (h) tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
+    tc_commit(w.bars + (kScoresFull + b) * 8, leader);
+    tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
+    if (++st == kKeyStages) st = 0, phase ^= 1;
   };
-  SharedPart p;
-  int it = 0, mine = 0, parts = 0;
+  Stretch p;
+  int it = 0, parts = 0;
   while (r.next(p, lane)) {
-    if (tile && p.n_rows <= kM) {
-      // nothing to do with this part's tiles but to let them go
+    w.wait(kQueryFull, parts++);
+    score(it);
+    if (p.count > 1) score(it + 1);
 #pragma unroll 1
-      for (int k = 0; k < p.count; ++k, ++it) {
-        w.wait(kKeysFull + (it & 1), it >> 1);
-        if (leader) w.arrive(kKeysEmpty + (it & 1));
-        w.wait(kValuesFull + (it & 1), it >> 1);
-        if (leader) w.arrive(kValuesEmpty + (it & 1));
-      }
-      continue;
-    }
-    w.wait(kQueryFull + tile, parts++);
-    w.wait(kKeysFull + (it & 1), it >> 1);
-    score(it & 1, 0);
-#pragma unroll 1
-    for (int k = 0; k < 2 * p.count; ++k, ++mine) {
-      const int h = k & 1, st = it & 1;
-      // the next half's scores, once these have been read
-      if (h && k + 1 < 2 * p.count) w.wait(kKeysFull + (st ^ 1), (it + 1) >> 1);
-      w.wait(kScoresRead + tile, mine);
-      if (k + 1 < 2 * p.count) score(h ? st ^ 1 : st, h ^ 1);
-      if (h == 0) w.wait(kValuesFull + st, it >> 1);
-      w.wait(kWeightsFull + tile * 2 + h, mine >> 1);
-      if (!w.dead()) {
-        tc_fence_after();
-#pragma unroll 1
-        for (int s = 0; s < kHalf / 16; ++s)
-          tc_mma(out, weights + h * (kHalf / 2) + s * 8,
-                 values + st * (Smem<D>::kOperand / 16) + h * (D * 128 / 16) + s * 2, tc_idesc(D, false), k > 0 || s > 0,
-                 leader);
-        tc_commit(w.bars + (kOutFull + tile * 2 + h) * 8, leader);
-        if (h) tc_commit(w.bars + (kValuesEmpty + st) * 8, leader);
-      }
-      it += h;
+    for (int k = 0; k < p.count; ++k, ++it) {
+      const int b = it & 1;
+      w.wait(kValuesFull + b, it >> 1);
+      w.wait(kWeightsFull + b, it >> 1);
+      if (w.dead()) continue;
+      tc_fence_after();
+      const uint32_t out = agreed(tmem + kOutAt), weights = agreed(tmem + kWeightsAt + b * (kTile / 2));
+      const uint64_t values = tc_operand(agreed(base + Smem<D>::values + b * Smem<D>::kOperand));
+      const bool add = agreed(k) > 0;
+#pragma unroll
+      for (int s = 0; s < kTile / 16; ++s)
+        tc_mma(out, weights + s * 8, values + (s >> 2) * (D * 128 / 16) + (s & 3) * 2, tc_idesc(D, false), add || s > 0,
+               leader);
+      tc_commit(w.bars + (kOutFull + b) * 8, leader);
+      tc_commit(w.bars + (kValuesEmpty + b) * 8, leader);
+      if (k + 2 < p.count) score(it + 2);
     }
   }
   if (w.dead() && leader) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
@@ -394,88 +400,104 @@ __device__ __forceinline__ void matrix_role(Roles r, int tile, int lane) {
   bar_wait(w.bars + kDone * 8, 0);
 }
 
-// ---- weights: a thread a row ----
+// ---- weights ----
 
-template <int D>
-__device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
-  const SharedLaunch& L = r.L;
-  const int lane = tid & 31;
-  const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
-  const uint32_t scores = r.tmem + lanes + kScoresAt + tile * kHalf;
-  const uint32_t weights = r.tmem + lanes + kWeightsAt + tile * kHalf, out = r.tmem + lanes + kOutAt + tile * D;
-  const uint32_t query = r.base + Smem<D>::query + tile * Smem<D>::kOperand + tid * 128;
-  const bool vec =
-      (reinterpret_cast<uintptr_t>(L.a.q) & 15) == 0 && ((L.a.qs[0] | L.a.qs[1] | L.a.qs[2]) & 7) == 0;  // (in elements)
-  Waiter& w = r.w;
-  SharedPart p;
-  int mine = 0;
-  while (r.next(p, lane)) {
-    if (tile && p.n_rows <= kM) continue;
-    const int row = tile * kM + tid;
-    float f;
-    {
-      // the query as fp16, a power of two up: its largest element to [2^12, 2^13), the
-      // scale's sign on it (exact down to 2^-26 of the largest)
-      const SharedRow at(L, p, row);
-      const unsigned short* q =
-          static_cast<const unsigned short*>(L.a.q) + at.b * L.a.qs[0] + at.i * L.a.qs[1] + at.head * L.a.qs[2];
-      const auto load = [&](int c) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (at.real) {
-          if (vec) {
-            v = __ldg(reinterpret_cast<const uint4*>(q) + c);
-          } else {
-#pragma unroll 1
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t h = q[c * 8 + e];
-              v.x = __funnelshift_r(v.x, v.y, 16), v.y = __funnelshift_r(v.y, v.z, 16);
-              v.z = __funnelshift_r(v.z, v.w, 16), v.w = __funnelshift_r(v.w, h, 16);
-            }
-          }
-        }
-        return v;
-      };
-      uint32_t top = 0;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = load(c);
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-      }
-      int ex = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127;
-      ex = max(-100, min(ex, 127));
-      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), L.a.scale_log2);
-      // (not zero, which would make a NaN of what is behind the prefix)
-      f = fmaxf(fabsf(L.a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23), 1e-37f);
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = load(c);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        uint32_t y[4];
+// Writes 32 floats, 32 bytes at a time.
+__device__ __forceinline__ void store_row(float* to, const float (&x)[32], float up) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y[e] = half2_bits(__floats2half2_rn(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up));
-        sts128(query + (c >> 3) * (kM * 128) + (((c & 7) ^ (tid & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + i), "f"(x[i] * up), "f"(x[i + 1] * up),
+                 "f"(x[i + 2] * up), "f"(x[i + 3] * up), "f"(x[i + 4] * up), "f"(x[i + 5] * up), "f"(x[i + 6] * up),
+                 "f"(x[i + 7] * up)
+                 : "memory");
+}
+
+// The part's queries as fp16, a power of two up: a row's largest element to [2^12,
+// 2^13), the scale's sign on it (exact down to 2^-26 of the largest).  D / 8 lanes have
+// a row, a warp 16.
+template <int D>
+__device__ __forceinline__ void load_queries(const Roles& r, const Stretch& p, int warp, int lane) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kTimes = 16 / kRows;
+  const KvAttnArgs& a = r.L.a;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && ((a.qs[0] | a.qs[1] | a.qs[2]) & 7) == 0;  // (in elements)
+  const int c = lane % kLanes;
+  uint4 v[kTimes];
+#pragma unroll
+  for (int t = 0; t < kTimes; ++t) {
+    const int row = warp * 16 + t * kRows + lane / kLanes, k = p.k0 + row, b = p.b + k / r.L.rows, j = k % r.L.rows;
+    const int i = j / r.L.per;
+    v[t] = make_uint4(0, 0, 0, 0);
+    if (row < p.n_rows && i < (a.n_q ? a.n_q[b] : a.nq)) {
+      const unsigned short* q = static_cast<const unsigned short*>(a.q) + b * a.qs[0] + i * a.qs[1] +
+                                (p.h * r.L.per + j - i * r.L.per) * a.qs[2] + c * 8;
+      if (vec) {
+        v[t] = __ldg(reinterpret_cast<const uint4*>(q));
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t x = q[e];
+          v[t].x = __funnelshift_r(v[t].x, v[t].y, 16), v[t].y = __funnelshift_r(v[t].y, v[t].z, 16);
+          v[t].z = __funnelshift_r(v[t].z, v[t].w, 16), v[t].w = __funnelshift_r(v[t].w, x, 16);
+        }
       }
     }
+  }
+#pragma unroll
+  for (int t = 0; t < kTimes; ++t) {
+    const int row = warp * 16 + t * kRows + lane / kLanes;
+    uint32_t top = __vmaxu2(__vmaxu2(v[t].x & 0x7FFF7FFFu, v[t].y & 0x7FFF7FFFu),
+                            __vmaxu2(v[t].z & 0x7FFF7FFFu, v[t].w & 0x7FFF7FFFu));
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+    int ex = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127;
+    ex = max(-100, min(ex, 127));
+    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(12 - ex + 127) << 23), a.scale_log2);
+    const uint32_t x[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+    uint32_t y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      y[e] = half2_bits(__floats2half2_rn(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up));
+    sts128(r.base + Smem<D>::query + (c >> 3) * (kM * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+           make_uint4(y[0], y[1], y[2], y[3]));
+    // (not zero, which would make a NaN of what is behind the prefix)
+    if (c == 0)
+      sts_f(r.base + kFactorsAt + row * 4,
+            fmaxf(fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ex - 12 + 127) << 23), 1e-37f));
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void weight_role(Roles r, int warp, int lane) {
+  constexpr int kAll = 1, kPair = 2;  // barriers: of the role, of the two warps of the same rows
+  const SharedLaunch& L = r.L;
+  const int h = warp >> 2, row = (warp & 3) * 32 + lane;  // half of the tokens, and of the elements of the sums
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t scores = r.tmem + lanes + kScoresAt + h * kHalf, weights = r.tmem + lanes + kWeightsAt + h * (kHalf / 2);
+  const uint32_t out = r.tmem + lanes + kOutAt + h * (D / 2), tops = r.base + kTopsAt + row * 4;
+  const int pair = kPair + (warp & 3);
+  Waiter& w = r.w;
+  Stretch p;
+  int it = 0;
+  while (r.next(p, lane)) {
+    load_queries<D>(r, p, warp, lane);
     async_fence();
-    __syncwarp();
-    if (lane == 0) w.arrive(kQueryFull + tile);
+    group_sync<256>(kAll);
+    if (lane == 0) w.arrive(kQueryFull);
+    const float f = lds_f(r.base + kFactorsAt + row * 4);
     float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-    for (int k = 0; k < 2 * p.count; ++k, ++mine) {
-      const int h = k & 1;
-      const int seen = p.len - p.t0 * kTile - k * kHalf;  // tokens of the half tile
-      w.wait(kScoresFull + tile, mine);
+    for (int k = 0; k < p.count; ++k, ++it) {
+      const int b = it & 1, seen = p.len - (p.t0 + k) * kTile - h * kHalf;  // tokens of the half
+      w.wait(kScoresFull + b, it >> 1);
       tc_fence_after();
       float x[2][32];
-      tc_ld32(scores, x[0]);
-      tc_ld32(scores + 32, x[1]);
+      tc_ld32(scores + b * kTile, x[0]);
+      tc_ld32(scores + b * kTile + 32, x[1]);
       tc_wait_ld<32>(x[0]);
       tc_wait_ld<32>(x[1]);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) w.arrive(kScoresRead + tile);
+      if (lane == 0) w.arrive(kScoresRead + b);
       if (seen < kHalf) {
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) x[i >> 5][i & 31] = i < seen ? x[i >> 5][i & 31] : -INFINITY;
@@ -491,19 +513,22 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
 #pragma unroll
           for (int i = 1; i < 32; ++i) top = fmaxf(top, x[0][i]), top1 = fmaxf(top1, x[1][i]);
           top = fmaxf(top, top1);
+          sts_f(tops + h * (kM * 4), top);
+          group_sync<64>(pair);
+          top = fmaxf(top, lds_f(tops + (h ^ 1) * (kM * 4)));
           const float now = top == -INFINITY ? m : fmaxf(m, top * f), fall = ex2(m - now);
           if (k > 0) {
-            w.wait(kOutFull + tile * 2 + (h ^ 1), (mine - 1) >> 1);
+            w.wait(kOutFull + (b ^ 1), (it - 1) >> 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
+            for (int c = 0; c < D / 2; c += 8) {
               float o[8];
               uint32_t z[8];
-              tc_ld8(out + c * 8, o);
+              tc_ld8(out + c, o);
               tc_wait_ld<8>(o);
 #pragma unroll
               for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(o[i] * fall);
-              tc_st8(out + c * 8, z);
+              tc_st8(out + c, z);
             }
             l *= fall;
           }
@@ -513,50 +538,46 @@ __device__ __forceinline__ void weight_role(Roles r, int tile, int tid) {
         float part[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float a = 0.f, b = 0.f;
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float e0 = x[c][i], e1 = x[c][i + 1];
             fma_pair(e0, e1, make_uint4(fb, fb, rb, rb));
             e0 = ex2(e0), e1 = ex2(e1);
-            add_pair(a, b, e0, e1);
+            add_pair(s0, s1, e0, e1);
             y[c][i >> 1] = half2_bits(__floats2half2_rn(e0, e1));
           }
-          part[c] = a + b;
+          part[c] = s0 + s1;
         }
         sum = part[0] + part[1];
-        if (move || __all_sync(~0u, sum <= 65504.f)) break;
+        if (move || !group_any<64>(pair, !(sum <= 65504.f))) break;
       }
       l += sum;
-      // (the half before the last's weights have been read)
-      w.wait(kOutFull + tile * 2 + h, (mine >> 1) ^ 1);
+      // (the weights of the tile before the last have been read)
+      w.wait(kOutFull + b, (it >> 1) ^ 1);
       tc_fence_after();
-      tc_st16(weights + h * (kHalf / 2), y[0]);
-      tc_st16(weights + h * (kHalf / 2) + 16, y[1]);
+      tc_st16(weights + b * (kTile / 2), y[0]);
+      tc_st16(weights + b * (kTile / 2) + 16, y[1]);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) w.arrive(kWeightsFull + tile * 2 + h);
+      if (lane == 0) w.arrive(kWeightsFull + b);
     }
-    // this part's sums
-    w.wait(kOutFull + tile * 2, (mine - 2) >> 1);
-    w.wait(kOutFull + tile * 2 + 1, (mine - 1) >> 1);
+    // this part's sums, once the last products (and so all before them) are added
+    w.wait(kOutFull + ((it - 1) & 1), (it - 1) >> 1);
     tc_fence_after();
     const bool real = row < p.n_rows;
-    const long long at = p.row0 + row + static_cast<long long>(blockIdx.x) * (2 * kM);
+    const long long at = p.row0 + row + static_cast<long long>(blockIdx.x) * kM;
     constexpr float kUp = 1 << (kTop - kFast);  // (parts are kept 2^15 up)
-    if (real) L.ml[at] = make_float2(m, w.dead() ? __int_as_float(0x7FC00000) : l * kUp);
-#pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      float x[32];
-      tc_ld32(out + c * 32, x);
-      tc_wait_ld<32>(x);
-      if (real) {
-        float4* o = reinterpret_cast<float4*>(L.o + at * D + c * 32);
+    if (h) sts_f(tops, l);
+    group_sync<64>(pair);
+    if (real && h == 0) L.ml[at] = make_float2(m, w.dead() ? __int_as_float(0x7FC00000) : (l + lds_f(tops)) * kUp);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          o[i] = make_float4(x[4 * i] * kUp, x[4 * i + 1] * kUp, x[4 * i + 2] * kUp, x[4 * i + 3] * kUp);
-      }
+    for (int c = 0; c < D / 2; c += 32) {
+      float x[32];
+      tc_ld32(out + c, x);
+      tc_wait_ld<32>(x);
+      if (real) store_row(L.o + at * D + h * (D / 2) + c, x, kUp);
     }
     tc_fence_before();
   }
@@ -572,12 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   if (tid < kBars) {
     // how many warps (or commits) arrive
     int count = 1;
-    if ((tid >= kKeysFull && tid < kKeysEmpty) || (tid >= kValuesFull && tid < kValuesEmpty) ||
-        (tid >= kQueryFull && tid < kScoresFull) || (tid >= kScoresRead && tid < kOutFull))
-      count = 4;
+    if (tid < kKeysEmpty || (tid >= kValuesFull && tid < kValuesEmpty)) count = 4;
+    if ((tid >= kScoresRead && tid < kOutFull) || tid == kQueryFull || tid >= kPlaceEmpty) count = 8;
     if (tid >= kPartEmpty && tid < kPlaceFull) count = kReaders;
-    if (tid >= kPlaceEmpty) count = 8;
-    if ((tid >= kKeysEmpty && tid < kValuesFull) || (tid >= kValuesEmpty && tid < kQueryFull) || tid == kDone) count = 2;
     bar_init(base + tid * 8, count);
   }
   if (warp == 16) {
@@ -594,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   // 128 x (128 + 128 + 80 + 88 + 48) registers: within the 640 x 96 of the launch
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-    weight_role<D>(r, warp >> 2, tid & 127);
+    weight_role<D>(r, warp, lane);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     key_role<D>(r, tid & 127);
@@ -603,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     value_role<D>(r, tid & 127);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp < 18) matrix_role<D>(r, warp - 16, lane);
-    else if (warp == 18) part_role(L, list, base, r.w, lane, kv_block_bytes(D));
+    if (warp == 16) matrix_role<D>(r, lane);
+    else if (warp == 17) part_role(L, list, base, r.w, lane, kv_block_bytes(D));
   }
   tc_fence_before();
   __syncthreads();
