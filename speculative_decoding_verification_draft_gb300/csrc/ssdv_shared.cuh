@@ -53,6 +53,11 @@ struct SharedPart {
   long long row0;         // the block's first row in the list of all rows
 };
 
+// (64-bit divisions take hundreds of cycles)
+__device__ __forceinline__ long long quotient(long long x, int y) {
+  return static_cast<unsigned long long>(x) >> 32 ? x / y : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
+}
+
 struct GroupList {
   const SharedLaunch& L;
   const long long* scan;
@@ -67,7 +72,7 @@ struct GroupList {
   __device__ __forceinline__ long long group_rows(int g) const {
     return static_cast<long long>(L.group_start[g + 1] - L.group_start[g]) * L.rows;
   }
-  __device__ __forceinline__ int blocks(int g) const { return static_cast<int>((group_rows(g) + L.R - 1) / L.R); }
+  __device__ __forceinline__ int blocks(int g) const { return static_cast<int>(quotient(group_rows(g) + L.R - 1, L.R)); }
   __device__ __forceinline__ int tiles(int g) const { return static_cast<int>((length(g) + L.tile - 1ll) / L.tile); }
   __device__ __forceinline__ long long units(int g) const {
     return static_cast<long long>(L.a.c.kv_heads) * blocks(g) * tiles(g);
@@ -81,20 +86,19 @@ struct GroupList {
     chunk = (L.G + threads - 1) / threads;
     const int g0 = min(tid * chunk, L.G), g1 = min(g0 + chunk, L.G);
     bool broken = false;
-    for (int g = g0; g < g1; ++g)
-      broken |= L.group_start[g] > L.group_start[g + 1] || (g == 0 && L.group_start[g] != 0) ||
-                (g == L.G - 1 && L.group_start[g + 1] != L.a.B);
-    broken = __syncthreads_or(broken);
     long long mine = 0;
-    if (!broken)
-      for (int g = g0; g < g1; ++g) mine += units(g);
+    for (int g = g0; g < g1; ++g) {
+      const int from = L.group_start[g], to = L.group_start[g + 1];
+      broken |= from > to || (g == 0 && from != 0) || (g == L.G - 1 && to != L.a.B);
+      mine += units(g);
+    }
     long long x = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(~0u, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) sums[warp] = x;
-    __syncthreads();
+    broken = __syncthreads_or(broken);
     long long before = 0;
     total = 0;
     for (int v = 0; v < threads / 32; ++v) {
@@ -102,14 +106,17 @@ struct GroupList {
       total += sums[v];
     }
     scan_[tid] = before + x - mine;
-    quota = max((total + L.teams - 1) / L.teams, 1ll);
+    if (broken) total = 0;
+    quota = total < 0x80000000ll
+                ? max((static_cast<unsigned>(total) + static_cast<unsigned>(L.teams) - 1) / static_cast<unsigned>(L.teams), 1u)
+                : (total + L.teams - 1) / L.teams;
     // what the kernels after this one need to know
     if (blockIdx.x == 0) {
       if (tid == 0) L.head[0] = quota;
       long long u = before + x - mine;
       for (int g = g0; g < g1; ++g) {
         L.unit0[g] = u;
-        if (!broken) u += units(g);
+        u += units(g);
       }
     }
     for (int b = blockIdx.x * threads + tid; b < L.a.B; b += gridDim.x * threads) {
@@ -138,8 +145,8 @@ struct GroupList {
     long long u0 = scan[lo];
     while (u0 + units(p.g) <= u) u0 += units(p.g++);
     const int n = tiles(p.g), nb = blocks(p.g);
-    const long long k = u - u0, rb = k / n, rows = group_rows(p.g);
-    p.h = static_cast<int>(rb / nb);
+    const long long k = u - u0, rb = quotient(k, n), rows = group_rows(p.g);
+    p.h = static_cast<int>(quotient(rb, nb));
     p.block = static_cast<int>(rb - static_cast<long long>(p.h) * nb);
     p.len = length(p.g);
     p.t0 = static_cast<int>(k - rb * n);

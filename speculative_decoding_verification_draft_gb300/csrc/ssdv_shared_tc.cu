@@ -12,7 +12,9 @@
 //          4-7 the second): 2^x, sum, weights to tensor memory, corrections, results
 //   8-11   keys: a token a thread, from global memory to a shared operand
 //   12-15  values: two elements of some blocks a thread, likewise
-//   16     issues the matrix instructions
+//   16, 18 issue the matrix instructions of the scores and of the sums: a wait costs 140
+//          cycles and a commit 100 even where nothing is to be waited for, so one warp
+//          for both left the tensor cores idle half of the time
 //   17     finds the CTA's parts of the list and the tiles' blocks
 // Scores and weights are double, so that a tile's weights are computed while the
 // products of the tiles beside it run: the matrix instructions of M = 128 take 62
@@ -38,7 +40,7 @@ constexpr int kTile = 128, kM = 128, kThreads = 640;
 constexpr int kHalf = 64;  // tokens of a tile that a thread has
 constexpr int kFast = 9, kTop = 15;
 constexpr int kKeyStages = 3, kValueStages = 2;
-constexpr int kRing = 4, kReaders = 17, kPlaces = 8;
+constexpr int kRing = 4, kReaders = 18, kPlaces = 8;
 
 enum : int {
   kKeysFull = 0,       // [kKeyStages] keys unpacked      -> matrix
@@ -134,7 +136,7 @@ __device__ __forceinline__ void part_role(const SharedLaunch& L, const GroupList
     if (lane == 0) {
       const uint32_t to = base + kPartsAt + n % kRing * 64;
       const long long first = static_cast<long long>(p.block) * L.R;
-      const int b = p.count ? static_cast<int>(first / L.rows) : 0;
+      const int b = p.count ? static_cast<int>(quotient(first, L.rows)) : 0;
       sts128(to, make_uint4(p.h, static_cast<int>(first - static_cast<long long>(b) * L.rows), p.b0 + b, p.n_rows));
       sts128(to + 16, make_uint4(p.len, p.t0, p.count, 0));
       sts64(to + 32, make_uint2(static_cast<uint32_t>(p.row0), static_cast<uint32_t>(p.row0 >> 32)));
@@ -345,37 +347,46 @@ __device__ __forceinline__ void value_role(Roles r, int tid) {
 __device__ __forceinline__ uint32_t agreed(uint32_t x) { return __shfl_sync(~0u, x, 0); }
 
 template <int D>
-__device__ __forceinline__ void matrix_role(Roles r, int lane) {
+__device__ __forceinline__ void score_role(Roles r, int lane) {
   const bool leader = lane == 0;
-  const uint32_t base = r.base, tmem = r.tmem;
   Waiter& w = r.w;
-  int st = 0;
-  uint32_t phase = 0;
-  // scores of the CTA's tile `it`
-  const auto score = [&](int it) {
-    const int b = it & 1;
-    w.wait(kKeysFull + st, phase);
-    w.wait(kScoresRead + b, (it >> 1) ^ 1);
-    if (w.dead()) return;
-    tc_fence_after();
-    const uint32_t to = agreed(tmem + kScoresAt + b * kTile);
-    const uint64_t query = tc_operand(agreed(base + Smem<D>::query));
-    const uint64_t keys = tc_operand(agreed(base + Smem<D>::keys + st * Smem<D>::kOperand));
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const int at = (s >> 2) * (kTile * 128 / 16) + (s & 3) * 2;
-      tc_mma_shared(to, query + at, keys + at, tc_idesc(kTile, false), s > 0, leader);
-    }
-    tc_commit(w.bars + (kScoresFull + b) * 8, leader);
-    tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
-    if (++st == kKeyStages) st = 0, phase ^= 1;
-  };
   Stretch p;
-  int it = 0, parts = 0;
+  int it = 0, parts = 0, st = 0;
+  uint32_t phase = 0;
   while (r.next(p, lane)) {
     w.wait(kQueryFull, parts++);
-    score(it);
-    if (p.count > 1) score(it + 1);
+#pragma unroll 1
+    for (int k = 0; k < p.count; ++k, ++it) {
+      const int b = it & 1;
+      w.wait(kScoresRead + b, (it >> 1) ^ 1);
+      w.wait(kKeysFull + st, phase);
+      if (w.dead()) continue;
+      tc_fence_after();
+      const uint32_t to = agreed(r.tmem + kScoresAt + b * kTile);
+      const uint64_t query = tc_operand(agreed(r.base + Smem<D>::query));
+      const uint64_t keys = tc_operand(agreed(r.base + Smem<D>::keys + st * Smem<D>::kOperand));
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const int at = (s >> 2) * (kTile * 128 / 16) + (s & 3) * 2;
+        tc_mma_shared(to, query + at, keys + at, tc_idesc(kTile, false), s > 0, leader);
+      }
+      tc_commit(w.bars + (kScoresFull + b) * 8, leader);
+      tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
+      if (++st == kKeyStages) st = 0, phase ^= 1;
+    }
+  }
+  if (w.dead() && leader) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
+  tc_commit(w.bars + kDone * 8, leader);
+  bar_wait(w.bars + kDone * 8, 0);
+}
+
+template <int D>
+__device__ __forceinline__ void sum_role(Roles r, int lane) {
+  const bool leader = lane == 0;
+  Waiter& w = r.w;
+  Stretch p;
+  int it = 0;
+  while (r.next(p, lane)) {
 #pragma unroll 1
     for (int k = 0; k < p.count; ++k, ++it) {
       const int b = it & 1;
@@ -383,8 +394,8 @@ __device__ __forceinline__ void matrix_role(Roles r, int lane) {
       w.wait(kWeightsFull + b, it >> 1);
       if (w.dead()) continue;
       tc_fence_after();
-      const uint32_t out = agreed(tmem + kOutAt), weights = agreed(tmem + kWeightsAt + b * (kTile / 2));
-      const uint64_t values = tc_operand(agreed(base + Smem<D>::values + b * Smem<D>::kOperand));
+      const uint32_t out = agreed(r.tmem + kOutAt), weights = agreed(r.tmem + kWeightsAt + b * (kTile / 2));
+      const uint64_t values = tc_operand(agreed(r.base + Smem<D>::values + b * Smem<D>::kOperand));
       const bool add = agreed(k) > 0;
 #pragma unroll
       for (int s = 0; s < kTile / 16; ++s)
@@ -392,7 +403,6 @@ __device__ __forceinline__ void matrix_role(Roles r, int lane) {
                leader);
       tc_commit(w.bars + (kOutFull + b) * 8, leader);
       tc_commit(w.bars + (kValuesEmpty + b) * 8, leader);
-      if (k + 2 < p.count) score(it + 2);
     }
   }
   if (w.dead() && leader) atomicOr(r.L.a.status, 1 << SSD_ERR_CUDA);
@@ -422,25 +432,30 @@ __device__ __forceinline__ void load_queries(const Roles& r, const Stretch& p, i
   const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && ((a.qs[0] | a.qs[1] | a.qs[2]) & 7) == 0;  // (in elements)
   const int c = lane % kLanes;
   uint4 v[kTimes];
+  long long at[kTimes];
+  bool real[kTimes];
 #pragma unroll
   for (int t = 0; t < kTimes; ++t) {
-    const int row = warp * 16 + t * kRows + lane / kLanes, k = p.k0 + row, b = p.b + k / r.L.rows, j = k % r.L.rows;
-    const int i = j / r.L.per;
+    const int row = warp * 16 + t * kRows + lane / kLanes, k = p.k0 + row, n = k / r.L.rows, j = k - n * r.L.rows;
+    const int b = p.b + n, i = j / r.L.per;
+    at[t] = b * a.qs[0] + i * a.qs[1] + (p.h * r.L.per + j - i * r.L.per) * a.qs[2] + c * 8;
+    const int count = a.n_q ? __ldg(a.n_q + min(b, a.B - 1)) : a.nq;
+    real[t] = row < p.n_rows && i < count;
+  }
+#pragma unroll
+  for (int t = 0; t < kTimes; ++t) {
     v[t] = make_uint4(0, 0, 0, 0);
-    if (row < p.n_rows && i < (a.n_q ? a.n_q[b] : a.nq)) {
-      const unsigned short* q = static_cast<const unsigned short*>(a.q) + b * a.qs[0] + i * a.qs[1] +
-                                (p.h * r.L.per + j - i * r.L.per) * a.qs[2] + c * 8;
-      if (vec) {
-        v[t] = __ldg(reinterpret_cast<const uint4*>(q));
-      } else {
+    if (real[t] && vec) v[t] = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + at[t]));
+  }
+  if (!vec) {
+#pragma unroll
+    for (int t = 0; t < kTimes; ++t)
 #pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t x = q[e];
-          v[t].x = __funnelshift_r(v[t].x, v[t].y, 16), v[t].y = __funnelshift_r(v[t].y, v[t].z, 16);
-          v[t].z = __funnelshift_r(v[t].z, v[t].w, 16), v[t].w = __funnelshift_r(v[t].w, x, 16);
-        }
+      for (int e = 0; e < 8 && real[t]; ++e) {
+        const uint32_t x = static_cast<const unsigned short*>(a.q)[at[t] + e];
+        v[t].x = __funnelshift_r(v[t].x, v[t].y, 16), v[t].y = __funnelshift_r(v[t].y, v[t].z, 16);
+        v[t].z = __funnelshift_r(v[t].z, v[t].w, 16), v[t].w = __funnelshift_r(v[t].w, x, 16);
       }
-    }
   }
 #pragma unroll
   for (int t = 0; t < kTimes; ++t) {
@@ -596,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (tid < kKeysEmpty || (tid >= kValuesFull && tid < kValuesEmpty)) count = 4;
     if ((tid >= kScoresRead && tid < kOutFull) || tid == kQueryFull || tid >= kPlaceEmpty) count = 8;
     if (tid >= kPartEmpty && tid < kPlaceFull) count = kReaders;
+    if (tid == kDone) count = 2;
     bar_init(base + tid * 8, count);
   }
   if (warp == 16) {
@@ -621,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     value_role<D>(r, tid & 127);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 16) matrix_role<D>(r, lane);
+    if (warp == 16) score_role<D>(r, lane);
+    else if (warp == 18) sum_role<D>(r, lane);
     else if (warp == 17) part_role(L, list, base, r.w, lane, kv_block_bytes(D));
   }
   tc_fence_before();
