@@ -3,24 +3,23 @@
 //
 // Rows are the M side here (a group has hundreds of them): 128 rows of a row block
 // meet tiles of 128 tokens.
-//   S [128 rows x 128 tokens]    = Q K^T     both operands in shared memory
+//   S [128 rows x 128 tokens]    = Q K^T     Q in tensor memory
 //   O [128 rows x D elements]   += P V       P in tensor memory
 // Keys and values are unpacked to fp16, where n s is exact.
 //
-// Twenty warps:
+// Twenty-four warps:
 //   0-7    weights: a thread has a row and half of a tile's tokens (0-3 the first half,
 //          4-7 the second): 2^x, sum, weights to tensor memory, corrections, results
 //   8-11   keys: a token a thread, from global memory to a shared operand
-//   12-15  values: two elements of some blocks a thread, likewise
-//   16, 18 issue the matrix instructions of the scores and of the sums: a wait costs 140
+//   12-19  values: two elements of some blocks a thread, likewise
+//   20, 22 issue the matrix instructions of the scores and of the sums: a wait costs 140
 //          cycles and a commit 100 even where nothing is to be waited for, so one warp
 //          for both left the tensor cores idle half of the time
-//   17     finds the CTA's parts of the list and the tiles' blocks
-// Scores and weights are double, so that a tile's weights are computed while the
-// products of the tiles beside it run: the matrix instructions of M = 128 take 62
-// cycles each however few the columns (and 81 with weights from tensor memory), 1150
-// a tile, and a handshake from one to the other takes 450 cycles, which one tile at a
-// time would wait for four times.
+//   21     finds the CTA's parts of the list and the tiles' blocks
+// Scores are double, so that a tile's weights are computed while the products of the
+// tiles beside it run.  Matrix instructions of M = 128, N = 128 take 83 cycles each, so
+// a tile takes 1330; with queries from shared memory they and the unpacked keys and
+// values need more of its bandwidth than there is (2100 a tile).
 //
 // Weights are fp16, 2^(x - m + 9), with m the row's maximum when it was last moved:
 // first taken from a part's first tile, it moves when a tile's weights add up to more
@@ -36,11 +35,11 @@ namespace ssdv {
 
 namespace {
 
-constexpr int kTile = 128, kM = 128, kThreads = 640;
+constexpr int kTile = 128, kM = 128, kThreads = 768;
 constexpr int kHalf = 64;  // tokens of a tile that a thread has
 constexpr int kFast = 9, kTop = 15;
 constexpr int kKeyStages = 3, kValueStages = 2;
-constexpr int kRing = 4, kReaders = 18, kPlaces = 8;
+constexpr int kRing = 4, kReaders = 22, kPlaces = 8;
 
 enum : int {
   kKeysFull = 0,       // [kKeyStages] keys unpacked      -> matrix
@@ -49,8 +48,8 @@ enum : int {
   kValuesEmpty = 8,    // [2] products added              -> values
   kScoresFull = 10,    // [2] scores computed             -> weights
   kScoresRead = 12,    // [2] and in registers            -> matrix
-  kWeightsFull = 14,   // [2] weights written, sums corrected  -> matrix
-  kOutFull = 16,       // [2] a tile's products added     -> weights
+  kWeightsFull = 14,   // weights written, sums corrected  -> matrix
+  kOutFull = 16,       // a tile's products added         -> weights
   kQueryFull = 18,     // queries written                 -> matrix
   kDone = 19,          // all matrix instructions are done
   kPartFull = 20,      // [kRing] a part is described          -> all
@@ -69,8 +68,9 @@ struct Smem {
   static constexpr int query = 3072, keys = query + kOperand, values = keys + kKeyStages * kOperand;
   static constexpr int total = values + kValueStages * kOperand + 1024;  // operands begin at a multiple of 1024
 };
-// Columns of tensor memory: scores of two tiles, their weights (two fp16 a column), sums.
-constexpr int kScoresAt = 0, kWeightsAt = 2 * kTile, kOutAt = 3 * kTile;
+// Columns of tensor memory: scores of two tiles, weights and queries (two fp16 a column),
+// sums.
+constexpr int kScoresAt = 0, kWeightsAt = 2 * kTile, kQueryAt = kWeightsAt + kTile / 2, kOutAt = 3 * kTile;
 
 __device__ __forceinline__ void tc_ld32(uint32_t at, float (&x)[32]) {
   asm volatile(
@@ -83,15 +83,6 @@ __device__ __forceinline__ void tc_ld32(uint32_t at, float (&x)[32]) {
         "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
       : "r"(at));
 }
-// D [128 x N] in tensor memory (+)= A [128 x 16] B [N x 16], both in shared memory.
-__device__ __forceinline__ void tc_mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, bool leader) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(leader))
-      : "memory");
-}
-
 // What the roles know of a part: request and place among its rows of the first row.
 struct Stretch {
   int h, b, k0, n_rows, len, t0, count;
@@ -254,7 +245,7 @@ __device__ __forceinline__ void key_role(Roles r, int tid) {
 
 template <int D>
 __device__ __forceinline__ void value_role(Roles r, int tid) {
-  constexpr int kI = D / 16, kB = D / 32;  // blocks a thread
+  constexpr int kI = D / 16, kB = D / 64;  // blocks a thread
   const int lane = tid & 31, warp = tid >> 5, i = lane & (kI - 1), swap = (lane >> 2) & 1;
   const int g = lane / kI + (D == 128 ? 4 * (warp & 1) : 0), b0 = (D == 128 ? warp >> 1 : warp) * kB;
   const int d0 = g * (D / 8) + 2 * i;
@@ -273,9 +264,9 @@ __device__ __forceinline__ void value_role(Roles r, int tid) {
     const int slot = it % kPlaces;
     r.w.wait(kPlaceFull + slot, it / kPlaces);
 #pragma unroll
-    for (int b = 0; b < kB; b += 2) {
-      const uint4 v = lds128(r.base + kPlacesAt + slot * 64 + (b0 + b) * 8);
-      at[2 * b] = v.x, at[2 * b + 1] = v.y, at[2 * b + 2] = v.z, at[2 * b + 3] = v.w;
+    for (int b = 0; b < kB; ++b) {
+      const uint2 v = lds64(r.base + kPlacesAt + slot * 64 + (b0 + b) * 8);
+      at[2 * b] = v.x, at[2 * b + 1] = v.y;
     }
     __syncwarp();
     if (lane == 0) r.w.arrive(kPlaceEmpty + slot);
@@ -362,14 +353,11 @@ __device__ __forceinline__ void score_role(Roles r, int lane) {
       w.wait(kKeysFull + st, phase);
       if (w.dead()) continue;
       tc_fence_after();
-      const uint32_t to = agreed(r.tmem + kScoresAt + b * kTile);
-      const uint64_t query = tc_operand(agreed(r.base + Smem<D>::query));
+      const uint32_t to = agreed(r.tmem + kScoresAt + b * kTile), query = agreed(r.tmem + kQueryAt);
       const uint64_t keys = tc_operand(agreed(r.base + Smem<D>::keys + st * Smem<D>::kOperand));
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const int at = (s >> 2) * (kTile * 128 / 16) + (s & 3) * 2;
-        tc_mma_shared(to, query + at, keys + at, tc_idesc(kTile, false), s > 0, leader);
-      }
+      for (int s = 0; s < D / 16; ++s)
+        tc_mma(to, query + s * 8, keys + (s >> 2) * (kTile * 128 / 16) + (s & 3) * 2, tc_idesc(kTile, false), s > 0, leader);
       tc_commit(w.bars + (kScoresFull + b) * 8, leader);
       tc_commit(w.bars + (kKeysEmpty + st) * 8, leader);
       if (++st == kKeyStages) st = 0, phase ^= 1;
@@ -391,17 +379,17 @@ __device__ __forceinline__ void sum_role(Roles r, int lane) {
     for (int k = 0; k < p.count; ++k, ++it) {
       const int b = it & 1;
       w.wait(kValuesFull + b, it >> 1);
-      w.wait(kWeightsFull + b, it >> 1);
+      w.wait(kWeightsFull, it);
       if (w.dead()) continue;
       tc_fence_after();
-      const uint32_t out = agreed(r.tmem + kOutAt), weights = agreed(r.tmem + kWeightsAt + b * (kTile / 2));
+      const uint32_t out = agreed(r.tmem + kOutAt), weights = agreed(r.tmem + kWeightsAt);
       const uint64_t values = tc_operand(agreed(r.base + Smem<D>::values + b * Smem<D>::kOperand));
       const bool add = agreed(k) > 0;
 #pragma unroll
       for (int s = 0; s < kTile / 16; ++s)
         tc_mma(out, weights + s * 8, values + (s >> 2) * (D * 128 / 16) + (s & 3) * 2, tc_idesc(D, false), add || s > 0,
                leader);
-      tc_commit(w.bars + (kOutFull + b) * 8, leader);
+      tc_commit(w.bars + kOutFull * 8, leader);
       tc_commit(w.bars + (kValuesEmpty + b) * 8, leader);
     }
   }
@@ -495,8 +483,21 @@ __device__ __forceinline__ void weight_role(Roles r, int warp, int lane) {
   int it = 0;
   while (r.next(p, lane)) {
     load_queries<D>(r, p, warp, lane);
-    async_fence();
     group_sync<256>(kAll);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {  // 32 elements of the thread's row, half of which are the other warp's
+      uint32_t q[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int chunk = (h * (D / 64) + c) * 4 + i;
+        const uint4 v = lds128(r.base + Smem<D>::query + (chunk >> 3) * (kM * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+        q[4 * i] = v.x, q[4 * i + 1] = v.y, q[4 * i + 2] = v.z, q[4 * i + 3] = v.w;
+      }
+      tc_st16(r.tmem + lanes + kQueryAt + (h * (D / 64) + c) * 16, q);
+    }
+    tc_wait_st();
+    tc_fence_before();
+    group_sync<256>(kAll);  // (and the rows in shared memory are read before the next part's come)
     if (lane == 0) w.arrive(kQueryFull);
     const float f = lds_f(r.base + kFactorsAt + row * 4);
     float m = -INFINITY, l = 0.f;
@@ -533,7 +534,7 @@ __device__ __forceinline__ void weight_role(Roles r, int warp, int lane) {
           top = fmaxf(top, lds_f(tops + (h ^ 1) * (kM * 4)));
           const float now = top == -INFINITY ? m : fmaxf(m, top * f), fall = ex2(m - now);
           if (k > 0) {
-            w.wait(kOutFull + (b ^ 1), (it - 1) >> 1);
+            w.wait(kOutFull, it - 1);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 2; c += 8) {
@@ -568,18 +569,18 @@ __device__ __forceinline__ void weight_role(Roles r, int warp, int lane) {
         if (move || !group_any<64>(pair, !(sum <= 65504.f))) break;
       }
       l += sum;
-      // (the weights of the tile before the last have been read)
-      w.wait(kOutFull + b, (it >> 1) ^ 1);
+      // (once the weights of the tile before have been read)
+      w.wait(kOutFull, it ^ 1);
       tc_fence_after();
-      tc_st16(weights + b * (kTile / 2), y[0]);
-      tc_st16(weights + b * (kTile / 2) + 16, y[1]);
+      tc_st16(weights, y[0]);
+      tc_st16(weights + 16, y[1]);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) w.arrive(kWeightsFull + b);
+      if (lane == 0) w.arrive(kWeightsFull);
     }
     // this part's sums, once the last products (and so all before them) are added
-    w.wait(kOutFull + ((it - 1) & 1), (it - 1) >> 1);
+    w.wait(kOutFull, it - 1);
     tc_fence_after();
     const bool real = row < p.n_rows;
     const long long at = p.row0 + row + static_cast<long long>(blockIdx.x) * kM;
@@ -608,13 +609,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   if (tid < kBars) {
     // how many warps (or commits) arrive
     int count = 1;
-    if (tid < kKeysEmpty || (tid >= kValuesFull && tid < kValuesEmpty)) count = 4;
-    if ((tid >= kScoresRead && tid < kOutFull) || tid == kQueryFull || tid >= kPlaceEmpty) count = 8;
+    if (tid < kKeysEmpty) count = 4;
+    if ((tid >= kValuesFull && tid < kValuesEmpty) || (tid >= kScoresRead && tid < kOutFull) || tid == kQueryFull) count = 8;
+    if (tid >= kPlaceEmpty) count = 12;
     if (tid >= kPartEmpty && tid < kPlaceFull) count = kReaders;
     if (tid == kDone) count = 2;
     bar_init(base + tid * 8, count);
   }
-  if (warp == 16) {
+  if (warp == 20) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + kTmemAt) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -625,25 +627,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   tc_fence_after();
   Roles r = {L, base, lds32(base + kTmemAt), {}};
   r.w.bars = base;
-  // 128 x (128 + 128 + 80 + 88 + 48) registers: within the 640 x 96 of the launch
+  // 128 x (2 x 120 + 72 + 2 x 56 + 48) registers: within the 768 x 80 of the launch
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     weight_role<D>(r, warp, lane);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     key_role<D>(r, tid & 127);
-  } else if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    value_role<D>(r, tid & 127);
+  } else if (warp < 20) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    value_role<D>(r, tid - 384);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 16) score_role<D>(r, lane);
-    else if (warp == 18) sum_role<D>(r, lane);
-    else if (warp == 17) part_role(L, list, base, r.w, lane, kv_block_bytes(D));
+    if (warp == 20) score_role<D>(r, lane);
+    else if (warp == 22) sum_role<D>(r, lane);
+    else if (warp == 21) part_role(L, list, base, r.w, lane, kv_block_bytes(D));
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 20) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(lds32(base + kTmemAt)));
   }
