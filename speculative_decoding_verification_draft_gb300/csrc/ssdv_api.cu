@@ -1156,7 +1156,7 @@ ssd_status ssd_qk_norm_rope(const void* q, const int64_t q_strides[3], const voi
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
     return fail(SSD_ERR_SHAPE, "rot_dim=%d is no multiple of 16 up to %d", rot_dim, head_dim);
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SSD_ERR_SHAPE, "eps=%g is negative or not finite", eps);
-  if (static_cast<double>(B) * n * ((n_heads + n_kv_heads) / 8 + 1) >= 2147483648.0)
+  if (static_cast<double>(B) * n >= 2147483648.0)
     return fail(SSD_ERR_SHAPE, "grid too large");
   if (!aligned_to(kv_len, 4) || !aligned_to(n_new, 4) || !aligned_to(q_weight, 16) || !aligned_to(k_weight, 16) ||
       !aligned_to(inv_freq, 4) || !aligned_to(workspace, 16))

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant
     if (errors) atomicOr(a.status, errors);
   }
   // pages that come back, then pages that go: a warp looks at 32 requests at a time
+  const int top = static_cast<int>(total) - 1;
   for (int pass = 0; pass < 2; ++pass) {
     for (int b0 = warp * 32; b0 < a.B; b0 += kThreads) {
       const int4 p = b0 + lane < a.B ? plan[b0 + lane] : make_int4(0, 0, 0, 0);
@@ -172,16 +173,31 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant
         todo &= todo - 1;
         const int held = __shfl_sync(~0u, p.x, l), after = __shfl_sync(~0u, p.y, l), rank = __shfl_sync(~0u, p.z, l);
         const long long row = static_cast<long long>(b0 + l) * a.max_pages;
-        if (pass == 0) {
-          for (int c = after + lane; c < held; c += 32) {
-            a.out_free[n_free + rank + c - after] = a.table[row + c];
-            a.out_table[row + c] = -1;
+        // (four loads a lane before the first store: the arrays may be the same)
+        for (int c0 = min(held, after) + lane; c0 < max(held, after); c0 += 128) {
+          int page[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int c = c0 + 32 * x;
+            if (pass == 0) {
+              if (c < held) page[x] = a.table[row + c];
+            } else if (c < after) {
+              const int at = top - (rank + c - held);
+              page[x] = at >= n_free ? a.out_free[at] : a.free[at];
+            }
           }
-        } else {
-          for (int c = held + lane; c < after; c += 32) {
-            const int at = static_cast<int>(total) - 1 - (rank + c - held);
-            a.out_table[row + c] = at >= n_free ? a.out_free[at] : a.free[at];
-            a.out_free[at] = -1;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int c = c0 + 32 * x;
+            if (pass == 0) {
+              if (c < held) {
+                a.out_free[n_free + rank + c - after] = page[x];
+                a.out_table[row + c] = -1;
+              }
+            } else if (c < after) {
+              a.out_table[row + c] = page[x];
+              a.out_free[top - (rank + c - held)] = -1;
+            }
           }
         }
       }

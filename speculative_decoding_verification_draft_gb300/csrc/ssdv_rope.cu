@@ -10,10 +10,10 @@
 // left goes to fp32 in half-turns.  An angle is off by 2^-24 of itself and by
 // position * 2^-63 half-turns.
 //
-// D / 16 lanes take a head's row, 16 elements a lane as two vectors that hold the
-// lane's eight pairs whole, so a pair never crosses lanes.  A warp takes one token
-// and up to four rows of each of its groups of lanes, all loaded before the first
-// is used; its lanes share out the token's sines and cosines.
+// A CTA takes a token: its threads share out the sines and cosines, then its warps the
+// heads.  D / 16 lanes take a head's row, 16 elements a lane as two vectors that hold
+// eight pairs whole, so a pair never crosses lanes; up to four rows a lane are loaded
+// before the first is used.
 #include <cuda_bf16.h>
 
 #include "ssdv.h"
@@ -79,103 +79,120 @@ __device__ __forceinline__ unsigned long long turns(float freq) {
   return u >> 31 ? 0ull - f : f;
 }
 
+// (x, y) *= (a, b); (x, y) += (a, b)^2: two fp32 operations at once.
+__device__ __forceinline__ void mul_pair(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_squares(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "fma.rn.f32x2 a, b, b, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
+// The rows of queries or of keys of a token.
+template <typename E, int D, bool kInterleaved, bool kVec>
+__device__ __forceinline__ void turn_rows(const E* in, E* out, long long stride, long long out_stride, int heads,
+                                          const float* weight, float eps, bool real, float fill, bool turned, int d0, int d1,
+                                          const float* cosines, int warp, int lane) {
+  constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kStep = kThreads / 32 * kGroups;
+  const int first = warp * kGroups + lane / kLanes;
+  float w[16];
+#pragma unroll 1
+  for (int j0 = 0; j0 < heads; j0 += kStep * kRows) {
+    float x[kRows][16];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int j = j0 + r * kStep + first;
+      if (real && j < heads) {
+        load8<E, kVec>(in + j * stride + d0, x[r]);
+        load8<E, kVec>(in + j * stride + d1, x[r] + 8);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[r][e] = fill;
+      }
+    }
+    if (j0 == 0) {
+      __syncthreads();  // (the sines are there)
+      if (weight) {
+        load8<float, true>(weight + d0, w);
+        load8<float, true>(weight + d1, w + 8);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (j0 + r * kStep >= heads) break;  // (the CTA agrees)
+      const int j = j0 + r * kStep + first;
+      if (weight && real) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) add_squares(a, b, x[r][e], x[r][e + 1]);
+        a += b;
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
+        const float inv = 1.f / sqrtf(a * (1.f / D) + eps);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          mul_pair(x[r][e], x[r][e + 1], inv, inv);
+          mul_pair(x[r][e], x[r][e + 1], w[e], w[e + 1]);
+        }
+      }
+      if (turned && real) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float& p = x[r][kInterleaved ? 2 * e : e];
+          float& q = x[r][kInterleaved ? 2 * e + 1 : e + 8];
+          const float2 t = reinterpret_cast<const float2*>(cosines)[e];
+          const float y = p * t.x - q * t.y;
+          q = p * t.y + q * t.x;
+          p = y;
+        }
+      }
+      if (j < heads) {
+        store8<E, kVec>(out + j * out_stride + d0, x[r]);
+        store8<E, kVec>(out + j * out_stride + d1, x[r] + 8);
+      }
+    }
+  }
+}
+
 template <typename E, int D, bool kInterleaved, bool kVec>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kEach = 8 / kGroups;
-  const int lane = threadIdx.x & 31, l = lane % kLanes, group = lane / kLanes;
-  const int total = a.heads + a.kv_heads, per_token = (total + kGroups * kRows - 1) / (kGroups * kRows);
-  const long long id = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long token = id / per_token;
-  const int part = static_cast<int>(id - token * per_token);
-  if (token >= static_cast<long long>(a.B) * a.n) return;
-  const int b = static_cast<int>(token / a.n), i = static_cast<int>(token - static_cast<long long>(b) * a.n);
+  __shared__ __align__(16) float2 turn[D / 2];  // cosine and sine of each pair
+  const int tid = threadIdx.x, lane = tid & 31, l = lane % (D / 16), warp = tid >> 5;
+  const int b = blockIdx.x / a.n, i = blockIdx.x - b * a.n;
   const int len = a.len[b], count = a.n_new ? a.n_new[b] : a.n;
   const bool bad = len < 0 || count < 0 || count > a.n || static_cast<long long>(len) + count > (1ll << 30);
-  if (bad && i == 0 && part == 0 && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
+  if (bad && i == 0 && tid == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
   const bool real = !bad && i < count;
+  if (real && tid < a.rot / 2) {
+    const float freq = a.freq[tid];
+    const unsigned long long t = turns(freq) * static_cast<unsigned long long>(static_cast<unsigned>(len + i));
+    float2 y;
+    sincospif(__ll2float_rn(static_cast<long long>(t)) * 1.0842021724855044e-19f, &y.y, &y.x);  // 2^-63
+    if (!isfinite(freq)) y.x = y.y = __int_as_float(0x7FC00000);
+    turn[tid] = y;
+  }
   // the lane's two vectors: of the rotated pairs' first and second halves, or side by side
-  const bool turned = l < a.rot / 16;
-  const bool apart = !kInterleaved && turned;
+  const bool turned = l < a.rot / 16, apart = !kInterleaved && turned;
   const int d0 = apart ? 8 * l : 16 * l, d1 = apart ? 8 * l + a.rot / 2 : 16 * l + 8;
-
-  const auto row = [&](int j, bool out) -> long long {
-    const bool key = j >= a.heads;
-    const long long* s = out ? (key ? a.oks : a.oqs) : (key ? a.ks : a.qs);
-    return b * s[0] + i * s[1] + (key ? j - a.heads : j) * s[2];
-  };
-  float x[kRows][16];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int j = (part * kRows + r) * kGroups + group;
-    if (real && j < total) {
-      const E* p = static_cast<const E*>(j < a.heads ? a.q : a.k) + row(j, false);
-      load8<E, kVec>(p + d0, x[r]);
-      load8<E, kVec>(p + d1, x[r] + 8);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[r][e] = bad ? __int_as_float(0x7FC00000) : 0.f;
-    }
-  }
-  // pair 8 l + e of the token: group g of lanes computes kEach of the lane's eight
-  float c[8], s[8];
-  {
-    float mc[kEach], ms[kEach];
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      mc[e] = 1.f, ms[e] = 0.f;
-      if (turned && real) {
-        const float freq = a.freq[8 * l + group * kEach + e];
-        const unsigned long long t = turns(freq) * static_cast<unsigned long long>(static_cast<unsigned>(len + i));
-        sincospif(__ll2float_rn(static_cast<long long>(t)) * 1.0842021724855044e-19f, &ms[e], &mc[e]);  // 2^-63
-        if (!isfinite(freq)) mc[e] = ms[e] = __int_as_float(0x7FC00000);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      c[e] = __shfl_sync(~0u, mc[e % kEach], e / kEach * kLanes + l);
-      s[e] = __shfl_sync(~0u, ms[e % kEach], e / kEach * kLanes + l);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int j = (part * kRows + r) * kGroups + group;
-    const float* w = j < a.heads ? a.q_weight : a.k_weight;
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sum = fmaf(x[r][e], x[r][e], sum);
-#pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if (j >= total) continue;
-    if (w && real) {
-      const float inv = 1.f / sqrtf(sum * (1.f / D) + a.eps);
-      float v[16];
-      load8<float, true>(w + d0, v);
-      load8<float, true>(w + d1, v + 8);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[r][e] = x[r][e] * inv * v[e];
-    }
-    if (turned && real) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float& p = x[r][kInterleaved ? 2 * e : e];
-        float& q = x[r][kInterleaved ? 2 * e + 1 : e + 8];
-        const float y = p * c[e] - q * s[e];
-        q = p * s[e] + q * c[e];
-        p = y;
-      }
-    }
-    E* out = static_cast<E*>(j < a.heads ? a.out_q : a.out_k) + row(j, true);
-    store8<E, kVec>(out + d0, x[r]);
-    store8<E, kVec>(out + d1, x[r] + 8);
-  }
+  const float fill = bad ? __int_as_float(0x7FC00000) : 0.f;
+  const float* mine = reinterpret_cast<const float*>(turn + (turned ? 8 * l : 0));
+  turn_rows<E, D, kInterleaved, kVec>(static_cast<const E*>(a.q) + b * a.qs[0] + i * a.qs[1],
+                                      static_cast<E*>(a.out_q) + b * a.oqs[0] + i * a.oqs[1], a.qs[2], a.oqs[2], a.heads,
+                                      a.q_weight, a.eps, real, fill, turned, d0, d1, mine, warp, lane);
+  if (a.kv_heads)
+    turn_rows<E, D, kInterleaved, kVec>(static_cast<const E*>(a.k) + b * a.ks[0] + i * a.ks[1],
+                                        static_cast<E*>(a.out_k) + b * a.oks[0] + i * a.oks[1], a.ks[2], a.oks[2],
+                                        a.kv_heads, a.k_weight, a.eps, real, fill, turned, d0, d1, mine, warp, lane);
 }
 
 template <typename E, int D>
 cudaError_t launch_dim(const RopeArgs& a, bool interleaved, bool vec, cudaStream_t stream) {
-  constexpr int kGroups = 512 / D;
-  const long long per_token = (a.heads + a.kv_heads + kGroups * kRows - 1) / (kGroups * kRows);
-  const long long warps = per_token * a.B * a.n;
-  const unsigned grid = static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32));
+  const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.B) * a.n);
   if (interleaved) {
     if (vec) rope_kernel<E, D, true, true><<<grid, kThreads, 0, stream>>>(a);
     else rope_kernel<E, D, true, false><<<grid, kThreads, 0, stream>>>(a);

@@ -277,57 +277,65 @@ __global__ void __launch_bounds__(kThreads) shared_kernel(const __grid_constant_
   }
 }
 
-// Joins a row's own part and its parts of the prefix, in order: a warp a row.
+// Joins a row's own part and its parts of the prefix, in order: a CTA has the rows of a
+// request and kv head, a warp a row.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ SharedLaunch L) {
   constexpr int kPer = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const KvAttnArgs& a = L.a;
-  const int lane = threadIdx.x & 31;
-  const long long orow = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // (request, query, query head)
-  if (orow >= static_cast<long long>(a.B) * a.nq * a.heads) return;
-  const int head = static_cast<int>(orow % a.heads), i = static_cast<int>(orow / a.heads % a.nq);
-  const int b = static_cast<int>(orow / a.heads / a.nq), h = head / L.per, k = i * L.per + head - h * L.per;
+  const int lane = threadIdx.x & 31, h = blockIdx.x, b = blockIdx.y;
   const Span s = find_span<kTokens>(a, b);
-  float m = -INFINITY, l = 0.f, y[kPer] = {};
-  if (s.bad) {
-    l = __int_as_float(0x7FC00000);
-    if (i == 0 && head == 0 && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
-  } else if (i < s.nq) {
-    const int g = L.group_of[b], b0 = L.group_start[g], n = (s.first + L.tile - 1) / L.tile;
-    const long long rows = static_cast<long long>(L.group_start[g + 1] - b0) * L.rows;
-    const long long r = static_cast<long long>(b - b0) * L.rows + k, nb = (rows + L.R - 1) / L.R;
-    const long long quota = L.head[0], u0 = L.unit0[g] + (h * nb + r / L.R) * n;
-    const long long c0 = u0 / quota, c1 = n ? (u0 + n - 1) / quota : c0 - 1;  // teams
-    const long long at = static_cast<long long>(b0) * L.rows * a.c.kv_heads + h * rows + r;
-    const long long own = (static_cast<long long>(b) * a.c.kv_heads + h) * L.rows + k;
-    const auto sums = [&](long long c) { return c < c0 ? a.own_ml[own] : L.ml[at + c * L.R]; };  // c0 - 1: its own
-    for (long long c = c0 - 1 + lane; c <= c1; c += 32) {
-      const float2 x = sums(c);
-      if (x.y != 0.f) m = fmaxf(m, x.x);
-    }
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
+  if (s.bad && h == 0 && threadIdx.x == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
+  const int g = s.bad ? 0 : L.group_of[b], b0 = L.group_start[g], n = s.bad ? 0 : (s.first + L.tile - 1) / L.tile;
+  const long long rows = static_cast<long long>(L.group_start[g + 1] - b0) * L.rows, quota = L.head[0];
+  const long long r0 = static_cast<long long>(b - b0) * L.rows, u = L.unit0[g] + h * quotient(rows + L.R - 1, L.R) * n;
+  const long long at0 = static_cast<long long>(b0) * L.rows * a.c.kv_heads + h * rows + r0;
+  const long long own0 = (static_cast<long long>(b) * a.c.kv_heads + h) * L.rows;
+  for (int k = threadIdx.x >> 5; k < L.rows; k += 8) {
+    const int i = k / L.per;
+    float m = -INFINITY, l = 0.f, y[kPer] = {};
+    if (s.bad) {
+      l = __int_as_float(0x7FC00000);
+    } else if (i < s.nq) {
+      const long long u0 = u + quotient(r0 + k, L.R) * n;
+      const int c0 = static_cast<int>(quotient(u0, quota)), c1 = n ? static_cast<int>(quotient(u0 + n - 1, quota)) : c0 - 1;
+      const long long own = own0 + k, at = at0 + k;
+      const auto sums = [&](int c) { return c < c0 ? a.own_ml[own] : L.ml[at + static_cast<long long>(c) * L.R]; };  // c0 - 1: its own
+      for (int c = c0 - 1 + lane; c <= c1; c += 32) {
+        const float2 x = sums(c);
+        if (x.y != 0.f) m = fmaxf(m, x.x);
+      }
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+      const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
-    for (long long c = c0 - 1; c <= c1; ++c) {
-      const float2 x = sums(c);
-      const float f = x.y == 0.f ? 0.f : ex2(x.x - ref);
-      l += x.y * f;
-      const float* o = (c < c0 ? a.own_o + own * D : L.o + (at + c * L.R) * D) + lane * kPer;
-      if (x.y == 0.f) continue;
+      for (int c = c0 - 1; c <= c1; ++c) {
+        const float2 x = sums(c);
+        const float* o = (c < c0 ? a.own_o + own * D : L.o + (at + static_cast<long long>(c) * L.R) * D) + lane * kPer;
+        float z[kPer];
 #pragma unroll
-      for (int v = 0; v < kPer / 2; ++v) {
-        const float2 z = reinterpret_cast<const float2*>(o)[v];
-        y[2 * v] += z.x * f;
-        y[2 * v + 1] += z.y * f;
+        for (int v = 0; v < kPer; v += 2) {
+          const float2 t = *reinterpret_cast<const float2*>(o + v);
+          z[v] = t.x, z[v + 1] = t.y;
+        }
+        // (a part without weights was not written)
+        const float f = x.y == 0.f ? 0.f : ex2(x.x - ref);
+        l += x.y * f;
+#pragma unroll
+        for (int v = 0; v < kPer; ++v) y[v] += x.y == 0.f ? 0.f : z[v] * f;
       }
     }
-  }
-  const float inv = 1.f / l;
-  E* out = static_cast<E*>(a.out) + orow * D + lane * kPer;
+    const long long orow = (static_cast<long long>(b) * a.nq + i) * a.heads + h * L.per + k - i * L.per;
+    const float inv = 1.f / l;
+    E* out = static_cast<E*>(a.out) + orow * D + lane * kPer;
 #pragma unroll
-  for (int v = 0; v < kPer; ++v) out[v] = static_cast<E>(l == 0.f ? 0.f : y[v] * inv);
-  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + (log2f(l) - kBias)) * 0.69314718055994531f;
+    for (int v = 0; v < kPer; v += 2) {
+      const float y0 = l == 0.f ? 0.f : y[v] * inv, y1 = l == 0.f ? 0.f : y[v + 1] * inv;
+      if constexpr (sizeof(E) == 2) *reinterpret_cast<__nv_bfloat162*>(out + v) = __floats2bfloat162_rn(y0, y1);
+      else *reinterpret_cast<float2*>(out + v) = make_float2(y0, y1);
+    }
+    if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + (log2f(l) - kBias)) * 0.69314718055994531f;
+  }
 }
 
 template <typename E, int D>
@@ -345,7 +353,7 @@ cudaError_t launch_join(const SharedLaunch& L, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(L.a.B) * L.a.nq * L.a.heads + 7) / 8));
+  cfg.gridDim = dim3(L.a.c.kv_heads, L.a.B);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &attr;

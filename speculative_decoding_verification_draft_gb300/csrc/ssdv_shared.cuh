@@ -54,8 +54,8 @@ struct SharedPart {
 };
 
 // (64-bit divisions take hundreds of cycles)
-__device__ __forceinline__ long long quotient(long long x, int y) {
-  return static_cast<unsigned long long>(x) >> 32 ? x / y : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return static_cast<unsigned long long>(x | y) >> 32 ? x / y : static_cast<unsigned>(x) / static_cast<unsigned>(y);
 }
 
 struct GroupList {
