@@ -25,25 +25,34 @@ namespace {
 
 constexpr int kThreads = 128, kRows = 4;
 
-// A lane's 16 elements of a row: eight from d0, eight from d1.
-template <typename E, bool kVec>
-__device__ __forceinline__ void load8(const E* p, float* x) {
-  if constexpr (!kVec) {
+// Eight elements as they lie in memory.
+template <typename E>
+struct Raw {
+  uint4 v[sizeof(E) / 2];
+  template <bool kVec>
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (kVec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(p[i]);
-  } else if constexpr (sizeof(E) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      for (int i = 0; i < static_cast<int>(sizeof(E) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else if constexpr (sizeof(E) == 2) {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+      const auto two = [&](int i) { return h[i] | static_cast<uint32_t>(h[i + 1]) << 16; };
+      v[0] = make_uint4(two(0), two(2), two(4), two(6));
+    } else {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+      v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      v[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
-}
+  __device__ __forceinline__ void get(float* x) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(E) == 2) x[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+      else x[i] = __uint_as_float(w[i]);
+    }
+  }
+};
 template <typename E, bool kVec>
 __device__ __forceinline__ void store8(E* p, const float* x) {
   if constexpr (!kVec) {
@@ -93,101 +102,97 @@ __device__ __forceinline__ void add_squares(float& x, float& y, float a, float b
       : "f"(a), "f"(b));
 }
 
-// The rows of queries or of keys of a token.
-template <typename E, int D, bool kInterleaved, bool kVec>
-__device__ __forceinline__ void turn_rows(const E* in, E* out, long long stride, long long out_stride, int heads,
-                                          const float* weight, float eps, bool real, float fill, bool turned, int d0, int d1,
-                                          const float* cosines, int warp, int lane) {
-  constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kStep = kThreads / 32 * kGroups;
-  const int first = warp * kGroups + lane / kLanes;
-  float w[16];
-#pragma unroll 1
-  for (int j0 = 0; j0 < heads; j0 += kStep * kRows) {
-    float x[kRows][16];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int j = j0 + r * kStep + first;
-      if (real && j < heads) {
-        load8<E, kVec>(in + j * stride + d0, x[r]);
-        load8<E, kVec>(in + j * stride + d1, x[r] + 8);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[r][e] = fill;
-      }
-    }
-    if (j0 == 0) {
-      __syncthreads();  // (the sines are there)
-      if (weight) {
-        load8<float, true>(weight + d0, w);
-        load8<float, true>(weight + d1, w + 8);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (j0 + r * kStep >= heads) break;  // (the CTA agrees)
-      const int j = j0 + r * kStep + first;
-      if (weight && real) {
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) add_squares(a, b, x[r][e], x[r][e + 1]);
-        a += b;
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
-        const float inv = 1.f / sqrtf(a * (1.f / D) + eps);
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          mul_pair(x[r][e], x[r][e + 1], inv, inv);
-          mul_pair(x[r][e], x[r][e + 1], w[e], w[e + 1]);
-        }
-      }
-      if (turned && real) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float& p = x[r][kInterleaved ? 2 * e : e];
-          float& q = x[r][kInterleaved ? 2 * e + 1 : e + 8];
-          const float2 t = reinterpret_cast<const float2*>(cosines)[e];
-          const float y = p * t.x - q * t.y;
-          q = p * t.y + q * t.x;
-          p = y;
-        }
-      }
-      if (j < heads) {
-        store8<E, kVec>(out + j * out_stride + d0, x[r]);
-        store8<E, kVec>(out + j * out_stride + d1, x[r] + 8);
-      }
-    }
-  }
-}
-
 template <typename E, int D, bool kInterleaved, bool kVec>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kStep = kThreads / 32 * kGroups;
   __shared__ __align__(16) float2 turn[D / 2];  // cosine and sine of each pair
-  const int tid = threadIdx.x, lane = tid & 31, l = lane % (D / 16), warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, l = lane % kLanes;
   const int b = blockIdx.x / a.n, i = blockIdx.x - b * a.n;
   const int len = a.len[b], count = a.n_new ? a.n_new[b] : a.n;
   const bool bad = len < 0 || count < 0 || count > a.n || static_cast<long long>(len) + count > (1ll << 30);
   if (bad && i == 0 && tid == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
   const bool real = !bad && i < count;
-  if (real && tid < a.rot / 2) {
-    const float freq = a.freq[tid];
-    const unsigned long long t = turns(freq) * static_cast<unsigned long long>(static_cast<unsigned>(len + i));
-    float2 y;
-    sincospif(__ll2float_rn(static_cast<long long>(t)) * 1.0842021724855044e-19f, &y.y, &y.x);  // 2^-63
-    if (!isfinite(freq)) y.x = y.y = __int_as_float(0x7FC00000);
-    turn[tid] = y;
-  }
   // the lane's two vectors: of the rotated pairs' first and second halves, or side by side
   const bool turned = l < a.rot / 16, apart = !kInterleaved && turned;
   const int d0 = apart ? 8 * l : 16 * l, d1 = apart ? 8 * l + a.rot / 2 : 16 * l + 8;
-  const float fill = bad ? __int_as_float(0x7FC00000) : 0.f;
-  const float* mine = reinterpret_cast<const float*>(turn + (turned ? 8 * l : 0));
-  turn_rows<E, D, kInterleaved, kVec>(static_cast<const E*>(a.q) + b * a.qs[0] + i * a.qs[1],
-                                      static_cast<E*>(a.out_q) + b * a.oqs[0] + i * a.oqs[1], a.qs[2], a.oqs[2], a.heads,
-                                      a.q_weight, a.eps, real, fill, turned, d0, d1, mine, warp, lane);
-  if (a.kv_heads)
-    turn_rows<E, D, kInterleaved, kVec>(static_cast<const E*>(a.k) + b * a.ks[0] + i * a.ks[1],
-                                        static_cast<E*>(a.out_k) + b * a.oks[0] + i * a.oks[1], a.ks[2], a.oks[2],
-                                        a.kv_heads, a.k_weight, a.eps, real, fill, turned, d0, d1, mine, warp, lane);
+  const int first = (tid >> 5) * kGroups + lane / kLanes, heads = a.heads + a.kv_heads;
+  const E* q = static_cast<const E*>(a.q) + b * a.qs[0] + i * a.qs[1];
+  const E* k = static_cast<const E*>(a.k) + b * a.ks[0] + i * a.ks[1];
+  E* out_q = static_cast<E*>(a.out_q) + b * a.oqs[0] + i * a.oqs[1];
+  E* out_k = static_cast<E*>(a.out_k) + b * a.oks[0] + i * a.oks[1];
+#pragma unroll 1
+  for (int j0 = 0; j0 < heads; j0 += kStep * kRows) {
+    Raw<E> x0[kRows], x1[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int j = j0 + r * kStep + first;
+      if (real && j < heads) {
+        const E* p = j < a.heads ? q + j * a.qs[2] : k + (j - a.heads) * a.ks[2];
+        x0[r].template load<kVec>(p + d0);
+        x1[r].template load<kVec>(p + d1);
+      }
+    }
+    if (j0 == 0) {
+      if (real && tid < a.rot / 2) {
+        const float freq = a.freq[tid];
+        const unsigned long long t = turns(freq) * static_cast<unsigned long long>(static_cast<unsigned>(len + i));
+        float2 y;
+        sincospif(__ll2float_rn(static_cast<long long>(t)) * 1.0842021724855044e-19f, &y.y, &y.x);  // 2^-63
+        if (!isfinite(freq)) y.x = y.y = __int_as_float(0x7FC00000);
+        turn[tid] = y;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (j0 + r * kStep >= heads) break;  // (the CTA agrees)
+      const int j = j0 + r * kStep + first;
+      const float* w = j < a.heads ? a.q_weight : a.k_weight;
+      float x[16];
+      if (real) {
+        x0[r].get(x);
+        x1[r].get(x + 8);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = bad ? __int_as_float(0x7FC00000) : 0.f;
+      }
+      if (real && (a.q_weight || a.k_weight)) {
+        float s = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) add_squares(s, s1, x[e], x[e + 1]);
+        s += s1;
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+        if (w) {
+          const float inv = 1.f / sqrtf(s * (1.f / D) + a.eps);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(w + (e < 8 ? d0 + e : d1 + e - 8)));
+            mul_pair(x[e], x[e + 1], inv, inv);
+            mul_pair(x[e], x[e + 1], v.x, v.y);
+            mul_pair(x[e + 2], x[e + 3], inv, inv);
+            mul_pair(x[e + 2], x[e + 3], v.z, v.w);
+          }
+        }
+      }
+      if (turned && real) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float& p = x[kInterleaved ? 2 * e : e];
+          float& o = x[kInterleaved ? 2 * e + 1 : e + 8];
+          const float2 t = turn[8 * l + e];
+          const float y = p * t.x - o * t.y;
+          o = p * t.y + o * t.x;
+          p = y;
+        }
+      }
+      if (j < heads) {
+        E* p = j < a.heads ? out_q + j * a.oqs[2] : out_k + (j - a.heads) * a.oks[2];
+        store8<E, kVec>(p + d0, x);
+        store8<E, kVec>(p + d1, x + 8);
+      }
+    }
+  }
 }
 
 template <typename E, int D>

@@ -727,26 +727,32 @@ def kv_plan(page_table: torch.Tensor, n_held: torch.Tensor, free_pages: torch.Te
         raise ValueError(f"page_table must be [B, max_pages], got {list(page_table.shape)}")
     B, width = page_table.shape
     n, device, index = int(n), page_table.device, page_table.get_device()
-    state = (page_table, n_held, free_pages, n_free)
-    ins = [_dev(page_table, "page_table", torch.int32), _kv_counts(n_held, "n_held", B, index),
-           _kv_dev(free_pages, "free_pages", torch.int32, index), _kv_counts(n_free, "n_free", 1, index)]
+    ins = (_dev(page_table, "page_table", torch.int32), _kv_counts(n_held, "n_held", B, index),
+           _kv_dev(free_pages, "free_pages", torch.int32, index), _kv_counts(n_free, "n_free", 1, index))
     if free_pages.dim() != 1:
         raise ValueError(f"free_pages must be [n_pages], got {list(free_pages.shape)}")
+    pool = free_pages.shape[0]
     lens, news = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_new, "n_new", B, index)
     shared = _kv_counts(n_shared, "n_shared", B, index)
     raw, ctx = _kv_stream(stream, device)
     ws = workspace
     with ctx or _HERE:
         if out is None:
-            out = [torch.empty(t.shape, dtype=torch.int32, device=device) for t in state]
+            table = torch.empty((B, width), dtype=torch.int32, device=device)
+            held = torch.empty((B,), dtype=torch.int32, device=device)
+            stack = torch.empty((pool,), dtype=torch.int32, device=device)
+            left = torch.empty((1,), dtype=torch.int32, device=device)
+            out = (table, held, stack, left)
+            outs = (table.data_ptr(), held.data_ptr(), stack.data_ptr(), left.data_ptr())
+        else:
+            if len(out) != 4 or any(o.shape != t.shape for o, t in zip(out, (page_table, n_held, free_pages, n_free))):
+                raise ValueError("out must be four tensors shaped like page_table, n_held, free_pages and n_free")
+            outs = [_kv_dev(o, "out", torch.int32, index) for o in out]
         slots = torch.empty((B, max(n, 0)), dtype=torch.int64, device=device)
         if ws is None and B:
             ws = _kv_workspace(_kv_plan_bytes(B), device, raw)
-    if len(out) != 4 or any(o.shape != t.shape for o, t in zip(out, state)):
-        raise ValueError("out must be four tensors shaped like page_table, n_held, free_pages and n_free")
-    outs = [_kv_dev(o, "out", torch.int32, index) for o in out]
     if B:
-        _check(lib().ssd_kv_plan(*ins, B, width, free_pages.shape[0], int(page_size), lens, news, n, shared, *outs,
+        _check(lib().ssd_kv_plan(*ins, B, width, pool, int(page_size), lens, news, n, shared, *outs,
                                  slots.data_ptr() if n > 0 else None, _kv_dev(ws, "workspace", None, index),
                                  ws.numel(), raw))
     elif out[2] is not free_pages or out[3] is not n_free:
@@ -777,38 +783,50 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], kv_len: torch.Tenso
     kv_heads = 0
     if k is not None:
         kp, ks = _kv_rows(k, "k", None, dim, index)
-        kv_heads = k.shape[2]
-        if k.shape[:2] != q.shape[:2] or k.dtype != q.dtype:
+        kb, kn, kv_heads, _ = k.shape
+        if kb != B or kn != n or k.dtype != q.dtype:
             raise ValueError("q and k must have one dtype and the same requests and tokens")
     code = _dtype_code(q, "q and k")
-    weights = [None if w is None else _kv_dev(w, name, torch.float32, index)
-               for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
-    for w in (q_weight, k_weight):
-        if w is not None and w.shape != (dim,):
-            raise ValueError(f"weights must be [{dim}], got {list(w.shape)}")
-    rot = 0
+    qw = None if q_weight is None else _kv_weight(q_weight, "q_weight", dim, index)
+    kw = None if k_weight is None else _kv_weight(k_weight, "k_weight", dim, index)
+    rot, freq = 0, None
     if inv_freq is not None:
         if inv_freq.dim() != 1:
             raise ValueError(f"inv_freq must be [rot_dim / 2], got {list(inv_freq.shape)}")
         rot = 2 * inv_freq.shape[0]
-    freq = _kv_dev(inv_freq, "inv_freq", torch.float32, index) if rot else None
+        freq = _kv_dev(inv_freq, "inv_freq", torch.float32, index) if rot else None
     lens, news = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_new, "n_new", B, index)
     raw, ctx = _kv_stream(stream, device)
-    ws = workspace
+    ws, ok, okp, oks = workspace, None, None, None
     with ctx or _HERE:
-        oq, ok = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=device),
-                                              None if k is None else torch.empty(k.shape, dtype=q.dtype, device=device))
+        if out is None:
+            oq = torch.empty((B, n, heads, dim), dtype=q.dtype, device=device)
+            oqp, oqs = oq.data_ptr(), _KV_STRIDES.pack(n * heads * dim, heads * dim, dim)
+            if k is not None:
+                ok = torch.empty((B, n, kv_heads, dim), dtype=q.dtype, device=device)
+                okp, oks = ok.data_ptr(), _KV_STRIDES.pack(n * kv_heads * dim, kv_heads * dim, dim)
+        else:
+            oq, ok = out
+            oqp, oqs = _kv_rows(oq, "out q", heads, dim, index)
+            if oq.shape != q.shape or oq.dtype != q.dtype:
+                raise ValueError("out must be tensors like q and k")
+            if k is not None:
+                okp, oks = _kv_rows(ok, "out k", kv_heads, dim, index)
+                if ok.shape != k.shape or ok.dtype != q.dtype:
+                    raise ValueError("out must be tensors like q and k")
         if ws is None:
             ws = _kv_workspace(256, device, raw)
-    oqp, oqs = _kv_rows(oq, "out q", heads, dim, index)
-    okp, oks = (None, None) if k is None else _kv_rows(ok, "out k", kv_heads, dim, index)
-    if oq.shape != q.shape or oq.dtype != q.dtype or (k is not None and (ok.shape != k.shape or ok.dtype != q.dtype)):
-        raise ValueError("out must be tensors like q and k")
     if B and n:
-        _check(lib().ssd_qk_norm_rope(qp, qs, kp, ks, code, lens, news, B, n, heads, kv_heads, dim, *weights, float(eps),
+        _check(lib().ssd_qk_norm_rope(qp, qs, kp, ks, code, lens, news, B, n, heads, kv_heads, dim, qw, kw, float(eps),
                                       freq, rot, int(interleaved), oqp, oqs, okp, oks,
                                       _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
     return oq, ok
+
+
+def _kv_weight(w: torch.Tensor, name: str, dim: int, index: int) -> int:
+    if w.shape != (dim,):
+        raise ValueError(f"{name} must be [{dim}], got {list(w.shape)}")
+    return _kv_dev(w, name, torch.float32, index)
 
 
 def debug_rowstats(target, draft, draft_tokens, temperature, seed, workspace=None, stream=None):
