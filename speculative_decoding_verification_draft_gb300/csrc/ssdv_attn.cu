@@ -852,6 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_kernel(const __grid_
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long scan[kThreads], sums[kThreads / 32];
   __shared__ int2 spans[kWarps][NT * 8];
+  if constexpr (kMore) asm volatile("griddepcontrol.wait;" ::: "memory");
   const KvAttnArgs& a = L.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t bars = smem_u32(smem), data = bars + kHead;
@@ -945,8 +946,12 @@ cudaError_t launch_shape(const AttnLaunch& L, int sms, cudaStream_t s) {
   const int smem = kHead + L.p.t * (L.p.s * stage_bytes(D) + (P == 2 ? L.p.g * pair_bytes(D, NT, sizeof(E) == 4) : 0));
   cudaError_t e = allow_shared<kv_attention_kernel<E, D, NT, P>>(kSmem);
   if (e != cudaSuccess) return e;
-  kv_attention_kernel<E, D, NT, P><<<sms, kThreads, smem, s>>>(L);
-  e = cudaGetLastError();
+  if constexpr (kMore) {
+    e = launch_after(kv_attention_kernel<E, D, NT, P>, dim3(sms), kThreads, smem, s, L);
+  } else {
+    kv_attention_kernel<E, D, NT, P><<<sms, kThreads, smem, s>>>(L);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   return launch_join<E, D>(L, sms, s);
 }

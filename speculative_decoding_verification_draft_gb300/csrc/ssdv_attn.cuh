@@ -68,6 +68,23 @@ cudaError_t allow_shared(int bytes) {
   return e;
 }
 
+// Launches a kernel whose first act is to wait for the one before it (griddepcontrol.wait),
+// so that its launch overlaps that one's end.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- mbarriers and bulk copies ----
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

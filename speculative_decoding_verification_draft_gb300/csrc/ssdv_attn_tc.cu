@@ -1057,6 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   tc_fence_before();
+  if constexpr (kMore) asm volatile("griddepcontrol.wait;" ::: "memory");
   List<kTile> list;
   list.build(L.a, L.a.c.kv_heads * L.p.rt, gridDim.x, kPartTiles, scan, sums);
   tc_fence_after();
@@ -1089,6 +1090,7 @@ template <int N>
 cudaError_t launch_n(const AttnLaunch& L, int sms, cudaStream_t stream) {
   const cudaError_t e = allow_shared<kv_attention_tc_kernel<N>>(Smem<N>::total);
   if (e != cudaSuccess) return e;
+  if constexpr (kMore) return launch_after(kv_attention_tc_kernel<N>, dim3(sms), kThreads, Smem<N>::total, stream, L);
   kv_attention_tc_kernel<N><<<sms, kThreads, Smem<N>::total, stream>>>(L);
   return cudaGetLastError();
 }

@@ -21,6 +21,7 @@ constexpr int kRows = 64, kTokens = 64, kThreads = 128;
 constexpr int kBias = 15;
 constexpr int kPad = 8;  // halves between rows: eight rows' 16 bytes lie in different banks
 constexpr int kTeamsPerSm = 2;
+constexpr int kJoins = 1216;  // joining CTAs that run at a time
 
 template <int D, int kParts>
 struct Tile {
@@ -147,8 +148,10 @@ __global__ void __launch_bounds__(kThreads) shared_kernel(const __grid_constant_
   const uint32_t smem = smem_u32(bytes);
   const KvCacheArgs& c = L.a.c;
   const Bases bases = make_bases();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   GroupList list(L);
   list.build(scan, sums);
+  list.publish(tid, kThreads);
   const long long end = min((blockIdx.x + 1) * list.quota, list.total);
   for (long long u = blockIdx.x * list.quota; u < end;) {
     const SharedPart p = list.part(u, end);
@@ -292,37 +295,55 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   const long long r0 = static_cast<long long>(b - b0) * L.rows, u = L.unit0[g] + h * quotient(rows + L.R - 1, L.R) * n;
   const long long at0 = static_cast<long long>(b0) * L.rows * a.c.kv_heads + h * rows + r0;
   const long long own0 = (static_cast<long long>(b) * a.c.kv_heads + h) * L.rows;
-  for (int k = threadIdx.x >> 5; k < L.rows; k += 8) {
+  for (int k = blockIdx.z * 8 + (threadIdx.x >> 5); k < L.rows; k += gridDim.z * 8) {
     const int i = k / L.per;
-    float m = -INFINITY, l = 0.f, y[kPer] = {};
-    if (s.bad) {
-      l = __int_as_float(0x7FC00000);
-    } else if (i < s.nq) {
+    float m = -INFINITY, l = s.bad ? __int_as_float(0x7FC00000) : 0.f, y[kPer] = {};
+    if (!s.bad && i < s.nq) {
       const long long u0 = u + quotient(r0 + k, L.R) * n;
-      const int c0 = static_cast<int>(quotient(u0, quota)), c1 = n ? static_cast<int>(quotient(u0 + n - 1, quota)) : c0 - 1;
-      const long long own = own0 + k, at = at0 + k;
-      const auto sums = [&](int c) { return c < c0 ? a.own_ml[own] : L.ml[at + static_cast<long long>(c) * L.R]; };  // c0 - 1: its own
-      for (int c = c0 - 1 + lane; c <= c1; c += 32) {
-        const float2 x = sums(c);
-        if (x.y != 0.f) m = fmaxf(m, x.x);
-      }
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-      const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-      for (int c = c0 - 1; c <= c1; ++c) {
-        const float2 x = sums(c);
-        const float* o = (c < c0 ? a.own_o + own * D : L.o + (at + static_cast<long long>(c) * L.R) * D) + lane * kPer;
-        float z[kPer];
+      const int c0 = static_cast<int>(quotient(u0, quota)), parts = n ? static_cast<int>(quotient(u0 + n - 1, quota)) - c0 + 2 : 1;
+      // part 0 is the row's own, part p of the prefix that of team c0 + p - 1
+      const auto sums = [&](int p) { return p ? L.ml[at0 + k + static_cast<long long>(c0 + p - 1) * L.R] : a.own_ml[own0 + k]; };
+      const auto load = [&](int p, float (&z)[kPer]) {
+        const float* o = (p ? L.o + (at0 + k + static_cast<long long>(c0 + p - 1) * L.R) * D : a.own_o + (own0 + k) * D) + lane * kPer;
 #pragma unroll
         for (int v = 0; v < kPer; v += 2) {
           const float2 t = *reinterpret_cast<const float2*>(o + v);
           z[v] = t.x, z[v + 1] = t.y;
         }
-        // (a part without weights was not written)
-        const float f = x.y == 0.f ? 0.f : ex2(x.x - ref);
+      };
+      const auto add = [&](const float2& x, const float (&z)[kPer]) {
+        if (x.y == 0.f) return;  // (a part without weights was not written)
+        const float f = ex2(x.x - (m == -INFINITY ? 0.f : m));
         l += x.y * f;
 #pragma unroll
-        for (int v = 0; v < kPer; ++v) y[v] += x.y == 0.f ? 0.f : z[v] * f;
+        for (int v = 0; v < kPer; ++v) y[v] += z[v] * f;
+      };
+      // the first three parts' loads overlap; there are seldom more
+      float2 x[3];
+      float z[3][kPer];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        x[p] = make_float2(0.f, 0.f);
+        if (p < parts) {
+          x[p] = sums(p);
+          load(p, z[p]);
+        }
+        if (x[p].y != 0.f) m = fmaxf(m, x[p].x);
+      }
+      if (parts > 3) {
+        for (int p = 3 + lane; p < parts; p += 32) {
+          const float2 t = sums(p);
+          if (t.y != 0.f) m = fmaxf(m, t.x);
+        }
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+      }
+#pragma unroll
+      for (int p = 0; p < 3; ++p) add(x[p], z[p]);
+#pragma unroll 4
+      for (int p = 3; p < parts; ++p) {
+        const float2 t = sums(p);
+        load(p, z[0]);
+        add(t, z[0]);
       }
     }
     const long long orow = (static_cast<long long>(b) * a.nq + i) * a.heads + h * L.per + k - i * L.per;
@@ -343,22 +364,14 @@ cudaError_t launch_dim(const SharedLaunch& L, cudaStream_t stream) {
   using T = Tile<D, sizeof(E) == 4 ? 2 : 1>;
   cudaError_t e = allow_shared<shared_kernel<E, D>>(T::total);
   if (e != cudaSuccess) return e;
-  shared_kernel<E, D><<<L.teams, kThreads, T::total, stream>>>(L);
-  return cudaGetLastError();
+  return launch_after(shared_kernel<E, D>, dim3(L.teams), kThreads, T::total, stream, L);
 }
 
 template <typename E, int D>
 cudaError_t launch_join(const SharedLaunch& L, cudaStream_t stream) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(L.a.c.kv_heads, L.a.B);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_join_kernel<E, D>, L);
+  // with few requests, a row a warp: what a CTA looks up first takes longer than a row
+  const int pairs = L.a.c.kv_heads * L.a.B, z = std::min((L.rows + 7) / 8, std::max(1, kJoins / pairs));
+  return launch_after(shared_join_kernel<E, D>, dim3(L.a.c.kv_heads, L.a.B, z), 256, 0, stream, L);
 }
 
 template <typename E>

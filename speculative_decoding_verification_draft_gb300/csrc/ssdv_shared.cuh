@@ -63,6 +63,7 @@ struct GroupList {
   const long long* scan;
   int chunk, threads;
   long long total, quota;
+  bool broken;
   __device__ __forceinline__ GroupList(const SharedLaunch& L_) : L(L_) {}
 
   __device__ __forceinline__ int length(int g) const {
@@ -85,7 +86,7 @@ struct GroupList {
     scan = scan_;
     chunk = (L.G + threads - 1) / threads;
     const int g0 = min(tid * chunk, L.G), g1 = min(g0 + chunk, L.G);
-    bool broken = false;
+    broken = false;
     long long mine = 0;
     for (int g = g0; g < g1; ++g) {
       const int from = L.group_start[g], to = L.group_start[g + 1];
@@ -110,16 +111,21 @@ struct GroupList {
     quota = total < 0x80000000ll
                 ? max((static_cast<unsigned>(total) + static_cast<unsigned>(L.teams) - 1) / static_cast<unsigned>(L.teams), 1u)
                 : (total + L.teams - 1) / L.teams;
-    // what the kernels after this one need to know
+    __syncthreads();
+  }
+  // What the kernels after this one need to know, by `count` threads of every CTA.
+  __device__ __forceinline__ void publish(int me, int count) const {
     if (blockIdx.x == 0) {
-      if (tid == 0) L.head[0] = quota;
-      long long u = before + x - mine;
-      for (int g = g0; g < g1; ++g) {
-        L.unit0[g] = u;
-        u += units(g);
+      if (me == 0) L.head[0] = quota;
+      for (int t = me; t < threads && t * chunk < L.G; t += count) {
+        long long u = scan[t];
+        for (int g = t * chunk; g < min((t + 1) * chunk, L.G); ++g) {
+          L.unit0[g] = u;
+          u += units(g);
+        }
       }
     }
-    for (int b = blockIdx.x * threads + tid; b < L.a.B; b += gridDim.x * threads) {
+    for (int b = blockIdx.x * count + me; b < L.a.B; b += gridDim.x * count) {
       int lo = 0, hi = L.G - 1;  // the last group that begins at or before b
       while (!broken && lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -130,28 +136,34 @@ struct GroupList {
       L.group_of[b] = lo;
       L.first[b] = broken || n < 0 || n != length(lo) ? -1 : n;
     }
-    __syncthreads();
   }
   // The part that begins with unit u < end of the list, and goes on to `end` at most.
   __device__ __forceinline__ SharedPart part(long long u, long long end) const {
-    int lo = 0, hi = threads - 1;  // last thread whose groups begin at or before u
+    int lo = 0, hi = min(threads, (L.G + chunk - 1) / chunk) - 1;  // last thread whose groups begin at or before u
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (mid * chunk < L.G && scan[mid] <= u) lo = mid;
+      if (scan[mid] <= u) lo = mid;
       else hi = mid - 1;
     }
     SharedPart p;
     p.g = lo * chunk;
-    long long u0 = scan[lo];
-    while (u0 + units(p.g) <= u) u0 += units(p.g++);
-    const int n = tiles(p.g), nb = blocks(p.g);
-    const long long k = u - u0, rb = quotient(k, n), rows = group_rows(p.g);
+    long long u0 = scan[lo], rows;
+    int n, nb;
+    for (;; ++p.g) {
+      p.b0 = L.group_start[p.g];
+      rows = static_cast<long long>(L.group_start[p.g + 1] - p.b0) * L.rows;
+      p.len = length(p.g);
+      n = (p.len + L.tile - 1) / L.tile;
+      nb = static_cast<int>(quotient(rows + L.R - 1, L.R));
+      const long long mine = static_cast<long long>(L.a.c.kv_heads) * nb * n;
+      if (u0 + mine > u) break;
+      u0 += mine;
+    }
+    const long long k = u - u0, rb = quotient(k, n);
     p.h = static_cast<int>(quotient(rb, nb));
     p.block = static_cast<int>(rb - static_cast<long long>(p.h) * nb);
-    p.len = length(p.g);
     p.t0 = static_cast<int>(k - rb * n);
     p.count = static_cast<int>(min(static_cast<long long>(n - p.t0), end - u));
-    p.b0 = L.group_start[p.g];
     p.n_rows = static_cast<int>(min(static_cast<long long>(L.R), rows - static_cast<long long>(p.block) * L.R));
     p.row0 = static_cast<long long>(p.b0) * L.rows * L.a.c.kv_heads + p.h * rows + static_cast<long long>(p.block) * L.R;
     return p;

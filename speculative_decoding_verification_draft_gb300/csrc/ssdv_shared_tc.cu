@@ -420,30 +420,28 @@ __device__ __forceinline__ void load_queries(const Roles& r, const Stretch& p, i
   const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && ((a.qs[0] | a.qs[1] | a.qs[2]) & 7) == 0;  // (in elements)
   const int c = lane % kLanes;
   uint4 v[kTimes];
-  long long at[kTimes];
-  bool real[kTimes];
+  // lane l finds the warp's row l: request, query and head from its place
+  const int mine = warp * 16 + (lane & 15), k = p.k0 + mine, n = k / r.L.rows, j = k - n * r.L.rows;
+  const int b = p.b + n, i = j / r.L.per;
+  const long long at = b * a.qs[0] + i * a.qs[1] + (p.h * r.L.per + j - i * r.L.per) * a.qs[2];
+  const uint32_t there = __ballot_sync(~0u, mine < p.n_rows && i < (a.n_q ? __ldg(a.n_q + min(b, a.B - 1)) : a.nq));
 #pragma unroll
   for (int t = 0; t < kTimes; ++t) {
-    const int row = warp * 16 + t * kRows + lane / kLanes, k = p.k0 + row, n = k / r.L.rows, j = k - n * r.L.rows;
-    const int b = p.b + n, i = j / r.L.per;
-    at[t] = b * a.qs[0] + i * a.qs[1] + (p.h * r.L.per + j - i * r.L.per) * a.qs[2] + c * 8;
-    const int count = a.n_q ? __ldg(a.n_q + min(b, a.B - 1)) : a.nq;
-    real[t] = row < p.n_rows && i < count;
-  }
-#pragma unroll
-  for (int t = 0; t < kTimes; ++t) {
+    const int row = t * kRows + lane / kLanes;
+    const unsigned short* q = static_cast<const unsigned short*>(a.q) + __shfl_sync(~0u, at, row) + c * 8;
     v[t] = make_uint4(0, 0, 0, 0);
-    if (real[t] && vec) v[t] = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + at[t]));
-  }
-  if (!vec) {
-#pragma unroll
-    for (int t = 0; t < kTimes; ++t)
+    if (there >> row & 1) {
+      if (vec) {
+        v[t] = __ldg(reinterpret_cast<const uint4*>(q));
+      } else {
 #pragma unroll 1
-      for (int e = 0; e < 8 && real[t]; ++e) {
-        const uint32_t x = static_cast<const unsigned short*>(a.q)[at[t] + e];
-        v[t].x = __funnelshift_r(v[t].x, v[t].y, 16), v[t].y = __funnelshift_r(v[t].y, v[t].z, 16);
-        v[t].z = __funnelshift_r(v[t].z, v[t].w, 16), v[t].w = __funnelshift_r(v[t].w, x, 16);
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t x = q[e];
+          v[t].x = __funnelshift_r(v[t].x, v[t].y, 16), v[t].y = __funnelshift_r(v[t].y, v[t].z, 16);
+          v[t].z = __funnelshift_r(v[t].z, v[t].w, 16), v[t].w = __funnelshift_r(v[t].w, x, 16);
+        }
       }
+    }
   }
 #pragma unroll
   for (int t = 0; t < kTimes; ++t) {
@@ -622,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   tc_fence_before();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   GroupList list(L);
   list.build(scan, sums);
   tc_fence_after();
@@ -642,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (warp == 20) score_role<D>(r, lane);
     else if (warp == 22) sum_role<D>(r, lane);
     else if (warp == 21) part_role(L, list, base, r.w, lane, kv_block_bytes(D));
+    else list.publish(lane, 32);
   }
   tc_fence_before();
   __syncthreads();
@@ -655,8 +655,7 @@ template <int D>
 cudaError_t launch_dim(const SharedLaunch& L, cudaStream_t stream) {
   const cudaError_t e = allow_shared<shared_tc_kernel<D>>(Smem<D>::total);
   if (e != cudaSuccess) return e;
-  shared_tc_kernel<D><<<L.teams, kThreads, Smem<D>::total, stream>>>(L);
-  return cudaGetLastError();
+  return launch_after(shared_tc_kernel<D>, dim3(L.teams), kThreads, Smem<D>::total, stream, L);
 }
 
 }  // namespace
