@@ -23,7 +23,7 @@ namespace ssdv {
 
 namespace {
 
-constexpr int kThreads = 128, kRows = 4;
+constexpr int kThreads = 128, kRows = 2;
 
 // Eight elements as they lie in memory.
 template <typename E>
@@ -112,9 +112,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const bool bad = len < 0 || count < 0 || count > a.n || static_cast<long long>(len) + count > (1ll << 30);
   if (bad && i == 0 && tid == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
   const bool real = !bad && i < count;
-  // the lane's two vectors: of the rotated pairs' first and second halves, or side by side
-  const bool turned = l < a.rot / 16, apart = !kInterleaved && turned;
-  const int d0 = apart ? 8 * l : 16 * l, d1 = apart ? 8 * l + a.rot / 2 : 16 * l + 8;
+  // the lane's two vectors, neighbours' side by side: of the rotated pairs' first and
+  // second halves, or of the rest; interleaved, of the row's halves
+  const bool both = !kInterleaved && l < a.rot / 16;
+  const int d0 = kInterleaved || both ? 8 * l : 8 * l + a.rot / 2;
+  const int d1 = both ? d0 + a.rot / 2 : kInterleaved ? d0 + D / 2 : d0 + (D - a.rot) / 2;
   const int first = (tid >> 5) * kGroups + lane / kLanes, heads = a.heads + a.kv_heads;
   const E* q = static_cast<const E*>(a.q) + b * a.qs[0] + i * a.qs[1];
   const E* k = static_cast<const E*>(a.k) + b * a.ks[0] + i * a.ks[1];
@@ -175,12 +177,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
           }
         }
       }
-      if (turned && real) {
+      if (real) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
+          // pair e: of the two vectors' elements e, or two neighbours of one vector
+          const int first = e < 4 ? d0 + 2 * e : d1 + 2 * (e - 4);
+          if (kInterleaved ? first >= a.rot : !both) continue;
           float& p = x[kInterleaved ? 2 * e : e];
           float& o = x[kInterleaved ? 2 * e + 1 : e + 8];
-          const float2 t = turn[8 * l + e];
+          const float2 t = turn[kInterleaved ? first / 2 : d0 + e];
           const float y = p * t.x - o * t.y;
           o = p * t.y + o * t.x;
           p = y;
