@@ -447,6 +447,7 @@ _HERE = contextlib.nullcontext()
 # packs its structures itself and asks torch as little as it can.
 _KV_CACHE = struct.Struct("PqiiiiP")  # KvCacheStruct
 _KV_STRIDES = struct.Struct("qqq")
+_INT32, _F32 = torch.int32, torch.float32
 
 
 @functools.lru_cache(maxsize=None)
@@ -501,7 +502,9 @@ def _kv_counts(t: Optional[torch.Tensor], name: str, B: int, index: int):
         return None
     if t.shape != (B,):
         raise ValueError(f"{name} must be [{B}], got {list(t.shape)}")
-    return _kv_dev(t, name, torch.int32, index)
+    if t.dtype is not _INT32 or t.get_device() != index or not t.is_contiguous():
+        return _kv_dev(t, name, _INT32, index)
+    return t.data_ptr()
 
 
 def _kv_rows(t: torch.Tensor, name: str, heads: Optional[int], dim: int, index: int):
@@ -541,6 +544,15 @@ def _capture_id(raw: int) -> int:
     n = ctypes.c_uint64(0)
     _check(lib().ssd_stream_capture_id(raw, ctypes.byref(n)))
     return n.value
+
+
+def _kv_room(workspace: Optional[torch.Tensor], need, shape, device, raw: int, index: int):
+    """(address, bytes) of the workspace given, or of the stream's own of need(*shape) bytes (called with the stream
+    current)."""
+    if workspace is None:
+        ws = _kv_workspace(need(*shape), device, raw)
+        return ws.data_ptr(), ws.numel()
+    return _kv_dev(workspace, "workspace", None, index), workspace.numel()
 
 
 def _kv_workspace(need: int, device, raw: int):
@@ -644,22 +656,21 @@ def kv_attention(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Te
     qp, qs = _kv_rows(q, "q", None, dim, index)
     lens, counts = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_q, "n_q", B, index)
     raw, ctx = _kv_stream(stream, device)
-    ws = workspace
     with ctx or _HERE:
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=device)
         if lse is None and return_lse:
             lse = torch.empty((B, n, heads), dtype=torch.float32, device=device)
-        if ws is None and B and n:
-            ws = _kv_workspace(kv_workspace_bytes(n, heads, kv_heads, dim), device, raw)
+        ws = _kv_room(workspace, kv_workspace_bytes, (n, heads, kv_heads, dim), device, raw, index) if B and n else None
     if out.shape != shape or (lse is not None and lse.shape != (B, n, heads)):
         raise ValueError("out must be shaped like q and lse [B, n, n_heads]")
     if B and n:
-        _check(lib().ssd_kv_attention_sinks(c, lens, counts, qp, qs, _dtype_code(q, "q"), B, n, heads,
-                                            float(scale) if scale is not None else dim ** -0.5, window, sinks,
-                                            int(past_only), _kv_dev(out, "out", q.dtype, index),
-                                            _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None,
-                                            _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
+        status = lib().ssd_kv_attention_sinks(
+            c, lens, counts, qp, qs, _dtype_code(q, "q"), B, n, heads, float(scale) if scale is not None else dim ** -0.5,
+            window, sinks, int(past_only), _kv_dev(out, "out", q.dtype, index),
+            _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None, *ws, raw)
+        if status:
+            _check(status)
     return (out, lse) if lse is not None else out
 
 
@@ -689,22 +700,21 @@ def kv_attention_shared(cache: torch.Tensor, page_table: torch.Tensor, kv_len: t
     starts = _kv_counts(group_start, "group_start", groups + 1, index)
     shared = _kv_counts(shared_len, "shared_len", groups, index)
     raw, ctx = _kv_stream(stream, device)
-    ws = workspace
     with ctx or _HERE:
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=device)
         if lse is None and return_lse:
             lse = torch.empty((B, n, heads), dtype=torch.float32, device=device)
-        if ws is None and B and n:
-            ws = _kv_workspace(kv_shared_workspace_bytes(B, n, heads, kv_heads, dim, groups), device, raw)
+        ws = _kv_room(workspace, kv_shared_workspace_bytes, (B, n, heads, kv_heads, dim, groups), device, raw, index) if B and n else None
     if out.shape != shape or (lse is not None and lse.shape != (B, n, heads)):
         raise ValueError("out must be shaped like q and lse [B, n, n_heads]")
     if B and n:
-        _check(lib().ssd_kv_attention_shared(c, lens, counts, qp, qs, _dtype_code(q, "q"), B, n, heads,
-                                             float(scale) if scale is not None else dim ** -0.5, starts, shared, groups,
-                                             int(past_only), _kv_dev(out, "out", q.dtype, index),
-                                             _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None,
-                                             _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
+        status = lib().ssd_kv_attention_shared(
+            c, lens, counts, qp, qs, _dtype_code(q, "q"), B, n, heads, float(scale) if scale is not None else dim ** -0.5,
+            starts, shared, groups, int(past_only), _kv_dev(out, "out", q.dtype, index),
+            _kv_dev(lse, "lse", torch.float32, index) if lse is not None else None, *ws, raw)
+        if status:
+            _check(status)
     return (out, lse) if lse is not None else out
 
 
@@ -735,7 +745,6 @@ def kv_plan(page_table: torch.Tensor, n_held: torch.Tensor, free_pages: torch.Te
     lens, news = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_new, "n_new", B, index)
     shared = _kv_counts(n_shared, "n_shared", B, index)
     raw, ctx = _kv_stream(stream, device)
-    ws = workspace
     with ctx or _HERE:
         if out is None:
             table = torch.empty((B, width), dtype=torch.int32, device=device)
@@ -749,12 +758,12 @@ def kv_plan(page_table: torch.Tensor, n_held: torch.Tensor, free_pages: torch.Te
                 raise ValueError("out must be four tensors shaped like page_table, n_held, free_pages and n_free")
             outs = [_kv_dev(o, "out", torch.int32, index) for o in out]
         slots = torch.empty((B, max(n, 0)), dtype=torch.int64, device=device)
-        if ws is None and B:
-            ws = _kv_workspace(_kv_plan_bytes(B), device, raw)
+        ws = _kv_room(workspace, _kv_plan_bytes, (B,), device, raw, index) if B else None
     if B:
-        _check(lib().ssd_kv_plan(*ins, B, width, pool, int(page_size), lens, news, n, shared, *outs,
-                                 slots.data_ptr() if n > 0 else None, _kv_dev(ws, "workspace", None, index),
-                                 ws.numel(), raw))
+        status = lib().ssd_kv_plan(*ins, B, width, pool, int(page_size), lens, news, n, shared, *outs,
+                                             slots.data_ptr() if n > 0 else None, *ws, raw)
+        if status:
+            _check(status)
     elif out[2] is not free_pages or out[3] is not n_free:
         with ctx or _HERE:  # no request: the stack is what it was
             out[2].copy_(free_pages)
@@ -797,7 +806,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], kv_len: torch.Tenso
         freq = _kv_dev(inv_freq, "inv_freq", torch.float32, index) if rot else None
     lens, news = _kv_counts(kv_len, "kv_len", B, index), _kv_counts(n_new, "n_new", B, index)
     raw, ctx = _kv_stream(stream, device)
-    ws, ok, okp, oks = workspace, None, None, None
+    ok, okp, oks = None, None, None
     with ctx or _HERE:
         if out is None:
             oq = torch.empty((B, n, heads, dim), dtype=q.dtype, device=device)
@@ -814,19 +823,21 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], kv_len: torch.Tenso
                 okp, oks = _kv_rows(ok, "out k", kv_heads, dim, index)
                 if ok.shape != k.shape or ok.dtype != q.dtype:
                     raise ValueError("out must be tensors like q and k")
-        if ws is None:
-            ws = _kv_workspace(256, device, raw)
+        ws = _kv_room(workspace, kv_workspace_bytes, (), device, raw, index)
     if B and n:
-        _check(lib().ssd_qk_norm_rope(qp, qs, kp, ks, code, lens, news, B, n, heads, kv_heads, dim, qw, kw, float(eps),
-                                      freq, rot, int(interleaved), oqp, oqs, okp, oks,
-                                      _kv_dev(ws, "workspace", None, index), ws.numel(), raw))
+        status = lib().ssd_qk_norm_rope(qp, qs, kp, ks, code, lens, news, B, n, heads, kv_heads, dim, qw, kw,
+                                                  float(eps), freq, rot, int(interleaved), oqp, oqs, okp, oks, *ws, raw)
+        if status:
+            _check(status)
     return oq, ok
 
 
 def _kv_weight(w: torch.Tensor, name: str, dim: int, index: int) -> int:
     if w.shape != (dim,):
         raise ValueError(f"{name} must be [{dim}], got {list(w.shape)}")
-    return _kv_dev(w, name, torch.float32, index)
+    if w.dtype is not _F32 or w.get_device() != index or not w.is_contiguous():
+        return _kv_dev(w, name, _F32, index)
+    return w.data_ptr()
 
 
 def debug_rowstats(target, draft, draft_tokens, temperature, seed, workspace=None, stream=None):
