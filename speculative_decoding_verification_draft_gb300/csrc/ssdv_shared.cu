@@ -9,6 +9,12 @@
 // 2^(x - m + 15) with m the row's maximum so far, so fp16 keeps 11 bits down to 2^-29
 // of the largest and a multiple of 2^-40 of it below; maxima, sums of weights and of
 // values are fp32.
+//
+// Measured: 64 requests behind 4096 tokens, 5 x 32 heads over 8: 197 us for fp32 heads of
+// 128, 296 for bf16 heads of 256; bound by unpacking between two barriers a tile.  bf16
+// heads of 64 and 128 go to ssdv_shared_tc.cu whatever the rows: here against there 14 /
+// 11 us for 8 rows and 300 tokens, 95 / 43 for 16 groups of 32 rows, 158 / 38 for 1280
+// rows and 4096 tokens, 37 / 14 for 200 tokens.
 #include "ssdv_shared.cuh"
 
 #include <algorithm>
@@ -280,6 +286,8 @@ __global__ void __launch_bounds__(kThreads) shared_kernel(const __grid_constant_
   }
 }
 
+// (64 requests, 1280 rows a kv head: 11 us, mostly the loads that come one after another:
+// lengths, groups, shares, sums.  256 requests, 10240 rows: 41 us for 170 MB.)
 // Joins a row's own part and its parts of the prefix, in order: a CTA has the rows of a
 // request and kv head, a warp a row.
 template <typename E, int D>

@@ -17,9 +17,17 @@
 //          for both left the tensor cores idle half of the time
 //   21     finds the CTA's parts of the list and the tiles' blocks
 // Scores are double, so that a tile's weights are computed while the products of the
-// tiles beside it run.  Matrix instructions of M = 128, N = 128 take 83 cycles each, so
-// a tile takes 1330; with queries from shared memory they and the unpacked keys and
-// values need more of its bandwidth than there is (2100 a tile).
+// tiles beside it run.  A matrix instruction of M = 128, N = 128 takes 64 to 83 cycles
+// (the same for N = 64), so a tile takes at least 1020; with queries from shared memory
+// they and the unpacked keys and values need more of its bandwidth than there is.
+//
+// Measured: 256 requests behind 16001 tokens, 10240 rows a kv head: 710 us, 945 TFLOP/s of
+// the products.  A tile takes 2400 cycles, in which 1500 instructions a scheduler issue
+// at 0.6 a cycle: 340 for the weights, 250 for the keys, 390 for the values, the rest
+// handshakes and polls.  The tensor cores work 38 % of the time; without weights and
+// unpacking a tile takes 1020 cycles.  64 requests behind 4096 tokens, 1280 rows: 38 us,
+// of which 10 go by before the first weights (groups, part, queries, first tile: chains
+// of loads, and code that is fetched for the first time).
 //
 // Weights are fp16, 2^(x - m + 9), with m the row's maximum when it was last moved:
 // first taken from a part's first tile, it moves when a tile's weights add up to more
