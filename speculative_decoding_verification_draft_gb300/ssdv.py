@@ -736,7 +736,10 @@ def kv_plan(page_table: torch.Tensor, n_held: torch.Tensor, free_pages: torch.Te
     if page_table.dim() != 2:
         raise ValueError(f"page_table must be [B, max_pages], got {list(page_table.shape)}")
     B, width = page_table.shape
-    n, device, index = int(n), page_table.device, page_table.get_device()
+    n, page_size = int(n), int(page_size)
+    if not 0 <= n < 1 << 31 or not 0 < page_size < 1 << 31:
+        raise ValueError(f"n={n} or page_size={page_size} is negative or no 32-bit number")
+    device, index = page_table.device, page_table.get_device()
     ins = (_dev(page_table, "page_table", torch.int32), _kv_counts(n_held, "n_held", B, index),
            _kv_dev(free_pages, "free_pages", torch.int32, index), _kv_counts(n_free, "n_free", 1, index))
     if free_pages.dim() != 1:
@@ -757,11 +760,11 @@ def kv_plan(page_table: torch.Tensor, n_held: torch.Tensor, free_pages: torch.Te
             if len(out) != 4 or any(o.shape != t.shape for o, t in zip(out, (page_table, n_held, free_pages, n_free))):
                 raise ValueError("out must be four tensors shaped like page_table, n_held, free_pages and n_free")
             outs = [_kv_dev(o, "out", torch.int32, index) for o in out]
-        slots = torch.empty((B, max(n, 0)), dtype=torch.int64, device=device)
+        slots = torch.empty((B, n), dtype=torch.int64, device=device)
         ws = _kv_room(workspace, _kv_plan_bytes, (B,), device, raw, index) if B else None
     if B:
-        status = lib().ssd_kv_plan(*ins, B, width, pool, int(page_size), lens, news, n, shared, *outs,
-                                             slots.data_ptr() if n > 0 else None, *ws, raw)
+        status = lib().ssd_kv_plan(*ins, B, width, pool, page_size, lens, news, n, shared, *outs,
+                                             slots.data_ptr() if n else None, *ws, raw)
         if status:
             _check(status)
     elif out[2] is not free_pages or out[3] is not n_free:

@@ -281,3 +281,54 @@ def test_capture_streams_and_growth(ssdv, dtype, D):
     start.copy_(kc.ints([0, 3, 5]))
     graphs[0].replay()
     g.compare(*outs[0])
+
+
+@pytest.mark.parametrize("dtype,D,G,n", [(BF16, 64, 128, 32), (BF16, 128, 60, 5), (F32, 64, 128, 32)])
+def test_requests_of_more_rows_than_a_block(ssdv, dtype, D, G, n):
+    """A request's rows, 300 to 4096 a kv head, lie in several row blocks, some of which other requests share."""
+    check(ssdv, [2, 1], [50, 20], [0, 3, 1], n, 1, G, D, 16, dtype)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+def test_pages_far_into_a_large_pool(ssdv, dtype, D):
+    """Blocks beyond 4 GiB, some of the pool's last pages."""
+    g = Groups(ssdv, [3, 2], [200, 90], [9, 0, 40, 5, 30], 2, 1, 4, D, 64, dtype)
+    far = (5 << 30) // g.cache[0].numel()
+    pool = torch.empty((far + g.cache.shape[0],) + tuple(g.cache.shape[1:]), dtype=torch.uint8, device="cuda")
+    pool[far:] = g.cache
+    g.cache = pool
+    g.table += far
+    g.compare(*g.run())
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (F32, 64)])
+def test_two_streams_at_once(ssdv, dtype, D):
+    """Calls on two streams, each with the workspace of its stream, many times over."""
+    a = Groups(ssdv, [6], [900], np.arange(6) * 20, 3, 2, 4, D, 16, dtype, seed=1)
+    b = Groups(ssdv, [2, 4], [300, 700], np.arange(6) * 11, 3, 2, 4, D, 32, dtype, seed=5)
+    args = [(kc.ints(g.lens), kc.ints(g.start), kc.ints(g.pre)) for g in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for g, (lens, start, shared), s in zip((a, b), args, streams):
+            with torch.cuda.stream(s):
+                outs.append(ssdv.kv_attention_shared(g.cache, g.table, lens, g.q, start, shared, return_lse=True))
+    torch.cuda.synchronize()
+    a.compare(*outs[0])
+    b.compare(*outs[1])
+    for x, y in zip(outs, outs[2:]):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_bad_query_is_its_own_rows_loss(ssdv, D):
+    """NaN and infinite queries beside others of the same row block."""
+    g = Groups(ssdv, [4], [300], [3, 9, 0, 20], 2, 1, 4, D, 16, BF16)
+    q = g.q.clone()
+    q[1, 0, 2, 5], q[2, 1, 0, 7] = float("nan"), float("inf")
+    out, lse = g.run(q=q)
+    assert torch.isnan(out[1, 0, 2]).all() and torch.isnan(out[2, 1, 0]).all()
+    out[1, 0, 2], lse[1, 0, 2], out[2, 1, 0], lse[2, 1, 0] = g.run()[0][1, 0, 2], g.run()[1][1, 0, 2], g.run()[0][2, 1, 0], \
+        g.run()[1][2, 1, 0]
+    g.compare(out, lse)

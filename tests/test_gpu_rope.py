@@ -165,3 +165,14 @@ def test_capture_and_stream(ssdv):
     graph.replay()
     compare(b[0], q64, [6, 78], [3, 3], None, 0, f, False, BF16)
     compare(a[1], k64, [5, 77], [3, 3], None, 0, f, False, BF16)
+
+
+def test_many_tokens(ssdv):
+    """More CTAs than run at a time, ragged, against the rows of single calls."""
+    B, n = 3, 2500
+    q, q64 = kc.rows((B, n, 3, 64), BF16, 1)
+    k, k64 = kc.rows((B, n, 1, 64), BF16, 2)
+    news, lens, f = np.array([2500, 17, 1999]), np.array([0, 5, 100000]), freqs(64)
+    oq, ok = ssdv.qk_norm_rope(q, k, kc.ints(lens), inv_freq=f, n_new=kc.ints(news))
+    compare(oq, q64, lens, news, None, 0, f, False, BF16)
+    compare(ok, k64, lens, news, None, 0, f, False, BF16)

@@ -72,6 +72,9 @@ def test_binding_refuses():
     ints = lambda *s: torch.zeros(*s, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
         ssdv.kv_plan(ints(2, 4), ints(2), ints(9), ints(1), ints(2), 3, 16)
+    for n, page in ((-1, 16), (1 << 31, 16), (3, (1 << 32) + 16), (3, 0), (3, -16)):
+        with pytest.raises(ValueError, match="32-bit"):
+            ssdv.kv_plan(ints(2, 4), ints(2), ints(9), ints(1), ints(2), n, page)
     with pytest.raises(ValueError, match="max_pages"):
         ssdv.kv_plan(ints(8), ints(2), ints(9), ints(1), ints(2), 3, 16)
     with pytest.raises(ValueError, match="CUDA"):
