@@ -9,13 +9,14 @@
 // n_free + G_b + k, and the k-th that it takes lies at n_free + G - 1 - W_b - k: two
 // prefix sums over the batch, and every page has its place.
 //
-// One CTA does the sums and moves pages (a round moves few); the rest, copies of
-// the tables and the slots, is spread over the GPU when it is large.
+// Where no output is an input, one kernel of many CTAs does it all, each CTA going through
+// the sums again.  In place, one CTA does the sums and moves pages; the rest, copies and
+// slots, is spread over the GPU by a second kernel when it is large.
 //
-// Measured: 64 requests of a round, two ended and two beginning with up to 1500 tokens,
-// 6 + 5 us; 512 requests, 61 ended and 97 beginning, 15 + 10 us for 9.7 MB: chains of
-// dependent loads (lengths, sums, pages, the stack), each a microsecond.  In a
-// program the calls take 31 us each, which is the host's time.
+// Measured: 64 requests of a round, two ended and two beginning with up to 1500 tokens: 8
+// us (in place 10); 512 requests, 61 ended and 97 beginning: 13 us for 9.7 MB (in place
+// 18).  Chains of dependent loads take most: lengths, sums, pages, the stack.  In a
+// program the calls take 24 and 28 us each, which is the host's time.
 #include "ssdv_round.cuh"
 
 #include <algorithm>
@@ -28,11 +29,14 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kChunk = 256;  // cells of a row, or slots, that a warp takes at a time
-// Cells (of the table, the stack and the slots) up to which the one CTA also copies and
-// writes slots; above, a second kernel does, four CTAs an SM.  One against two: 6.4 and
-// 7.8 us for 1,000 cells, 8.0 and 11.3 for 5,000, 11.9 and 9.4 for 24,000, 22.8 and 10.2
-// for 110,000.
+// In place: cells (of the table, the stack and the slots) up to which the one CTA also
+// copies and writes slots; above, a second kernel does, four CTAs an SM.  One against two:
+// 6.4 and 7.8 us for 1,000 cells, 8.0 and 11.1 for 5,000, 11.9 and 9.3 for 24,000, 22.6
+// and 10.2 for 110,000.
 constexpr long long kAlone = 16384;
+// Not in place: one kernel of many CTAs (4.6, 8.4, 8.1 and 8.0 us for these), as long as
+// the plan of a batch fits 48 KB of shared memory.
+constexpr int kAllThreads = 512, kAllRequests = 2048;
 
 struct Want {
   int held, hold;
@@ -56,14 +60,15 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
   }
   return x;
 }
-// Inclusive sum over the CTA; total gets the sum of all.
+// Inclusive sum over the CTA's kWarps warps; total gets the sum of all.
+template <int kWarps>
 __device__ __forceinline__ long long block_scan(long long x, long long* sums, long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   x = warp_scan(x, lane);
   __syncthreads();
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  const long long s = warp_scan(sums[lane], lane);
+  const long long s = warp_scan(lane < kWarps ? sums[lane] : 0, lane);
   total = __shfl_sync(~0u, s, 31);
   const long long before = __shfl_sync(~0u, s, max(warp - 1, 0));
   return x + (warp ? before : 0);
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant
       const Want w = look(a, b0 + tid);
       mine = max(w.held - w.hold, 0);
     }
-    block_scan(mine, sums, sum);
+    block_scan<kWarps>(mine, sums, sum);
     given += sum;
   }
   const long long total = n_free + given;
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const __grid_constant
     if (b < a.B) w = look(a, b);
     const int give = max(w.held - w.hold, 0), want = max(w.hold - w.held, 0);
     long long sum_gives, sum_wants;
-    const long long g = gives + block_scan(give, sums, sum_gives), t = wants + block_scan(want, sums, sum_wants);
+    const long long g = gives + block_scan<kWarps>(give, sums, sum_gives), t = wants + block_scan<kWarps>(want, sums, sum_wants);
     gives += sum_gives;
     wants += sum_wants;
     if (b < a.B) {
@@ -220,6 +225,107 @@ __global__ void __launch_bounds__(256) kv_plan_finish_kernel(const __grid_consta
          threadIdx.x & 31);
 }
 
+// The same in one kernel, where no output is an input: every CTA goes through the sums
+// and writes its share of the outputs from the inputs alone.  A place of the stack at or
+// above n_free is a page that is given back, found by its rank among those.
+__global__ void __launch_bounds__(kAllThreads) kv_plan_all_kernel(const __grid_constant__ KvPlanArgs a) {
+  extern __shared__ int4 plan[];  // [B]: held, after, first rank of what it takes, served; then the pages given before it
+  __shared__ long long sums[kAllThreads / 32];
+  __shared__ unsigned long long taken_, errors_;
+  int* given_before = reinterpret_cast<int*>(plan + a.B);
+  constexpr int W = kAllThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) taken_ = errors_ = 0;
+  const int n_free = a.n_free[0];
+  long long given = 0, wants = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kAllThreads) {
+    const int b = b0 + tid;
+    Want w = {0, 0, false};
+    if (b < a.B) w = look(a, b);
+    const int give = max(w.held - w.hold, 0), want = max(w.hold - w.held, 0);
+    long long sum_gives, sum_wants;
+    const long long g = given + block_scan<W>(give, sums, sum_gives), t = wants + block_scan<W>(want, sums, sum_wants);
+    given += sum_gives;
+    wants += sum_wants;
+    if (b < a.B) {
+      // (sums beyond the stack are cut: such a request is not served)
+      plan[b] = make_int4(w.held, w.hold, static_cast<int>(min(t - want, 0x7FFFFFFFll)), w.bad ? -1 : 0);
+      given_before[b] = static_cast<int>(min(g - give, 0x7FFFFFFFll));
+    }
+  }
+  __syncthreads();
+  const long long total = n_free + given;
+  const bool broken = n_free < 0 || n_free > a.n_pages || total > a.n_pages;
+  for (int b = tid; b < a.B; b += kAllThreads) {
+    int4 p = plan[b];
+    const bool bad = p.w < 0;
+    const long long end = static_cast<long long>(p.z) + (p.y - p.x);  // of what it takes
+    const bool served = !bad && !broken && (p.y <= p.x || end <= total);
+    if (served && p.y > p.x) atomicMax(&taken_, static_cast<unsigned long long>(end));
+    if (bad || !served) atomicOr(&errors_, bad ? 1ull << SSD_ERR_LENGTH : broken ? 0ull : 1ull << SSD_ERR_POOL);
+    p.w = served;
+    if (!served) p.y = p.x;
+    plan[b] = p;
+    if (blockIdx.x == 0) a.out_held[b] = p.y;
+  }
+  __syncthreads();
+  const int left = broken ? n_free : static_cast<int>(total - static_cast<long long>(taken_));
+  const int top = static_cast<int>(total) - 1;
+  if (blockIdx.x == 0 && tid == 0) {
+    a.out_n_free[0] = left;
+    const int errors = static_cast<int>(errors_) | (broken ? 1 << SSD_ERR_PAGE : 0);
+    if (errors) atomicOr(a.status, errors);
+  }
+  const auto on_stack = [&](int at) {  // place `at` once all that is given back lies there
+    if (at < n_free) return a.free[at];
+    const int r = at - n_free;
+    int lo = 0, hi = a.B - 1;  // the last request with no more than r pages given before it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (given_before[mid] <= r) lo = mid;
+      else hi = mid - 1;
+    }
+    return a.table[static_cast<long long>(lo) * a.max_pages + plan[lo].y + r - given_before[lo]];
+  };
+  const long long me = static_cast<long long>(blockIdx.x) * W + (tid >> 5), warps = static_cast<long long>(gridDim.x) * W;
+  for (long long i = me * 32 + lane; i < a.n_pages; i += warps * 32)
+    a.out_free[i] = broken || i >= total ? a.free[i] : i < left ? on_stack(static_cast<int>(i)) : -1;
+  const int per = (a.max_pages + kChunk - 1) / kChunk;
+  for (long long u = me; u < static_cast<long long>(a.B) * per; u += warps) {
+    const int b = static_cast<int>(u / per), c0 = static_cast<int>(u % per) * kChunk;
+    const int4 p = plan[b];
+    const long long row = static_cast<long long>(b) * a.max_pages;
+    const int end = min(c0 + kChunk, a.max_pages);
+#pragma unroll 4
+    for (int c = c0 + lane; c < end; c += 32) {
+      int page;
+      if (c < min(p.x, p.y) || c >= max(p.x, p.y)) page = a.table[row + c];
+      else page = p.y < p.x ? -1 : on_stack(top - (p.z + c - p.x));
+      a.out_table[row + c] = page;
+    }
+  }
+  if (!a.slots) return;
+  const int chunks = (a.n + kChunk - 1) / kChunk;
+  for (long long u = me; u < static_cast<long long>(a.B) * chunks; u += warps) {
+    const int b = static_cast<int>(u / chunks), i0 = static_cast<int>(u % chunks) * kChunk;
+    const int4 p = plan[b];
+    const long long row = static_cast<long long>(b) * a.max_pages;
+    const int len = a.len[b], add = p.w ? (a.n_new ? a.n_new[b] : a.n) : 0, end = min(i0 + kChunk, a.n);
+    int64_t* out = a.slots + static_cast<long long>(b) * a.n;
+#pragma unroll 4
+    for (int i = i0 + lane; i < end; i += 32) {
+      long long slot = -1;
+      if (i < add) {
+        const unsigned pos = len + i, col = pos / static_cast<unsigned>(a.page_size);
+        const int c = static_cast<int>(col);
+        const int page = c < p.x ? a.table[row + c] : on_stack(top - (p.z + c - p.x));
+        if (page >= 0) slot = static_cast<long long>(page) * a.page_size + (pos - col * a.page_size);
+      }
+      out[i] = slot;
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
@@ -227,6 +333,13 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
   if (a.out_table != a.table) cells += static_cast<long long>(a.B) * a.max_pages;
   if (a.out_free != a.free) cells += a.n_pages;
   const bool alone = cells <= kAlone;
+  const auto blocks = [&](long long per) { return static_cast<unsigned>(std::min((cells + per - 1) / per, 608ll)); };
+  if (a.B <= kAllRequests && a.out_table != a.table && a.out_held != a.held && a.out_free != a.free &&
+      a.out_n_free != a.n_free) {
+    const unsigned grid = std::min(blocks(kAllThreads / 32 * kChunk), 304u);
+    kv_plan_all_kernel<<<grid, kAllThreads, a.B * (sizeof(int4) + 4), stream>>>(a);
+    return cudaGetLastError();
+  }
   kv_plan_kernel<<<1, kThreads, 0, stream>>>(a, alone);
   cudaError_t e = cudaGetLastError();
   if (alone || e != cudaSuccess) return e;
@@ -234,7 +347,7 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((cells + 8 * kChunk - 1) / (8 * kChunk), 608)));
+  cfg.gridDim = dim3(blocks(8 * kChunk));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &attr;
