@@ -722,6 +722,7 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
   int take = 0, phase = 0, buf = 0;
   int done = 0;
   bool dead = false;  // a copy did not arrive in time: go through the motions, without waiting
+  long long seg = kMore ? me * list.quota - share.row_unit : 0;  // unit of the row's first tile
   while (done < n_tiles) {
     const int b = at.b, h = at.hr / RT, pass0 = (at.hr % RT) * L.rows_pass;
     const int first = at.tile, count = min(n_tiles - done, at.s.tiles - at.tile);
@@ -822,6 +823,9 @@ __device__ __forceinline__ void consume(const AttnLaunch& L, const List<kTile>& 
           if (r == 0 && pw == 0) (kMore && whole ? a.own_ml : L.ml)[at_row] = make_float2(w.m[nt][x], l);
         }
       }
+    if (own_sums(a) && first == 0 && first_warp && lane == 0)
+      a.own_parts[static_cast<long long>(b) * list.per_request + at.hr] = list.row_parts(seg, sp.tiles, me);
+    if (kMore) seg += sp.tiles + list.extra;
     if (first == 0) {
       // rows past the request's own (all of them if its lengths are bad)
       if (sp.bad && at.hr == 0 && first_warp && lane == 0) atomicOr(a.status, 1 << SSD_ERR_LENGTH);
@@ -910,14 +914,6 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttnLaunch L) {
     }
   }
   const int i = row / L.per, h = d.y / RT;
-  if (own_sums(L.a)) {
-    const long long at = (static_cast<long long>(d.x) * L.a.c.kv_heads + h) * L.rows + row;
-    if (lane == 0) L.a.own_ml[at] = make_float2(ref, l);
-#pragma unroll
-    for (int v = 0; v < kPer / 2; ++v)
-      reinterpret_cast<float2*>(L.a.own_o + at * D + lane * kPer)[v] = make_float2(y[2 * v], y[2 * v + 1]);
-    return;
-  }
   const long long orow = (static_cast<long long>(d.x) * L.a.nq + i) * L.a.heads + h * L.per + row % L.per;
   const float inv = 1.f / l;
   E* out = static_cast<E*>(L.a.out) + orow * D + lane * kPer;
@@ -953,7 +949,7 @@ cudaError_t launch_shape(const AttnLaunch& L, int sms, cudaStream_t s) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_join<E, D>(L, sms, s);
+  return kMore && L.a.own_ml ? cudaSuccess : launch_join<E, D>(L, sms, s);
 }
 
 template <typename E, int D, int P, int NT>
@@ -989,6 +985,12 @@ WorkLayout work_layout(const AttnShape& p, int D) {
 }  // namespace
 
 #if SSDV_ATTN_MORE
+OwnSlots kv_own_slots(const KvAttnArgs& a, int D, int esize) {
+  const AttnShape p = attn_shape(a.nq * (a.heads / a.c.kv_heads), D, esize == 4);
+  const WorkLayout w = work_layout(p, D);
+  return {reinterpret_cast<const float2*>(a.work + w.ml), reinterpret_cast<const float*>(a.work + w.o), p.g * p.nt * 8, p.rt};
+}
+
 cudaError_t launch_attention_more(const KvAttnArgs& a, int D, int esize, cudaStream_t stream) {
 #else
 size_t kv_attention_work_bytes(int rows, int D) {
@@ -1015,7 +1017,7 @@ cudaError_t launch_kv_attention(const KvAttnArgs& a, int D, int esize, cudaStrea
   L.o = reinterpret_cast<float*>(a.work + w.o);
   if (L.p.tc) {
     e = kMore ? launch_attention_tc_more(L, sms, stream) : launch_attention_tc(L, sms, stream);
-    return e == cudaSuccess ? launch_join<__nv_bfloat16, 128>(L, sms, stream) : e;
+    return e == cudaSuccess && !(kMore && L.a.own_ml) ? launch_join<__nv_bfloat16, 128>(L, sms, stream) : e;
   }
   if (esize == 2) {
     if (D == 64) return launch_dim<__nv_bfloat16, 64>(L, sms, stream);

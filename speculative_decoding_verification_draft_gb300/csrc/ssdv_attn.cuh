@@ -374,6 +374,11 @@ struct List {
     units = tiles + static_cast<long long>(extra) * requests * per_request;
     quota = (units + teams - 1) / teams;
   }
+  // What a team that begins a row of `tiles` tiles, the first at unit seg, says of its parts.
+  __device__ __forceinline__ int2 row_parts(long long seg, int tiles, long long me) const {
+    return make_int2(static_cast<int>((seg + tiles - 1) / quota - me + 1),
+                     static_cast<int>(2 * me + (seg - extra > me * quota ? 1 : 0)));
+  }
   // What a team writes about the parts it begins with: the first team to begin
   // inside a row's tiles, past the first of them, has that row's parts joined.
   __device__ __forceinline__ int4 parts(const Share& x, long long me) const {

@@ -201,6 +201,7 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
   const List<kTile>::Share share = list.share(a, blockIdx.x);
   int left = share.count;
   Place<kTile> place = share.at;
+  long long seg = kMore ? blockIdx.x * list.quota - share.row_unit : 0;  // unit of the row's first tile
   if (lane == 0) L.desc[blockIdx.x] = list.parts(share, blockIdx.x);
   int st = 0;
   uint32_t phase = 1;
@@ -225,6 +226,9 @@ __device__ __forceinline__ void copy_role(const AttnLaunch& L, const List<kTile>
     }
     if (!left || w.dead()) break;
     const bool any = place.s.any();
+    if (own_sums(a) && p.first == 0 && lane == 0)
+      a.own_parts[static_cast<long long>(p.b) * list.per_request + place.hr] = list.row_parts(seg, place.s.tiles, blockIdx.x);
+    if (kMore) seg += place.s.tiles + list.extra;
     left -= p.count;
     place.tile += p.count - 1;
     if (left) place.next(a, list.per_request);

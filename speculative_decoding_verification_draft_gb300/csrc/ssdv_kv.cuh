@@ -88,12 +88,22 @@ struct KvAttnArgs {
   void* out;              // [B, nq, heads, D]
   float* lse;             // [B, nq, heads] or null
   float2* own_ml;         // in place of out and lse, or null: [B, kv_heads, nq * heads / kv_heads] maximum and sum
-  float* own_o;           // and [.., D] sums of the rows that are real, as parts keep them
+  float* own_o;           // and [.., D] sums of the rows that are real, as parts keep them;
+  int2* own_parts;        // [B, kv_heads, passes]: parts of the pass's rows and the first's slot.  Rows in
+                          // more parts than one are not in own_ml and own_o but where own_slots says
   int32_t* status;
   uint8_t* work;          // partial results
 };
 cudaError_t launch_kv_attention(const KvAttnArgs& a, int D, int esize, cudaStream_t stream);
 size_t kv_attention_work_bytes(int rows, int D);
+// Where a call with own_parts leaves the parts of rows in several: part k of row r of a
+// pass is at (k ? 2 (slot / 2 + k) : slot) * rows_pass + r.
+struct OwnSlots {
+  const float2* ml;
+  const float* o;
+  int rows_pass, passes;
+};
+OwnSlots kv_own_slots(const KvAttnArgs& a, int D, int esize);
 // The same for groups of requests that share a prefix (ssdv_shared.cu).
 cudaError_t launch_kv_shared(const KvAttnArgs& a, const int32_t* group_start, const int32_t* shared_len, int G, int D,
                              int esize, cudaStream_t stream);

@@ -286,10 +286,10 @@ __global__ void __launch_bounds__(kThreads) shared_kernel(const __grid_constant_
   }
 }
 
-// (64 requests, 1280 rows a kv head: 11 us, mostly the loads that come one after another:
-// lengths, groups, shares, sums.  256 requests, 10240 rows: 41 us for 170 MB.)
-// Joins a row's own part and its parts of the prefix, in order: a CTA has the rows of a
-// request and kv head, a warp a row.
+// Joins a row's own parts and its parts of the prefix, in order: a CTA has the rows of a
+// request and kv head, a warp a row.  (64 requests, 1280 rows a kv head: 12 us, mostly the
+// loads that come one after another: lengths, groups, shares, sums.  256 requests, 10240
+// rows: 48 us for 170 MB.)
 template <typename E, int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ SharedLaunch L) {
   constexpr int kPer = D / 32;
@@ -308,11 +308,19 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
     float m = -INFINITY, l = s.bad ? __int_as_float(0x7FC00000) : 0.f, y[kPer] = {};
     if (!s.bad && i < s.nq) {
       const long long u0 = u + quotient(r0 + k, L.R) * n;
-      const int c0 = static_cast<int>(quotient(u0, quota)), parts = n ? static_cast<int>(quotient(u0 + n - 1, quota)) - c0 + 2 : 1;
-      // part 0 is the row's own, part p of the prefix that of team c0 + p - 1
-      const auto sums = [&](int p) { return p ? L.ml[at0 + k + static_cast<long long>(c0 + p - 1) * L.R] : a.own_ml[own0 + k]; };
+      const int c0 = static_cast<int>(quotient(u0, quota));
+      const int pass = k / L.own.rows_pass, local = k - pass * L.own.rows_pass;
+      // the row's own parts come first, then those of the prefix, of teams c0 and on
+      const int2 own = a.own_parts[(static_cast<long long>(b) * a.c.kv_heads + h) * L.own.passes + pass];
+      const int parts = own.x + (n ? static_cast<int>(quotient(u0 + n - 1, quota)) - c0 + 1 : 0);
+      const auto place = [&](int p) -> long long {
+        if (p >= own.x) return at0 + k + static_cast<long long>(c0 + p - own.x) * L.R;
+        if (own.x == 1) return own0 + k;
+        return static_cast<long long>(p ? 2 * (own.y / 2 + p) : own.y) * L.own.rows_pass + local;
+      };
+      const auto sums = [&](int p) { return (p >= own.x ? L.ml : own.x == 1 ? a.own_ml : L.own.ml)[place(p)]; };
       const auto load = [&](int p, float (&z)[kPer]) {
-        const float* o = (p ? L.o + (at0 + k + static_cast<long long>(c0 + p - 1) * L.R) * D : a.own_o + (own0 + k) * D) + lane * kPer;
+        const float* o = (p >= own.x ? L.o : own.x == 1 ? a.own_o : L.own.o) + place(p) * D + lane * kPer;
 #pragma unroll
         for (int v = 0; v < kPer; v += 2) {
           const float2 t = *reinterpret_cast<const float2*>(o + v);
@@ -390,7 +398,7 @@ cudaError_t launch_type(const SharedLaunch& L, int D, cudaStream_t stream, bool 
 }
 
 struct SharedWork {
-  size_t unit0, first, group_of, own_ml, own_o, ml, o, attn, total;
+  size_t unit0, first, group_of, own_parts, own_ml, own_o, ml, o, attn, total;
 };
 SharedWork shared_work(long long B, int nq, int heads, int kv_heads, int D, int G, const SharedShape& s) {
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -399,7 +407,8 @@ SharedWork shared_work(long long B, int nq, int heads, int kv_heads, int D, int 
   w.unit0 = 256;
   w.first = w.unit0 + up(static_cast<size_t>(G) * 8);
   w.group_of = w.first + up(static_cast<size_t>(B) * 4);
-  w.own_ml = w.group_of + up(static_cast<size_t>(B) * 4);
+  w.own_parts = w.group_of + up(static_cast<size_t>(B) * 4);
+  w.own_ml = w.own_parts + up(static_cast<size_t>(B) * kv_heads * ((nq * (heads / kv_heads) + 7) / 8) * sizeof(int2));
   w.own_o = w.own_ml + up(rows * 8);
   w.ml = w.own_o + up(rows * D * 4);
   w.o = w.ml + up(parts * 8);
@@ -446,10 +455,12 @@ cudaError_t launch_kv_shared(const KvAttnArgs& a, const int32_t* group_start, co
   L.group_of = reinterpret_cast<int32_t*>(a.work + w.group_of);
   L.a.own_ml = reinterpret_cast<float2*>(a.work + w.own_ml);
   L.a.own_o = reinterpret_cast<float*>(a.work + w.own_o);
+  L.a.own_parts = reinterpret_cast<int2*>(a.work + w.own_parts);
   L.ml = reinterpret_cast<float2*>(a.work + w.ml);
   L.o = reinterpret_cast<float*>(a.work + w.o);
   L.a.first = L.first;
   L.a.work = a.work + w.attn;
+  L.own = kv_own_slots(L.a, D, esize);
   if (s.tc) e = launch_shared_tc(L, D, stream);
   else e = esize == 2 ? launch_type<__nv_bfloat16>(L, D, stream, false) : launch_type<float>(L, D, stream, false);
   if (e == cudaSuccess) e = launch_kv_attention(L.a, D, esize, stream);

@@ -9,8 +9,8 @@
 // group, kv head, request, query, query head) has its part of team c at place
 // r + c R: parts of one row block lie R apart, and those of one team as their rows
 // do, so no two meet.  Each request's own tokens go through the kernels of
-// ssdv_attn.cu from position first[b] on, and a last kernel joins a row's parts in
-// the teams' order.
+// ssdv_attn.cu from position first[b] on, and a last kernel joins a row's parts of
+// both in the teams' order.
 #pragma once
 
 #define SSDV_ATTN_MORE 1
@@ -25,6 +25,7 @@ struct SharedLaunch {
   int G;
   int per, rows;               // query heads per kv head; rows of a request and kv head
   int R, tile, teams;          // rows of a row block, tokens of a tile
+  OwnSlots own;                // where parts of the requests' own rows are
   // workspace
   long long* head;             // [0]: tiles a team
   long long* unit0;            // [G]: tiles in the list before a group's
