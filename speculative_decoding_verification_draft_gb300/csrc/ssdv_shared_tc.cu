@@ -73,7 +73,7 @@ constexpr int kTmemAt = 384, kPartsAt = 512, kPlacesAt = 768, kFactorsAt = 1280,
 template <int D>
 struct Smem {
   static constexpr int kOperand = kTile * D * 2;  // 128 rows or tokens x D, or D x 128
-  static constexpr int query = 3072, keys = query + kOperand, values = keys + kKeyStages * kOperand;
+  static constexpr int query = 3 * 1024, keys = query + kOperand, values = keys + kKeyStages * kOperand;
   static constexpr int total = values + kValueStages * kOperand + 1024;  // operands begin at a multiple of 1024
 };
 // Columns of tensor memory: scores of two tiles, weights and queries (two fp16 a column),
